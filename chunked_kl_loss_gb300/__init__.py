@@ -32,7 +32,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libfckl.so")
 
 OK, ERR_ARG, ERR_INDEX, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_UNSUPPORTED, ERR_CAPACITY = range(8)
-BF16, F32 = 0, 1
+BF16, F32, F16 = 0, 1, 2
 
 _lib = None
 
@@ -77,6 +77,7 @@ def load():
     lib.fckl_topk_overlap_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32]
     lib.fckl_teacher_topk.restype = i32
     lib.fckl_teacher_topk.argtypes = [vp, vp, i32, i64, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+    scoring._set_argtypes(lib)
     lib.fckl_check.restype = i32
     lib.fckl_check.argtypes = [vp, vp]
     lib.fckl_status_string.restype = c.c_char_p
@@ -148,6 +149,15 @@ class Workspace:
             raise FcklError(ERR_UNSUPPORTED, "workspace_bytes")
         self.nbytes = n
         self.tensor = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+    @classmethod
+    def status(cls, device=None):
+        """A workspace that holds only a status word, for the calls over logits."""
+        import torch
+        ws = cls.__new__(cls)
+        ws.nbytes = 256
+        ws.tensor = torch.zeros(ws.nbytes, dtype=torch.uint8, device=device or "cuda")
+        return ws
 
     @property
     def ptr(self):
@@ -439,3 +449,9 @@ def profile_read():
     if st != OK:
         raise FcklError(st, "fckl_profile_read")
     return {n: (ms[i], int(ln[i])) for i, n in enumerate(names)}
+
+
+from . import scoring  # noqa: E402  (uses the names above)
+from .scoring import *  # noqa: E402,F401,F403
+
+__all__ += scoring.__all__

@@ -52,6 +52,8 @@ enum Kind {
   KIND_BWD_GRAD_KEPT_SIDE,      // the instances launched on the second stream beside a product
   KIND_TOPK_COLLECT_KEPT_SIDE,
   KIND_TOPK_SELECT_SIDE,
+  KIND_TOKEN_LOGPROBS,
+  KIND_TOKEN_LOGPROBS_GRAD,
   KIND_COUNT
 };
 const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", "fwd_combine",
@@ -62,7 +64,8 @@ const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", 
                                             "fwd_logits_keep",        "bwd_grad_from_logits",
                                             "topk_logits_keep",       "topk_collect_from_logits",
                                             "bwd_grad_from_logits_side", "topk_collect_from_logits_side",
-                                            "topk_select_side"};
+                                            "topk_select_side",
+                                            "token_logprobs",         "token_logprobs_grad"};
 
 // ------------------------------------------------------------------ process state
 std::mutex g_mu;
@@ -1407,7 +1410,7 @@ const char* fckl_status_string(int status) {
   switch (status) {
     case FCKL_OK: return "ok";
     case FCKL_ERR_ARG: return "invalid argument (size, null or misaligned pointer)";
-    case FCKL_ERR_INDEX: return "teacher id outside [0, V)";
+    case FCKL_ERR_INDEX: return "teacher id, or token to score, outside [0, V)";
     case FCKL_ERR_CUDA: return "CUDA error (see fckl_last_error)";
     case FCKL_ERR_TIMEOUT: return "a bounded device wait ran out";
     case FCKL_ERR_WORKSPACE: return "workspace smaller than fckl_workspace_bytes()";
@@ -1603,3 +1606,5 @@ extern "C" int fckl_forward_static(const void* H, const void* W, int dtype, cons
   }
   return FCKL_OK;
 }
+
+#include "score_host.cuh"

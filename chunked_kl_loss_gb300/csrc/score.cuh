@@ -1,0 +1,629 @@
+// Scoring kernels over logits that are at hand: log-probabilities of given tokens, entropy and
+// top alternatives of a row of logits in one pass over it, and the gradient of the
+// log-probabilities and the entropy.
+//
+// With z the logits of a row, m = max z and the row's tokens t_1..t_T (an id of -1 is an empty
+// slot):
+//   s       = sum_v exp(z_v - m),  u = sum_v (z_v - m) exp(z_v - m)
+//   logp_t  = (z_t - m) - log s                    (empty slot: 0)
+//   entropy = log s - u / s                        (= - sum_v q_v log q_v, q = softmax(z))
+//   dz_v    = sum_t g_t [v = t] - q_v (sum_t g_t + g_e (log q_v + entropy))
+// The pair (m, log s) is kept, not their sum: where a mask leaves a row with nothing but the
+// type's lowest value, log s is lost in the rounding of m + log s.
+// A row whose logits are all -inf has m = -inf, log s = 0, log-probabilities -inf, entropy 0 and
+// a zero gradient. A NaN or +inf among a row's logits makes its results NaN.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+#include "simt.cuh"
+
+namespace fckl {
+
+constexpr int SCORE_THREADS = 256;
+constexpr int SCORE_GV = 4;            // 16-byte vectors of a group
+constexpr int SCORE_MAX_GROUPS = 8192; // group maxima that one block keeps in shared memory
+constexpr int TOKENS_MAX = 1024;       // given tokens, and alternatives, of a row
+constexpr float LN2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------- values of a row
+// max that keeps a NaN (fmaxf drops it, and a row with one would pass for a good row)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) {
+  return __float2half_rn(v);
+}
+
+// The two values of a 32-bit word, lower address first.
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, __nv_bfloat16) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b, __half) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack16(uint4 w, float (&x)[16 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  } else {
+    unpack2(w.x, x[0], x[1], T{});
+    unpack2(w.y, x[2], x[3], T{});
+    unpack2(w.z, x[4], x[5], T{});
+    unpack2(w.w, x[6], x[7], T{});
+  }
+}
+
+// A row seen as aligned 16-byte vectors: vector i covers columns [VE i - mis, VE i - mis + VE),
+// where mis is the row's distance, in values, from the 16-byte boundary below it. Rows of any
+// alignment (odd V, sliced views) so keep wide loads; columns outside [0, V) are never read.
+template <typename T>
+struct RowVecs {
+  static constexpr int VE = 16 / sizeof(T);
+  const T* row;
+  int V, mis, nvec;
+  __device__ __forceinline__ RowVecs(const T* r, int V_) : row(r), V(V_) {
+    mis = static_cast<int>((reinterpret_cast<uintptr_t>(r) & 15u) / sizeof(T));
+    nvec = (V + mis + VE - 1) / VE;
+  }
+  __device__ __forceinline__ int col(int i) const { return i * VE - mis; }
+  __device__ __forceinline__ bool whole(int i) const {
+    const int c = col(i);
+    return c >= 0 && c + VE <= V;
+  }
+  __device__ __forceinline__ uint4 raw(int i) const {
+    return *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(col(i)));
+  }
+  // Values of vector i; -inf outside the row.
+  __device__ __forceinline__ void load(int i, float (&x)[VE]) const {
+    if (i < nvec && whole(i)) {
+      unpack16<T>(raw(i), x);
+    } else {
+      const int c = col(i);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) x[j] = (i < nvec && c + j >= 0 && c + j < V) ? to_f32(row[c + j]) : -INFINITY;
+    }
+  }
+};
+
+// ---------------------------------------------------------------- running statistics
+// m: maximum so far, l = sum exp(z - m), t = sum y exp(z - m) with y = (z - m) log2(e).
+// y is formed from the difference z - m, which is exact near the maximum and has no overflow at
+// the lowest values of a type; it is held at or above -256, where 2^y is zero, so that masked
+// values add 0 * -256 rather than 0 * -inf.
+struct RowStat {
+  float m = -INFINITY, l = 0.f, t = 0.f;
+};
+constexpr float Y_FLOOR = -256.f;
+
+__device__ __forceinline__ RowStat merge(const RowStat& a, const RowStat& b) {
+  RowStat r;
+  r.m = fmaxf(a.m, b.m);
+  if (r.m == -INFINITY) {  // nothing yet on either side (or only a NaN, which the sums keep)
+    r.l = a.l + b.l;
+    r.t = a.t + b.t;
+    return r;
+  }
+  const float ya = fmaxf((a.m - r.m) * LOG2E, Y_FLOOR), yb = fmaxf((b.m - r.m) * LOG2E, Y_FLOOR);
+  const float fa = ex2_approx(ya), fb = ex2_approx(yb);
+  r.l = a.l * fa + b.l * fb;
+  r.t = fa * (a.t + ya * a.l) + fb * (b.t + yb * b.l);
+  return r;
+}
+
+// Adds one vector's values, whose maximum is at most s.m (or NaN).
+template <int VE>
+__device__ __forceinline__ void add_values(RowStat& s, const float (&x)[VE]) {
+#pragma unroll
+  for (int j = 0; j < VE; ++j) {
+    const float y = max_nan((x[j] - s.m) * LOG2E, Y_FLOOR);
+    const float e = ex2_approx(y);
+    s.l += e;
+    s.t = fmaf(y, e, s.t);
+  }
+}
+
+// Order of (logit, id) pairs in one 64-bit number: larger logit first, then smaller id.
+__device__ __forceinline__ uint32_t logit_key(float z) { return order_key(z + 0.f); }  // -0 counts as +0
+__device__ __forceinline__ unsigned long long pair_key(float z, int id) {
+  return (static_cast<unsigned long long>(logit_key(z)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+}
+
+// Sum over the block of one int per thread; every thread gets it. `buf` holds one int per warp.
+__device__ __forceinline__ int block_sum(int v, int* buf) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int s = 0;
+#pragma unroll
+  for (int w = 0; w < SCORE_THREADS / 32; ++w) s += buf[w];
+  return s;
+}
+
+// Descending bitonic sort of n (a power of two) 64-bit keys in shared memory.
+__device__ __forceinline__ void block_sort(unsigned long long* a, int n) {
+  for (int k = 2; k <= n; k <<= 1) {
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < n / 2; i += SCORE_THREADS) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+        const unsigned long long x = a[lo], y = a[hi];
+        if ((x < y) == ((lo & k) == 0)) {
+          a[lo] = y;
+          a[hi] = x;
+        }
+      }
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int pow2_at_least(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+struct ScoreParams {
+  const void* logits;
+  int64_t ld;
+  const int32_t* tokens;
+  int V, T, top;
+  int cand_cap;  // candidates that fit in shared memory (a power of two)
+  int groups;    // group maxima kept per block
+  int gsteps;    // steps of SCORE_GV vectors per thread that make up a group
+  int split;     // blocks (of a cluster) per row
+  float* logp;
+  float* entropy;
+  float* norm;
+  int32_t* top_idx;
+  float* top_logp;
+  unsigned* status;
+};
+
+// One block per row, or a cluster of `split` blocks that share a row's vectors in order.
+//
+// Statistics: each thread runs over its vectors once and keeps (m, l, t); the block and then the
+// cluster merge them in a fixed order.
+// Alternatives: the pass also leaves in shared memory the maximum of every group of vectors (the
+// ones that one thread took in one step). tau is a lower bound on the block's K-th largest logit:
+// at least K groups have their maximum at or above it (or tau = -inf with fewer groups than K).
+// Only groups whose maximum is above tau can hold a logit above tau; there are about K, and they
+// are read again (from L2) to collect their logits above tau, C of them.
+//   C <  K: the K-th largest logit is tau itself; the first K - C ids with logit tau, found by a
+//           scan in id order, complete the set.
+//   C >= K: the set is among the collected ones.
+//   C above the room: tau is raised by bisection over the live groups' logits until the logits
+//           above it fit (or it is the K-th largest itself, which is the first case).
+// The set is sorted by (logit, id). Each block of a cluster does this for its share of the row,
+// and block 0 sorts the blocks' sets together. Exact for every input, ties included.
+template <typename T>
+__global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const ScoreParams p) {
+  namespace cg = cooperative_groups;
+  constexpr int VE = 16 / sizeof(T);
+  constexpr int WARPS = SCORE_THREADS / 32;
+  extern __shared__ __align__(16) unsigned char score_smem[];
+  unsigned long long* cand = reinterpret_cast<unsigned long long*>(score_smem);  // [cand_cap]
+  uint32_t* gkey = reinterpret_cast<uint32_t*>(cand + (p.top ? p.cand_cap : 0));  // [groups]
+  __shared__ RowStat sstat[WARPS];
+  __shared__ RowStat bstat;  // this block's share of the row
+  __shared__ int ibuf[WARPS];
+  __shared__ int n_cand, n_live;
+  __shared__ uint16_t live[2 * TOKENS_MAX];
+
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = p.split > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+  const int64_t row = blockIdx.x / p.split;
+  const RowVecs<T> rv(static_cast<const T*>(p.logits) + row * p.ld, p.V);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // this block's vectors [v0, v1) and columns [c0, c1)
+  const int per = (rv.nvec + p.split - 1) / p.split;
+  const int v0 = min(rank * per, rv.nvec), v1 = min(v0 + per, rv.nvec);
+  const int c0 = max(0, rv.col(v0)), c1 = min(p.V, rv.col(v1));
+
+  // ---- statistics and group maxima
+  RowStat s;
+  constexpr int STEP = SCORE_THREADS * SCORE_GV;
+  const int steps = (v1 - v0 + STEP - 1) / STEP;
+  float gmax = -INFINITY;
+  for (int st = 0, in_group = 0, g = tid; st < steps; ++st) {
+    float x[SCORE_GV][VE];
+#pragma unroll
+    for (int j = 0; j < SCORE_GV; ++j) {
+      const int i = v0 + st * STEP + j * SCORE_THREADS + tid;
+      if (i < v1) {
+        rv.load(i, x[j]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[j][e] = -INFINITY;
+      }
+    }
+    float m = x[0][0];
+#pragma unroll
+    for (int j = 0; j < SCORE_GV; ++j)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) m = max_nan(m, x[j][e]);
+    if (!(m <= s.m)) {  // a new maximum (or a NaN): bring the sums to it
+      RowStat none;
+      none.m = m;
+      s = merge(s, none);
+    }
+    if (s.m != -INFINITY || m != m) {
+#pragma unroll
+      for (int j = 0; j < SCORE_GV; ++j) add_values<VE>(s, x[j]);
+    }
+    if (p.top) {
+      gmax = fmaxf(gmax, m);
+      if (++in_group == p.gsteps || st == steps - 1) {
+        gkey[g] = logit_key(gmax);
+        g += SCORE_THREADS;
+        gmax = -INFINITY;
+        in_group = 0;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    RowStat b;
+    b.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+    b.l = __shfl_xor_sync(0xffffffffu, s.l, o);
+    b.t = __shfl_xor_sync(0xffffffffu, s.t, o);
+    s = merge(s, b);
+  }
+  if (lane == 0) sstat[warp] = s;
+  if (tid == 0) n_cand = n_live = 0;
+  __syncthreads();
+  s = sstat[0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) s = merge(s, sstat[w]);
+  if (tid == 0) bstat = s;
+
+  // ---- this block's alternatives: cand[0..k), sorted
+  const int k = min(p.top, c1 - c0);
+  if (k > 0 && !(s.l != s.l)) {
+    const int per_group = p.gsteps * SCORE_GV;
+    const int ng = ((steps + p.gsteps - 1) / p.gsteps) * SCORE_THREADS;
+    // tau: the largest prefix of key bits that at least k group maxima reach, refined only until
+    // few more than k do
+    uint32_t tau = order_key(-INFINITY);
+    if (ng >= k) {
+      const int enough = k + k / 4 + 16;
+      uint32_t prefix = 0;
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t c = prefix | (1u << bit);
+        int n = 0;
+        for (int g = tid; g < ng; g += SCORE_THREADS) n += gkey[g] >= c;
+        n = block_sum(n, ibuf);
+        if (n >= k) {
+          prefix = c;
+          if (n <= enough) break;
+        }
+      }
+      tau = max(prefix, tau);
+    }
+    for (int g = tid; g < ng; g += SCORE_THREADS) {
+      if (gkey[g] > tau) {  // at most `enough` of them, or fewer than k at an exact tau
+        const int at = atomicAdd(&n_live, 1);
+        live[at] = static_cast<uint16_t>(g);
+      }
+    }
+    __syncthreads();
+    const int items = n_live * per_group;
+    auto item_vec = [&](int it) {  // vector of item it of the live groups
+      const int g = live[it / per_group], j = it % per_group;
+      const int st = (g / SCORE_THREADS) * p.gsteps + j / SCORE_GV;
+      return v0 + st * STEP + (j % SCORE_GV) * SCORE_THREADS + g % SCORE_THREADS;
+    };
+    auto collect = [&]() {  // logits above tau into cand (as many as fit); n_cand counts them all
+      for (int it = tid; it < items; it += SCORE_THREADS) {
+        const int i = item_vec(it);
+        if (i >= v1) continue;
+        float x[VE];
+        rv.load(i, x);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          if (logit_key(x[e]) > tau) {  // columns outside the row are -inf, never above tau
+            const int at = atomicAdd(&n_cand, 1);
+            if (at < p.cand_cap) cand[at] = pair_key(x[e], rv.col(i) + e);
+          }
+        }
+      }
+      __syncthreads();
+    };
+    collect();
+    if (n_cand > p.cand_cap) {
+      // bisect: lo is reached by at least k logits; stop when those above it fit
+      uint32_t lo = tau, hi = 0xffffffffu;
+      while (hi - lo > 1) {
+        const uint32_t mid = lo + (hi - lo) / 2;
+        int n = 0;
+        for (int it = tid; it < items; it += SCORE_THREADS) {
+          const int i = item_vec(it);
+          if (i >= v1) continue;
+          float x[VE];
+          rv.load(i, x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) n += logit_key(x[e]) >= mid;
+        }
+        n = block_sum(n, ibuf);
+        if (n >= k) {
+          lo = mid;
+          if (n <= p.cand_cap) break;
+        } else {
+          hi = mid;
+        }
+      }
+      tau = lo;
+      __syncthreads();
+      if (tid == 0) n_cand = 0;
+      __syncthreads();
+      collect();
+    }
+    int c = n_cand;
+    if (c < k) {
+      // ids in order whose logit is tau, until the set is complete
+      for (int base = v0; base < v1 && c < k; base += SCORE_THREADS) {
+        const int i = base + tid;
+        uint32_t hit = 0;
+        float x[VE];
+        if (i < v1) {
+          rv.load(i, x);
+          const int col = rv.col(i);
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (col + e >= 0 && col + e < p.V && logit_key(x[e]) == tau) hit |= 1u << e;
+        }
+        const int mine = __popc(hit);
+        int before = mine;  // inclusive prefix within the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += v;
+        }
+        __syncthreads();
+        if (lane == 31) ibuf[warp] = before;
+        __syncthreads();
+        int total = 0, at = c + before - mine;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          if (w < warp) at += ibuf[w];
+          total += ibuf[w];
+        }
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (hit & (1u << e)) {
+            if (at < k) cand[at] = pair_key(x[e], rv.col(i) + e);
+            ++at;
+          }
+        c += total;
+      }
+      c = min(c, k);
+    }
+    const int n2 = pow2_at_least(c);
+    for (int i = c + tid; i < n2; i += SCORE_THREADS) cand[i] = 0ull;
+    block_sort(cand, n2);
+  }
+
+  // ---- the whole row, in block 0 of the cluster
+  if (p.split > 1) {
+    cluster.sync();
+    if (rank == 0) {
+      const RowStat mine = s;
+      s = mine;
+      for (int r = 1; r < p.split; ++r) s = merge(s, *cluster.map_shared_rank(&bstat, r));
+      if (p.top && !(s.l != s.l)) {
+        int n = k;
+        for (int r = 1; r < p.split; ++r) {
+          const int a = max(0, rv.col(min(r * per, rv.nvec)));
+          const int b = min(p.V, rv.col(min(min(r * per, rv.nvec) + per, rv.nvec)));
+          const int kr = min(p.top, max(0, b - a));
+          const unsigned long long* theirs = cluster.map_shared_rank(cand, r);
+          for (int i = tid; i < kr; i += SCORE_THREADS) cand[n + i] = theirs[i];
+          n += kr;
+        }
+        const int n2 = pow2_at_least(n);
+        for (int i = n + tid; i < n2; i += SCORE_THREADS) cand[i] = 0ull;
+        block_sort(cand, n2);
+      }
+    }
+    cluster.sync();  // the others' shared memory has been read
+    if (rank != 0) return;
+  }
+
+  const bool nothing = s.m == -INFINITY && s.l == 0.f;
+  const float log_s = nothing ? 0.f : logf(s.l);
+  if (tid == 0) {
+    const float ent = nothing ? 0.f : log_s - LN2 * (s.t / s.l);
+    p.entropy[row] = ent < 0.f ? 0.f : ent;  // rounding may leave a sharp row just below zero
+    p.norm[2 * row] = s.m;
+    p.norm[2 * row + 1] = log_s;
+  }
+  for (int t = tid; t < p.T; t += SCORE_THREADS) {
+    const int id = p.tokens[row * p.T + t];
+    float lp = 0.f;
+    if (id < -1 || id >= p.V) {
+      atomicOr(p.status, ST_BAD_INDEX);
+      lp = NAN;
+    } else if (id >= 0) {
+      lp = nothing ? -INFINITY : (to_f32(rv.row[id]) - s.m) - log_s;
+    }
+    p.logp[row * p.T + t] = lp;
+  }
+  const bool bad = s.l != s.l;
+  for (int i = tid; i < p.top; i += SCORE_THREADS) {
+    int id = i;
+    float lp = NAN;
+    if (!bad) {
+      const unsigned long long c = cand[i];
+      id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(c));
+      lp = nothing ? -INFINITY : (order_key_inv(static_cast<uint32_t>(c >> 32)) - s.m) - log_s;
+    }
+    p.top_idx[row * p.top + i] = id;
+    p.top_logp[row * p.top + i] = lp;
+  }
+}
+
+// ---------------------------------------------------------------- gradient
+struct ScoreGradParams {
+  const void* logits;  // may be the same array as dlogits
+  int64_t ld, ld_out;
+  const int32_t* tokens;
+  int V, T, segs;
+  const float* norm;
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;  // null: zero
+  void* dlogits;
+  unsigned* status;
+};
+constexpr int SCORE_GRAD_VECS = 8;  // vectors per thread of a segment
+constexpr int SCORE_GRAD_STEP = SCORE_THREADS * SCORE_GRAD_VECS;
+
+// A block takes one segment of a row: dense part first, then the (few) tokens of the row that
+// fall into the segment, each written once with all its slots' gradients. Their logits are read
+// before anything is written, so dlogits may be logits itself. A row without any upstream
+// gradient is written as zeros without being read (positions that a loss masks out may hold
+// anything).
+template <typename T>
+__global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_grad_kernel(const ScoreGradParams p) {
+  constexpr int VE = 16 / sizeof(T);
+  constexpr int WARPS = SCORE_THREADS / 32;
+  constexpr int PER = TOKENS_MAX / SCORE_THREADS;
+  __shared__ int ids[TOKENS_MAX];
+  __shared__ float gs[TOKENS_MAX];
+  __shared__ float wsum[WARPS];
+  __shared__ int wany[WARPS];
+  const int64_t row = blockIdx.x / p.segs;
+  const int seg = static_cast<int>(blockIdx.x % p.segs);
+  const T* zrow = static_cast<const T*>(p.logits) + row * p.ld;
+  T* orow = static_cast<T*>(p.dlogits) + row * p.ld_out;
+  const RowVecs<T> ov(orow, p.V);  // vectors of the output: every store is wide but the ends
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int v0 = seg * SCORE_GRAD_STEP;
+  if (v0 >= ov.nvec) return;
+  const int v1 = min(v0 + SCORE_GRAD_STEP, ov.nvec);
+  const int c0 = max(0, ov.col(v0)), c1 = min(p.V, ov.col(v1));
+
+  // the row's tokens and their gradients
+  float sg = 0.f;
+  int any = 0;
+  float zt[PER];
+#pragma unroll
+  for (int a = 0; a < PER; ++a) {
+    const int t = a * SCORE_THREADS + tid;
+    zt[a] = 0.f;
+    if (t < p.T) {
+      const int id = p.tokens[row * p.T + t];
+      const bool ok = id >= 0 && id < p.V;
+      if (id < -1 || id >= p.V) atomicOr(p.status, ST_BAD_INDEX);
+      const float g = ok ? p.g_logp[row * p.T + t] : 0.f;
+      ids[t] = ok ? id : -1;
+      gs[t] = g;
+      sg += g;
+      any |= g != 0.f;
+      if (ok && id >= c0 && id < c1) zt[a] = to_f32(zrow[id]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sg += __shfl_xor_sync(0xffffffffu, sg, o);
+  any = __any_sync(0xffffffffu, any);
+  if (lane == 0) {
+    wsum[warp] = sg;
+    wany[warp] = any;
+  }
+  __syncthreads();
+  sg = 0.f;
+  any = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    sg += wsum[w];
+    any |= wany[w];
+  }
+  const float ge = p.g_entropy ? p.g_entropy[row] : 0.f;
+  const float m = p.norm[2 * row], log_s = p.norm[2 * row + 1];
+  const bool zero = (!any && ge == 0.f) || m == -INFINITY;
+  const float a0 = sg + ge * p.entropy[row];
+  // dense part: - q (a0 + ge log q)
+  auto dense = [&](float z) {
+    const float lq = max_nan((z - m) - log_s, -1e30f);  // masked: 0 * -1e30 rather than 0 * -inf
+    return -ex2_approx(lq * LOG2E) * fmaf(ge, lq, a0);
+  };
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(zrow) & 15u) / sizeof(T)) - ov.mis;
+  const bool same = shift == 0;  // logits and output vectors line up
+#pragma unroll
+  for (int j = 0; j < SCORE_GRAD_VECS; ++j) {
+    const int i = v0 + j * SCORE_THREADS + tid;
+    if (i >= v1) continue;
+    const int c = ov.col(i);
+    if (ov.whole(i)) {
+      float x[VE];
+      if (zero) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[e] = 0.f;
+      } else {
+        if (same) {
+          unpack16<T>(*reinterpret_cast<const uint4*>(zrow + c), x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) x[e] = to_f32(zrow[c + e]);
+        }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[e] = dense(x[e]);
+      }
+      __align__(16) T y[VE];
+#pragma unroll
+      for (int e = 0; e < VE; ++e) y[e] = from_f32<T>(x[e]);
+      *reinterpret_cast<uint4*>(orow + c) = *reinterpret_cast<const uint4*>(y);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (c + e >= 0 && c + e < p.V) orow[c + e] = from_f32<T>(zero ? 0.f : dense(to_f32(zrow[c + e])));
+    }
+  }
+  if (zero) return;
+  __syncthreads();  // the dense values are written; the tokens' entries replace theirs
+#pragma unroll
+  for (int a = 0; a < PER; ++a) {
+    const int t = a * SCORE_THREADS + tid;
+    if (t >= p.T) continue;
+    const int id = ids[t];
+    if (id < c0 || id >= c1) continue;
+    float g = 0.f;
+    bool first = true;
+    for (int u = 0; u < p.T; ++u) {
+      if (ids[u] != id) continue;
+      if (u < t) {
+        first = false;
+        break;
+      }
+      g += gs[u];
+    }
+    if (first) orow[id] = from_f32<T>(dense(zt[a]) + g);
+  }
+}
+
+}  // namespace fckl

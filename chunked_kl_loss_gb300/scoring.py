@@ -1,0 +1,215 @@
+"""Scoring of given tokens: log-probabilities, entropy and most probable tokens, with gradients.
+
+Argument marshalling only, as in the package itself: every step runs in the CUDA library.
+
+    logp, entropy, norm, top_idx, top_logp = fckl.token_logprobs(logits, tokens, top=20)
+    dlogits = fckl.token_logprobs_backward(logits, tokens, norm, entropy, g_logp, g_entropy)
+    logp, entropy = fckl.differentiable_token_logprobs(logits, tokens)         # autograd
+
+``logits [N, V]`` are bf16, fp16 or fp32 (rows may lie apart: only the last dimension has to be
+dense); ``tokens [N, T]`` are int32, -1 marks an empty slot. Logits of -inf are masked tokens.
+
+``stream`` launches on a stream other than the current one: outputs are then allocated for that
+stream and the inputs are marked as used on it; making the inputs' data ready there is the
+caller's part. Under CUDA graph capture call the functions that take gradients directly rather
+than autograd (whose accumulation nodes remember the stream that an eager pass used).
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import chunked_kl_loss_gb300 as _pkg
+
+__all__ = ["token_logprobs", "token_logprobs_backward", "differentiable_token_logprobs"]
+
+_status_ws = {}  # device index -> workspace that holds only a status word
+
+
+def _set_argtypes(lib):
+    c = ctypes
+    vp, i64, i32, sz = c.c_void_p, c.c_int64, c.c_int, c.c_size_t
+    lib.fckl_token_logprobs.restype = i32
+    lib.fckl_token_logprobs.argtypes = [vp, i32, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fckl_token_logprobs_backward.restype = i32
+    lib.fckl_token_logprobs_backward.argtypes = [vp, i32, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, i64, vp, sz, vp]
+
+
+def _status_workspace(device):
+    """The device's status word: zeroed once, shared by every call that is given no workspace (the
+    word only gathers bits, so calls on several streams may share it)."""
+    import torch
+    ws = _status_ws.get(device.index)
+    if ws is None:
+        ws = _pkg.Workspace.status(device)
+        if torch.cuda.is_current_stream_capturing():
+            return ws  # belongs to the graph being captured
+        torch.cuda.current_stream(device).synchronize()  # zeroed before any stream uses it
+        _status_ws[device.index] = ws
+    return ws
+
+
+def _ws(ws, device):
+    import weakref
+    if ws is None:
+        ws = _status_workspace(device)
+        _pkg._last_ws = ws
+    else:
+        _pkg._last_ws = weakref.ref(ws)
+    return ws
+
+
+def _value_code(t, what):
+    import torch
+    code = {torch.bfloat16: _pkg.BF16, torch.float16: _pkg.F16, torch.float32: _pkg.F32}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _on_device(device, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device != device):
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {device}")
+
+
+def _dense(name, t, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {list(shape)}, got {list(t.shape)}")
+
+
+def _rows(name, t):
+    """Row pitch of a [N, V] tensor whose rows are dense."""
+    N, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    if N <= 1:
+        return V
+    if t.stride(0) < V:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.stride(0)
+
+
+def _for_stream(stream, *inputs):
+    """Context for allocations that `stream` will use (None: the current stream)."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _logits_args(logits, tokens):
+    import torch
+    if logits.dim() != 2 or tokens.dim() != 2 or tokens.shape[0] != logits.shape[0]:
+        raise ValueError("expected logits [N,V] and tokens [N,T]")
+    code = _value_code(logits, "logits")
+    N, V = logits.shape
+    T = tokens.shape[1]
+    _dense("tokens", tokens, torch.int32, (N, T))
+    return code, N, V, T, _rows("logits", logits)
+
+
+def token_logprobs(logits, tokens, top=0, ws=None, stream=None):
+    """(logp fp32 [N, T], entropy fp32 [N], norm fp32 [N, 2], top_idx int32 [N, top],
+    top_logp fp32 [N, top]) of logits [N, V]: the given tokens' log-probabilities, the entropy,
+    (max z, log sum exp(z - max z)), and the ``top`` most probable tokens, largest first, equal
+    ones by smaller id. An id outside [0, V) is reported by check() (its logp is NaN)."""
+    import torch
+    code, N, V, T, ld = _logits_args(logits, tokens)
+    dev = logits.device
+    _on_device(dev, logits=logits, tokens=tokens)
+    f32 = torch.float32
+    with _for_stream(stream, logits, tokens):
+        ws = _ws(ws, dev)
+        logp = torch.empty(N, T, dtype=f32, device=dev)
+        entropy = torch.empty(N, dtype=f32, device=dev)
+        norm = torch.empty(N, 2, dtype=f32, device=dev)
+        top_idx = torch.empty(N, max(top, 0), dtype=torch.int32, device=dev)
+        top_logp = torch.empty(N, max(top, 0), dtype=f32, device=dev)
+    p = _pkg._ptr
+    st = _pkg.load().fckl_token_logprobs(p(logits), code, ld, p(tokens), N, V, T, top, p(logp), p(entropy), p(norm),
+                                         p(top_idx), p(top_logp), ws.ptr, ws.nbytes, _pkg._stream_ptr(stream))
+    if st != _pkg.OK:
+        raise _pkg.FcklError(st, "fckl_token_logprobs")
+    return logp, entropy, norm, top_idx, top_logp
+
+
+def token_logprobs_backward(logits, tokens, norm, entropy, g_logp, g_entropy=None, out=None, ws=None, stream=None):
+    """Gradient [N, V], of the logits' type, of sum g_logp * logp + sum g_entropy * entropy with
+    respect to the logits; ``norm`` and ``entropy`` as token_logprobs returned them. ``out`` may be
+    ``logits`` itself, whose values are then lost."""
+    import torch
+    code, N, V, T, ld = _logits_args(logits, tokens)
+    dev = logits.device
+    _on_device(dev, logits=logits, tokens=tokens, norm=norm, entropy=entropy, g_logp=g_logp, g_entropy=g_entropy,
+               out=out)
+    f32 = torch.float32
+    _dense("norm", norm, f32, (N, 2))
+    _dense("entropy", entropy, f32, (N,))
+    _dense("g_logp", g_logp, f32, (N, T))
+    if g_entropy is not None:
+        _dense("g_entropy", g_entropy, f32, (N,))
+    if out is not None and (out.dtype != logits.dtype or out.shape != logits.shape):
+        raise ValueError("out must have the logits' type and shape")
+    with _for_stream(stream, logits, tokens, norm, entropy, g_logp, g_entropy, out):
+        ws = _ws(ws, dev)
+        if out is None:
+            out = torch.empty(N, V, dtype=logits.dtype, device=dev)
+    p = _pkg._ptr
+    st = _pkg.load().fckl_token_logprobs_backward(p(logits), code, ld, p(tokens), N, V, T, p(norm), p(entropy),
+                                                  p(g_logp), p(g_entropy), p(out), _rows("out", out), ws.ptr,
+                                                  ws.nbytes, _pkg._stream_ptr(stream))
+    if st != _pkg.OK:
+        raise _pkg.FcklError(st, "fckl_token_logprobs_backward")
+    return out
+
+
+def _upstream(g, shape, device):
+    """An upstream gradient as the library reads it: dense fp32 (autograd hands over expanded ones)."""
+    import torch
+    if g is None:
+        return torch.zeros(shape, dtype=torch.float32, device=device)
+    return g.to(torch.float32).contiguous()
+
+
+def _autograd_function():
+    import torch
+
+    class TokenLogprobs(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, tokens):
+            logp, entropy, norm, _, _ = token_logprobs(logits, tokens)
+            ctx.save_for_backward(logits, tokens, norm, entropy)
+            ctx.set_materialize_grads(False)
+            return logp, entropy
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, g_logp, g_entropy):
+            logits, tokens, norm, entropy = ctx.saved_tensors
+            if g_logp is None and g_entropy is None:
+                return None, None
+            ge = None if g_entropy is None else _upstream(g_entropy, None, logits.device)
+            gl = _upstream(g_logp, tuple(tokens.shape), logits.device)
+            return token_logprobs_backward(logits, tokens, norm, entropy, gl, ge), None
+
+    return TokenLogprobs
+
+
+_TokenLogprobs = None
+
+
+def differentiable_token_logprobs(logits, tokens):
+    """(logp [N, T], entropy [N]) of logits [N, V], differentiable in the logits."""
+    global _TokenLogprobs
+    if _TokenLogprobs is None:
+        _TokenLogprobs = _autograd_function()
+    return _TokenLogprobs.apply(logits, tokens)

@@ -65,7 +65,7 @@ extern "C" {
 typedef enum {
     FCKL_OK = 0,
     FCKL_ERR_ARG = 1,         /* bad size, null or misaligned pointer */
-    FCKL_ERR_INDEX = 2,       /* a teacher id outside [0, V) (device-detected) */
+    FCKL_ERR_INDEX = 2,       /* a teacher id, or a token to score, outside [0, V) (device-detected) */
     FCKL_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed; see fckl_last_error() */
     FCKL_ERR_TIMEOUT = 4,     /* a bounded device wait ran out (device-detected) */
     FCKL_ERR_WORKSPACE = 5,   /* ws_bytes below fckl_workspace_bytes() */
@@ -74,7 +74,8 @@ typedef enum {
                                  holds (device-detected; that position's output is not exact) */
 } fckl_status;
 
-typedef enum { FCKL_BF16 = 0, FCKL_F32 = 1 } fckl_dtype;
+/* FCKL_F16 is taken by the calls over logits and by fckl_block_quantize only. */
+typedef enum { FCKL_BF16 = 0, FCKL_F32 = 1, FCKL_F16 = 2 } fckl_dtype;
 
 /* Bytes of device workspace that fckl_forward, fckl_backward and fckl_forward_backward need
  * for this shape ("Hugging Face：让知识蒸馏廉价到可大规模运行", paragraph "Fused, chunked KL
@@ -228,6 +229,49 @@ int fckl_teacher_topk(const void* Ht, const void* Wt, int dtype,
                       int64_t N, int d, int V, int K, int chunk,
                       int32_t* idx, float* logp,
                       void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Scoring of given tokens. Interface additions, no counterpart on the pages: the loss reads a
+ * student through the teacher's tokens only; these read a model's log-probabilities of any given
+ * tokens, its entropy and its most probable tokens, with gradients.
+ *
+ * With z the V logits of a position, q = softmax(z) and its tokens t_1..t_T:
+ *   logp_t  = z_t - log sum_v exp(z_v)
+ *   entropy = - sum_v q_v log q_v                        (0 log 0 = 0)
+ *   norm    = (m, log sum_v exp(z_v - m)),  m = max z    (their sum is the log-partition)
+ *   dz_v    = sum_t g_t [v = t] - q_v (sum_t g_t + g_e (log q_v + entropy))
+ * tokens is int32 [N, T], 0 <= T <= 1024, in any order and with repeats; -1 marks an empty slot
+ * (logp 0, no gradient). Any other id outside [0, V) sets FCKL_ERR_INDEX in the status word; its
+ * logp is NaN and it takes no part in the gradient. A position with nothing left (every logit
+ * -inf) has logp -inf, entropy 0, norm (-inf, 0) and a zero gradient; a NaN or +inf among a
+ * position's logits makes its results NaN (its alternatives: ids 0..top-1).
+ *
+ * The workspace of the calls over logits holds only the status word: at least 256 bytes, zeroed
+ * once by the caller before its first use. These calls OR into the word and do not clear it
+ * (no launch is spent on that); fckl_check reads and clears it. N = 0 is allowed and does
+ * nothing. */
+
+/* Statistics of logits [N, V], of type FCKL_BF16, FCKL_F16 or FCKL_F32; row n starts ld elements
+ * after row n-1 (ld >= V; rows need only the alignment of their elements).
+ *   logp     : fp32 [N, T] (may be NULL when T = 0)
+ *   entropy  : fp32 [N]
+ *   norm     : fp32 [N, 2], kept for the backward call
+ *   top_idx  : int32 [N, top], the `top` largest logits' ids, largest first, equal logits by
+ *              smaller id; 0 <= top <= min(V, 1024). NULL when top = 0, as top_logp.
+ *   top_logp : fp32 [N, top], their log-probabilities
+ * One launch that reads the logits once. */
+int fckl_token_logprobs(const void* logits, int dtype, int64_t ld, const int32_t* tokens, int64_t N, int V, int T,
+                        int top, float* logp, float* entropy, float* norm, int32_t* top_idx, float* top_logp,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient with respect to the logits: g_logp fp32 [N, T] and g_entropy fp32 [N] (NULL: zero) are
+ * the upstream derivatives, norm and entropy what fckl_token_logprobs wrote for the same logits.
+ *   dlogits : [N, V] of the logits' type, rows ld_out >= V elements apart. It may be `logits`
+ *             itself (then ld_out = ld); otherwise the two must not overlap.
+ * A position without any upstream gradient gets zeros, whatever its logits hold. */
+int fckl_token_logprobs_backward(const void* logits, int dtype, int64_t ld, const int32_t* tokens, int64_t N, int V,
+                                 int T, const float* norm, const float* entropy, const float* g_logp,
+                                 const float* g_entropy, void* dlogits, int64_t ld_out, void* ws, size_t ws_bytes,
+                                 void* stream);
 
 /* Interface addition, no counterpart on the pages (they describe no device interface).
  * Synchronises `stream`, returns the status found on the device by the last call that
