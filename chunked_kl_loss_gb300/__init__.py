@@ -129,7 +129,8 @@ class Workspace:
     of one chunk's buffers with which forward_backward overlaps consecutive chunks), "topk"
     (teacher cache builder keeping each chunk's logits), "topk_overlap" (the same plus a second
     set of one chunk's buffers, with which the builder overlaps consecutive chunks) or
-    "topk_min" (the builder's minimum, which projects each chunk twice)."""
+    "topk_min" (the builder's minimum, which projects each chunk twice); "projected" and
+    "projected_backward" (projected_logprobs and its gradient; K is then the tokens per position)."""
 
     def __init__(self, N, d, V, K, chunk, dtype=BF16, device=None, kind="loss"):
         import torch
@@ -143,6 +144,9 @@ class Workspace:
             n = workspace_bytes(N, d, V, K, chunk, dtype)
         elif kind == "loss_overlap":
             n = overlap_workspace_bytes(N, d, V, K, chunk, dtype)
+        elif kind in ("projected", "projected_backward"):
+            n = int(load().fckl_projected_logprobs_workspace_bytes(N, d, V, K, chunk, dtype,
+                                                                   int(kind == "projected_backward")))
         else:
             raise ValueError(f"unknown workspace kind {kind!r}")
         if n == 0:

@@ -54,6 +54,10 @@ enum Kind {
   KIND_TOPK_SELECT_SIDE,
   KIND_TOKEN_LOGPROBS,
   KIND_TOKEN_LOGPROBS_GRAD,
+  KIND_TOKEN_ORDER,
+  KIND_HEAD_LOGITS,
+  KIND_HEAD_COMBINE,
+  KIND_HEAD_GRAD,
   KIND_COUNT
 };
 const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", "fwd_combine",
@@ -65,7 +69,9 @@ const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", 
                                             "topk_logits_keep",       "topk_collect_from_logits",
                                             "bwd_grad_from_logits_side", "topk_collect_from_logits_side",
                                             "topk_select_side",
-                                            "token_logprobs",         "token_logprobs_grad"};
+                                            "token_logprobs",         "token_logprobs_grad",
+                                            "token_order",            "head_logits_stats",
+                                            "head_combine",           "head_logit_grad"};
 
 // ------------------------------------------------------------------ process state
 std::mutex g_mu;
@@ -1608,3 +1614,4 @@ extern "C" int fckl_forward_static(const void* H, const void* W, int dtype, cons
 }
 
 #include "score_host.cuh"
+#include "head_host.cuh"

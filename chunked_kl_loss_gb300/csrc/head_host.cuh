@@ -1,0 +1,258 @@
+// Host side of the scoring from hidden states (score_gemm.cuh): workspace, chunk loop and the C
+// entry points declared in include/fckl.h. Part of the translation unit of fckl.cu; the gradient
+// products are the loss's own (chunk_products).
+#pragma once
+
+#include "score_gemm.cuh"
+#include "score_host.cuh"
+
+namespace fckl {
+namespace {
+
+int head_shape(int64_t N, int d, int V, int T, int chunk, int dt) {
+  if (N < 0 || T < 0) return FCKL_ERR_ARG;
+  if (T > TOKENS_MAX) return FCKL_ERR_UNSUPPORTED;
+  return check_shape(std::max<int64_t>(N, 1), d, V, 1, chunk, dt);
+}
+
+// The loss's plan with the regions that scoring uses: ordered tokens in sidx, their slots in T
+// (rows x T ints), their gradients in sp, the sums of those in S, the tiles' statistics, and for the
+// backward pass the gradient slab and dH partials.
+Plan head_plan(int64_t N, int d, int V, int T, int chunk, int dt, bool backward) {
+  Plan p = make_plan(std::max<int64_t>(N, 1), d, V, 1, chunk, dt);
+  p.K = T;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    size_t r = o;
+    o = static_cast<size_t>(rup(static_cast<int64_t>(o + bytes), 1024));
+    return r;
+  };
+  const size_t R = p.rows_alloc, D = d;
+  p.off_status = take(256);
+  p.off_sidx = take(R * T * 4);
+  p.off_T = take(R * T * 4);
+  p.off_sp = take(backward ? R * T * 4 : 0);
+  p.off_S = take(backward ? R * 4 : 0);
+  p.off_pm = take(backward ? 0 : size_t(p.tiles_v) * R * 4);
+  p.off_pl = take(backward ? 0 : size_t(p.tiles_v) * R * 4);
+  p.off_pc = take(backward ? 0 : size_t(p.tiles_v) * R * 4);
+  p.off_G = take(backward ? R * p.ldG * 2 : 0);
+  p.off_dhp = take(backward ? MAX_SPLITS * R * D * 4 : 0);
+  const bool f32 = dt == FCKL_F32;
+  p.off_Hb = take(f32 && backward ? R * D * 2 : 0);
+  p.off_Wb = take(f32 && backward ? size_t(V) * D * 2 : 0);
+  p.off_Ht = take(f32 ? R * D * 4 : 0);
+  p.off_Wt = take(f32 ? size_t(V) * D * 4 : 0);
+  p.total = p.total_overlap = o;
+  return p;
+}
+
+int head_setup(Run& r, const void* H, const void* W, int dt, const int32_t* tokens, int64_t N, int d, int V, int T,
+               int chunk, bool backward, void* ws, size_t ws_bytes, void* stream) {
+  int st = head_shape(N, d, V, T, chunk, dt);
+  if (st) return st;
+  if (!ws || !aligned(ws, 256)) return FCKL_ERR_ARG;
+  if (N > 0 && (!H || !aligned(H, 16) || (T > 0 && (!tokens || !aligned(tokens, 4))))) return FCKL_ERR_ARG;
+  if (!W || !aligned(W, 16)) return FCKL_ERR_ARG;
+  r.pl = head_plan(N, d, V, T, chunk, dt, backward);
+  if (ws_bytes < r.pl.total) return FCKL_ERR_WORKSPACE;
+  r.s = static_cast<cudaStream_t>(stream);
+  r.w = static_cast<uint8_t*>(ws);
+  r.status = reinterpret_cast<unsigned*>(r.w + r.pl.off_status);
+  r.H = H;
+  r.Wraw = W;
+  r.Wb = W;
+  r.dtype = dt;
+  r.idx = tokens;
+  return FCKL_OK;
+}
+
+// Orders the chunk's tokens and returns its hidden states as the products read them (as
+// chunk_prepare does for the loss).
+int head_prepare(Run& r, int64_t r0, int rows, const float* g, const void** Hl, const void** Hc, bool backward) {
+  const Plan& pl = r.pl;
+  const int T = pl.K;
+  int st;
+  if (T > 0 || g) {
+    const unsigned blocks = static_cast<unsigned>(cdiv(rows, PRE_WARPS));
+    cudaStream_t s = r.s;
+    uint8_t* w = r.w;
+    unsigned* status = r.status;
+    const int32_t* tok = r.idx + r0 * T;
+    st = launch(KIND_TOKEN_ORDER, s, "token_order", [&] {
+      token_order_kernel<<<blocks, 32 * PRE_WARPS, size_t(PRE_WARPS) * T * 4, s>>>(
+          tok, g, rows, T, pl.V, reinterpret_cast<int*>(w + pl.off_sidx), reinterpret_cast<int*>(w + pl.off_T),
+          reinterpret_cast<float*>(w + pl.off_sp), reinterpret_cast<float*>(w + pl.off_S), status);
+    });
+    if (st) return st;
+  }
+  const size_t esz = r.dtype == FCKL_F32 ? 4 : 2;
+  *Hl = static_cast<const uint8_t*>(r.H) + static_cast<size_t>(r0) * pl.d * esz;
+  *Hc = *Hl;
+  if (r.dtype == FCKL_F32) {
+    if ((st = launch_cvt(static_cast<const float*>(*Hl), r.w + pl.off_Ht, backward ? r.w + pl.off_Hb : nullptr,
+                         int64_t(rows) * pl.d, r.di, r.s)))
+      return st;
+    *Hl = r.w + pl.off_Ht;
+    *Hc = r.w + pl.off_Hb;
+  }
+  return FCKL_OK;
+}
+
+// Persistent launch of one instance: as many SM pairs as can be resident, capped by the units.
+template <int EPI, bool TF32>
+int launch_head(int kind, DevInfo* di, const HeadParams& p, cudaStream_t s, const char* what) {
+  auto k = head_score_kernel<EPI, TF32>;
+  constexpr uint32_t smem = TcSmem<2, VOCAB_TILE, TF32 ? 1 : 2>::DYN_BYTES;
+  static int max_pairs[64] = {};
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs;
+  {
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    if (!max_pairs[di->id]) {
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) {
+        set_error("cudaFuncSetAttribute(head_score)", e);
+        return FCKL_ERR_CUDA;
+      }
+      int n = di->sms / 2, m = 0;
+      cfg.gridDim = dim3(static_cast<unsigned>(2 * n));
+      if (cudaOccupancyMaxActiveClusters(&m, k, &cfg) == cudaSuccess && m > 0) n = std::min(n, m);
+      cudaGetLastError();
+      max_pairs[di->id] = n;
+    }
+    pairs = max_pairs[di->id];
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.num_units, pairs)));
+  cfg.stream = s;
+  return launch(kind, s, what, [&] { cudaLaunchKernelEx(&cfg, k, p); });
+}
+
+// What both passes over a chunk's logits share.
+int head_params(Run& r, const void* Hl, int rows, HeadParams* p) {
+  const Plan& pl = r.pl;
+  memset(p, 0, sizeof(*p));
+  int st = map_logits_A(r, &p->tmA, Hl, rows, &p->a_3d);
+  if (st) return st;
+  p->tmB = r.tmW_k;
+  p->b_3d = r.w_k_3d;
+  const int kb = logits_kblocks(r);
+  p->sch = {static_cast<int>(cdiv(rows, TILE_M)), pl.tiles_v, kb, 1, kb, 1};
+  p->num_units = p->sch.m_blocks * p->sch.n_blocks;
+  p->status = r.status;
+  p->rows = rows;
+  p->V = pl.V;
+  p->T = pl.K;
+  p->sid = reinterpret_cast<const int*>(r.w + pl.off_sidx);
+  p->sslot = reinterpret_cast<const int*>(r.w + pl.off_T);
+  return FCKL_OK;
+}
+
+}  // namespace
+}  // namespace fckl
+
+extern "C" {
+
+size_t fckl_projected_logprobs_workspace_bytes(int64_t N, int d, int V, int T, int chunk, int dtype, int backward) {
+  if (head_shape(N, d, V, T, chunk, dtype) != FCKL_OK) return 0;
+  return head_plan(N, d, V, T, chunk, dtype, backward != 0).total;
+}
+
+int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d, int V,
+                            int T, int chunk, float* logp, float* entropy, float* lse, void* ws, size_t ws_bytes,
+                            void* stream) {
+  return guarded("fckl_projected_logprobs", [&]() -> int {
+    Run r;
+    int st = head_setup(r, H, W, dtype, tokens, N, d, V, T, chunk, false, ws, ws_bytes, stream);
+    if (st) return st;
+    if (N > 0 && (!entropy || !lse || (T > 0 && !logp))) return FCKL_ERR_ARG;
+    if (!aligned(logp, 4) || !aligned(entropy, 4) || !aligned(lse, 4)) return FCKL_ERR_ARG;
+    if ((st = device_info(&r.di))) return st;
+    if (N == 0) return cudaMemsetAsync(r.status, 0, 4, r.s) == cudaSuccess ? FCKL_OK : FCKL_ERR_CUDA;
+    if ((st = run_begin(r, false))) return st;
+    const Plan& pl = r.pl;
+    cudaStream_t s = r.s;
+    for (int64_t r0 = 0; r0 < N; r0 += pl.chunk) {
+      const int rows = static_cast<int>(std::min<int64_t>(pl.chunk, N - r0));
+      const void *Hl = nullptr, *Hc = nullptr;
+      if ((st = head_prepare(r, r0, rows, nullptr, &Hl, &Hc, false))) return st;
+      HeadParams p;
+      if ((st = head_params(r, Hl, rows, &p))) return st;
+      p.pm = reinterpret_cast<float*>(r.w + pl.off_pm);
+      p.pl = reinterpret_cast<float*>(r.w + pl.off_pl);
+      p.pt = reinterpret_cast<float*>(r.w + pl.off_pc);
+      p.ld_part = pl.rows_alloc;
+      p.zt = logp + r0 * T;
+      st = dtype == FCKL_F32 ? launch_head<HEAD_STATS, true>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats")
+                             : launch_head<HEAD_STATS, false>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats");
+      if (st) return st;
+      const unsigned blocks = static_cast<unsigned>(cdiv(rows, 32));
+      st = launch(KIND_HEAD_COMBINE, s, "head_combine", [&] {
+        head_combine_kernel<<<blocks, 32 * COMBINE_WARPS, 0, s>>>(p.pm, p.pl, p.pt, p.ld_part, pl.tiles_v, rows,
+                                                                   tokens + r0 * T, T, V, p.zt, entropy + r0,
+                                                                   lse + r0);
+      });
+      if (st) return st;
+    }
+    return FCKL_OK;
+  });
+}
+
+int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d,
+                                     int V, int T, int chunk, const float* lse, const float* entropy,
+                                     const float* g_logp, const float* g_entropy, void* dH, float* dW, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  return guarded("fckl_projected_logprobs_backward", [&]() -> int {
+    Run r;
+    int st = head_setup(r, H, W, dtype, tokens, N, d, V, T, chunk, true, ws, ws_bytes, stream);
+    if (st) return st;
+    if (!dW || !aligned(dW, 16)) return FCKL_ERR_ARG;
+    if (N > 0 && (!lse || !entropy || !dH || (T > 0 && !g_logp))) return FCKL_ERR_ARG;
+    if (!aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4) || !aligned(dH, 16))
+      return FCKL_ERR_ARG;
+    if ((st = device_info(&r.di))) return st;
+    if (N == 0) {
+      cudaError_t e = cudaMemsetAsync(r.status, 0, 4, r.s);
+      if (e == cudaSuccess) e = cudaMemsetAsync(dW, 0, size_t(V) * d * 4, r.s);
+      if (e == cudaSuccess) return FCKL_OK;
+      set_error("cudaMemsetAsync", e);
+      return FCKL_ERR_CUDA;
+    }
+    r.dH = dH;
+    r.dW = dW;
+    if ((st = run_begin(r, true))) return st;
+    const Plan& pl = r.pl;
+    // With no tokens the order kernel still writes the (zero) sums: it is given any gradient pointer.
+    const float* g = T > 0 ? g_logp : lse;
+    for (int64_t r0 = 0; r0 < N; r0 += pl.chunk) {
+      const int rows = static_cast<int>(std::min<int64_t>(pl.chunk, N - r0));
+      const void *Hl = nullptr, *Hc = nullptr;
+      if ((st = head_prepare(r, r0, rows, g + r0 * T, &Hl, &Hc, true))) return st;
+      HeadParams p;
+      if ((st = head_params(r, Hl, rows, &p))) return st;
+      if ((st = make_map(&p.tmC, r.w + pl.off_G, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, V, rows, uint64_t(pl.ldG) * 2, 64,
+                         32)))
+        return st;
+      p.sgrad = reinterpret_cast<const float*>(r.w + pl.off_sp);
+      p.gsum = reinterpret_cast<const float*>(r.w + pl.off_S);
+      p.lse = lse + r0;
+      p.entropy = entropy + r0;
+      p.g_entropy = g_entropy ? g_entropy + r0 : nullptr;
+      st = dtype == FCKL_F32 ? launch_head<HEAD_GRAD, true>(KIND_HEAD_GRAD, r.di, p, r.s, "head_logit_grad")
+                             : launch_head<HEAD_GRAD, false>(KIND_HEAD_GRAD, r.di, p, r.s, "head_logit_grad");
+      if (st) return st;
+      if ((st = chunk_products(r, 0, r0, rows, Hc))) return st;
+    }
+    return FCKL_OK;
+  });
+}
+
+}  // extern "C"

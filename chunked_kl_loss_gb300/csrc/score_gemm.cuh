@@ -1,0 +1,423 @@
+// Scoring of given tokens straight from hidden states: the logits z = H W^T live in TMEM only.
+//
+// head_score_kernel is the logits product of tc_gemm.cuh (persistent, one CTA per SM, SM pairs,
+// TMA ring, two TMEM accumulators; K-major operands) with two epilogues of its own:
+//   HEAD_STATS : per row and 256-column tile the statistics (m, l, t) of score.cuh, and the logits
+//                of the row's given tokens
+//   HEAD_GRAD  : G = sum_t g_t [v = t] - q_v (sum_t g_t + g_e (log q_v + entropy)) from the row's
+//                log-partition, rounded to bf16 and stored with TMA into the chunk's gradient
+//                slab, which the dH and dW products read. As in the loss, G is rounded to bf16
+//                because the tensor cores take both operands in one type (half a step, 2^-8 of
+//                each entry, independent over the V or N entries that a product sums).
+#pragma once
+
+#include "score.cuh"
+#include "tc_gemm.cuh"
+
+namespace fckl {
+
+enum { HEAD_STATS = 0, HEAD_GRAD = 1 };
+
+struct HeadParams {
+  CUtensorMap tmA;  // H rows of the chunk
+  CUtensorMap tmB;  // W
+  CUtensorMap tmC;  // gradient slab (HEAD_GRAD)
+  Sched sch;
+  int num_units;
+  int a_3d, b_3d;  // one copy fetches a stage's two K-blocks
+  unsigned* status;
+  int rows, V, T;
+  const int* sid;    // [rows][T] tokens of the chunk, ascending per row
+  const int* sslot;  // [rows][T] the slot each came from
+  // HEAD_STATS
+  float* pm;  // [tiles][ld_part]
+  float* pl;
+  float* pt;
+  int ld_part;
+  float* zt;  // [rows][T] logits of the tokens, by slot
+  // HEAD_GRAD
+  const float* sgrad;  // [rows][T] upstream gradients in the order of sid
+  const float* gsum;   // [rows] their sum
+  const float* lse;
+  const float* entropy;
+  const float* g_entropy;  // or null
+};
+
+template <int EPI, bool TF32>
+__global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid_constant__ HeadParams p) {
+  constexpr int CGS = 2, BN = VOCAB_TILE, BN_CTA = BN / CGS;
+  constexpr int KPS = TF32 ? 1 : 2;
+  using L = TcSmem<CGS, BN, KPS>;
+  constexpr int NST = L::STAGES;
+  constexpr int KE = TF32 ? BK / 2 : BK;  // K elements per K-block (128 bytes of each row)
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  uint64_t* empty = full + NST;
+  uint64_t* tfull = empty + NST;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x / CGS;
+  const int num_pairs = gridDim.x / CGS;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], EPI_WARPS * CGS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&p.tmA);
+    prefetch_tmap(&p.tmB);
+    if (EPI == HEAD_GRAD) prefetch_tmap(&p.tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers exist before anyone signals them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (each CTA)
+    if (lane == 0) {
+      uint32_t cnt = 0, armed = 0, armed_par = 0;
+      bool ok = true;
+      const uint32_t full_base = mapa_shared(smem_u32(full), 0);
+      for (int u = pair; ok && u < p.num_units; u += num_pairs) {
+        int mb, nb, sp, kb0, kb1;
+        decode_unit(p.sch, u, mb, nb, sp, kb0, kb1);
+        const int arow = (mb * CGS + static_cast<int>(rank)) * BM;
+        const int brow = nb * BN + static_cast<int>(rank) * BN_CTA;
+        for (int kb = kb0; kb < kb1; kb += KPS, ++cnt) {
+          const uint32_t s = cnt % NST, ph = (cnt / NST) & 1u;
+          if (!wait_phase(&empty[s], ph ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            mbar_arrive_expect_tx(&full[s], CGS * L::STAGE_BYTES);
+            armed |= 1u << s;
+            armed_par = (armed_par & ~(1u << s)) | (ph << s);
+          }
+          uint8_t* a = smem + s * L::STAGE_BYTES;
+          uint8_t* b = a + L::A_BYTES;
+          const uint32_t fb = full_base + s * 8u;
+          if (!TF32 && p.a_3d) {
+            tma_load_3d_pair(a, &p.tmA, fb, 0, arow, kb);
+          } else {
+#pragma unroll
+            for (int j = 0; j < KPS; ++j) tma_load_2d_pair(a + j * L::A_KB, &p.tmA, fb, (kb + j) * KE, arow);
+          }
+          if (!TF32 && p.b_3d) {
+            tma_load_3d_pair(b, &p.tmB, fb, 0, brow, kb);
+          } else {
+#pragma unroll
+            for (int j = 0; j < KPS; ++j) tma_load_2d_pair(b + j * L::B_KB, &p.tmB, fb, (kb + j) * KE, brow);
+          }
+        }
+      }
+      // every copy this pair started lands before a CTA may exit (see tc_gemm.cuh)
+      if (leader) {
+        for (int s = 0; s < NST; ++s)
+          if (armed & (1u << s)) drain_phase(&full[s], (armed_par >> s) & 1u, p.status);
+      } else if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader CTA)
+    if (lane == 0 && leader) {
+      constexpr uint32_t IDESC =
+          TF32 ? make_idesc_tf32(BM * CGS, BN) : make_idesc_bf16(BM * CGS, BN, false, false);
+      uint32_t cnt = 0, it = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < p.num_units; u += num_pairs, ++it) {
+        int mb, nb, sp, kb0, kb1;
+        decode_unit(p.sch, u, mb, nb, sp, kb0, kb1);
+        const uint32_t acc = it & 1u, use = it >> 1;
+        if (!wait_phase_cluster(&tempty[acc], (use & 1u) ^ 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * ACC_STRIDE;
+        for (int kb = kb0; kb < kb1; kb += KPS, ++cnt) {
+          const uint32_t s = cnt % NST, ph = (cnt / NST) & 1u;
+          if (!wait_phase(&full[s], ph, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + s * L::STAGE_BYTES);
+          const uint32_t b_addr = a_addr + L::A_BYTES;
+#pragma unroll
+          for (int q = 0; q < KPS * (BK / 16); ++q) {
+            const int j = q / (BK / 16), kk = q % (BK / 16);
+            if (KPS > 1 && kb + j >= kb1) break;
+            const uint64_t ad = make_sdesc_sw128(a_addr + j * L::A_KB + kk * 32, 16, 1024);
+            const uint64_t bd = make_sdesc_sw128(b_addr + j * L::B_KB + kk * 32, 16, 1024);
+            const uint32_t accum = (kb > kb0 || q > 0) ? 1u : 0u;
+            if constexpr (TF32)
+              umma_tf32_pair(d_tmem, ad, bd, IDESC, accum);
+            else
+              umma_bf16_pair(d_tmem, ad, bd, IDESC, accum);
+          }
+          umma_commit_pair(&empty[s], 0x3);
+        }
+        if (!ok) break;
+        umma_commit_pair(&tfull[acc], 0x3);
+      }
+      umma_commit_pair(drain, 0x1);  // all MMAs finish before TMEM is released
+      drain_phase(drain, 0, p.status);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (each CTA)
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    uint8_t* ebuf0 = smem + L::EPI_OFF + (warp - 2) * 2 * EPI_BUF_BYTES;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
+    auto release_acc = [&](uint32_t acc) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (!leader)
+          mbar_arrive_cluster(tempty_leader + acc * 8u);
+        else
+          mbar_arrive(&tempty[acc]);
+      }
+    };
+    uint32_t it = 0, ecnt = 0;
+    for (int u = pair; u < p.num_units; u += num_pairs, ++it) {
+      int mb, nb, sp, kb0, kb1;
+      decode_unit(p.sch, u, mb, nb, sp, kb0, kb1);
+      const uint32_t acc = it & 1u, use = it >> 1;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * ACC_STRIDE;
+      const int row0 = (mb * CGS + static_cast<int>(rank)) * BM + 32 * q;  // first row of this warp
+      const int row = row0 + lane;
+      const bool valid = row < p.rows;
+      const int v0 = nb * BN;
+      // cursor over the row's ordered tokens, at the first one of this tile (empty slots, -1,
+      // sort before every tile)
+      const size_t tk = static_cast<size_t>(valid ? row : 0) * p.T;
+      const int* ids = p.sid + tk;
+      int k = p.T, nxt = INT_MAX;
+      if (valid) {
+        k = lower_bound_ids(ids, p.T, v0);
+        nxt = k < p.T ? __ldg(ids + k) : INT_MAX;
+      }
+      if constexpr (EPI == HEAD_STATS) {
+        if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+        RowStat s;
+#pragma unroll 1
+        for (int j = 0; j < BN / 32; ++j) {
+          float x[32];
+          __syncwarp();
+          tmem_ld32(taddr + 32 * j, x);
+          if (j == BN / 32 - 1) release_acc(acc);
+          const int cb = v0 + 32 * j;
+          while (nxt < cb + 32) {  // nxt < V or INT_MAX: ids past the vocabulary were put last
+            p.zt[tk + __ldg(p.sslot + tk + k)] = pick32(x, nxt - cb);
+            ++k;
+            nxt = k < p.T ? __ldg(ids + k) : INT_MAX;
+          }
+          if (cb + 32 > p.V) {
+#pragma unroll
+            for (int t = 0; t < 32; ++t)
+              if (cb + t >= p.V) x[t] = -INFINITY;
+          }
+          const float cm = max32(x);
+          if (cm > s.m) {
+            RowStat none;
+            none.m = cm;
+            s = merge(s, none);
+          }
+          add_values<32>(s, x);  // column v0 is in the vocabulary: s.m is finite (or the row is NaN)
+        }
+        if (valid) {
+          const size_t o = static_cast<size_t>(nb) * p.ld_part + row;
+          p.pm[o] = s.m;
+          p.pl[o] = s.l;
+          p.pt[o] = s.t;
+        }
+      } else {
+        const float ge = valid && p.g_entropy ? __ldg(p.g_entropy + row) : 0.f;
+        const float lse = valid ? __ldg(p.lse + row) : 0.f;
+        const float a0 = valid ? fmaf(ge, __ldg(p.entropy + row), __ldg(p.gsum + row)) : 0.f;
+        if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int jj = 0; jj < BN / 64; ++jj, ++ecnt) {
+          uint8_t* buf = ebuf0 + (ecnt & 1u) * EPI_BUF_BYTES;
+          if (ecnt >= 2 && lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = 2 * jj + h;
+            float x[32];
+            __syncwarp();
+            tmem_ld32(taddr + 32 * j, x);
+            if (j == BN / 32 - 1) release_acc(acc);
+            const int cb = v0 + 32 * j;
+#pragma unroll
+            for (int t = 0; t < 32; ++t) {
+              const float lq = x[t] - lse;
+              x[t] = -ex2_approx(lq * LOG2E) * fmaf(ge, lq, a0);
+            }
+            while (nxt < cb + 32) {
+              sub32(x, nxt - cb, -__ldg(p.sgrad + tk + k));
+              ++k;
+              nxt = k < p.T ? __ldg(ids + k) : INT_MAX;
+            }
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) {
+              uint4 w;
+              w.x = pack_bf16x2(x[8 * cc + 0], x[8 * cc + 1]);
+              w.y = pack_bf16x2(x[8 * cc + 2], x[8 * cc + 3]);
+              w.z = pack_bf16x2(x[8 * cc + 4], x[8 * cc + 5]);
+              w.w = pack_bf16x2(x[8 * cc + 6], x[8 * cc + 7]);
+              const int chunk16 = (4 * h + cc) ^ (lane & 7);
+              *reinterpret_cast<uint4*>(buf + lane * 128 + chunk16 * 16) = w;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int sx = v0 + 64 * jj;
+            if (sx < p.V && row0 < p.rows) tma_store_2d(&p.tmC, buf, sx, row0);
+            bulk_commit();
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the leader's MMAs into this CTA's TMEM are done
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// One warp per position: the row's tokens in ascending order (by id, then slot) with the slot and
+// the upstream gradient of each, and the sum of the gradients. An id outside [0, V), -1 aside,
+// is reported and put last, where no tile reaches it, without a gradient.
+__global__ void __launch_bounds__(32 * PRE_WARPS) token_order_kernel(
+    const int32_t* __restrict__ tokens, const float* __restrict__ g, int rows, int T, int V, int* __restrict__ sid,
+    int* __restrict__ sslot, float* __restrict__ sgrad, float* __restrict__ gsum, unsigned* __restrict__ status) {
+  extern __shared__ int order_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * PRE_WARPS + warp;
+  if (row >= rows) return;  // warp-uniform; no block barrier below
+  int* ids = order_smem + warp * T;
+  const size_t o = static_cast<size_t>(row) * T;
+  int bad = 0;
+  for (int t = lane; t < T; t += 32) {
+    int i = tokens[o + t];
+    if (i < -1 || i >= V) {
+      bad = 1;
+      i = INT_MAX;
+    }
+    ids[t] = i;
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(status, ST_BAD_INDEX);
+  __syncwarp();
+  float s = 0.f;
+  for (int t = lane; t < T; t += 32) {
+    const int key = ids[t];
+    int r = 0;
+    for (int j = 0; j < T; ++j) {
+      const int i = ids[j];
+      r += (i < key) | ((i == key) & (j < t));
+    }
+    sid[o + r] = key;
+    sslot[o + r] = t;
+    if (g) {
+      const float gt = key >= 0 && key != INT_MAX ? g[o + t] : 0.f;
+      sgrad[o + r] = gt;
+      s += gt;
+    }
+  }
+  if (g) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (lane == 0) gsum[row] = s;
+  }
+}
+
+// Merges the tiles' statistics of 32 positions per block (lane = position, COMBINE_WARPS warps
+// split the tiles, fixed order) into the log-partition, the entropy and the tokens'
+// log-probabilities (logp holds the tokens' logits on entry).
+__global__ void __launch_bounds__(32 * COMBINE_WARPS) head_combine_kernel(
+    const float* __restrict__ pm, const float* __restrict__ pl, const float* __restrict__ pt, int ld, int tiles,
+    int rows, const int32_t* __restrict__ tokens, int T, int V, float* __restrict__ logp,
+    float* __restrict__ entropy, float* __restrict__ lse) {
+  __shared__ RowStat part[COMBINE_WARPS][32];
+  __shared__ float rm[32], rs[32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  RowStat s;
+  if (row < rows) {
+    constexpr int B = 8;  // the loads of 8 tiles are issued before any of them is merged
+    for (int t0 = w; t0 < tiles; t0 += COMBINE_WARPS * B) {
+      RowStat x[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int t = t0 + COMBINE_WARPS * b;
+        if (t < tiles) {
+          const size_t o = static_cast<size_t>(t) * ld + row;
+          x[b].m = pm[o];
+          x[b].l = pl[o];
+          x[b].t = pt[o];
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) s = merge(s, x[b]);
+    }
+  }
+  part[w][lane] = s;
+  __syncthreads();
+  if (w == 0) {
+    for (int j = 1; j < COMBINE_WARPS; ++j) s = merge(s, part[j][lane]);
+    const float log_s = logf(s.l);
+    rm[lane] = s.m;
+    rs[lane] = log_s;
+    if (row < rows) {
+      const float e = log_s - LN2 * (s.t / s.l);
+      entropy[row] = e < 0.f ? 0.f : e;
+      lse[row] = s.m + log_s;
+    }
+  }
+  __syncthreads();
+  const int n = min(32, rows - blockIdx.x * 32) * T;
+  const size_t o = static_cast<size_t>(blockIdx.x) * 32 * T;
+  for (int i = threadIdx.x; i < n; i += 32 * COMBINE_WARPS) {
+    const int id = tokens[o + i], r = i / T;
+    float lp = 0.f;
+    if (id < -1 || id >= V)
+      lp = NAN;
+    else if (id >= 0)
+      lp = (logp[o + i] - rm[r]) - rs[r];
+    logp[o + i] = lp;
+  }
+}
+
+}  // namespace fckl

@@ -5,9 +5,13 @@ Argument marshalling only, as in the package itself: every step runs in the CUDA
     logp, entropy, norm, top_idx, top_logp = fckl.token_logprobs(logits, tokens, top=20)
     dlogits = fckl.token_logprobs_backward(logits, tokens, norm, entropy, g_logp, g_entropy)
     logp, entropy = fckl.differentiable_token_logprobs(logits, tokens)         # autograd
+    logp, entropy, lse = fckl.projected_logprobs(H, W, tokens, chunk)           # from hidden states
+    dH, dW = fckl.projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy, chunk=chunk)
+    logp, entropy = fckl.fused_token_logprobs(H, W, tokens, chunk)             # autograd
 
 ``logits [N, V]`` are bf16, fp16 or fp32 (rows may lie apart: only the last dimension has to be
 dense); ``tokens [N, T]`` are int32, -1 marks an empty slot. Logits of -inf are masked tokens.
+``H [N, d]`` and ``W [V, d]`` are bf16 or fp32 as for the loss; their logits are never stored.
 
 ``stream`` launches on a stream other than the current one: outputs are then allocated for that
 stream and the inputs are marked as used on it; making the inputs' data ready there is the
@@ -21,7 +25,8 @@ import ctypes
 
 import chunked_kl_loss_gb300 as _pkg
 
-__all__ = ["token_logprobs", "token_logprobs_backward", "differentiable_token_logprobs"]
+__all__ = ["token_logprobs", "token_logprobs_backward", "differentiable_token_logprobs", "projected_logprobs",
+           "projected_logprobs_backward", "fused_token_logprobs"]
 
 _status_ws = {}  # device index -> workspace that holds only a status word
 
@@ -29,6 +34,13 @@ _status_ws = {}  # device index -> workspace that holds only a status word
 def _set_argtypes(lib):
     c = ctypes
     vp, i64, i32, sz = c.c_void_p, c.c_int64, c.c_int, c.c_size_t
+    lib.fckl_projected_logprobs_workspace_bytes.restype = sz
+    lib.fckl_projected_logprobs_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32]
+    lib.fckl_projected_logprobs.restype = i32
+    lib.fckl_projected_logprobs.argtypes = [vp, vp, i32, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
+    lib.fckl_projected_logprobs_backward.restype = i32
+    lib.fckl_projected_logprobs_backward.argtypes = [vp, vp, i32, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp,
+                                                     vp, sz, vp]
     lib.fckl_token_logprobs.restype = i32
     lib.fckl_token_logprobs.argtypes = [vp, i32, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fckl_token_logprobs_backward.restype = i32
@@ -213,3 +225,125 @@ def differentiable_token_logprobs(logits, tokens):
     if _TokenLogprobs is None:
         _TokenLogprobs = _autograd_function()
     return _TokenLogprobs.apply(logits, tokens)
+
+
+# ------------------------------------------------------------------ from hidden states
+def _head_args(H, W, tokens):
+    import torch
+    if H.dim() != 2 or W.dim() != 2 or tokens.dim() != 2 or W.shape[1] != H.shape[1] or \
+            tokens.shape[0] != H.shape[0]:
+        raise ValueError("expected H [N,d], W [V,d], tokens [N,T]")
+    if H.dtype != W.dtype:
+        raise TypeError("H and W must share a dtype")
+    dt = _pkg._dtype_code(H)
+    for name, t in (("H", H), ("W", W)):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    N, d = H.shape
+    V, T = W.shape[0], tokens.shape[1]
+    _dense("tokens", tokens, torch.int32, (N, T))
+    return dt, N, d, V, T
+
+
+def _head_ws(ws, N, d, V, T, chunk, dt, device, kind):
+    import weakref
+    if ws is None:
+        ws = _pkg.Workspace(N, d, V, T, chunk, dt, device, kind=kind)
+        _pkg._last_ws = ws
+    else:
+        _pkg._last_ws = weakref.ref(ws)
+    return ws
+
+
+def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
+    """(logp fp32 [N, T], entropy fp32 [N], lse fp32 [N]) of the logits H W^T, ``chunk`` positions
+    at a time. ``ws``: Workspace(N, d, V, T, chunk, kind="projected")."""
+    import torch
+    dt, N, d, V, T = _head_args(H, W, tokens)
+    dev = H.device
+    _on_device(dev, H=H, W=W, tokens=tokens)
+    with _for_stream(stream, H, W, tokens):
+        ws = _head_ws(ws, N, d, V, T, chunk, dt, dev, "projected")
+        logp = torch.empty(N, T, dtype=torch.float32, device=dev)
+        entropy = torch.empty(N, dtype=torch.float32, device=dev)
+        lse = torch.empty(N, dtype=torch.float32, device=dev)
+    p = _pkg._ptr
+    st = _pkg.load().fckl_projected_logprobs(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(logp), p(entropy),
+                                             p(lse), ws.ptr, ws.nbytes, _pkg._stream_ptr(stream))
+    if st != _pkg.OK:
+        raise _pkg.FcklError(st, "fckl_projected_logprobs")
+    return logp, entropy, lse
+
+
+def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=None, chunk=2048, ws=None, stream=None,
+                                dH=None, dW=None):
+    """(dH [N, d] in H's dtype, dW fp32 [V, d]) of sum g_logp * logp + sum g_entropy * entropy;
+    ``lse`` and ``entropy`` as projected_logprobs returned them.
+    ``ws``: Workspace(N, d, V, T, chunk, kind="projected_backward")."""
+    import torch
+    dt, N, d, V, T = _head_args(H, W, tokens)
+    dev = H.device
+    _on_device(dev, H=H, W=W, tokens=tokens, lse=lse, entropy=entropy, g_logp=g_logp, g_entropy=g_entropy, dH=dH,
+               dW=dW)
+    f32 = torch.float32
+    _dense("lse", lse, f32, (N,))
+    _dense("entropy", entropy, f32, (N,))
+    _dense("g_logp", g_logp, f32, (N, T))
+    if g_entropy is not None:
+        _dense("g_entropy", g_entropy, f32, (N,))
+    if dH is not None:
+        _dense("dH", dH, H.dtype, (N, d))
+    if dW is not None:
+        _dense("dW", dW, f32, (V, d))
+    with _for_stream(stream, H, W, tokens, lse, entropy, g_logp, g_entropy, dH, dW):
+        ws = _head_ws(ws, N, d, V, T, chunk, dt, dev, "projected_backward")
+        if dH is None:
+            dH = torch.empty(N, d, dtype=H.dtype, device=dev)
+        if dW is None:
+            dW = torch.empty(V, d, dtype=f32, device=dev)
+    p = _pkg._ptr
+    st = _pkg.load().fckl_projected_logprobs_backward(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(lse), p(entropy),
+                                                      p(g_logp), p(g_entropy), p(dH), p(dW), ws.ptr, ws.nbytes,
+                                                      _pkg._stream_ptr(stream))
+    if st != _pkg.OK:
+        raise _pkg.FcklError(st, "fckl_projected_logprobs_backward")
+    return dH, dW
+
+
+def _head_autograd_function():
+    import torch
+
+    class ProjectedLogprobs(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, H, W, tokens, chunk):
+            logp, entropy, lse = projected_logprobs(H, W, tokens, chunk)
+            ctx.save_for_backward(H, W, tokens, lse, entropy)
+            ctx.chunk = chunk
+            ctx.set_materialize_grads(False)
+            return logp, entropy
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, g_logp, g_entropy):
+            H, W, tokens, lse, entropy = ctx.saved_tensors
+            if g_logp is None and g_entropy is None:
+                return None, None, None, None
+            ge = None if g_entropy is None else _upstream(g_entropy, None, H.device)
+            gl = _upstream(g_logp, tuple(tokens.shape), H.device)
+            dH, dW = projected_logprobs_backward(H, W, tokens, lse, entropy, gl, ge, chunk=ctx.chunk)
+            return (dH if ctx.needs_input_grad[0] else None, dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
+                    None, None)
+
+    return ProjectedLogprobs
+
+
+_ProjectedLogprobs = None
+
+
+def fused_token_logprobs(H, W, tokens, chunk):
+    """(logp [N, T], entropy [N]) of the logits H W^T, differentiable in H and W (W's gradient is
+    summed in fp32 and rounded once to W's dtype)."""
+    global _ProjectedLogprobs
+    if _ProjectedLogprobs is None:
+        _ProjectedLogprobs = _head_autograd_function()
+    return _ProjectedLogprobs.apply(H, W, tokens, chunk)

@@ -273,6 +273,27 @@ int fckl_token_logprobs_backward(const void* logits, int dtype, int64_t ld, cons
                                  const float* g_entropy, void* dlogits, int64_t ld_out, void* ws, size_t ws_bytes,
                                  void* stream);
 
+/* The same straight from hidden states H [N, d] and the output matrix W [V, d] (FCKL_BF16 or
+ * FCKL_F32, as for the loss): the logits z = W h are reduced in the tensor-core product's
+ * epilogue and never stored, one chunk of positions at a time. Conventions, limits and workspace
+ * alignment are the loss's (T in the place of K, 0 <= T <= 1024; N = 0 is allowed); the workspace's
+ * status word is cleared by the call. Hidden states have to be finite, those of positions without
+ * an upstream gradient too (dW sums over all positions).
+ *   lse : fp32 [N], the log-partition, kept for the backward call */
+size_t fckl_projected_logprobs_workspace_bytes(int64_t N, int d, int V, int T, int chunk, int dtype, int backward);
+int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d, int V,
+                            int T, int chunk, float* logp, float* entropy, float* lse, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Gradients of sum g_logp logp + sum g_entropy entropy: dH [N, d] of type `dtype` and dW fp32
+ * [V, d], both overwritten. Each chunk's logits are recomputed; the logit gradient is formed in
+ * fp32 and rounded to bf16 for the dH and dW products, as in fckl_backward. The workspace is that
+ * of backward = 1 above. */
+int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d,
+                                     int V, int T, int chunk, const float* lse, const float* entropy,
+                                     const float* g_logp, const float* g_entropy, void* dH, float* dW, void* ws,
+                                     size_t ws_bytes, void* stream);
+
 /* Interface addition, no counterpart on the pages (they describe no device interface).
  * Synchronises `stream`, returns the status found on the device by the last call that
  * used `ws` (FCKL_OK if none), and clears it. */

@@ -1,0 +1,281 @@
+"""Scoring from hidden states (projected_logprobs and its gradients) against the fp64 oracle.
+
+Tolerances, from the arithmetic (u = 2^-24):
+* bf16 products are exact in fp32; a logit is a sum of d of them accumulated in fp32 in some order,
+  each addition truncated at worst (a whole step, 2u) of the running sum: |dz| <= 2 d u sum |h w|, and
+  sum |h w| <= |h| |w| (norms). The statistics add r (a tile's 256 values and the tiles' merges), as
+  for logits at hand. For fp32 inputs the oracle gets the tf32-rounded inputs, whose products are
+  exact in fp32 as well.
+* G is rounded to bf16 (half a step, 2^-8 relative) and dH, dW sum V and N such entries: off by at
+  most 2^-8 sum |G| |w| (resp. |h|), plus the products' own sums and the rounding of dH to its type.
+  For fp32 inputs the factor w (h) is rounded to bf16 too: twice 2^-8.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import synthetic
+from oracle import scoring_oracle as orc
+
+gpu = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def make(N, d, V, T, dtype, seed, sharp=1.0):
+    rng = np.random.default_rng(seed)
+    H = (rng.normal(size=(N, d)) * sharp).astype(np.float32)
+    W = (rng.normal(size=(V, d)) / np.sqrt(d)).astype(np.float32)
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    Ht, Wt = torch.from_numpy(H).cuda().to(tdt), torch.from_numpy(W).cuda().to(tdt)
+    tokens = rng.integers(0, V, size=(N, T))
+    tokens[rng.random((N, T)) < 0.1] = -1
+    if T > 2:
+        tokens[:, 1] = tokens[:, 0]  # repeats
+    return Ht, Wt, torch.from_numpy(tokens).int().cuda()
+
+
+def exact_inputs(Ht, Wt):
+    H, W = Ht.float().cpu().numpy(), Wt.float().cpu().numpy()
+    if Ht.dtype == torch.float32:
+        H, W = synthetic.round_tf32(H), synthetic.round_tf32(W)
+    return H.astype(np.float64), W.astype(np.float64)
+
+
+def close(got, want, tol):
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4], np.broadcast_to(tol, got.shape)[bad][:4])
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def logit_error(H, W):
+    """Per position, the most that a logit can be off."""
+    return 2 * H.shape[1] * U * np.linalg.norm(H, axis=1) * np.linalg.norm(W, axis=1).max() + 4 * U
+
+
+def check(fckl, Ht, Wt, tokens, chunk, with_entropy=True, seed=0):
+    logp, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, chunk)
+    assert fckl.check() == fckl.OK
+    H, W = exact_inputs(Ht, Wt)
+    tk = tokens.cpu().numpy()
+    w_logp, w_ent, w_lse = orc.projected(H, W, tk)
+    V, r = W.shape[0], (256 + W.shape[0] // 8192 + 80) * U + 2.0 ** -21
+    dz = logit_error(H, W)
+    close(f64(lse), w_lse, dz + r + 8 * U * np.abs(w_lse))
+    close(f64(logp), w_logp, (2 * dz + r)[:, None] + 8 * U * np.abs(w_logp))
+    spread = np.maximum(w_ent, np.log(V)) + 2
+    close(f64(ent), w_ent, (dz * 2 * spread + r * (1 + 2 * spread)))
+
+    rng = np.random.default_rng(seed)
+    g = rng.normal(size=tk.shape).astype(np.float32)
+    ge = rng.normal(size=len(H)).astype(np.float32) if with_entropy else np.zeros(len(H), np.float32)
+    dH, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, torch.from_numpy(g).cuda(),
+                                              torch.from_numpy(ge).cuda() if with_entropy else None, chunk=chunk)
+    assert fckl.check() == fckl.OK
+    G = orc.logits_gradient(H @ W.T, tk, g, ge)
+    w_dH, w_dW = G @ W, G.T @ H
+    half = 2.0 ** -8 * (2 if Ht.dtype == torch.float32 else 1)
+    # G's own error before its rounding: q off by its exponent's, factors of the upstream sums
+    lq = orc._log_softmax(H @ W.T)[0]
+    q = np.exp(lq)
+    a = np.abs(np.where(tk < 0, 0, g)).sum(1, keepdims=True) + np.abs(ge)[:, None] * (1 + np.abs(lq) + w_ent[:, None])
+    eG = half * 1.01 * np.abs(G) + q * a * (4 * (dz + r)[:, None] * (1 + spread[:, None]) + 2.0 ** -19)
+    out = 2.0 ** -8 if Ht.dtype == torch.bfloat16 else 2.0 ** -23
+    close(f64(dH), w_dH, eG @ np.abs(W) + 4 * V * U * (np.abs(G) @ np.abs(W)) / 16 + out * np.abs(w_dH) + 1e-30)
+    close(f64(dW), w_dW, eG.T @ np.abs(H) + 4 * len(H) * U * (np.abs(G).T @ np.abs(H)) + 1e-30)
+    return logp, ent, lse, dH, dW
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N,d,V,T,chunk", [
+    (1, 8, 1, 1, 1), (1, 64, 300, 1, 16), (5, 72, 257, 3, 2), (130, 256, 2057, 2, 100), (256, 128, 256, 1, 256),
+    (300, 320, 1000, 20, 128), (33, 1024, 5001, 4, 2048), (2, 2880, 700, 300, 8), (520, 64, 4100, 1, 512),
+])
+def test_projected(fckl, dtype, N, d, V, T, chunk):
+    check(fckl, *make(N, d, V, T, dtype, seed=N + V), chunk)
+
+
+@gpu
+def test_projected_without_tokens_and_without_entropy(fckl):
+    Ht, Wt, tokens = make(40, 128, 900, 2, "bf16", 3)
+    check(fckl, Ht, Wt, tokens, 16, with_entropy=False)
+    check(fckl, Ht, Wt, tokens[:, :0].contiguous(), 16)
+    # every slot empty
+    none = torch.full_like(tokens, -1)
+    logp, ent, lse, dH, dW = check(fckl, Ht, Wt, none, 16, with_entropy=False)
+    assert (logp == 0).all() and (dH == 0).all() and (dW == 0).all()
+
+
+@gpu
+def test_projected_sharp(fckl):
+    """Logits of tens: the softmax is all but one-hot, its entropy near 0."""
+    check(fckl, *make(64, 256, 3000, 2, "bf16", 9, sharp=12.0), 64)
+
+
+@gpu
+def test_projected_large_vocabulary(fckl):
+    """The vocabulary of the workloads, a decode-sized batch; forward only."""
+    Ht, Wt, tokens = make(3, 256, 201088, 2, "bf16", 4)
+    logp, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, 2048)
+    H, W = exact_inputs(Ht, Wt)
+    w_logp, w_ent, w_lse = orc.projected(H, W, tokens.cpu().numpy())
+    tol = 2 * logit_error(H, W) + 400 * U + 2.0 ** -21
+    close(f64(lse), w_lse, tol)
+    close(f64(logp), w_logp, tol[:, None] + 8 * U * np.abs(w_logp))
+    close(f64(ent), w_ent, 30 * tol)
+
+
+@gpu
+def test_projected_matches_loss_statistics(fckl):
+    """The loss against a one-token teacher of mass 1 is minus the log-probability: same lse, same
+    gradient, to the loss's tolerances."""
+    N, d, V = 200, 256, 3001
+    Ht, Wt, tokens = make(N, d, V, 1, "bf16", 6)
+    tokens = tokens.clamp(min=0)
+    logp, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, 64)
+    zero = torch.zeros(N, 1, device="cuda")
+    loss, lse2, dH2, dW2 = fckl.forward_backward(Ht, Wt, tokens, zero, 64)
+    fckl.check()
+    assert torch.allclose(lse, lse2, atol=1e-4)
+    assert abs(float(loss) + float(logp.sum())) <= 1e-4 * abs(float(loss))
+    dH, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, -torch.ones(N, 1, device="cuda"), chunk=64)
+    fckl.check()
+    assert (dH.float() - dH2.float()).abs().max() <= 2e-2 * dH2.float().abs().max()
+    assert (dW - dW2).abs().max() <= 2e-2 * dW2.abs().max()
+
+
+@gpu
+def test_projected_autograd(fckl):
+    """Gradients through autograd: the direct call's, W's rounded to its type; a missing and a
+    broadcast upstream gradient; only one leaf wanting a gradient; differences of the oracle."""
+    Ht, Wt, tokens = make(50, 128, 700, 2, "bf16", 8)
+    H, W = Ht.clone().requires_grad_(), Wt.clone().requires_grad_()
+    logp, ent = fckl.fused_token_logprobs(H, W, tokens, 32)
+    (logp.sum() - 0.25 * ent.sum()).backward()
+    _, ent0, lse0 = fckl.projected_logprobs(Ht, Wt, tokens, 32)
+    one = torch.ones(50, 2, device="cuda")
+    dH, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse0, ent0, one, torch.full((50,), -0.25, device="cuda"),
+                                              chunk=32)
+    assert torch.equal(H.grad, dH) and torch.equal(W.grad, dW.to(torch.bfloat16))
+    W2 = Wt.clone().requires_grad_()
+    fckl.fused_token_logprobs(Ht, W2, tokens, 32)[1].mean().backward()  # entropy alone
+    zero = torch.zeros(50, 2, device="cuda")
+    _, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse0, ent0, zero, torch.full((50,), 1 / 50, device="cuda"),
+                                             chunk=32)
+    assert torch.equal(W2.grad, dW.to(torch.bfloat16))
+    # directional differences of the fp64 value; bf16 gradients: each entry within 2^-7 of itself
+    # and G's rounding, so the sum over random directions within 2^-6 of its root sum of squares
+    Hd, Wd = exact_inputs(Ht, Wt)
+    tk = tokens.cpu().numpy()
+    value = lambda h, w: (lambda a, b, _: a.sum() - 0.25 * b.sum())(*orc.projected(h, w, tk))  # noqa: E731
+    rng = np.random.default_rng(1)
+    for A, grad, f in ((Hd, f64(H.grad), lambda x: value(x, Wd)), (Wd, f64(W.grad), lambda x: value(Hd, x))):
+        for _ in range(3):
+            v = rng.normal(size=A.shape)
+            diff = (f(A + 1e-5 * v) - f(A - 1e-5 * v)) / 2e-5
+            assert abs(diff - (grad * v).sum()) <= 2.0 ** -6 * np.sqrt(((grad * v) ** 2).sum()) + 1e-6 * abs(diff)
+
+
+@gpu
+def test_projected_deterministic_streams_graph_and_chunks(fckl):
+    Ht, Wt, tokens = make(300, 256, 5000, 3, "bf16", 10)
+    g, ge = torch.randn(300, 3, device="cuda"), torch.randn(300, device="cuda")
+    a = fckl.projected_logprobs(Ht, Wt, tokens, 100)
+    da = fckl.projected_logprobs_backward(Ht, Wt, tokens, a[2], a[1], g, ge, chunk=100)
+    b = fckl.projected_logprobs(Ht, Wt, tokens, 300)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))  # the chunk does not change a position's result
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    c = fckl.projected_logprobs(Ht, Wt, tokens, 100, stream=side)
+    dc = fckl.projected_logprobs_backward(Ht, Wt, tokens, c[2], c[1], g, ge, chunk=100, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a + da, c + dc))
+    ws = fckl.Workspace(300, 256, 5000, 3, 100, kind="projected_backward")
+    wf = fckl.Workspace(300, 256, 5000, 3, 100, kind="projected")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        e = fckl.projected_logprobs(Ht, Wt, tokens, 100, ws=wf)
+        de = fckl.projected_logprobs_backward(Ht, Wt, tokens, e[2], e[1], g, ge, chunk=100, ws=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert fckl.check(ws) == fckl.OK and fckl.check(wf) == fckl.OK
+    assert all(torch.equal(x, y) for x, y in zip(a + da, e + de))
+
+
+@gpu
+def test_projected_bad_token_and_empty(fckl):
+    Ht, Wt, tokens = make(4, 64, 500, 2, "bf16", 2)
+    bad = tokens.clone()
+    bad[1, 0] = 500
+    ws = fckl.Workspace(4, 64, 500, 2, 4, kind="projected")
+    logp = fckl.projected_logprobs(Ht, Wt, bad, 4, ws=ws)[0]
+    assert fckl.check(ws, raise_on_error=False) == fckl.ERR_INDEX
+    assert torch.isnan(logp[1, 0]) and torch.isfinite(logp[0]).all()
+    logp, ent, lse = fckl.projected_logprobs(Ht[:0], Wt, tokens[:0], 4)
+    assert fckl.check() == fckl.OK and tuple(logp.shape) == (0, 2) and tuple(ent.shape) == (0,)
+    dW = torch.full((500, 64), 7.0, device="cuda")
+    dH, dW = fckl.projected_logprobs_backward(Ht[:0], Wt, tokens[:0], lse, ent, logp, chunk=4, dW=dW)
+    assert tuple(dH.shape) == (0, 64) and (dW == 0).all()
+
+
+# ------------------------------------------------------------------ refusals and sizes (CPU)
+def test_argument_errors_launch_nothing(fckl):
+    lib = fckl.load()
+    before = lib.fckl_launch_count()
+    p, z, odd = ctypes.c_void_p(256), ctypes.c_void_p(0), ctypes.c_void_p(258)
+    big = 1 << 40
+
+    def fwd(H=p, W=p, dt=0, tok=p, N=64, d=256, V=4096, T=2, chunk=16, logp=p, ent=p, lse=p, ws=p, n=big):
+        return lib.fckl_projected_logprobs(H, W, dt, tok, N, d, V, T, chunk, logp, ent, lse, ws, n, z)
+
+    for bad in (dict(N=-1), dict(T=-1), dict(V=0), dict(d=0), dict(chunk=0), dict(dt=2), dict(H=z), dict(H=odd),
+                dict(W=z), dict(W=odd), dict(tok=z), dict(tok=ctypes.c_void_p(257)), dict(logp=z), dict(ent=z),
+                dict(lse=z), dict(lse=odd), dict(ws=z), dict(ws=ctypes.c_void_p(128))):
+        assert fwd(**bad) == fckl.ERR_ARG, bad
+    for bad in (dict(T=1025), dict(d=250), dict(V=(1 << 30) + 1), dict(N=1 << 30, chunk=(1 << 24) + 1)):
+        assert fwd(**bad) == fckl.ERR_UNSUPPORTED, bad
+    assert fwd(n=256) == fckl.ERR_WORKSPACE
+
+    def bwd(H=p, W=p, dt=0, tok=p, N=64, d=256, V=4096, T=2, chunk=16, lse=p, ent=p, g=p, ge=z, dH=p, dW=p, ws=p,
+            n=big):
+        return lib.fckl_projected_logprobs_backward(H, W, dt, tok, N, d, V, T, chunk, lse, ent, g, ge, dH, dW, ws, n,
+                                                    z)
+
+    for bad in (dict(lse=z), dict(ent=z), dict(g=z), dict(dH=z), dict(dW=z), dict(dW=odd), dict(dH=odd),
+                dict(ge=ctypes.c_void_p(257))):
+        assert bwd(**bad) == fckl.ERR_ARG, bad
+    assert bwd(n=256) == fckl.ERR_WORKSPACE
+    assert lib.fckl_launch_count() == before
+
+
+def test_workspace_sizes(fckl):
+    n = fckl.load().fckl_projected_logprobs_workspace_bytes
+    f = n(32768, 2880, 201088, 1, 2048, fckl.BF16, 0)
+    b = n(32768, 2880, 201088, 1, 2048, fckl.BF16, 1)
+    tiles = -(-201088 // 256)
+    assert 0 <= f - (3 * tiles * 2048 * 4 + 2 * 2048 * 4) < 8 * 1024  # statistics, not logits
+    assert 0 <= b - (2048 * 201088 * 2 + 4 * 2048 * 2880 * 4 + 4 * 2048 * 4) < 8 * 1024
+    assert f == n(65536, 2880, 201088, 1, 2048, fckl.BF16, 0)  # the chunk bounds it, not N
+    assert n(0, 2880, 201088, 0, 2048, fckl.BF16, 0) > 0
+    for bad in ((-1, 64, 100, 1, 16, 0, 0), (4, 60, 100, 1, 16, 0, 0), (4, 64, 100, 1025, 16, 0, 0),
+                (4, 64, 100, 1, 0, 0, 0), (4, 64, 100, 1, 16, 2, 0)):
+        assert n(*bad) == 0, bad
+
+
+@pytest.mark.parametrize("bad", [
+    lambda f, H, W, t: f.projected_logprobs(H, W, t, 4), lambda f, H, W, t: f.projected_logprobs(H, W.float(), t, 4),
+    lambda f, H, W, t: f.projected_logprobs(H.half(), W.half(), t, 4),
+    lambda f, H, W, t: f.projected_logprobs(H, W, t.long(), 4),
+    lambda f, H, W, t: f.projected_logprobs(H, W[:, :8], t, 4), lambda f, H, W, t: f.projected_logprobs(H[0], W, t, 4),
+    lambda f, H, W, t: f.fused_token_logprobs(H, W, t[:2], 4),
+    lambda f, H, W, t: f.projected_logprobs_backward(H, W, t, t, t, t),
+])
+def test_binding_refusals(fckl, bad):
+    H, W = torch.zeros(3, 16, dtype=torch.bfloat16), torch.zeros(50, 16, dtype=torch.bfloat16)
+    with pytest.raises((TypeError, ValueError)):
+        bad(fckl, H, W, torch.zeros(3, 2, dtype=torch.int32))
