@@ -78,6 +78,7 @@ def load():
     lib.fckl_teacher_topk.restype = i32
     lib.fckl_teacher_topk.argtypes = [vp, vp, i32, i64, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     scoring._set_argtypes(lib)
+    block_scaled._set_argtypes(lib)
     lib.fckl_check.restype = i32
     lib.fckl_check.argtypes = [vp, vp]
     lib.fckl_status_string.restype = c.c_char_p
@@ -455,7 +456,8 @@ def profile_read():
     return {n: (ms[i], int(ln[i])) for i, n in enumerate(names)}
 
 
-from . import scoring  # noqa: E402  (uses the names above)
+from . import block_scaled, scoring  # noqa: E402  (they use the names above)
+from .block_scaled import *  # noqa: E402,F401,F403
 from .scoring import *  # noqa: E402,F401,F403
 
-__all__ += scoring.__all__
+__all__ += scoring.__all__ + block_scaled.__all__

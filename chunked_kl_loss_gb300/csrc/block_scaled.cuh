@@ -1,0 +1,390 @@
+// Output projection in 8-bit floating point (e4m3) with a scale for each block of 128.
+//
+// block_quantize_kernel: x [R, C] to e4m3 values and one fp32 scale per block_rows x 128 block
+// (block_rows 1: hidden states, one scale per position and 128 channels; 128: output matrices):
+//   s = max(amax / 448, 2^-126),   q = e4m3(x / s)
+// 448 is the largest e4m3 value. Both quotients are rounded to nearest in fp32 before anything
+// else is done with them, so the values are the same wherever the definition is followed.
+//
+// block_matmul_kernel: C[m, n] = sum_kb sa[m, kb] sb[n / 128, kb] sum_{k in kb} A[m, k] B[n, k],
+// with A [M, K] and B [N, K] in e4m3. The tensor cores sum one K-block of 128 at a time in fp32
+// (TMEM); the epilogue warps scale each K-block's sums and add them up in fp32 registers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cstdint>
+
+#include "score.cuh"
+#include "tc_gemm.cuh"
+
+namespace fckl {
+
+constexpr int QB = 128;  // values of a scale block along K
+constexpr float E4M3_MAX = 448.f;
+constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126: a block of zeros, or of tiny values
+
+// ---------------------------------------------------------------- quantisation
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int left, bool wide, float (&x)[8]) {
+  if (wide && left >= 8) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+      unpack16<T>(*reinterpret_cast<const uint4*>(p), x);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = e < left ? to_f32(p[e]) : 0.f;
+  }
+}
+
+__device__ __forceinline__ float absmax8(const float (&x)[8]) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int e = 1; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+  return m;
+}
+
+__device__ __forceinline__ float block_scale(float amax) { return fmaxf(__fdiv_rn(amax, E4M3_MAX), SCALE_MIN); }
+
+__device__ __forceinline__ void store8(uint8_t* q, int left, const float (&x)[8], float s) {
+  union {
+    __nv_fp8x2_storage_t h[4];
+    uint8_t b[8];
+    uint2 v;
+  } u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    u.h[e] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s)), __NV_SATFINITE,
+                                      __NV_E4M3);
+  if (left >= 8) {
+    *reinterpret_cast<uint2*>(q) = u.v;  // rows of q start on 16-byte boundaries
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) q[e] = u.b[e];
+  }
+}
+
+struct QuantParams {
+  const void* x;
+  int64_t ldx, rows;
+  int cols, kblocks;
+  int wide;  // x's rows start on 16-byte boundaries
+  uint8_t* q;
+  int64_t ldq;
+  float* scale;
+  int64_t rs, cs;  // element (row block, K-block) of scale at rb * rs + kb * cs
+  int64_t blocks;  // scale blocks in all
+};
+
+constexpr int QUANT_THREADS = 256;
+
+// One scale per row and 128 columns: 16 lanes a block, 8 values each.
+template <typename T>
+__global__ void __launch_bounds__(QUANT_THREADS) quantize_rows_kernel(const QuantParams p) {
+  const int l = threadIdx.x & 15;
+  // every lane of a warp takes part in the exchange, so the loop runs by the block's first index
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (QUANT_THREADS / 16);
+  const int64_t i = base + threadIdx.x / 16;
+  const bool on = i < p.blocks;
+  const int64_t row = on ? i / p.kblocks : 0;
+  const int kb = on ? static_cast<int>(i - row * p.kblocks) : 0;
+  const int c = kb * QB + 8 * l, left = on ? p.cols - c : 0;
+  float x[8];
+  load8(static_cast<const T*>(p.x) + row * p.ldx + c, left, p.wide, x);
+  float m = absmax8(x);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float s = block_scale(m);
+  if (left > 0) store8(p.q + row * p.ldq + c, left, x, s);
+  if (on && l == 0) p.scale[row * p.rs + kb * p.cs] = s;
+}
+
+// One scale per 128 x 128 block: a thread block each, the values held in registers between the
+// maximum and the conversion.
+template <typename T>
+__global__ void __launch_bounds__(QUANT_THREADS) quantize_blocks_kernel(const QuantParams p) {
+  constexpr int RSTEP = QUANT_THREADS / 16, STEPS = QB / RSTEP;
+  __shared__ float wmax[QUANT_THREADS / 32];
+  const int l = threadIdx.x & 15, r = threadIdx.x / 16;
+  const int64_t rb = blockIdx.x / p.kblocks;
+  const int kb = static_cast<int>(blockIdx.x - rb * p.kblocks);
+  const int c = kb * QB + 8 * l;
+  const T* x = static_cast<const T*>(p.x);
+  float v[STEPS][8];
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int64_t row = rb * QB + j * RSTEP + r;
+    const int left = row < p.rows ? p.cols - c : 0;
+    load8(x + (row < p.rows ? row : 0) * p.ldx + c, left, p.wide, v[j]);
+    m = fmaxf(m, absmax8(v[j]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < QUANT_THREADS / 32; ++w) m = fmaxf(m, wmax[w]);
+  const float s = block_scale(m);
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int64_t row = rb * QB + j * RSTEP + r;
+    if (row < p.rows && c < p.cols) store8(p.q + row * p.ldq + c, p.cols - c, v[j], s);
+  }
+  if (threadIdx.x == 0) p.scale[rb * p.rs + kb * p.cs] = s;
+}
+
+// ---------------------------------------------------------------- product
+// Instruction descriptor for kind::f8f6f4 with e4m3 A and B (format 0), fp32 D, both K-major.
+__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem of both CTAs] (+)= A * B^T over the CTA pair, e4m3 operands, K = 32 per instruction.
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns, as tmem_ld32. Beside the 128 sums of a thread there is
+// room for 16 more values, not for 32.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+constexpr int BS_EPI_WARPS = 8;  // two per TMEM lane quarter: 128 fp32 sums per thread
+constexpr int BS_THREADS = 64 + 32 * BS_EPI_WARPS;
+constexpr int BS_STAGES = 6;
+constexpr uint32_t BS_A_BYTES = BM * QB, BS_B_BYTES = BM * QB;
+constexpr uint32_t BS_STAGE_BYTES = BS_A_BYTES + BS_B_BYTES;
+constexpr uint32_t BS_BAR_OFF = BS_STAGES * BS_STAGE_BYTES;
+constexpr uint32_t BS_SMEM = BS_BAR_OFF + (2 * BS_STAGES + 5) * 8 + 16 + 1024;
+
+struct BlockMatmulParams {
+  CUtensorMap tmA;  // A [M, K] e4m3, 128 x 128 boxes
+  CUtensorMap tmB;  // B [N, K]
+  int m_blocks, n_blocks, k_blocks, num_units;
+  int64_t M, N;
+  const float* sa;
+  int64_t sa_rs, sa_cs;
+  const float* sb;
+  int64_t sb_rs, sb_cs;
+  void* c;
+  int64_t ldc;
+  int wide;  // c's rows start on 16-byte boundaries
+  unsigned* status;
+};
+
+// Persistent, one CTA per SM, SM pairs: a pair computes 256 x 256 of C (each CTA 128 rows). Warp 0
+// fills a ring of K-blocks (16 KB of A, 16 KB of B per CTA), warp 1 of the even CTA issues four
+// MMAs per K-block into one of two 256-column TMEM buffers, and the eight epilogue warps of both
+// CTAs fold each buffer into their registers while the next K-block is multiplied into the other.
+template <typename TC>
+__global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __grid_constant__ BlockMatmulParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BS_BAR_OFF);
+  uint64_t* empty = full + BS_STAGES;
+  uint64_t* tfull = empty + BS_STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x / 2, num_pairs = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < BS_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * BS_EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&p.tmA);
+    prefetch_tmap(&p.tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers exist before anyone signals them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t cnt = 0, armed = 0, armed_par = 0;
+      bool ok = true;
+      const uint32_t full_base = mapa_shared(smem_u32(full), 0);
+      for (int u = pair; ok && u < p.num_units; u += num_pairs) {
+        const int nb = u / p.m_blocks, mb = u - nb * p.m_blocks;
+        const int arow = (2 * mb + static_cast<int>(rank)) * BM;
+        const int brow = (2 * nb + static_cast<int>(rank)) * BM;
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++cnt) {
+          const uint32_t s = cnt % BS_STAGES, ph = (cnt / BS_STAGES) & 1u;
+          if (!wait_phase(&empty[s], ph ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            mbar_arrive_expect_tx(&full[s], 2 * BS_STAGE_BYTES);
+            armed |= 1u << s;
+            armed_par = (armed_par & ~(1u << s)) | (ph << s);
+          }
+          uint8_t* a = smem + s * BS_STAGE_BYTES;
+          const uint32_t fb = full_base + s * 8u;
+          tma_load_2d_pair(a, &p.tmA, fb, kb * QB, arow);
+          tma_load_2d_pair(a + BS_A_BYTES, &p.tmB, fb, kb * QB, brow);
+        }
+      }
+      // every copy this pair started lands before a CTA may exit (see tc_gemm.cuh)
+      if (leader) {
+        for (int s = 0; s < BS_STAGES; ++s)
+          if (armed & (1u << s)) drain_phase(&full[s], (armed_par >> s) & 1u, p.status);
+      } else if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      constexpr uint32_t IDESC = make_idesc_e4m3(2 * BM, 256);
+      uint32_t cnt = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < p.num_units; u += num_pairs) {
+        for (int kb = 0; kb < p.k_blocks; ++kb, ++cnt) {
+          const uint32_t acc = cnt & 1u, use = cnt >> 1;
+          const uint32_t s = cnt % BS_STAGES, ph = (cnt / BS_STAGES) & 1u;
+          if (!wait_phase_cluster(&tempty[acc], (use & 1u) ^ 1u, abort_flag, p.status) ||
+              !wait_phase(&full[s], ph, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + s * BS_STAGE_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_e4m3_pair(tmem_base + acc * ACC_STRIDE, make_sdesc_sw128(a_addr + kk * 32, 16, 1024),
+                           make_sdesc_sw128(a_addr + BS_A_BYTES + kk * 32, 16, 1024), IDESC, kk > 0);
+          umma_commit_pair(&empty[s], 0x3);
+          umma_commit_pair(&tfull[acc], 0x3);
+        }
+      }
+      umma_commit_pair(drain, 0x1);  // all MMAs finish before TMEM is released
+      drain_phase(drain, 0, p.status);
+    }
+  } else {
+    const int q = warp & 3;             // TMEM lane quarter this warp may access
+    const int half = (warp - 2) / 4;    // columns [128 half, 128 half + 128) of the tile
+    const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
+    uint32_t cnt = 0;
+    bool ok = true;
+    for (int u = pair; ok && u < p.num_units; u += num_pairs) {
+      const int nb = u / p.m_blocks, mb = u - nb * p.m_blocks;
+      const int64_t row = (2 * mb + static_cast<int64_t>(rank)) * BM + 32 * q + lane;
+      const int64_t col = static_cast<int64_t>(nb) * 256 + 128 * half;
+      const bool live = row < p.M && col < p.N;
+      const float* sa = p.sa + (live ? row : 0) * p.sa_rs;
+      const float* sb = p.sb + (live ? col / QB : 0) * p.sb_rs;
+      float a_next = live ? __ldg(sa) : 0.f, b_next = live ? __ldg(sb) : 0.f;
+      float sum[8][16];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int t = 0; t < 16; ++t) sum[c][t] = 0.f;
+      for (int kb = 0; kb < p.k_blocks; ++kb, ++cnt) {
+        const uint32_t acc = cnt & 1u, use = cnt >> 1;
+        const float sc = a_next * b_next;
+        if (live && kb + 1 < p.k_blocks) {  // the next K-block's scales, while this one is awaited
+          a_next = __ldg(sa + (kb + 1) * p.sa_cs);
+          b_next = __ldg(sb + (kb + 1) * p.sb_cs);
+        }
+        if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * ACC_STRIDE + 128 * half;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float x[16];
+          __syncwarp();
+          tmem_ld16(taddr + 16 * c, x);
+          if (c == 7) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (!leader)
+                mbar_arrive_cluster(tempty_leader + acc * 8u);
+              else
+                mbar_arrive(&tempty[acc]);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 16; ++t) sum[c][t] = fmaf(x[t], sc, sum[c][t]);
+        }
+      }
+      if (!ok || !live) continue;
+      TC* out = static_cast<TC*>(p.c) + row * p.ldc + col;
+      constexpr int VE = 16 / sizeof(TC);
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int v = 0; v < 16 / VE; ++v) {
+          const int o = 16 * c + VE * v;
+          __align__(16) TC y[VE];
+#pragma unroll
+          for (int e = 0; e < VE; ++e) y[e] = from_f32<TC>(sum[c][VE * v + e]);
+          if (p.wide && col + o + VE <= p.N) {
+            *reinterpret_cast<uint4*>(out + o) = *reinterpret_cast<const uint4*>(y);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+              if (col + o + e < p.N) out[o + e] = y[e];
+          }
+        }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the leader's MMAs into this CTA's TMEM are done
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+}  // namespace fckl

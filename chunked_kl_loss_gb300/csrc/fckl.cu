@@ -58,6 +58,8 @@ enum Kind {
   KIND_HEAD_LOGITS,
   KIND_HEAD_COMBINE,
   KIND_HEAD_GRAD,
+  KIND_BLOCK_QUANTIZE,
+  KIND_BLOCK_MATMUL,
   KIND_COUNT
 };
 const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", "fwd_combine",
@@ -71,7 +73,8 @@ const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", 
                                             "topk_select_side",
                                             "token_logprobs",         "token_logprobs_grad",
                                             "token_order",            "head_logits_stats",
-                                            "head_combine",           "head_logit_grad"};
+                                            "head_combine",           "head_logit_grad",
+                                            "block_quantize",         "block_scaled_matmul"};
 
 // ------------------------------------------------------------------ process state
 std::mutex g_mu;
@@ -1615,3 +1618,4 @@ extern "C" int fckl_forward_static(const void* H, const void* W, int dtype, cons
 
 #include "score_host.cuh"
 #include "head_host.cuh"
+#include "block_scaled_host.cuh"

@@ -294,6 +294,31 @@ int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, co
                                      const float* g_logp, const float* g_entropy, void* dH, float* dW, void* ws,
                                      size_t ws_bytes, void* stream);
 
+/* ---- Output projection in 8-bit floating point (e4m3) with a scale for each block of 128 along
+ * the contraction. Interface additions, no counterpart on the pages: they serve a teacher whose
+ * output matrix is stored in 8 bits, whose logits then feed fckl_token_logprobs. No gradient runs
+ * through them.
+ *
+ * fckl_block_quantize: x [rows, cols] (FCKL_BF16, FCKL_F16 or FCKL_F32, rows ldx elements apart) to
+ * e4m3 values q [rows, cols] (rows ldq bytes apart) and fp32 scales, one for each block of
+ * block_rows x 128 values, block_rows 1 (hidden states) or 128 (output matrices); the last blocks
+ * may be short. The scale of row block r and column block k is stored at r * scale_rs + k * scale_cs.
+ *   s = max(amax / 448, 2^-126),  q = e4m3(x / s)
+ * amax over the block's values; both quotients are rounded to nearest fp32, q to nearest even.
+ * A NaN stays a NaN. q is 16-byte aligned and ldq a multiple of 16; rows = 0 is allowed. */
+int fckl_block_quantize(const void* x, int dtype, int64_t ldx, int64_t rows, int64_t cols, int block_rows, void* q,
+                        int64_t ldq, float* scale, int64_t scale_rs, int64_t scale_cs, void* stream);
+
+/* C [M, N] = sum over blocks k of 128 of  sa[m, k] * sb[n / 128, k] * (A_k B_k^T)[m, n]
+ * A [M, K] and B [N, K] are e4m3, rows lda and ldb bytes apart (multiples of 16, arrays 16-byte
+ * aligned); sa and sb fp32 with the strides of fckl_block_quantize at block_rows 1 and 128. C is
+ * FCKL_BF16 or FCKL_F32, rows ldc elements apart. Products and sums are fp32 throughout; a bf16 C is
+ * rounded once. ws holds the status word (at least 256 bytes, see fckl_token_logprobs). M = 0 is
+ * allowed. */
+int fckl_block_scaled_matmul(const void* a, int64_t lda, const float* sa, int64_t sa_rs, int64_t sa_cs, const void* b,
+                             int64_t ldb, const float* sb, int64_t sb_rs, int64_t sb_cs, int64_t M, int64_t N,
+                             int64_t K, void* c, int c_dtype, int64_t ldc, void* ws, size_t ws_bytes, void* stream);
+
 /* Interface addition, no counterpart on the pages (they describe no device interface).
  * Synchronises `stream`, returns the status found on the device by the last call that
  * used `ws` (FCKL_OK if none), and clears it. */
