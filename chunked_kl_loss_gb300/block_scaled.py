@@ -64,7 +64,7 @@ def _scale_strides(name, s, shape):
 def block_quantize(x, rows=1, stream=None):
     """(e4m3 values [R, K], fp32 scales [ceil(R / rows), ceil(K / 128)]) of x [R, K] (bf16, fp16 or
     fp32): each block of ``rows`` (1 or 128) x 128 values is divided by max(amax / 448, 2^-126). The
-    scales of single rows are laid out by K-block, as the product reads them."""
+    scales of single rows lie a multiple of 16 bytes apart, as the product reads them four at a time."""
     import torch
     if x.dim() != 2:
         raise ValueError("expected x [R,K]")
@@ -78,10 +78,10 @@ def block_quantize(x, rows=1, stream=None):
     with _for_stream(stream, x):
         q = torch.empty(R, -(-K // 16) * 16, dtype=torch.float8_e4m3fn, device=x.device)[:, :K]
         if rows == 1:
-            scale = torch.empty(kb, R, dtype=torch.float32, device=x.device).t()
+            scale = torch.empty(R, -(-kb // 4) * 4, dtype=torch.float32, device=x.device)[:, :kb]
         else:
             scale = torch.empty(-(-R // rows), kb, dtype=torch.float32, device=x.device)
-    rs, cs = (1, max(R, 1)) if rows == 1 else (max(kb, 1), 1)
+    rs, cs = (-(-kb // 4) * 4 if rows == 1 else kb), 1
     p = _pkg._ptr
     st = _pkg.load().fckl_block_quantize(p(x), code, ldx, R, K, rows, p(q), -(-K // 16) * 16, p(scale), rs, cs,
                                          _pkg._stream_ptr(stream))

@@ -156,33 +156,74 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, 
       : "memory");
 }
 
-// 32 lanes x 16 consecutive 32-bit columns, as tmem_ld32. Beside the 128 sums of a thread there is
-// room for 16 more values, not for 32.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// Bounded wait: polls for a while before it reads the clock for its limit (wait_phase reads
+// %globaltimer as soon as its first poll fails).
+constexpr int POLLS = 512;
+__device__ __forceinline__ bool poll_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                           unsigned* status) {
+#pragma unroll 1
+  for (int i = 0; i < POLLS; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wait_phase(bar, parity, abort_flag, status);
+}
+
+// 32 lanes x 64 consecutive 32-bit columns, as tmem_ld32: two such loads read a thread's share of a
+// K-block, 3.56 ms against 4.25 ms with 16 columns at a time (8192 x 2880 x 201088).
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]),
+        "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]),
+        "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]),
+        "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
+        "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t on;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(on));
+  return on != 0;
+}
+
+// Arrive on an mbarrier of another CTA of the cluster. Only TMEM is handed over with it, which the
+// tcgen05 fences order: no memory of this thread has to be made visible to the other SM (with
+// cluster-wide release and acquire on this hand-off a K-block took 2400 cycles rather than 1400).
+__device__ __forceinline__ void arrive_peer(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 constexpr int BS_EPI_WARPS = 8;  // two per TMEM lane quarter: 128 fp32 sums per thread
-constexpr int BS_THREADS = 64 + 32 * BS_EPI_WARPS;
-constexpr int BS_STAGES = 6;
+constexpr int BS_THREADS = 128 + 32 * BS_EPI_WARPS;
+// Registers per thread: a block of 384 threads is launched with 168 (65536 / 384, rounded down to 8);
+// the first four warps give up what the epilogue's 128 sums and 64 values read at once need.
+constexpr int BS_REGS_FEW = 56, BS_REGS_EPI = 224;
+static_assert(128 * BS_REGS_FEW + 32 * BS_EPI_WARPS * BS_REGS_EPI <= BS_THREADS * 168, "registers at launch");
+constexpr int BS_STAGES = 5;
 constexpr uint32_t BS_A_BYTES = BM * QB, BS_B_BYTES = BM * QB;
 constexpr uint32_t BS_STAGE_BYTES = BS_A_BYTES + BS_B_BYTES;
-constexpr uint32_t BS_BAR_OFF = BS_STAGES * BS_STAGE_BYTES;
+constexpr uint32_t BS_OUT_OFF = BS_STAGES * BS_STAGE_BYTES;  // two staging boxes per epilogue warp
+constexpr uint32_t BS_BAR_OFF = BS_OUT_OFF + BS_EPI_WARPS * 2 * EPI_BUF_BYTES;
 constexpr uint32_t BS_SMEM = BS_BAR_OFF + (2 * BS_STAGES + 5) * 8 + 16 + 1024;
 
 struct BlockMatmulParams {
   CUtensorMap tmA;  // A [M, K] e4m3, 128 x 128 boxes
   CUtensorMap tmB;  // B [N, K]
+  CUtensorMap tmC;  // C, boxes of 32 rows x 128 bytes (wide)
   int m_blocks, n_blocks, k_blocks, num_units;
   int64_t M, N;
   const float* sa;
@@ -199,6 +240,18 @@ struct BlockMatmulParams {
 // fills a ring of K-blocks (16 KB of A, 16 KB of B per CTA), warp 1 of the even CTA issues four
 // MMAs per K-block into one of two 256-column TMEM buffers, and the eight epilogue warps of both
 // CTAs fold each buffer into their registers while the next K-block is multiplied into the other.
+//
+// What bounds it: a K-block is 512 cycles of MMA, and TMEM holds two. A buffer's round (MMA, its
+// commit seen by the epilogue, read into registers, its release seen by the MMA warp) has to fit
+// the MMA of the other one; it takes about 1400 cycles, of which the barriers' hand-offs are more
+// than half, so the MMAs run about 70% of the time. Measured steps at 8192 x 2880 x 201088 (bf16 C):
+// 9.7 ms with cluster-scope release and acquire on that hand-off; 5.8 ms without; 4.25 ms with the
+// MMA warp converged (its loop was 1000 cycles) and C staged and stored with TMA; 3.7 ms with half
+// the reads, twice as wide; 3.56 ms with the next tile's scales fetched early. With one hand-off per
+// tile instead of one per K-block, which cannot apply the scales, the same loop takes 3.2 ms.
+// Four 128-column buffers (4.5 ms: A is read twice from shared memory, whose bandwidth the MMAs'
+// operands and the copies already fill), sixteen epilogue warps (3.9 ms) and two K-blocks per ring
+// stage were slower.
 template <typename TC>
 __global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __grid_constant__ BlockMatmulParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -242,8 +295,10 @@ __global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __gri
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BS_REGS_FEW));
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------- TMA producer (each CTA)
       uint32_t cnt = 0, armed = 0, armed_par = 0;
       bool ok = true;
       const uint32_t full_base = mapa_shared(smem_u32(full), 0);
@@ -253,7 +308,7 @@ __global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __gri
         const int brow = (2 * nb + static_cast<int>(rank)) * BM;
         for (int kb = 0; kb < p.k_blocks; ++kb, ++cnt) {
           const uint32_t s = cnt % BS_STAGES, ph = (cnt / BS_STAGES) & 1u;
-          if (!wait_phase(&empty[s], ph ^ 1u, abort_flag, p.status)) {
+          if (!poll_phase(&empty[s], ph ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
           }
@@ -277,53 +332,72 @@ __global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __gri
         while (globaltimer_ns() - t0 < 200000ull) {
         }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
+      // -------------------------------------------------------- MMA issuer (leader CTA)
+      // The whole warp walks the loop and one elected lane issues: converged, the compiler keeps
+      // descriptors and addresses in uniform registers, which the MMAs take.
       constexpr uint32_t IDESC = make_idesc_e4m3(2 * BM, 256);
+      const uint64_t a0 = make_sdesc_sw128(smem_u32(smem), 16, 1024);
       uint32_t cnt = 0;
       bool ok = true;
       for (int u = pair; ok && u < p.num_units; u += num_pairs) {
         for (int kb = 0; kb < p.k_blocks; ++kb, ++cnt) {
           const uint32_t acc = cnt & 1u, use = cnt >> 1;
           const uint32_t s = cnt % BS_STAGES, ph = (cnt / BS_STAGES) & 1u;
-          if (!wait_phase_cluster(&tempty[acc], (use & 1u) ^ 1u, abort_flag, p.status) ||
-              !wait_phase(&full[s], ph, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+          ok = poll_phase(&full[s], ph, abort_flag, p.status) &&
+               poll_phase(&tempty[acc], (use & 1u) ^ 1u, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + s * BS_STAGE_BYTES);
+          if (elect_lane()) {
+            const uint64_t ad = a0 + static_cast<uint64_t>(s * (BS_STAGE_BYTES >> 4));
+            const uint32_t d = tmem_base + acc * ACC_STRIDE;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_e4m3_pair(tmem_base + acc * ACC_STRIDE, make_sdesc_sw128(a_addr + kk * 32, 16, 1024),
-                           make_sdesc_sw128(a_addr + BS_A_BYTES + kk * 32, 16, 1024), IDESC, kk > 0);
-          umma_commit_pair(&empty[s], 0x3);
-          umma_commit_pair(&tfull[acc], 0x3);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_e4m3_pair(d, ad + 2 * kk, ad + (BS_A_BYTES >> 4) + 2 * kk, IDESC, kk > 0);
+            umma_commit_pair(&tfull[acc], 0x3);
+            umma_commit_pair(&empty[s], 0x3);
+          }
+          __syncwarp();
         }
       }
-      umma_commit_pair(drain, 0x1);  // all MMAs finish before TMEM is released
-      drain_phase(drain, 0, p.status);
+      // all MMAs finish before TMEM is released; committed by the lane that issued them
+      if (elect_lane()) umma_commit_pair(drain, 0x1);
+      __syncwarp();
+      if (lane == 0) drain_phase(drain, 0, p.status);
     }
   } else {
-    const int q = warp & 3;             // TMEM lane quarter this warp may access
-    const int half = (warp - 2) / 4;    // columns [128 half, 128 half + 128) of the tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BS_REGS_EPI));
+    // ---------------------------------------------------------- epilogue (each CTA)
+    const int q = warp & 3;           // TMEM lane quarter this warp may access
+    const int half = (warp - 4) / 4;  // columns [128 half, 128 half + 128) of the tile
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
-    uint32_t cnt = 0;
+    uint8_t* obuf = smem + BS_OUT_OFF + (warp - 4) * 2 * EPI_BUF_BYTES;
+    uint32_t cnt = 0, ocnt = 0;
     bool ok = true;
-    for (int u = pair; ok && u < p.num_units; u += num_pairs) {
+    // This thread's row and first column of C and their scales. A tile's first scales are fetched
+    // before the tile ahead of it is written out, later ones a K-block ahead.
+    int64_t row = 0, col = 0;
+    bool live = false;
+    const float *sa = p.sa, *sb = p.sb;
+    float a_next = 0.f, b_next = 0.f;
+    auto enter = [&](int u) {
       const int nb = u / p.m_blocks, mb = u - nb * p.m_blocks;
-      const int64_t row = (2 * mb + static_cast<int64_t>(rank)) * BM + 32 * q + lane;
-      const int64_t col = static_cast<int64_t>(nb) * 256 + 128 * half;
-      const bool live = row < p.M && col < p.N;
-      const float* sa = p.sa + (live ? row : 0) * p.sa_rs;
-      const float* sb = p.sb + (live ? col / QB : 0) * p.sb_rs;
-      float a_next = live ? __ldg(sa) : 0.f, b_next = live ? __ldg(sb) : 0.f;
-      float sum[8][16];
+      row = (2 * mb + static_cast<int64_t>(rank)) * BM + 32 * q + lane;
+      col = static_cast<int64_t>(nb) * 256 + 128 * half;
+      live = row < p.M && col < p.N;
+      sa = p.sa + (live ? row : 0) * p.sa_rs;
+      sb = p.sb + (live ? col / QB : 0) * p.sb_rs;
+      a_next = live ? __ldg(sa) : 0.f;
+      b_next = live ? __ldg(sb) : 0.f;
+    };
+    if (pair < p.num_units) enter(pair);
+    for (int u = pair; ok && u < p.num_units; u += num_pairs) {
+      float sum[4][32];
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int t = 0; t < 16; ++t) sum[c][t] = 0.f;
+        for (int t = 0; t < 32; ++t) sum[c][t] = 0.f;
       for (int kb = 0; kb < p.k_blocks; ++kb, ++cnt) {
         const uint32_t acc = cnt & 1u, use = cnt >> 1;
         const float sc = a_next * b_next;
@@ -331,51 +405,69 @@ __global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __gri
           a_next = __ldg(sa + (kb + 1) * p.sa_cs);
           b_next = __ldg(sb + (kb + 1) * p.sb_cs);
         }
-        if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, poll_phase(&tfull[acc], use & 1u, abort_flag, p.status));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * ACC_STRIDE + 128 * half;
+        float x[64];
+        __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float x[16];
-          __syncwarp();
-          tmem_ld16(taddr + 16 * c, x);
-          if (c == 7) {
+        for (int c = 0; c < 2; ++c) {
+          tmem_ld64(taddr + 64 * c, x);
+          if (c == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
               if (!leader)
-                mbar_arrive_cluster(tempty_leader + acc * 8u);
+                arrive_peer(tempty_leader + acc * 8u);
               else
                 mbar_arrive(&tempty[acc]);
             }
           }
 #pragma unroll
-          for (int t = 0; t < 16; ++t) sum[c][t] = fmaf(x[t], sc, sum[c][t]);
+          for (int t = 0; t < 64; ++t) sum[2 * c + t / 32][t % 32] = fmaf(x[t], sc, sum[2 * c + t / 32][t % 32]);
         }
       }
-      if (!ok || !live) continue;
-      TC* out = static_cast<TC*>(p.c) + row * p.ldc + col;
-      constexpr int VE = 16 / sizeof(TC);
+      if (!ok) break;
+      const int64_t orow = row, ocol = col;
+      const bool olive = live;
+      if (u + num_pairs < p.num_units) enter(u + num_pairs);
+      constexpr int VE = 16 / sizeof(TC), BOX = 128 / sizeof(TC);  // values of 16 bytes, of a box's row
+      if (p.wide && (ocol + 128 <= p.N || p.N % VE == 0)) {
+        // staged 32 rows x 128 bytes at a time (128-byte swizzle) and stored with TMA, which leaves
+        // out what lies beyond C, but only in steps of 16 bytes along a row
+        const int64_t row0 = orow - lane;
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+        for (int bx = 0; bx < 128 / BOX; ++bx, ++ocnt) {
+          uint8_t* buf = obuf + (ocnt & 1u) * EPI_BUF_BYTES;
+          if (ocnt >= 2 && lane == 0) bulk_wait_read<1>();
+          __syncwarp();
 #pragma unroll
-        for (int v = 0; v < 16 / VE; ++v) {
-          const int o = 16 * c + VE * v;
-          __align__(16) TC y[VE];
+          for (int v = 0; v < 8; ++v) {
+            __align__(16) TC y[VE];
 #pragma unroll
-          for (int e = 0; e < VE; ++e) y[e] = from_f32<TC>(sum[c][VE * v + e]);
-          if (p.wide && col + o + VE <= p.N) {
-            *reinterpret_cast<uint4*>(out + o) = *reinterpret_cast<const uint4*>(y);
-          } else {
-#pragma unroll
-            for (int e = 0; e < VE; ++e)
-              if (col + o + e < p.N) out[o + e] = y[e];
+            for (int e = 0; e < VE; ++e) y[e] = from_f32<TC>(sum[(BOX * bx + VE * v) / 32][(BOX * bx + VE * v) % 32 + e]);
+            *reinterpret_cast<uint4*>(buf + lane * 128 + (v ^ (lane & 7)) * 16) = *reinterpret_cast<const uint4*>(y);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.M && ocol + BOX * bx < p.N)
+              tma_store_2d(&p.tmC, buf, static_cast<int>(ocol) + BOX * bx, static_cast<int>(row0));
+            bulk_commit();
           }
         }
+      } else if (olive) {
+        TC* out = static_cast<TC*>(p.c) + orow * p.ldc + ocol;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (ocol + 32 * c + e < p.N) out[32 * c + e] = from_f32<TC>(sum[c][e]);
+      }
     }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
   }
 
   tc_fence_before();

@@ -109,7 +109,7 @@ int fckl_block_scaled_matmul(const void* a, int64_t lda, const float* sa, int64_
     if (M > BS_MAX_ROWS || N > BS_MAX_ROWS || K > BS_MAX_COLS) return FCKL_ERR_UNSUPPORTED;
     // pitches of the tensor maps: multiples of 16 bytes below 2^40
     if (lda % 16 != 0 || ldb % 16 != 0 || lda >= (int64_t(1) << 40) || ldb >= (int64_t(1) << 40) ||
-        ldc > (int64_t(1) << 40))
+        ldc >= (int64_t(1) << 38))
       return FCKL_ERR_UNSUPPORTED;
     int st = status_ws_checks(ws, ws_bytes);
     if (st) return st;
@@ -139,7 +139,12 @@ int fckl_block_scaled_matmul(const void* a, int64_t lda, const float* sa, int64_
     p.sb_cs = sb_cs;
     p.c = c;
     p.ldc = ldc;
-    p.wide = aligned(c, 16) && ldc * value_bytes(c_dtype) % 16 == 0;
+    const size_t cb = value_bytes(c_dtype);
+    p.wide = aligned(c, 16) && ldc * cb % 16 == 0;
+    if (p.wide && (st = make_map(&p.tmC, c, c_dtype == FCKL_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                 N, M, ldc * cb, static_cast<uint32_t>(128 / cb), 32)))
+      return st;
     p.status = static_cast<unsigned*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return c_dtype == FCKL_BF16 ? launch_block_matmul<__nv_bfloat16>(di, p, s) : launch_block_matmul<float>(di, p, s);
