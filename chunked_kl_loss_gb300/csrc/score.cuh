@@ -26,6 +26,7 @@ namespace fckl {
 constexpr int SCORE_THREADS = 256;
 constexpr int SCORE_GV = 4;            // 16-byte vectors of a group
 constexpr int SCORE_MAX_GROUPS = 8192; // group maxima that one block keeps in shared memory
+constexpr int FEW_TOP = 128;           // alternatives that the threads' maxima bound well
 constexpr int TOKENS_MAX = 1024;       // given tokens, and alternatives, of a row
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -101,6 +102,8 @@ struct RowVecs {
   __device__ __forceinline__ uint4 raw(int i) const {
     return *reinterpret_cast<const uint4*>(row + static_cast<int64_t>(col(i)));
   }
+  // Vector i as it lies in memory; -inf outside the row.
+  __device__ __forceinline__ uint4 words(int i) const;
   // Values of vector i; -inf outside the row.
   __device__ __forceinline__ void load(int i, float (&x)[VE]) const {
     if (i < nvec && whole(i)) {
@@ -112,6 +115,26 @@ struct RowVecs {
     }
   }
 };
+
+template <typename T>
+__device__ __forceinline__ uint32_t fill_word(float v);
+
+template <typename T>
+__device__ __forceinline__ uint4 RowVecs<T>::words(int i) const {
+  if (i < nvec && whole(i)) return raw(i);
+  const uint32_t none = fill_word<T>(-INFINITY);
+  uint4 w = make_uint4(none, none, none, none);
+  if (i < nvec) {  // an end of the row
+    __align__(16) T v[VE];
+    *reinterpret_cast<uint4*>(v) = w;
+    const int c = col(i);
+#pragma unroll
+    for (int j = 0; j < VE; ++j)
+      if (c + j >= 0 && c + j < V) v[j] = row[c + j];
+    w = *reinterpret_cast<const uint4*>(v);
+  }
+  return w;
+}
 
 // ---------------------------------------------------------------- running statistics
 // m: maximum so far, l = sum exp(z - m), t = sum y exp(z - m) with y = (z - m) log2(e).
@@ -150,6 +173,116 @@ __device__ __forceinline__ void add_values(RowStat& s, const float (&x)[VE]) {
   }
 }
 
+// The fast form of the same sums, for whole groups of 16-byte vectors: two values at a time through
+// the packed fp32 instructions. Values are raised to at least low() first, which stands in for the
+// floor on y (finite times zero is zero): far below any maximum but one that is itself masked. A
+// block whose maximum ends below low_limit() is summed again by add_values.
+template <typename T>
+__device__ __forceinline__ float low();
+template <>
+__device__ __forceinline__ float low<__half>() {
+  return -6e4f;
+}
+template <>
+__device__ __forceinline__ float low<__nv_bfloat16>() {
+  return -1e30f;
+}
+template <>
+__device__ __forceinline__ float low<float>() {
+  return -1e30f;
+}
+template <typename T>
+__device__ __forceinline__ float low_limit() {
+  return low<T>() * 0.5f;
+}
+
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2f(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Per 32-bit word of a row: the larger of two words (by value; a NaN stays), the values of a word
+// raised to low(), and the word that stands for -inf.
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b, __half) {
+  uint32_t r;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b, float) {
+  return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ float max_of_word(uint32_t w, float) { return __uint_as_float(w); }
+template <typename T>
+__device__ __forceinline__ float max_of_word(uint32_t w, T) {
+  float a, b;
+  unpack2(w, a, b, T{});
+  return max_nan(a, b);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t fill_word(float v) {  // v in every value of a word
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(v);
+  } else {
+    const T t = from_f32<T>(v);
+    const uint16_t h = *reinterpret_cast<const uint16_t*>(&t);
+    return h | (static_cast<uint32_t>(h) << 16);
+  }
+}
+
+struct FastStat {
+  float m = -INFINITY;           // maximum so far, at least low()
+  unsigned long long l, t;       // the sums, two interleaved parts each
+  __device__ __forceinline__ FastStat() : l(pack2(0.f, 0.f)), t(pack2(0.f, 0.f)) {}
+  __device__ __forceinline__ void raise(float to) {  // brings the sums to a new maximum
+    const float y = fmaxf((m - to) * LOG2E, Y_FLOOR), f = ex2_approx(y);
+    t = mul2(pack2(f, f), fma2(pack2(y, y), l, t));
+    l = mul2(pack2(f, f), l);
+    m = to;
+  }
+  __device__ __forceinline__ void add(float a, float b) {
+    const unsigned long long y = mul2(add2(pack2(a, b), pack2(-m, -m)), pack2(LOG2E, LOG2E));
+    float ya, yb;
+    unpack2f(y, ya, yb);
+    const unsigned long long e = pack2(ex2_approx(ya), ex2_approx(yb));
+    l = add2(l, e);
+    t = fma2(y, e, t);
+  }
+  __device__ __forceinline__ RowStat stat() const {
+    RowStat s;
+    float a, b;
+    unpack2f(l, a, b);
+    s.l = a + b;
+    unpack2f(t, a, b);
+    s.t = a + b;
+    s.m = m;
+    return s;
+  }
+};
+
 // Order of (logit, id) pairs in one 64-bit number: larger logit first, then smaller id.
 __device__ __forceinline__ uint32_t logit_key(float z) { return order_key(z + 0.f); }  // -0 counts as +0
 __device__ __forceinline__ unsigned long long pair_key(float z, int id) {
@@ -187,6 +320,27 @@ __device__ __forceinline__ void block_sort(unsigned long long* a, int n) {
 }
 
 __device__ __forceinline__ int pow2_at_least(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+// Orders n distinct keys in shared memory, largest first. Up to a block's threads each key's place is
+// the number of larger ones (n reads and two barriers instead of a sort's dozens); `a` has room
+// for the next power of two.
+__device__ __forceinline__ void block_order(unsigned long long* a, int n) {
+  const int tid = threadIdx.x;
+  if (n <= SCORE_THREADS) {
+    __syncthreads();
+    const unsigned long long mine = tid < n ? a[tid] : 0ull;
+    int place = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) place += a[j] > mine;
+    __syncthreads();
+    if (tid < n) a[place] = mine;
+    __syncthreads();
+    return;
+  }
+  const int n2 = pow2_at_least(n);
+  for (int i = n + tid; i < n2; i += SCORE_THREADS) a[i] = 0ull;
+  block_sort(a, n2);
+}
 
 struct ScoreParams {
   const void* logits;
@@ -229,11 +383,12 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   extern __shared__ __align__(16) unsigned char score_smem[];
   unsigned long long* cand = reinterpret_cast<unsigned long long*>(score_smem);  // [cand_cap]
   uint32_t* gkey = reinterpret_cast<uint32_t*>(cand + (p.top ? p.cand_cap : 0));  // [groups]
+  uint16_t* live = reinterpret_cast<uint16_t*>(gkey + p.groups);                 // [groups]
   __shared__ RowStat sstat[WARPS];
   __shared__ RowStat bstat;  // this block's share of the row
   __shared__ int ibuf[WARPS];
+  __shared__ uint32_t tkey[SCORE_THREADS], tau_s;
   __shared__ int n_cand, n_live;
-  __shared__ uint16_t live[2 * TOKENS_MAX];
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = p.split > 1 ? static_cast<int>(cluster.block_rank()) : 0;
@@ -246,45 +401,62 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   const int c0 = max(0, rv.col(v0)), c1 = min(p.V, rv.col(v1));
 
   // ---- statistics and group maxima
-  RowStat s;
   constexpr int STEP = SCORE_THREADS * SCORE_GV;
   const int steps = (v1 - v0 + STEP - 1) / STEP;
-  float gmax = -INFINITY;
-  for (int st = 0, in_group = 0, g = tid; st < steps; ++st) {
-    float x[SCORE_GV][VE];
+  float tmax = -INFINITY;  // this thread's largest logit
+  RowStat s;
+  {
+    FastStat f;
+    float gmax = -INFINITY;
+    const uint32_t lo = fill_word<T>(low<T>());
+    uint4 next[SCORE_GV];
+    auto fetch = [&](int st) {
 #pragma unroll
-    for (int j = 0; j < SCORE_GV; ++j) {
-      const int i = v0 + st * STEP + j * SCORE_THREADS + tid;
-      if (i < v1) {
-        rv.load(i, x[j]);
-      } else {
+      for (int j = 0; j < SCORE_GV; ++j) {
+        const int i = v0 + st * STEP + j * SCORE_THREADS + tid;
+        next[j] = rv.words(i < v1 ? i : rv.nvec);
+      }
+    };
+    fetch(0);
+    for (int st = 0, in_group = 0, g = tid; st < steps; ++st) {
+      uint32_t w[4 * SCORE_GV];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) x[j][e] = -INFINITY;
+      for (int j = 0; j < SCORE_GV; ++j) {
+        w[4 * j] = next[j].x;
+        w[4 * j + 1] = next[j].y;
+        w[4 * j + 2] = next[j].z;
+        w[4 * j + 3] = next[j].w;
+      }
+      if (st + 1 < steps) fetch(st + 1);  // on its way while this step is summed
+      uint32_t wm = w[0];
+#pragma unroll
+      for (int j = 1; j < 4 * SCORE_GV; ++j) wm = max_words(wm, w[j], T{});
+      const float m = max_of_word(wm, T{});
+      const float mc = fmaxf(m, low<T>());
+      if (mc > f.m) f.raise(mc);
+#pragma unroll
+      for (int j = 0; j < 4 * SCORE_GV; j += sizeof(T) / 2) {
+        float a, b;
+        if constexpr (sizeof(T) == 4) {
+          a = __uint_as_float(max_words(w[j], lo, T{}));
+          b = __uint_as_float(max_words(w[j + 1], lo, T{}));
+        } else {
+          unpack2(max_words(w[j], lo, T{}), a, b, T{});
+        }
+        f.add(a, b);
+      }
+      if (p.top) {
+        gmax = fmaxf(gmax, m);
+        tmax = fmaxf(tmax, m);
+        if (++in_group == p.gsteps || st == steps - 1) {
+          gkey[g] = logit_key(gmax);
+          g += SCORE_THREADS;
+          gmax = -INFINITY;
+          in_group = 0;
+        }
       }
     }
-    float m = x[0][0];
-#pragma unroll
-    for (int j = 0; j < SCORE_GV; ++j)
-#pragma unroll
-      for (int e = 0; e < VE; ++e) m = max_nan(m, x[j][e]);
-    if (!(m <= s.m)) {  // a new maximum (or a NaN): bring the sums to it
-      RowStat none;
-      none.m = m;
-      s = merge(s, none);
-    }
-    if (s.m != -INFINITY || m != m) {
-#pragma unroll
-      for (int j = 0; j < SCORE_GV; ++j) add_values<VE>(s, x[j]);
-    }
-    if (p.top) {
-      gmax = fmaxf(gmax, m);
-      if (++in_group == p.gsteps || st == steps - 1) {
-        gkey[g] = logit_key(gmax);
-        g += SCORE_THREADS;
-        gmax = -INFINITY;
-        in_group = 0;
-      }
-    }
+    s = f.stat();
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -300,6 +472,36 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   s = sstat[0];
 #pragma unroll
   for (int w = 1; w < WARPS; ++w) s = merge(s, sstat[w]);
+  if (s.m < low_limit<T>()) {  // masked throughout: exact sums, slowly (the same for the whole block)
+    s = RowStat();
+    for (int i = v0 + tid; i < v1; i += SCORE_THREADS) {
+      float x[VE];
+      rv.load(i, x);
+      float m = x[0];
+#pragma unroll
+      for (int e = 1; e < VE; ++e) m = max_nan(m, x[e]);
+      if (!(m <= s.m)) {
+        RowStat none;
+        none.m = m;
+        s = merge(s, none);
+      }
+      if (s.m != -INFINITY || m != m) add_values<VE>(s, x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      RowStat b;
+      b.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+      b.l = __shfl_xor_sync(0xffffffffu, s.l, o);
+      b.t = __shfl_xor_sync(0xffffffffu, s.t, o);
+      s = merge(s, b);
+    }
+    __syncthreads();
+    if (lane == 0) sstat[warp] = s;
+    __syncthreads();
+    s = sstat[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) s = merge(s, sstat[w]);
+  }
   if (tid == 0) bstat = s;
 
   // ---- this block's alternatives: cand[0..k), sorted
@@ -307,10 +509,43 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   if (k > 0 && !(s.l != s.l)) {
     const int per_group = p.gsteps * SCORE_GV;
     const int ng = ((steps + p.gsteps - 1) / p.gsteps) * SCORE_THREADS;
-    // tau: the largest prefix of key bits that at least k group maxima reach, refined only until
-    // few more than k do
     uint32_t tau = order_key(-INFINITY);
-    if (ng >= k) {
+    if (k <= FEW_TOP) {
+      // the k-th largest of the threads' maxima, or a little less: 256 values, one warp. Each is the
+      // largest of hundreds of logits, so few more than k logits lie above it.
+      tkey[tid] = logit_key(tmax);
+      __syncthreads();
+      if (warp == 0) {
+        uint32_t key[WARPS], lo = 0xffffffffu, hi = 0;
+#pragma unroll
+        for (int j = 0; j < WARPS; ++j) {
+          key[j] = tkey[32 * j + lane];
+          lo = min(lo, key[j]);
+          hi = max(hi, key[j]);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);      // reached by all 256
+        hi = __reduce_max_sync(0xffffffffu, hi) + 1;  // reached by none (a key is never the largest uint32)
+        const int enough = k + k / 8;
+        while (hi - lo > 1) {
+          const uint32_t mid = lo + (hi - lo) / 2;
+          int n = 0;
+#pragma unroll
+          for (int j = 0; j < WARPS; ++j) n += key[j] >= mid;
+          n = __reduce_add_sync(0xffffffffu, n);
+          if (n >= k) {
+            lo = mid;
+            if (n <= enough) break;
+          } else {
+            hi = mid;
+          }
+        }
+        if (lane == 0) tau_s = lo;
+      }
+      __syncthreads();
+      tau = max(tau, tau_s);
+    } else if (ng >= k) {
+      // the largest prefix of key bits that at least k group maxima reach, refined only until few
+      // more than k do
       const int enough = k + k / 4 + 16;
       uint32_t prefix = 0;
       for (int bit = 31; bit >= 0; --bit) {
@@ -326,7 +561,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
       tau = max(prefix, tau);
     }
     for (int g = tid; g < ng; g += SCORE_THREADS) {
-      if (gkey[g] > tau) {  // at most `enough` of them, or fewer than k at an exact tau
+      if (gkey[g] > tau) {
         const int at = atomicAdd(&n_live, 1);
         live[at] = static_cast<uint16_t>(g);
       }
@@ -423,9 +658,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
       }
       c = min(c, k);
     }
-    const int n2 = pow2_at_least(c);
-    for (int i = c + tid; i < n2; i += SCORE_THREADS) cand[i] = 0ull;
-    block_sort(cand, n2);
+    block_order(cand, c);
   }
 
   // ---- the whole row, in block 0 of the cluster
@@ -445,9 +678,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
           for (int i = tid; i < kr; i += SCORE_THREADS) cand[n + i] = theirs[i];
           n += kr;
         }
-        const int n2 = pow2_at_least(n);
-        for (int i = n + tid; i < n2; i += SCORE_THREADS) cand[i] = 0ull;
-        block_sort(cand, n2);
+        block_order(cand, n);
       }
     }
     cluster.sync();  // the others' shared memory has been read

@@ -56,8 +56,8 @@ int launch_token_logprobs(DevInfo* di, ScoreParams p, int64_t N, cudaStream_t s)
   // twice the alternatives, so that ordinary rows' candidates fit; and the blocks' sets together
   p.cand_cap = 256;
   while (p.cand_cap < 2 * p.top || (p.split > 1 && p.cand_cap < p.split * p.top)) p.cand_cap *= 2;
-  const size_t smem = p.top ? size_t(p.cand_cap) * 8 + size_t(p.groups) * 4 : 0;
-  constexpr size_t SMEM_MAX = 8 * TOKENS_MAX * 8 + SCORE_MAX_GROUPS * 4;
+  const size_t smem = p.top ? size_t(p.cand_cap) * 8 + size_t(p.groups) * 6 : 0;
+  constexpr size_t SMEM_MAX = 8 * TOKENS_MAX * 8 + SCORE_MAX_GROUPS * 6;
   auto k = token_logprobs_kernel<T>;
   {
     static bool done[64] = {};
