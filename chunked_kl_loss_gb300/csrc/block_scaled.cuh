@@ -26,41 +26,112 @@ constexpr float E4M3_MAX = 448.f;
 constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126: a block of zeros, or of tiny values
 
 // ---------------------------------------------------------------- quantisation
+// 8 values as they lie in memory; zeros for those that are not there.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int left, bool wide, float (&x)[8]) {
+struct Eight {
+  static constexpr int WORDS = 2 * sizeof(T);
+  uint32_t w[WORDS];
+};
+
+template <typename T>
+__device__ __forceinline__ Eight<T> load8(const T* p, int left, bool wide) {
+  Eight<T> v;
   if (wide && left >= 8) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-      unpack16<T>(*reinterpret_cast<const uint4*>(p), x);
+#pragma unroll
+    for (int i = 0; i < Eight<T>::WORDS / 4; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + 4 * i);
+      v.w[4 * i] = u.x;
+      v.w[4 * i + 1] = u.y;
+      v.w[4 * i + 2] = u.z;
+      v.w[4 * i + 3] = u.w;
     }
   } else {
+    __align__(16) T x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = e < left ? to_f32(p[e]) : 0.f;
+    for (int e = 0; e < 8; ++e) x[e] = e < left ? p[e] : from_f32<T>(0.f);
+#pragma unroll
+    for (int i = 0; i < Eight<T>::WORDS; ++i) v.w[i] = reinterpret_cast<const uint32_t*>(x)[i];
+  }
+  return v;
+}
+
+__device__ __forceinline__ void values_of_words(const uint32_t* w, float& a, float& b, float) {
+  a = __uint_as_float(w[0]);
+  b = __uint_as_float(w[1]);
+}
+template <typename T>
+__device__ __forceinline__ void values_of_words(const uint32_t* w, float& a, float& b, T) {
+  unpack2(w[0], a, b, T{});
+}
+
+// Largest magnitude of a value in words, as words again (NaNs drop out).
+__device__ __forceinline__ uint32_t absmax_words(uint32_t m, uint32_t w, __nv_bfloat16) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w & 0x7fff7fffu));
+  return r;
+}
+__device__ __forceinline__ uint32_t absmax_words(uint32_t m, uint32_t w, __half) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w & 0x7fff7fffu));
+  return r;
+}
+__device__ __forceinline__ uint32_t absmax_words(uint32_t m, uint32_t w, float) {
+  return __float_as_uint(fmaxf(__uint_as_float(m), fabsf(__uint_as_float(w))));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t absmax8(uint32_t m, const Eight<T>& v) {
+#pragma unroll
+  for (int i = 0; i < Eight<T>::WORDS; ++i) m = absmax_words(m, v.w[i], T{});
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ float absmax_value(uint32_t m) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(m);
+  } else {
+    float a, b;
+    unpack2(m, a, b, T{});
+    return fmaxf(a, b);
   }
 }
 
-__device__ __forceinline__ float absmax8(const float (&x)[8]) {
-  float m = fabsf(x[0]);
-#pragma unroll
-  for (int e = 1; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-  return m;
-}
+// The scale of a block and how to divide by it. The quotient has to be the nearest fp32 number: with
+// r the reciprocal rounded to nearest, q = x r and e = x - q s (exact in an FMA), q + e r rounds to
+// the correctly rounded quotient (P. Markstein, IBM J. Res. Dev. 34, 1990). Its steps neither over-
+// nor underflow where s is in the range below, except in quotients too small to be anything but 0
+// in 8 bits; outside the range (a block with an infinity, or of nothing above 1e-27) the division
+// operator does it.
+struct BlockScale {
+  float s, r;
+  bool plain;  // plain division
+  __device__ __forceinline__ explicit BlockScale(float amax) {
+    s = fmaxf(__fdiv_rn(amax, E4M3_MAX), SCALE_MIN);
+    plain = !(s > 2.5e-30f && s < 1e36f);
+    r = __frcp_rn(s);
+  }
+};
 
-__device__ __forceinline__ float block_scale(float amax) { return fmaxf(__fdiv_rn(amax, E4M3_MAX), SCALE_MIN); }
-
-__device__ __forceinline__ void store8(uint8_t* q, int left, const float (&x)[8], float s) {
+template <typename T>
+__device__ __forceinline__ void store8(uint8_t* q, int left, const Eight<T>& v, const BlockScale& bs) {
   union {
     __nv_fp8x2_storage_t h[4];
     uint8_t b[8];
     uint2 v;
   } u;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    u.h[e] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s)), __NV_SATFINITE,
-                                      __NV_E4M3);
+  for (int e = 0; e < 4; ++e) {
+    float a, b;
+    values_of_words(v.w + e * Eight<T>::WORDS / 4, a, b, T{});
+    if (bs.plain) {
+      a = __fdiv_rn(a, bs.s);
+      b = __fdiv_rn(b, bs.s);
+    } else {
+      const unsigned long long x = pack2(a, b), r = pack2(bs.r, bs.r);
+      const unsigned long long q0 = mul2(x, r);
+      unpack2f(fma2(fma2(q0, pack2(-bs.s, -bs.s), x), r, q0), a, b);
+    }
+    u.h[e] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  }
   if (left >= 8) {
     *reinterpret_cast<uint2*>(q) = u.v;  // rows of q start on 16-byte boundaries
   } else {
@@ -95,20 +166,19 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows_kernel(const Quan
   const int64_t row = on ? i / p.kblocks : 0;
   const int kb = on ? static_cast<int>(i - row * p.kblocks) : 0;
   const int c = kb * QB + 8 * l, left = on ? p.cols - c : 0;
-  float x[8];
-  load8(static_cast<const T*>(p.x) + row * p.ldx + c, left, p.wide, x);
-  float m = absmax8(x);
+  const Eight<T> x = load8(static_cast<const T*>(p.x) + row * p.ldx + c, left, p.wide);
+  float m = absmax_value<T>(absmax8(0u, x));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float s = block_scale(m);
+  const BlockScale s(m);
   if (left > 0) store8(p.q + row * p.ldq + c, left, x, s);
-  if (on && l == 0) p.scale[row * p.rs + kb * p.cs] = s;
+  if (on && l == 0) p.scale[row * p.rs + kb * p.cs] = s.s;
 }
 
 // One scale per 128 x 128 block: a thread block each, the values held in registers between the
 // maximum and the conversion.
 template <typename T>
-__global__ void __launch_bounds__(QUANT_THREADS) quantize_blocks_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(QUANT_THREADS, sizeof(T) == 4 ? 2 : 4) quantize_blocks_kernel(const QuantParams p) {
   constexpr int RSTEP = QUANT_THREADS / 16, STEPS = QB / RSTEP;
   __shared__ float wmax[QUANT_THREADS / 32];
   const int l = threadIdx.x & 15, r = threadIdx.x / 16;
@@ -116,28 +186,30 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_blocks_kernel(const Qu
   const int kb = static_cast<int>(blockIdx.x - rb * p.kblocks);
   const int c = kb * QB + 8 * l;
   const T* x = static_cast<const T*>(p.x);
-  float v[STEPS][8];
-  float m = 0.f;
+  Eight<T> v[STEPS];
+  uint32_t mw = 0;
 #pragma unroll
   for (int j = 0; j < STEPS; ++j) {
     const int64_t row = rb * QB + j * RSTEP + r;
     const int left = row < p.rows ? p.cols - c : 0;
-    load8(x + (row < p.rows ? row : 0) * p.ldx + c, left, p.wide, v[j]);
-    m = fmaxf(m, absmax8(v[j]));
+    v[j] = load8(x + (row < p.rows ? row : 0) * p.ldx + c, left, p.wide);
   }
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) mw = absmax8(mw, v[j]);
+  float m = absmax_value<T>(mw);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < QUANT_THREADS / 32; ++w) m = fmaxf(m, wmax[w]);
-  const float s = block_scale(m);
+  const BlockScale s(m);
 #pragma unroll
   for (int j = 0; j < STEPS; ++j) {
     const int64_t row = rb * QB + j * RSTEP + r;
     if (row < p.rows && c < p.cols) store8(p.q + row * p.ldq + c, p.cols - c, v[j], s);
   }
-  if (threadIdx.x == 0) p.scale[rb * p.rs + kb * p.cs] = s;
+  if (threadIdx.x == 0) p.scale[rb * p.rs + kb * p.cs] = s.s;
 }
 
 // ---------------------------------------------------------------- product

@@ -4,6 +4,7 @@
 
 #include "block_scaled.cuh"
 #include "score_host.cuh"
+#include "skinny.cuh"
 
 namespace fckl {
 namespace {
@@ -57,6 +58,39 @@ int launch_block_matmul(DevInfo* di, const BlockMatmulParams& p, cudaStream_t s)
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.num_units, pairs)));
   cfg.stream = s;
   return launch(KIND_BLOCK_MATMUL, s, "block_scaled_matmul", [&] { cudaLaunchKernelEx(&cfg, k, p); });
+}
+
+size_t skinny_matmul_smem(int NG, int K) {
+  return size_t(8 * NG) * skinny_pitch(K) + size_t(2) * SK_WARPS * SK8_ROWS * 8 * NG * 4 +
+         size_t(cdiv(K, QB)) * 8 * NG * 4;
+}
+
+template <int NG, typename TC>
+int launch_matmul_skinny(DevInfo* di, SkinnyMatmulParams p, cudaStream_t s) {
+  auto k = block_matmul_skinny_kernel<NG, TC>;
+  static bool done[64] = {};
+  {
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    if (!done[di->id]) {
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SK8_SMEM_MAX);
+      if (e != cudaSuccess) {
+        set_error("cudaFuncSetAttribute(block_matmul_skinny)", e);
+        return FCKL_ERR_CUDA;
+      }
+      done[di->id] = true;
+    }
+  }
+  p.tiles = static_cast<int>(cdiv(p.N, SK8_ROWS));
+  const unsigned grid = static_cast<unsigned>(std::min(p.tiles, 2 * di->sms));
+  const size_t smem = skinny_matmul_smem(NG, p.K);
+  return launch(KIND_MATMUL_SKINNY, s, "block_matmul_skinny", [&] { k<<<grid, SK_THREADS, smem, s>>>(p); });
+}
+template <typename TC>
+int launch_matmul_skinny_any(DevInfo* di, const SkinnyMatmulParams& p, cudaStream_t s) {
+  switch (cdiv(p.M, 8)) {
+    case 1: return launch_matmul_skinny<1, TC>(di, p, s);
+    default: return launch_matmul_skinny<2, TC>(di, p, s);
+  }
 }
 
 }  // namespace
@@ -123,6 +157,28 @@ int fckl_block_scaled_matmul(const void* a, int64_t lda, const float* sa, int64_
     if (mb * nb > INT_MAX - 1024) return FCKL_ERR_UNSUPPORTED;
     DevInfo* di = nullptr;
     if ((st = device_info(&di))) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M <= SK_MAX_POS && skinny_matmul_smem(static_cast<int>(cdiv(M, 8)), static_cast<int>(K)) <= SK8_SMEM_MAX) {
+      SkinnyMatmulParams q{};
+      q.a = static_cast<const uint8_t*>(a);
+      q.lda = lda;
+      q.sa = sa;
+      q.sa_rs = sa_rs;
+      q.sa_cs = sa_cs;
+      q.b = static_cast<const uint8_t*>(b);
+      q.ldb = ldb;
+      q.sb = sb;
+      q.sb_rs = sb_rs;
+      q.sb_cs = sb_cs;
+      q.M = static_cast<int>(M);
+      q.K = static_cast<int>(K);
+      q.k_blocks = static_cast<int>(cdiv(K, QB));
+      q.N = N;
+      q.c = c;
+      q.ldc = ldc;
+      return c_dtype == FCKL_BF16 ? launch_matmul_skinny_any<__nv_bfloat16>(di, q, s)
+                                  : launch_matmul_skinny_any<float>(di, q, s);
+    }
     if ((st = make_map(&p.tmA, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, K, M, lda, QB, BM))) return st;
     if ((st = make_map(&p.tmB, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, K, N, ldb, QB, BM))) return st;
     p.m_blocks = static_cast<int>(mb);
@@ -146,7 +202,6 @@ int fckl_block_scaled_matmul(const void* a, int64_t lda, const float* sa, int64_
                                  N, M, ldc * cb, static_cast<uint32_t>(128 / cb), 32)))
       return st;
     p.status = static_cast<unsigned*>(ws);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     return c_dtype == FCKL_BF16 ? launch_block_matmul<__nv_bfloat16>(di, p, s) : launch_block_matmul<float>(di, p, s);
   });
 }

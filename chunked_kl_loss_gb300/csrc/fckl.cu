@@ -60,6 +60,8 @@ enum Kind {
   KIND_HEAD_GRAD,
   KIND_BLOCK_QUANTIZE,
   KIND_BLOCK_MATMUL,
+  KIND_HEAD_SKINNY,
+  KIND_MATMUL_SKINNY,
   KIND_COUNT
 };
 const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", "fwd_combine",
@@ -74,7 +76,8 @@ const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", 
                                             "token_logprobs",         "token_logprobs_grad",
                                             "token_order",            "head_logits_stats",
                                             "head_combine",           "head_logit_grad",
-                                            "block_quantize",         "block_scaled_matmul"};
+                                            "block_quantize",         "block_scaled_matmul",
+                                            "head_skinny",            "block_matmul_skinny"};
 
 // ------------------------------------------------------------------ process state
 std::mutex g_mu;

@@ -5,9 +5,15 @@
 
 #include "score_gemm.cuh"
 #include "score_host.cuh"
+#include "skinny.cuh"
 
 namespace fckl {
 namespace {
+
+// A chunk of fewer positions is copied to this many rows, zeros after it, before the product: with
+// fewer than 24 rows behind the tensor map every SM fetches the same few lines again and again, and
+// the product takes 235 to 300 us where it takes 200 with 24 and more (2880 x 201088).
+constexpr int HEAD_MIN_ROWS = 32;
 
 int head_shape(int64_t N, int d, int V, int T, int chunk, int dt) {
   if (N < 0 || T < 0) return FCKL_ERR_ARG;
@@ -33,15 +39,18 @@ Plan head_plan(int64_t N, int d, int V, int T, int chunk, int dt, bool backward)
   p.off_T = take(R * T * 4);
   p.off_sp = take(backward ? R * T * 4 : 0);
   p.off_S = take(backward ? R * 4 : 0);
-  p.off_pm = take(backward ? 0 : size_t(p.tiles_v) * R * 4);
-  p.off_pl = take(backward ? 0 : size_t(p.tiles_v) * R * 4);
-  p.off_pc = take(backward ? 0 : size_t(p.tiles_v) * R * 4);
+  // statistics: of every 256-column tile and row of a chunk, or of every block of the skinny kernel
+  const size_t skinny = N <= SK_MAX_POS ? size_t(std::min<int64_t>(cdiv(V, SK_ROWS), SK_MAX_BLOCKS)) * N : 0;
+  const size_t stat = backward ? 0 : std::max(size_t(p.tiles_v) * R, skinny) * 4;
+  p.off_pm = take(stat);
+  p.off_pl = take(stat);
+  p.off_pc = take(stat);
   p.off_G = take(backward ? R * p.ldG * 2 : 0);
   p.off_dhp = take(backward ? MAX_SPLITS * R * D * 4 : 0);
   const bool f32 = dt == FCKL_F32;
   p.off_Hb = take(f32 && backward ? R * D * 2 : 0);
   p.off_Wb = take(f32 && backward ? size_t(V) * D * 2 : 0);
-  p.off_Ht = take(f32 ? R * D * 4 : 0);
+  p.off_Ht = take(f32 ? R * D * 4 : size_t(HEAD_MIN_ROWS) * D * 2);
   p.off_Wt = take(f32 ? size_t(V) * D * 4 : 0);
   p.total = p.total_overlap = o;
   return p;
@@ -95,6 +104,16 @@ int head_prepare(Run& r, int64_t r0, int rows, const float* g, const void** Hl, 
       return st;
     *Hl = r.w + pl.off_Ht;
     *Hc = r.w + pl.off_Hb;
+  } else if (rows < HEAD_MIN_ROWS) {
+    uint8_t* pad = r.w + pl.off_Ht;
+    const size_t have = size_t(rows) * pl.d * 2, all = size_t(HEAD_MIN_ROWS) * pl.d * 2;
+    cudaError_t e = cudaMemcpyAsync(pad, *Hl, have, cudaMemcpyDeviceToDevice, r.s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(pad + have, 0, all - have, r.s);
+    if (e != cudaSuccess) {
+      set_error("short chunk", e);
+      return FCKL_ERR_CUDA;
+    }
+    *Hl = pad;
   }
   return FCKL_OK;
 }
@@ -136,11 +155,56 @@ int launch_head(int kind, DevInfo* di, const HeadParams& p, cudaStream_t s, cons
   return launch(kind, s, what, [&] { cudaLaunchKernelEx(&cfg, k, p); });
 }
 
+// One block per 32 positions, or per 4 where that leaves most SMs without one.
+int launch_head_combine(const float* pm, const float* pl, const float* pt, int ld, int tiles, int rows,
+                        const int32_t* tokens, int T, int V, float* logp, float* entropy, float* lse,
+                        cudaStream_t s) {
+  return launch(KIND_HEAD_COMBINE, s, "head_combine", [&] {
+    if (rows > 512)
+      head_combine_kernel<32><<<static_cast<unsigned>(cdiv(rows, 32)), COMBINE_THREADS, 0, s>>>(
+          pm, pl, pt, ld, tiles, rows, tokens, T, V, logp, entropy, lse);
+    else
+      head_combine_kernel<4><<<static_cast<unsigned>(cdiv(rows, 4)), COMBINE_THREADS, 0, s>>>(
+          pm, pl, pt, ld, tiles, rows, tokens, T, V, logp, entropy, lse);
+  });
+}
+
+// Few positions, few tokens each, and hidden states that fit beside two steps' partial sums.
+size_t skinny_smem(int NG, int d, int64_t N, int T) {
+  return size_t(8 * NG) * skinny_pitch(d * 2) + size_t(2) * SK_WARPS * SK_ROWS * 8 * NG * 4 + size_t(N) * T * 4;
+}
+bool head_is_skinny(const Run& r, int64_t N, int d, int T) {
+  return r.dtype == FCKL_BF16 && N <= SK_MAX_POS && T <= SK_MAX_TOKENS &&
+         skinny_smem(static_cast<int>(cdiv(N, 8)), d, N, T) <= SK_SMEM_MAX;
+}
+
+template <int NG>
+int launch_head_skinny(DevInfo* di, HeadSkinnyParams p, cudaStream_t s, int* blocks) {
+  auto k = head_skinny_kernel<NG>;
+  const size_t smem = skinny_smem(NG, p.d, p.N, p.T);
+  static bool done[64] = {};
+  {
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    if (!done[di->id]) {
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SK_SMEM_MAX);
+      if (e != cudaSuccess) {
+        set_error("cudaFuncSetAttribute(head_skinny)", e);
+        return FCKL_ERR_CUDA;
+      }
+      done[di->id] = true;
+    }
+  }
+  p.tiles = static_cast<int>(cdiv(p.V, SK_ROWS));
+  *blocks = std::min({p.tiles, 2 * di->sms, SK_MAX_BLOCKS});
+  const unsigned grid = static_cast<unsigned>(*blocks);
+  return launch(KIND_HEAD_SKINNY, s, "head_skinny", [&] { k<<<grid, SK_THREADS, smem, s>>>(p); });
+}
+
 // What both passes over a chunk's logits share.
 int head_params(Run& r, const void* Hl, int rows, HeadParams* p) {
   const Plan& pl = r.pl;
   memset(p, 0, sizeof(*p));
-  int st = map_logits_A(r, &p->tmA, Hl, rows, &p->a_3d);
+  int st = map_logits_A(r, &p->tmA, Hl, std::max(rows, r.dtype == FCKL_BF16 ? HEAD_MIN_ROWS : 1), &p->a_3d);
   if (st) return st;
   p->tmB = r.tmW_k;
   p->b_3d = r.w_k_3d;
@@ -180,6 +244,29 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
     if ((st = run_begin(r, false))) return st;
     const Plan& pl = r.pl;
     cudaStream_t s = r.s;
+    if (head_is_skinny(r, N, d, T)) {
+      HeadSkinnyParams p{};
+      p.H = static_cast<const __nv_bfloat16*>(H);
+      p.W = static_cast<const __nv_bfloat16*>(W);
+      p.tokens = tokens;
+      p.N = static_cast<int>(N);
+      p.d = d;
+      p.V = V;
+      p.T = T;
+      p.pm = reinterpret_cast<float*>(r.w + pl.off_pm);
+      p.pl = reinterpret_cast<float*>(r.w + pl.off_pl);
+      p.pt = reinterpret_cast<float*>(r.w + pl.off_pc);
+      p.ld = p.N;
+      p.zt = logp;
+      p.status = r.status;
+      int blocks = 0;
+      switch (cdiv(N, 8)) {
+        case 1: st = launch_head_skinny<1>(r.di, p, s, &blocks); break;
+        default: st = launch_head_skinny<2>(r.di, p, s, &blocks); break;
+      }
+      if (st) return st;
+      return launch_head_combine(p.pm, p.pl, p.pt, p.ld, blocks, p.N, tokens, T, V, logp, entropy, lse, s);
+    }
     for (int64_t r0 = 0; r0 < N; r0 += pl.chunk) {
       const int rows = static_cast<int>(std::min<int64_t>(pl.chunk, N - r0));
       const void *Hl = nullptr, *Hc = nullptr;
@@ -194,12 +281,8 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
       st = dtype == FCKL_F32 ? launch_head<HEAD_STATS, true>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats")
                              : launch_head<HEAD_STATS, false>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats");
       if (st) return st;
-      const unsigned blocks = static_cast<unsigned>(cdiv(rows, 32));
-      st = launch(KIND_HEAD_COMBINE, s, "head_combine", [&] {
-        head_combine_kernel<<<blocks, 32 * COMBINE_WARPS, 0, s>>>(p.pm, p.pl, p.pt, p.ld_part, pl.tiles_v, rows,
-                                                                   tokens + r0 * T, T, V, p.zt, entropy + r0,
-                                                                   lse + r0);
-      });
+      st = launch_head_combine(p.pm, p.pl, p.pt, p.ld_part, pl.tiles_v, rows, tokens + r0 * T, T, V, p.zt,
+                               entropy + r0, lse + r0, s);
       if (st) return st;
     }
     return FCKL_OK;

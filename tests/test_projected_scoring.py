@@ -101,6 +101,39 @@ def test_projected(fckl, dtype, N, d, V, T, chunk):
 
 
 @gpu
+@pytest.mark.parametrize("N,d,V,T", [
+    (1, 2880, 5000, 1), (2, 8, 1, 1), (7, 64, 200, 3), (8, 520, 1000, 32), (9, 128, 333, 2), (24, 256, 4097, 1),
+    (25, 72, 17, 4), (32, 1000, 16, 1), (32, 2880, 3000, 2), (16, 4096, 700, 0), (32, 4096, 700, 1), (33, 512, 900, 1),
+    (3, 256, 900, 33), (1, 2880, 100003, 1),
+])
+def test_projected_decode(fckl, N, d, V, T):
+    """Few positions: both sides of every limit of the decoding form (positions, tokens, shared
+    memory), odd vocabularies, a vocabulary below one step."""
+    Ht, Wt, tokens = make(N, d, V, max(T, 1), "bf16", seed=N + V)
+    tokens = tokens[:, :T].contiguous()
+    logp, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, 2048)
+    assert fckl.check() == fckl.OK
+    H, W = exact_inputs(Ht, Wt)
+    w_logp, w_ent, w_lse = orc.projected(H, W, tokens.cpu().numpy())
+    dz, r = logit_error(H, W), (V // 16 + 80) * U + 2.0 ** -21
+    close(f64(lse), w_lse, dz + r + 8 * U * np.abs(w_lse))
+    close(f64(logp), w_logp, (2 * dz + r)[:, None] + 8 * U * np.abs(w_logp))
+    spread = np.maximum(w_ent, np.log(V)) + 2
+    close(f64(ent), w_ent, (dz * 2 * spread + r * (1 + 2 * spread)))
+    again = fckl.projected_logprobs(Ht, Wt, tokens, 2048)
+    assert all(torch.equal(a, b) for a, b in zip(again, (logp, ent, lse)))
+
+
+@gpu
+def test_projected_decode_bad_token(fckl):
+    Ht, Wt, tokens = make(2, 64, 500, 2, "bf16", 2)
+    tokens[0, 1] = 500
+    logp = fckl.projected_logprobs(Ht, Wt, tokens, 4)[0]
+    assert fckl.check(raise_on_error=False) == fckl.ERR_INDEX
+    assert torch.isnan(logp[0, 1]) and torch.isfinite(logp[1]).all()
+
+
+@gpu
 def test_projected_without_tokens_and_without_entropy(fckl):
     Ht, Wt, tokens = make(40, 128, 900, 2, "bf16", 3)
     check(fckl, Ht, Wt, tokens, 16, with_entropy=False)
@@ -258,8 +291,8 @@ def test_workspace_sizes(fckl):
     f = n(32768, 2880, 201088, 1, 2048, fckl.BF16, 0)
     b = n(32768, 2880, 201088, 1, 2048, fckl.BF16, 1)
     tiles = -(-201088 // 256)
-    assert 0 <= f - (3 * tiles * 2048 * 4 + 2 * 2048 * 4) < 8 * 1024  # statistics, not logits
-    assert 0 <= b - (2048 * 201088 * 2 + 4 * 2048 * 2880 * 4 + 4 * 2048 * 4) < 8 * 1024
+    assert 0 <= f - (3 * tiles * 2048 * 4 + 2 * 2048 * 4) < 8 * 1024 + 32 * 2880 * 2  # statistics, not logits
+    assert 0 <= b - (2048 * 201088 * 2 + 4 * 2048 * 2880 * 4 + 4 * 2048 * 4) < 8 * 1024 + 32 * 2880 * 2
     assert f == n(65536, 2880, 201088, 1, 2048, fckl.BF16, 0)  # the chunk bounds it, not N
     assert n(0, 2880, 201088, 0, 2048, fckl.BF16, 0) > 0
     for bad in ((-1, 64, 100, 1, 16, 0, 0), (4, 60, 100, 1, 16, 0, 0), (4, 64, 100, 1025, 16, 0, 0),
