@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _for_stream, _on_device, _rows, _value_code, _ws
+from .scoring import _address, _for_stream, _on_device, _rows, _stream, _value_code, _ws
 
 __all__ = ["block_quantize", "block_scaled_matmul", "block_scaled_projection"]
 
@@ -82,9 +82,9 @@ def block_quantize(x, rows=1, stream=None):
         else:
             scale = torch.empty(-(-R // rows), kb, dtype=torch.float32, device=x.device)
     rs, cs = (-(-kb // 4) * 4 if rows == 1 else kb), 1
-    p = _pkg._ptr
+    p = _address
     st = _pkg.load().fckl_block_quantize(p(x), code, ldx, R, K, rows, p(q), -(-K // 16) * 16, p(scale), rs, cs,
-                                         _pkg._stream_ptr(stream))
+                                         _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_block_quantize")
     return q, scale
@@ -115,10 +115,10 @@ def block_scaled_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, ws=Non
         ws = _ws(ws, dev)
         if out is None:
             out = torch.empty(M, N, dtype=out_dtype, device=dev)
-    p = _pkg._ptr
+    p = _address
     st = _pkg.load().fckl_block_scaled_matmul(p(a), lda, p(a_scale), *sa, p(b), ldb, p(b_scale), *sb, M, N, K, p(out),
-                                              _value_code(out, "out"), _rows("out", out), ws.ptr, ws.nbytes,
-                                              _pkg._stream_ptr(stream))
+                                              _value_code(out, "out"), _rows("out", out), ws.tensor.data_ptr(), ws.nbytes,
+                                              _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_block_scaled_matmul")
     return out

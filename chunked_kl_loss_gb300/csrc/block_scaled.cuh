@@ -150,29 +150,40 @@ struct QuantParams {
   int64_t ldq;
   float* scale;
   int64_t rs, cs;  // element (row block, K-block) of scale at rb * rs + kb * cs
-  int64_t blocks;  // scale blocks in all
 };
 
 constexpr int QUANT_THREADS = 256;
 
-// One scale per row and 128 columns: 16 lanes a block, 8 values each.
+// One scale per row and 128 columns: 16 lanes a row, 8 values each. A thread block takes 16 rows and
+// QUANT_UNROLL adjacent scale blocks of them, whose loads are issued together.
+constexpr int QUANT_UNROLL = 4;
+constexpr int QUANT_ROWS = QUANT_THREADS / 16;
 template <typename T>
 __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows_kernel(const QuantParams p) {
   const int l = threadIdx.x & 15;
-  // every lane of a warp takes part in the exchange, so the loop runs by the block's first index
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * (QUANT_THREADS / 16);
-  const int64_t i = base + threadIdx.x / 16;
-  const bool on = i < p.blocks;
-  const int64_t row = on ? i / p.kblocks : 0;
-  const int kb = on ? static_cast<int>(i - row * p.kblocks) : 0;
-  const int c = kb * QB + 8 * l, left = on ? p.cols - c : 0;
-  const Eight<T> x = load8(static_cast<const T*>(p.x) + row * p.ldx + c, left, p.wide);
-  float m = absmax_value<T>(absmax8(0u, x));
+  const unsigned kgroups = (p.kblocks + QUANT_UNROLL - 1) / QUANT_UNROLL;
+  const int64_t row = static_cast<int64_t>(blockIdx.x / kgroups) * QUANT_ROWS + threadIdx.x / 16;
+  const int kb0 = static_cast<int>(blockIdx.x % kgroups) * QUANT_UNROLL;
+  const bool on = row < p.rows;
+  const T* x0 = static_cast<const T*>(p.x) + (on ? row : 0) * p.ldx;
+  Eight<T> x[QUANT_UNROLL];
+  int left[QUANT_UNROLL];
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const BlockScale s(m);
-  if (left > 0) store8(p.q + row * p.ldq + c, left, x, s);
-  if (on && l == 0) p.scale[row * p.rs + kb * p.cs] = s.s;
+  for (int j = 0; j < QUANT_UNROLL; ++j) {
+    const int c = (kb0 + j) * QB + 8 * l;
+    left[j] = on ? p.cols - c : 0;
+    x[j] = load8(x0 + c, left[j], p.wide);
+  }
+#pragma unroll
+  for (int j = 0; j < QUANT_UNROLL; ++j) {
+    float m = absmax_value<T>(absmax8(0u, x[j]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const BlockScale s(m);
+    if (left[j] > 0) store8(p.q + row * p.ldq + (kb0 + j) * QB + 8 * l, left[j], x[j], s);
+    // lane 0's values are there whenever its block is
+    if (left[j] > 0 && l == 0) p.scale[row * p.rs + (kb0 + j) * p.cs] = s.s;
+  }
 }
 
 // One scale per 128 x 128 block: a thread block each, the values held in registers between the

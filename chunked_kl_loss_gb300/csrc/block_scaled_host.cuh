@@ -15,11 +15,11 @@ constexpr int64_t BS_MAX_COLS = int64_t(1) << 20;  // the framework's limit of d
 template <typename T>
 int launch_quantize(const QuantParams& p, int block_rows, cudaStream_t s) {
   if (block_rows == 1) {
-    const unsigned grid = static_cast<unsigned>(cdiv(p.blocks, QUANT_THREADS / 16));
+    const unsigned grid = static_cast<unsigned>(cdiv(p.rows, QUANT_ROWS) * cdiv(p.kblocks, QUANT_UNROLL));
     return launch(KIND_BLOCK_QUANTIZE, s, "block_quantize",
                   [&] { quantize_rows_kernel<T><<<grid, QUANT_THREADS, 0, s>>>(p); });
   }
-  const unsigned grid = static_cast<unsigned>(p.blocks);
+  const unsigned grid = static_cast<unsigned>(cdiv(p.rows, QB) * p.kblocks);
   return launch(KIND_BLOCK_QUANTIZE, s, "block_quantize",
                 [&] { quantize_blocks_kernel<T><<<grid, QUANT_THREADS, 0, s>>>(p); });
 }
@@ -124,9 +124,10 @@ int fckl_block_quantize(const void* x, int dtype, int64_t ldx, int64_t rows, int
     p.scale = scale;
     p.rs = scale_rs;
     p.cs = scale_cs;
-    p.blocks = cdiv(rows, block_rows) * p.kblocks;
-    // one grid: 2^31 - 1 thread blocks of 16 row blocks, or of one 128 x 128 block
-    if (cdiv(p.blocks, block_rows == 1 ? QUANT_THREADS / 16 : 1) > INT_MAX) return FCKL_ERR_UNSUPPORTED;
+    // one grid of up to 2^31 - 1 thread blocks
+    if ((block_rows == 1 ? cdiv(rows, QUANT_ROWS) * cdiv(p.kblocks, QUANT_UNROLL) : cdiv(rows, QB) * p.kblocks) >
+        INT_MAX)
+      return FCKL_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == FCKL_BF16) return launch_quantize<__nv_bfloat16>(p, block_rows, s);
     if (dtype == FCKL_F16) return launch_quantize<__half>(p, block_rows, s);

@@ -82,7 +82,7 @@ int head_prepare(Run& r, int64_t r0, int rows, const float* g, const void** Hl, 
   const Plan& pl = r.pl;
   const int T = pl.K;
   int st;
-  if (T > 0 || g) {
+  if (T > DIRECT_TOKENS) {
     const unsigned blocks = static_cast<unsigned>(cdiv(rows, PRE_WARPS));
     cudaStream_t s = r.s;
     uint8_t* w = r.w;
@@ -277,6 +277,7 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
       p.pl = reinterpret_cast<float*>(r.w + pl.off_pl);
       p.pt = reinterpret_cast<float*>(r.w + pl.off_pc);
       p.ld_part = pl.rows_alloc;
+      p.tokens = tokens + r0 * T;
       p.zt = logp + r0 * T;
       st = dtype == FCKL_F32 ? launch_head<HEAD_STATS, true>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats")
                              : launch_head<HEAD_STATS, false>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats");
@@ -313,17 +314,17 @@ int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, co
     r.dW = dW;
     if ((st = run_begin(r, true))) return st;
     const Plan& pl = r.pl;
-    // With no tokens the order kernel still writes the (zero) sums: it is given any gradient pointer.
-    const float* g = T > 0 ? g_logp : lse;
     for (int64_t r0 = 0; r0 < N; r0 += pl.chunk) {
       const int rows = static_cast<int>(std::min<int64_t>(pl.chunk, N - r0));
       const void *Hl = nullptr, *Hc = nullptr;
-      if ((st = head_prepare(r, r0, rows, g + r0 * T, &Hl, &Hc, true))) return st;
+      if ((st = head_prepare(r, r0, rows, g_logp + r0 * T, &Hl, &Hc, true))) return st;
       HeadParams p;
       if ((st = head_params(r, Hl, rows, &p))) return st;
       if ((st = make_map(&p.tmC, r.w + pl.off_G, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, V, rows, uint64_t(pl.ldG) * 2, 64,
                          32)))
         return st;
+      p.tokens = tokens + r0 * T;
+      p.g_logp = g_logp + r0 * T;
       p.sgrad = reinterpret_cast<const float*>(r.w + pl.off_sp);
       p.gsum = reinterpret_cast<const float*>(r.w + pl.off_S);
       p.lse = lse + r0;

@@ -754,9 +754,10 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_grad_kernel(cons
   T* orow = static_cast<T*>(p.dlogits) + row * p.ld_out;
   const RowVecs<T> ov(orow, p.V);  // vectors of the output: every store is wide but the ends
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int v0 = seg * SCORE_GRAD_STEP;
+  const int per = (ov.nvec + p.segs - 1) / p.segs;  // at most SCORE_GRAD_STEP
+  const int v0 = seg * per;
   if (v0 >= ov.nvec) return;
-  const int v1 = min(v0 + SCORE_GRAD_STEP, ov.nvec);
+  const int v1 = min(v0 + per, ov.nvec);
   const int c0 = max(0, ov.col(v0)), c1 = min(p.V, ov.col(v1));
 
   // the row's tokens and their gradients
@@ -805,9 +806,18 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_grad_kernel(cons
   };
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(zrow) & 15u) / sizeof(T)) - ov.mis;
   const bool same = shift == 0;  // logits and output vectors line up
+  constexpr int GB = 4;  // vectors whose loads are issued together (stores may be to the same array)
+  uint4 ahead[GB];
 #pragma unroll
   for (int j = 0; j < SCORE_GRAD_VECS; ++j) {
     const int i = v0 + j * SCORE_THREADS + tid;
+    if (j % GB == 0) {
+#pragma unroll
+      for (int b = 0; b < GB; ++b) {
+        const int ib = i + b * SCORE_THREADS;
+        if (same && !zero && ib < v1 && ov.whole(ib)) ahead[b] = *reinterpret_cast<const uint4*>(zrow + ov.col(ib));
+      }
+    }
     if (i >= v1) continue;
     const int c = ov.col(i);
     if (ov.whole(i)) {
@@ -817,7 +827,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_grad_kernel(cons
         for (int e = 0; e < VE; ++e) x[e] = 0.f;
       } else {
         if (same) {
-          unpack16<T>(*reinterpret_cast<const uint4*>(zrow + c), x);
+          unpack16<T>(ahead[j % GB], x);
         } else {
 #pragma unroll
           for (int e = 0; e < VE; ++e) x[e] = to_f32(zrow[c + e]);

@@ -18,6 +18,11 @@ namespace fckl {
 
 enum { HEAD_STATS = 0, HEAD_GRAD = 1 };
 
+// Up to this many tokens per position are compared with every tile's columns as they are; more are
+// ordered first (token_order_kernel), and a cursor walks them. Ordering is a launch of 6 us, the
+// comparisons are hidden behind the product.
+constexpr int DIRECT_TOKENS = 8;
+
 struct HeadParams {
   CUtensorMap tmA;  // H rows of the chunk
   CUtensorMap tmB;  // W
@@ -27,8 +32,10 @@ struct HeadParams {
   int a_3d, b_3d;  // one copy fetches a stage's two K-blocks
   unsigned* status;
   int rows, V, T;
-  const int* sid;    // [rows][T] tokens of the chunk, ascending per row
-  const int* sslot;  // [rows][T] the slot each came from
+  const int32_t* tokens;  // [rows][T] as given, for T <= DIRECT_TOKENS
+  const float* g_logp;    // [rows][T] (HEAD_GRAD)
+  const int* sid;         // else: [rows][T] tokens of the chunk, ascending per row
+  const int* sslot;       // [rows][T] the slot each came from
   // HEAD_STATS
   float* pm;  // [tiles][ld_part]
   float* pl;
@@ -210,14 +217,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
       const int row = row0 + lane;
       const bool valid = row < p.rows;
       const int v0 = nb * BN;
-      // cursor over the row's ordered tokens, at the first one of this tile (empty slots, -1,
-      // sort before every tile)
       const size_t tk = static_cast<size_t>(valid ? row : 0) * p.T;
+      const bool direct = p.T <= DIRECT_TOKENS;
+      // few tokens: each one's place in this tile, or -1, and its gradient
+      int rel[DIRECT_TOKENS];
+      float gt[DIRECT_TOKENS], gsum = 0.f;
+      // more: a cursor over the row's ordered tokens, at the first one of this tile (empty slots,
+      // -1, sort before every tile)
       const int* ids = p.sid + tk;
       int k = p.T, nxt = INT_MAX;
-      if (valid) {
+      if (direct) {
+#pragma unroll
+        for (int q = 0; q < DIRECT_TOKENS; ++q) {
+          const int id = valid && q < p.T ? __ldg(p.tokens + tk + q) : -1;
+          const bool in = id >= 0 && id < p.V;
+          if (nb == 0 && !in && id != -1) atomicOr(p.status, ST_BAD_INDEX);
+          rel[q] = in && id >= v0 && id < v0 + BN ? id - v0 : -1;
+          if constexpr (EPI == HEAD_GRAD) {
+            gt[q] = in ? __ldg(p.g_logp + tk + q) : 0.f;
+            gsum += gt[q];
+          }
+        }
+      } else if (valid) {
         k = lower_bound_ids(ids, p.T, v0);
         nxt = k < p.T ? __ldg(ids + k) : INT_MAX;
+        if constexpr (EPI == HEAD_GRAD) gsum = __ldg(p.gsum + row);
       }
       if constexpr (EPI == HEAD_STATS) {
         if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
@@ -230,6 +254,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
           tmem_ld32(taddr + 32 * j, x);
           if (j == BN / 32 - 1) release_acc(acc);
           const int cb = v0 + 32 * j;
+          if (direct) {
+#pragma unroll
+            for (int t = 0; t < DIRECT_TOKENS; ++t)
+              if (rel[t] >> 5 == j) p.zt[tk + t] = pick32(x, rel[t] & 31);
+          }
           while (nxt < cb + 32) {  // nxt < V or INT_MAX: ids past the vocabulary were put last
             p.zt[tk + __ldg(p.sslot + tk + k)] = pick32(x, nxt - cb);
             ++k;
@@ -257,7 +286,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
       } else {
         const float ge = valid && p.g_entropy ? __ldg(p.g_entropy + row) : 0.f;
         const float lse = valid ? __ldg(p.lse + row) : 0.f;
-        const float a0 = valid ? fmaf(ge, __ldg(p.entropy + row), __ldg(p.gsum + row)) : 0.f;
+        const float a0 = valid ? fmaf(ge, __ldg(p.entropy + row), gsum) : 0.f;
         if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -277,6 +306,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
             for (int t = 0; t < 32; ++t) {
               const float lq = x[t] - lse;
               x[t] = -ex2_approx(lq * LOG2E) * fmaf(ge, lq, a0);
+            }
+            if (direct) {
+#pragma unroll
+              for (int t = 0; t < DIRECT_TOKENS; ++t)
+                if (rel[t] >> 5 == j) sub32(x, rel[t] & 31, -gt[t]);
             }
             while (nxt < cb + 32) {
               sub32(x, nxt - cb, -__ldg(p.sgrad + tk + k));

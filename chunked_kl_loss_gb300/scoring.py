@@ -47,6 +47,14 @@ def _set_argtypes(lib):
     lib.fckl_token_logprobs_backward.argtypes = [vp, i32, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, i64, vp, sz, vp]
 
 
+def _stream(stream):
+    """Handle of ``stream``, or of the current stream."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _status_workspace(device):
     """The device's status word: zeroed once, shared by every call that is given no workspace (the
     word only gathers bits, so calls on several streams may share it)."""
@@ -81,11 +89,11 @@ def _value_code(t, what):
 
 def _on_device(device, **tensors):
     import torch
-    for name, t in tensors.items():
-        if t is not None and (not t.is_cuda or t.device != device):
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
     if device.type != "cuda" or device.index != torch.cuda.current_device():
         raise ValueError(f"tensors must be on the current CUDA device, got {device}")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
 def _dense(name, t, dtype, shape):
@@ -107,11 +115,18 @@ def _rows(name, t):
     return t.stride(0)
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+_here = contextlib.nullcontext()
+
+
 def _for_stream(stream, *inputs):
     """Context for allocations that `stream` will use (None: the current stream)."""
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _here
     for t in inputs:
         if t is not None:
             t.record_stream(stream)
@@ -146,9 +161,9 @@ def token_logprobs(logits, tokens, top=0, ws=None, stream=None):
         norm = torch.empty(N, 2, dtype=f32, device=dev)
         top_idx = torch.empty(N, max(top, 0), dtype=torch.int32, device=dev)
         top_logp = torch.empty(N, max(top, 0), dtype=f32, device=dev)
-    p = _pkg._ptr
+    p = _address
     st = _pkg.load().fckl_token_logprobs(p(logits), code, ld, p(tokens), N, V, T, top, p(logp), p(entropy), p(norm),
-                                         p(top_idx), p(top_logp), ws.ptr, ws.nbytes, _pkg._stream_ptr(stream))
+                                         p(top_idx), p(top_logp), ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_token_logprobs")
     return logp, entropy, norm, top_idx, top_logp
@@ -175,10 +190,10 @@ def token_logprobs_backward(logits, tokens, norm, entropy, g_logp, g_entropy=Non
         ws = _ws(ws, dev)
         if out is None:
             out = torch.empty(N, V, dtype=logits.dtype, device=dev)
-    p = _pkg._ptr
+    p = _address
     st = _pkg.load().fckl_token_logprobs_backward(p(logits), code, ld, p(tokens), N, V, T, p(norm), p(entropy),
                                                   p(g_logp), p(g_entropy), p(out), _rows("out", out), ws.ptr,
-                                                  ws.nbytes, _pkg._stream_ptr(stream))
+                                                  ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_token_logprobs_backward")
     return out
@@ -267,9 +282,9 @@ def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
         logp = torch.empty(N, T, dtype=torch.float32, device=dev)
         entropy = torch.empty(N, dtype=torch.float32, device=dev)
         lse = torch.empty(N, dtype=torch.float32, device=dev)
-    p = _pkg._ptr
+    p = _address
     st = _pkg.load().fckl_projected_logprobs(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(logp), p(entropy),
-                                             p(lse), ws.ptr, ws.nbytes, _pkg._stream_ptr(stream))
+                                             p(lse), ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_projected_logprobs")
     return logp, entropy, lse
@@ -301,10 +316,10 @@ def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=No
             dH = torch.empty(N, d, dtype=H.dtype, device=dev)
         if dW is None:
             dW = torch.empty(V, d, dtype=f32, device=dev)
-    p = _pkg._ptr
+    p = _address
     st = _pkg.load().fckl_projected_logprobs_backward(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(lse), p(entropy),
-                                                      p(g_logp), p(g_entropy), p(dH), p(dW), ws.ptr, ws.nbytes,
-                                                      _pkg._stream_ptr(stream))
+                                                      p(g_logp), p(g_entropy), p(dH), p(dW), ws.tensor.data_ptr(), ws.nbytes,
+                                                      _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_projected_logprobs_backward")
     return dH, dW
