@@ -21,6 +21,27 @@ int head_shape(int64_t N, int d, int V, int T, int chunk, int dt) {
   return check_shape(std::max<int64_t>(N, 1), d, V, 1, chunk, dt);
 }
 
+// K-splits (over V) of the dH product: the least estimated time, waves of 256 x 256 tiles over the 76 SM
+// pairs at a K-block's 0.34 us each (1900 TFLOP/s) plus the fp32 partials written and read back
+// (6.8 TB/s). With chunks of 512 rows at d = 1024 the loss's limit of 4 keeps 32 pairs busy (44 us);
+// 9 splits take TIME.
+constexpr int HEAD_MAX_SPLITS = 16;
+int head_splits(int rows, int d, int V) {
+  const int64_t kb = cdiv(V, BK), tiles = cdiv(rows, TILE_M) * cdiv(d, 256), pairs = 76;
+  int best = 1;
+  double least = 1e30;
+  for (int sp = 1; sp <= HEAD_MAX_SPLITS && sp <= kb; ++sp) {
+    const int64_t per = cdiv(kb, sp);
+    if (cdiv(kb, per) != sp) continue;
+    const double us = double(cdiv(tiles * sp, pairs)) * double(per) * 0.34 + 8.0 * sp * rows * double(d) / 6.8e6;
+    if (us < least) {
+      least = us;
+      best = sp;
+    }
+  }
+  return best;
+}
+
 // The loss's plan with the regions that scoring uses: ordered tokens in sidx, their slots in T
 // (rows x T ints), their gradients in sp, the sums of those in S, the tiles' statistics, and for the
 // backward pass the gradient slab and dH partials.
@@ -46,7 +67,7 @@ Plan head_plan(int64_t N, int d, int V, int T, int chunk, int dt, bool backward)
   p.off_pl = take(stat);
   p.off_pc = take(stat);
   p.off_G = take(backward ? R * p.ldG * 2 : 0);
-  p.off_dhp = take(backward ? MAX_SPLITS * R * D * 4 : 0);
+  p.off_dhp = take(backward ? std::max(MAX_SPLITS, head_splits(p.chunk, d, V)) * R * D * 4 : 0);
   const bool f32 = dt == FCKL_F32;
   p.off_Hb = take(f32 && backward ? R * D * 2 : 0);
   p.off_Wb = take(f32 && backward ? size_t(V) * D * 2 : 0);
@@ -314,6 +335,7 @@ int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, co
     r.dW = dW;
     if ((st = run_begin(r, true))) return st;
     const Plan& pl = r.pl;
+    if (!std::getenv("FCKL_SPLITS")) r.splits = head_splits(pl.chunk, d, V);
     for (int64_t r0 = 0; r0 < N; r0 += pl.chunk) {
       const int rows = static_cast<int>(std::min<int64_t>(pl.chunk, N - r0));
       const void *Hl = nullptr, *Hc = nullptr;

@@ -365,14 +365,14 @@ struct ScoreParams {
 // cluster merge them in a fixed order.
 // Alternatives: the pass also leaves in shared memory the maximum of every group of vectors (the
 // ones that one thread took in one step). tau is a lower bound on the block's K-th largest logit:
-// at least K groups have their maximum at or above it (or tau = -inf with fewer groups than K).
-// Only groups whose maximum is above tau can hold a logit above tau; there are about K, and they
-// are read again (from L2) to collect their logits above tau, C of them.
-//   C <  K: the K-th largest logit is tau itself; the first K - C ids with logit tau, found by a
-//           scan in id order, complete the set.
-//   C >= K: the set is among the collected ones.
-//   C above the room: tau is raised by bisection over the live groups' logits until the logits
-//           above it fit (or it is the K-th largest itself, which is the first case).
+// at least K threads, or groups, have their maximum at or above it (or tau = -inf).
+// Only groups whose maximum reaches tau can hold a logit at or above it; there are about K, and they
+// are read again (from L2) to collect those logits. They are K or more, and the set is among them.
+// Where they are more than there is room for (equal logits, masked rows):
+//   the logits above tau, C of them, are collected instead. C < K: the K-th largest logit is tau
+//   itself, and the first K - C ids with logit tau, found by a scan in id order, complete the set.
+//   C above the room: tau is raised by bisection over the listed groups' logits until the logits at
+//   or above it fit, or it is the K-th largest itself, which is the case before.
 // The set is sorted by (logit, id). Each block of a cluster does this for its share of the row,
 // and block 0 sorts the blocks' sets together. Exact for every input, ties included.
 template <typename T>
@@ -525,7 +525,9 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         }
         lo = __reduce_min_sync(0xffffffffu, lo);      // reached by all 256
         hi = __reduce_max_sync(0xffffffffu, hi) + 1;  // reached by none (a key is never the largest uint32)
-        const int enough = k + k / 8;
+        // a little more, but not so much that nearly every thread counts
+        const int bins = min(SCORE_THREADS, v1 - v0);
+        const int enough = k + min(k / 8 + 16, max(0, bins - k) / 4);
         while (hi - lo > 1) {
           const uint32_t mid = lo + (hi - lo) / 2;
           int n = 0;
@@ -560,20 +562,23 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
       }
       tau = max(prefix, tau);
     }
-    for (int g = tid; g < ng; g += SCORE_THREADS) {
-      if (gkey[g] > tau) {
-        const int at = atomicAdd(&n_live, 1);
-        live[at] = static_cast<uint16_t>(g);
-      }
-    }
-    __syncthreads();
-    const int items = n_live * per_group;
-    auto item_vec = [&](int it) {  // vector of item it of the live groups
+    auto list = [&](uint32_t cut) {  // groups that hold a logit at or above cut
+      __syncthreads();
+      if (tid == 0) n_live = n_cand = 0;
+      __syncthreads();
+      for (int g = tid; g < ng; g += SCORE_THREADS)
+        if (gkey[g] >= cut) live[atomicAdd(&n_live, 1)] = static_cast<uint16_t>(g);
+      __syncthreads();
+    };
+    auto item_vec = [&](int it) {  // vector of item it of the listed groups
       const int g = live[it / per_group], j = it % per_group;
       const int st = (g / SCORE_THREADS) * p.gsteps + j / SCORE_GV;
       return v0 + st * STEP + (j % SCORE_GV) * SCORE_THREADS + g % SCORE_THREADS;
     };
-    auto collect = [&]() {  // logits above tau into cand (as many as fit); n_cand counts them all
+    // logits at or above cut into cand, as many as fit; n_cand counts them all. Columns outside the
+    // row read as -inf, which no cut above it takes.
+    auto collect = [&](uint32_t cut) {
+      const int items = n_live * per_group;
       for (int it = tid; it < items; it += SCORE_THREADS) {
         const int i = item_vec(it);
         if (i >= v1) continue;
@@ -581,7 +586,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         rv.load(i, x);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          if (logit_key(x[e]) > tau) {  // columns outside the row are -inf, never above tau
+          if (logit_key(x[e]) >= cut) {
             const int at = atomicAdd(&n_cand, 1);
             if (at < p.cand_cap) cand[at] = pair_key(x[e], rv.col(i) + e);
           }
@@ -589,34 +594,43 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
       }
       __syncthreads();
     };
-    collect();
-    if (n_cand > p.cand_cap) {
-      // bisect: lo is reached by at least k logits; stop when those above it fit
-      uint32_t lo = tau, hi = 0xffffffffu;
-      while (hi - lo > 1) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        int n = 0;
-        for (int it = tid; it < items; it += SCORE_THREADS) {
-          const int i = item_vec(it);
-          if (i >= v1) continue;
-          float x[VE];
-          rv.load(i, x);
+    const uint32_t none = order_key(-INFINITY);
+    list(tau);
+    if (tau > none && n_live <= p.cand_cap) collect(tau);
+    if (tau == none || n_live > p.cand_cap || n_cand > p.cand_cap) {
+      // too many at tau (equal logits, or a mask): those above it, and then the first ones at it
+      list(tau + 1);
+      collect(tau + 1);
+      if (n_cand > p.cand_cap) {
+        // bisect: lo is reached by at least k logits; stop when those at or above it fit
+        const int items = n_live * per_group;
+        uint32_t lo = tau, hi = 0xffffffffu;
+        bool fits = false;
+        while (!fits && hi - lo > 1) {
+          const uint32_t mid = lo + (hi - lo) / 2;
+          int n = 0;
+          for (int it = tid; it < items; it += SCORE_THREADS) {
+            const int i = item_vec(it);
+            if (i >= v1) continue;
+            float x[VE];
+            rv.load(i, x);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) n += logit_key(x[e]) >= mid;
+            for (int e = 0; e < VE; ++e) n += logit_key(x[e]) >= mid;
+          }
+          n = block_sum(n, ibuf);
+          if (n >= k) {
+            lo = mid;
+            fits = n <= p.cand_cap;
+          } else {
+            hi = mid;
+          }
         }
-        n = block_sum(n, ibuf);
-        if (n >= k) {
-          lo = mid;
-          if (n <= p.cand_cap) break;
-        } else {
-          hi = mid;
-        }
+        tau = lo;
+        __syncthreads();
+        if (tid == 0) n_cand = 0;
+        __syncthreads();
+        collect(fits ? tau : tau + 1);
       }
-      tau = lo;
-      __syncthreads();
-      if (tid == 0) n_cand = 0;
-      __syncthreads();
-      collect();
     }
     int c = n_cand;
     if (c < k) {

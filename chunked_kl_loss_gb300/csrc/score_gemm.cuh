@@ -21,7 +21,7 @@ enum { HEAD_STATS = 0, HEAD_GRAD = 1 };
 // Up to this many tokens per position are compared with every tile's columns as they are; more are
 // ordered first (token_order_kernel), and a cursor walks them. Ordering is a launch of 6 us, the
 // comparisons are hidden behind the product.
-constexpr int DIRECT_TOKENS = 8;
+constexpr int DIRECT_TOKENS = 2;
 
 struct HeadParams {
   CUtensorMap tmA;  // H rows of the chunk

@@ -54,7 +54,7 @@ int launch_token_logprobs(DevInfo* di, ScoreParams p, int64_t N, cudaStream_t s)
   p.gsteps = static_cast<int>(cdiv(steps, SCORE_MAX_GROUPS / SCORE_THREADS));
   p.groups = static_cast<int>(cdiv(steps, p.gsteps)) * SCORE_THREADS;
   // twice the alternatives, so that ordinary rows' candidates fit; and the blocks' sets together
-  p.cand_cap = 256;
+  p.cand_cap = 512;
   while (p.cand_cap < 2 * p.top || (p.split > 1 && p.cand_cap < p.split * p.top)) p.cand_cap *= 2;
   const size_t smem = p.top ? size_t(p.cand_cap) * 8 + size_t(p.groups) * 6 : 0;
   constexpr size_t SMEM_MAX = 8 * TOKENS_MAX * 8 + SCORE_MAX_GROUPS * 6;

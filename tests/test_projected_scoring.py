@@ -292,7 +292,9 @@ def test_workspace_sizes(fckl):
     b = n(32768, 2880, 201088, 1, 2048, fckl.BF16, 1)
     tiles = -(-201088 // 256)
     assert 0 <= f - (3 * tiles * 2048 * 4 + 2 * 2048 * 4) < 8 * 1024 + 32 * 2880 * 2  # statistics, not logits
-    assert 0 <= b - (2048 * 201088 * 2 + 4 * 2048 * 2880 * 4 + 4 * 2048 * 4) < 8 * 1024 + 32 * 2880 * 2
+    # one chunk's gradient slab, 4 to 16 partial dH of a chunk, the ordered tokens
+    b -= 2048 * 201088 * 2 + 4 * 2048 * 4
+    assert 4 * 2048 * 2880 * 4 <= b < 16 * 2048 * 2880 * 4 + 8 * 1024 + 32 * 2880 * 2
     assert f == n(65536, 2880, 201088, 1, 2048, fckl.BF16, 0)  # the chunk bounds it, not N
     assert n(0, 2880, 201088, 0, 2048, fckl.BF16, 0) > 0
     for bad in ((-1, 64, 100, 1, 16, 0, 0), (4, 60, 100, 1, 16, 0, 0), (4, 64, 100, 1025, 16, 0, 0),
