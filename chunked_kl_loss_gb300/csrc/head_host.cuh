@@ -60,9 +60,9 @@ Plan head_plan(int64_t N, int d, int V, int T, int chunk, int dt, bool backward)
   p.off_T = take(R * T * 4);
   p.off_sp = take(backward ? R * T * 4 : 0);
   p.off_S = take(backward ? R * 4 : 0);
-  // statistics: of every 256-column tile and row of a chunk, or of every block of the skinny kernel
+  // statistics: of every HEAD_COLS columns and row of a chunk, or of every block of the skinny kernel
   const size_t skinny = N <= SK_MAX_POS ? size_t(std::min<int64_t>(cdiv(V, SK_ROWS), SK_MAX_BLOCKS)) * N : 0;
-  const size_t stat = backward ? 0 : std::max(size_t(p.tiles_v) * R, skinny) * 4;
+  const size_t stat = backward ? 0 : std::max(size_t(cdiv(V, HEAD_COLS)) * R, skinny) * 4;
   p.off_pm = take(stat);
   p.off_pl = take(stat);
   p.off_pc = take(stat);
@@ -150,7 +150,7 @@ int launch_head(int kind, DevInfo* di, const HeadParams& p, cudaStream_t s, cons
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.blockDim = dim3(HEAD_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -303,7 +303,7 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
       st = dtype == FCKL_F32 ? launch_head<HEAD_STATS, true>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats")
                              : launch_head<HEAD_STATS, false>(KIND_HEAD_LOGITS, r.di, p, s, "head_logits_stats");
       if (st) return st;
-      st = launch_head_combine(p.pm, p.pl, p.pt, p.ld_part, pl.tiles_v, rows, tokens + r0 * T, T, V, p.zt,
+      st = launch_head_combine(p.pm, p.pl, p.pt, p.ld_part, static_cast<int>(cdiv(V, HEAD_COLS)), rows, tokens + r0 * T, T, V, p.zt,
                                entropy + r0, lse + r0, s);
       if (st) return st;
     }

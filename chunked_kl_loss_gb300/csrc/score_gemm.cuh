@@ -50,8 +50,16 @@ struct HeadParams {
   const float* g_entropy;  // or null
 };
 
+// Eight epilogue warps, two per TMEM lane quarter (the loss's product has four): each takes 128 of a
+// tile's columns, a statistics tile of its own. With four, one per scheduler, nothing hid a warp's
+// latencies and the epilogue outlasted the product below d of about 1000.
+constexpr int HEAD_EPI_WARPS = 8;
+constexpr int HEAD_THREADS = 64 + 32 * HEAD_EPI_WARPS;
+constexpr int HEAD_COLS = VOCAB_TILE / 2;  // columns of a warp, and of a statistics tile
+static_assert(HEAD_EPI_WARPS * EPI_BUF_BYTES == EPI_WARPS * 2 * EPI_BUF_BYTES, "one staging box per warp");
+
 template <int EPI, bool TF32>
-__global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid_constant__ HeadParams p) {
+__global__ void __launch_bounds__(HEAD_THREADS, 1) head_score_kernel(const __grid_constant__ HeadParams p) {
   constexpr int CGS = 2, BN = VOCAB_TILE, BN_CTA = BN / CGS;
   constexpr int KPS = TF32 ? 1 : 2;
   using L = TcSmem<CGS, BN, KPS>;
@@ -81,7 +89,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], EPI_WARPS * CGS);
+      mbar_init(&tempty[a], HEAD_EPI_WARPS * CGS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -195,7 +203,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
   } else {
     // ------------------------------------------------------------ epilogue (each CTA)
     const int q = warp & 3;  // TMEM lane quarter this warp may access
-    uint8_t* ebuf0 = smem + L::EPI_OFF + (warp - 2) * 2 * EPI_BUF_BYTES;
+    const int half = (warp - 2) / 4;  // columns [HEAD_COLS half, + HEAD_COLS) of a tile
+    uint8_t* buf = smem + L::EPI_OFF + (warp - 2) * EPI_BUF_BYTES;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
     auto release_acc = [&](uint32_t acc) {
       tc_fence_before();
@@ -207,16 +216,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
           mbar_arrive(&tempty[acc]);
       }
     };
-    uint32_t it = 0, ecnt = 0;
+    uint32_t it = 0;
+    bool stored = false;
     for (int u = pair; u < p.num_units; u += num_pairs, ++it) {
       int mb, nb, sp, kb0, kb1;
       decode_unit(p.sch, u, mb, nb, sp, kb0, kb1);
       const uint32_t acc = it & 1u, use = it >> 1;
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * ACC_STRIDE;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * ACC_STRIDE + half * HEAD_COLS;
       const int row0 = (mb * CGS + static_cast<int>(rank)) * BM + 32 * q;  // first row of this warp
       const int row = row0 + lane;
       const bool valid = row < p.rows;
-      const int v0 = nb * BN;
+      const int v0 = nb * BN + half * HEAD_COLS;  // this warp's first column; may lie past V
       const size_t tk = static_cast<size_t>(valid ? row : 0) * p.T;
       const bool direct = p.T <= DIRECT_TOKENS;
       // few tokens: each one's place in this tile, or -1, and its gradient
@@ -231,8 +241,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
         for (int q = 0; q < DIRECT_TOKENS; ++q) {
           const int id = valid && q < p.T ? __ldg(p.tokens + tk + q) : -1;
           const bool in = id >= 0 && id < p.V;
-          if (nb == 0 && !in && id != -1) atomicOr(p.status, ST_BAD_INDEX);
-          rel[q] = in && id >= v0 && id < v0 + BN ? id - v0 : -1;
+          if (v0 == 0 && !in && id != -1) atomicOr(p.status, ST_BAD_INDEX);
+          rel[q] = in && id >= v0 && id < v0 + HEAD_COLS ? id - v0 : -1;
           if constexpr (EPI == HEAD_GRAD) {
             gt[q] = in ? __ldg(p.g_logp + tk + q) : 0.f;
             gsum += gt[q];
@@ -246,13 +256,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
       if constexpr (EPI == HEAD_STATS) {
         if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
         tc_fence_after();
-        RowStat s;
+        FastStat s[2];  // two sets of sums, for their latency; one maximum
 #pragma unroll 1
-        for (int j = 0; j < BN / 32; ++j) {
+        for (int j = 0; j < HEAD_COLS / 32; ++j) {
           float x[32];
           __syncwarp();
           tmem_ld32(taddr + 32 * j, x);
-          if (j == BN / 32 - 1) release_acc(acc);
+          if (j == HEAD_COLS / 32 - 1) release_acc(acc);
           const int cb = v0 + 32 * j;
           if (direct) {
 #pragma unroll
@@ -267,21 +277,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
           if (cb + 32 > p.V) {
 #pragma unroll
             for (int t = 0; t < 32; ++t)
-              if (cb + t >= p.V) x[t] = -INFINITY;
+              if (cb + t >= p.V) x[t] = low<float>();  // far below any logit, and no 0 * -inf
           }
           const float cm = max32(x);
-          if (cm > s.m) {
-            RowStat none;
-            none.m = cm;
-            s = merge(s, none);
+          if (cm > s[0].m) {
+            s[0].raise(cm);
+            s[1].raise(cm);
           }
-          add_values<32>(s, x);  // column v0 is in the vocabulary: s.m is finite (or the row is NaN)
+#pragma unroll
+          for (int t = 0; t < 32; t += 4) {
+            s[0].add(x[t], x[t + 1]);
+            s[1].add(x[t + 2], x[t + 3]);
+          }
         }
-        if (valid) {
-          const size_t o = static_cast<size_t>(nb) * p.ld_part + row;
-          p.pm[o] = s.m;
-          p.pl[o] = s.l;
-          p.pt[o] = s.t;
+        if (valid && v0 < p.V) {
+          const RowStat a = s[0].stat(), b = s[1].stat();  // of the same maximum
+          const size_t o = static_cast<size_t>(2 * nb + half) * p.ld_part + row;
+          p.pm[o] = a.m;
+          p.pl[o] = a.l + b.l;
+          p.pt[o] = a.t + b.t;
         }
       } else {
         const float ge = valid && p.g_entropy ? __ldg(p.g_entropy + row) : 0.f;
@@ -290,17 +304,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) head_score_kernel(const __grid
         if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int jj = 0; jj < BN / 64; ++jj, ++ecnt) {
-          uint8_t* buf = ebuf0 + (ecnt & 1u) * EPI_BUF_BYTES;
-          if (ecnt >= 2 && lane == 0) bulk_wait_read<1>();
+        for (int jj = 0; jj < HEAD_COLS / 64; ++jj) {
+          if (stored && lane == 0) bulk_wait_read<0>();
           __syncwarp();
+          stored = true;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int j = 2 * jj + h;
             float x[32];
             __syncwarp();
             tmem_ld32(taddr + 32 * j, x);
-            if (j == BN / 32 - 1) release_acc(acc);
+            if (j == HEAD_COLS / 32 - 1) release_acc(acc);
             const int cb = v0 + 32 * j;
 #pragma unroll
             for (int t = 0; t < 32; ++t) {

@@ -290,7 +290,7 @@ def test_workspace_sizes(fckl):
     n = fckl.load().fckl_projected_logprobs_workspace_bytes
     f = n(32768, 2880, 201088, 1, 2048, fckl.BF16, 0)
     b = n(32768, 2880, 201088, 1, 2048, fckl.BF16, 1)
-    tiles = -(-201088 // 256)
+    tiles = -(-201088 // 128)
     assert 0 <= f - (3 * tiles * 2048 * 4 + 2 * 2048 * 4) < 8 * 1024 + 32 * 2880 * 2  # statistics, not logits
     # one chunk's gradient slab, 4 to 16 partial dH of a chunk, the ordered tokens
     b -= 2048 * 201088 * 2 + 4 * 2048 * 4
