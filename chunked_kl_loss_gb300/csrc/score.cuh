@@ -330,8 +330,15 @@ __device__ __forceinline__ void block_order(unsigned long long* a, int n) {
     __syncthreads();
     const unsigned long long mine = tid < n ? a[tid] : 0ull;
     int place = 0;
+    if ((tid & ~31) < n) {  // warps that hold a key
+      const ulonglong2* two = reinterpret_cast<const ulonglong2*>(a);
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) place += a[j] > mine;
+      for (int j = 0; j < n / 2; ++j) {
+        const ulonglong2 v = two[j];
+        place += (v.x > mine) + (v.y > mine);
+      }
+      if (n & 1) place += a[n - 1] > mine;
+    }
     __syncthreads();
     if (tid < n) a[place] = mine;
     __syncthreads();
@@ -579,16 +586,29 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
     // row read as -inf, which no cut above it takes.
     auto collect = [&](uint32_t cut) {
       const int items = n_live * per_group;
-      for (int it = tid; it < items; it += SCORE_THREADS) {
-        const int i = item_vec(it);
-        if (i >= v1) continue;
-        float x[VE];
-        rv.load(i, x);
+      constexpr int AT_ONCE = 4;  // vectors of a thread whose loads are issued together
+      for (int it0 = tid; it0 < items; it0 += AT_ONCE * SCORE_THREADS) {
+        uint4 w[AT_ONCE];
+        int vec[AT_ONCE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          if (logit_key(x[e]) >= cut) {
-            const int at = atomicAdd(&n_cand, 1);
-            if (at < p.cand_cap) cand[at] = pair_key(x[e], rv.col(i) + e);
+        for (int b = 0; b < AT_ONCE; ++b) {
+          const int it = it0 + b * SCORE_THREADS;
+          const int i = it < items ? item_vec(it) : v1;
+          vec[b] = i < v1 ? i : rv.nvec;  // no such vector: -inf
+          w[b] = rv.words(vec[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < AT_ONCE; ++b) {
+          const uint32_t top2 = max_words(max_words(w[b].x, w[b].y, T{}), max_words(w[b].z, w[b].w, T{}), T{});
+          if (logit_key(max_of_word(top2, T{})) < cut) continue;  // most of a group's vectors
+          float x[VE];
+          unpack16<T>(w[b], x);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            if (logit_key(x[e]) >= cut) {
+              const int at = atomicAdd(&n_cand, 1);
+              if (at < p.cand_cap) cand[at] = pair_key(x[e], rv.col(vec[b]) + e);
+            }
           }
         }
       }
