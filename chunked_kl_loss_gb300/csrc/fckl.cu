@@ -542,8 +542,8 @@ int run_begin(Run& r, bool backward) {
   }
   if (!backward) return FCKL_OK;
   if ((st = map_mnmajor(&r.tmW_mn, r.Wb, d, V, uint64_t(d) * 2, KPS_GRAD, &r.w_mn_3d))) return st;
-  if ((st = make_map(&r.tmDW, r.dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, V, uint64_t(d) * 4, 32, 32))) return st;
-  if ((st = make_map(&r.tmDWp, r.dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, V, uint64_t(d) * 4, 256, BM,
+  if (r.dW && (st = make_map(&r.tmDW, r.dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, V, uint64_t(d) * 4, 32, 32))) return st;
+  if (r.dW && (st = make_map(&r.tmDWp, r.dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, V, uint64_t(d) * 4, 256, BM,
                      CU_TENSOR_MAP_SWIZZLE_NONE)))
     return st;
   // K-splits of dH = G W (K = V): the count that best fills the SM pairs.
@@ -737,7 +737,7 @@ int grad_from_kept(Run& r, int set, int64_t r0, int rows, cudaStream_t s, bool b
 }
 
 // The gradient products of one chunk whose G is in its slab: dH_chunk = G W and
-// dW (+)= G^T H_chunk.
+// dW (+)= G^T H_chunk; one whose output is null is left out.
 int chunk_products(Run& r, int set, int64_t r0, int rows, const void* Hc) {
   const Plan& pl = r.plan(set);
   const int d = pl.d, V = pl.V;
@@ -752,39 +752,42 @@ int chunk_products(Run& r, int set, int64_t r0, int rows, const void* Hc) {
   // --- dH_chunk = G W, split over the vocabulary into fp32 partials, then summed
   const int nbd = static_cast<int>(cdiv(d, pl.bn_d));
   const int splits = r.splits;
-  TcParams ph;
-  memset(&ph, 0, sizeof(ph));
-  if ((st = map_kmajor(&ph.tmA, G, V, rows, uint64_t(pl.ldG) * 2, BM, KPS_GRAD, &ph.a_3d))) return st;
-  ph.tmB = r.tmW_mn;
-  ph.b_3d = r.w_mn_3d;
-  if ((st = make_map(&ph.tmC, dhp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, uint64_t(splits) * pl.rows_alloc,
-                     uint64_t(d) * 4, 32, 32)))
-    return st;
-  const int kbps = static_cast<int>(cdiv(kb_v, splits));
-  ph.sch = {mbr, nbd, kb_v, splits, kbps, 1};
-  ph.num_units = mbr * nbd * splits;
-  ph.status = r.status;
-  ph.c_split_rows = pl.rows_alloc;
-  ph.c_reduce = 0;
-  ph.c_xlim = d;
-  ph.c_ylim = splits * pl.rows_alloc;
-  if ((st = launch_tc<256, false, true, EPI_STORE_F32>(KIND_BWD_DH, r.di, ph, s, "bwd_dH_gemm"))) return st;
-  {
-    const int64_t n4 = int64_t(rows) * d / 4;
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cdiv(n4, 256), int64_t(r.di->sms) * 8)));
-    const int64_t stride = int64_t(pl.rows_alloc) * d;
-    if (r.dtype == FCKL_F32) {
-      float* out = static_cast<float*>(r.dH) + static_cast<size_t>(r0) * d;
-      st = launch(KIND_BWD_DH_REDUCE, s, "bwd_dH_reduce",
-                  [&] { dh_reduce_kernel<float><<<grid, 256, 0, s>>>(dhp, splits, stride, rows, d, out); });
-    } else {
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(r.dH) + static_cast<size_t>(r0) * d;
-      st = launch(KIND_BWD_DH_REDUCE, s, "bwd_dH_reduce", [&] {
-        dh_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(dhp, splits, stride, rows, d, out);
-      });
+  if (r.dH) {
+    TcParams ph;
+    memset(&ph, 0, sizeof(ph));
+    if ((st = map_kmajor(&ph.tmA, G, V, rows, uint64_t(pl.ldG) * 2, BM, KPS_GRAD, &ph.a_3d))) return st;
+    ph.tmB = r.tmW_mn;
+    ph.b_3d = r.w_mn_3d;
+    if ((st = make_map(&ph.tmC, dhp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, d, uint64_t(splits) * pl.rows_alloc,
+                       uint64_t(d) * 4, 32, 32)))
+      return st;
+    const int kbps = static_cast<int>(cdiv(kb_v, splits));
+    ph.sch = {mbr, nbd, kb_v, splits, kbps, 1};
+    ph.num_units = mbr * nbd * splits;
+    ph.status = r.status;
+    ph.c_split_rows = pl.rows_alloc;
+    ph.c_reduce = 0;
+    ph.c_xlim = d;
+    ph.c_ylim = splits * pl.rows_alloc;
+    if ((st = launch_tc<256, false, true, EPI_STORE_F32>(KIND_BWD_DH, r.di, ph, s, "bwd_dH_gemm"))) return st;
+    {
+      const int64_t n4 = int64_t(rows) * d / 4;
+      const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cdiv(n4, 256), int64_t(r.di->sms) * 8)));
+      const int64_t stride = int64_t(pl.rows_alloc) * d;
+      if (r.dtype == FCKL_F32) {
+        float* out = static_cast<float*>(r.dH) + static_cast<size_t>(r0) * d;
+        st = launch(KIND_BWD_DH_REDUCE, s, "bwd_dH_reduce",
+                    [&] { dh_reduce_kernel<float><<<grid, 256, 0, s>>>(dhp, splits, stride, rows, d, out); });
+      } else {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(r.dH) + static_cast<size_t>(r0) * d;
+        st = launch(KIND_BWD_DH_REDUCE, s, "bwd_dH_reduce", [&] {
+          dh_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(dhp, splits, stride, rows, d, out);
+        });
+      }
+      if (st) return st;
     }
-    if (st) return st;
   }
+  if (!r.dW) return FCKL_OK;
 
   // --- dW (+)= G^T H_chunk: the first chunk stores, later chunks reduce-add
   TcParams pw;

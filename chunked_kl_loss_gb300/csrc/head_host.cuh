@@ -319,14 +319,14 @@ int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, co
     Run r;
     int st = head_setup(r, H, W, dtype, tokens, N, d, V, T, chunk, true, ws, ws_bytes, stream);
     if (st) return st;
-    if (!dW || !aligned(dW, 16)) return FCKL_ERR_ARG;
-    if (N > 0 && (!lse || !entropy || !dH || (T > 0 && !g_logp))) return FCKL_ERR_ARG;
+    if ((!dH && !dW) || !aligned(dW, 16)) return FCKL_ERR_ARG;
+    if (N > 0 && (!lse || !entropy || (T > 0 && !g_logp))) return FCKL_ERR_ARG;
     if (!aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4) || !aligned(dH, 16))
       return FCKL_ERR_ARG;
     if ((st = device_info(&r.di))) return st;
     if (N == 0) {
       cudaError_t e = cudaMemsetAsync(r.status, 0, 4, r.s);
-      if (e == cudaSuccess) e = cudaMemsetAsync(dW, 0, size_t(V) * d * 4, r.s);
+      if (e == cudaSuccess && dW) e = cudaMemsetAsync(dW, 0, size_t(V) * d * 4, r.s);
       if (e == cudaSuccess) return FCKL_OK;
       set_error("cudaMemsetAsync", e);
       return FCKL_ERR_CUDA;

@@ -291,9 +291,10 @@ def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
 
 
 def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=None, chunk=2048, ws=None, stream=None,
-                                dH=None, dW=None):
+                                dH=None, dW=None, need=(True, True)):
     """(dH [N, d] in H's dtype, dW fp32 [V, d]) of sum g_logp * logp + sum g_entropy * entropy;
-    ``lse`` and ``entropy`` as projected_logprobs returned them.
+    ``lse`` and ``entropy`` as projected_logprobs returned them. ``need``: which of the two to
+    compute (the other is None and its product is left out).
     ``ws``: Workspace(N, d, V, T, chunk, kind="projected_backward")."""
     import torch
     dt, N, d, V, T = _head_args(H, W, tokens)
@@ -312,10 +313,16 @@ def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=No
         _dense("dW", dW, f32, (V, d))
     with _for_stream(stream, H, W, tokens, lse, entropy, g_logp, g_entropy, dH, dW):
         ws = _head_ws(ws, N, d, V, T, chunk, dt, dev, "projected_backward")
-        if dH is None:
+        if not need[0]:
+            dH = None
+        elif dH is None:
             dH = torch.empty(N, d, dtype=H.dtype, device=dev)
-        if dW is None:
+        if not need[1]:
+            dW = None
+        elif dW is None:
             dW = torch.empty(V, d, dtype=f32, device=dev)
+        if N == 0 and dW is None:
+            return dH, dW
     p = _address
     st = _pkg.load().fckl_projected_logprobs_backward(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(lse), p(entropy),
                                                       p(g_logp), p(g_entropy), p(dH), p(dW), ws.tensor.data_ptr(), ws.nbytes,
@@ -345,9 +352,9 @@ def _head_autograd_function():
                 return None, None, None, None
             ge = None if g_entropy is None else _upstream(g_entropy, None, H.device)
             gl = _upstream(g_logp, tuple(tokens.shape), H.device)
-            dH, dW = projected_logprobs_backward(H, W, tokens, lse, entropy, gl, ge, chunk=ctx.chunk)
-            return (dH if ctx.needs_input_grad[0] else None, dW.to(W.dtype) if ctx.needs_input_grad[1] else None,
-                    None, None)
+            dH, dW = projected_logprobs_backward(H, W, tokens, lse, entropy, gl, ge, chunk=ctx.chunk,
+                                                 need=ctx.needs_input_grad[:2])
+            return dH, None if dW is None else dW.to(W.dtype), None, None
 
     return ProjectedLogprobs
 

@@ -215,6 +215,23 @@ def test_projected_autograd(fckl):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_projected_one_gradient(fckl, dtype):
+    """A frozen output matrix, or fixed hidden states: the other gradient has the same bits."""
+    Ht, Wt, tokens = make(70, 128, 900, 2, dtype, 14)
+    _, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, 32)
+    g = torch.randn(70, 2, device="cuda")
+    dH, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=32)
+    a, none = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=32, need=(True, False))
+    assert none is None and torch.equal(a, dH)
+    none, b = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=32, need=(False, True))
+    assert none is None and torch.equal(b, dW)
+    H = Ht.clone().requires_grad_()
+    (fckl.fused_token_logprobs(H, Wt, tokens, 32)[0] * g).sum().backward()
+    assert torch.equal(H.grad, dH)
+
+
+@gpu
 def test_projected_deterministic_streams_graph_and_chunks(fckl):
     Ht, Wt, tokens = make(300, 256, 5000, 3, "bf16", 10)
     g, ge = torch.randn(300, 3, device="cuda"), torch.randn(300, device="cuda")
@@ -279,7 +296,7 @@ def test_argument_errors_launch_nothing(fckl):
         return lib.fckl_projected_logprobs_backward(H, W, dt, tok, N, d, V, T, chunk, lse, ent, g, ge, dH, dW, ws, n,
                                                     z)
 
-    for bad in (dict(lse=z), dict(ent=z), dict(g=z), dict(dH=z), dict(dW=z), dict(dW=odd), dict(dH=odd),
+    for bad in (dict(lse=z), dict(ent=z), dict(g=z), dict(dH=z, dW=z), dict(dW=odd), dict(dH=odd),
                 dict(ge=ctypes.c_void_p(257))):
         assert bwd(**bad) == fckl.ERR_ARG, bad
     assert bwd(n=256) == fckl.ERR_WORKSPACE
