@@ -513,40 +513,54 @@ __global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __gri
       }
       if (!ok) break;
       const int64_t orow = row, ocol = col;
-      const bool olive = live;
       if (u + num_pairs < p.num_units) enter(u + num_pairs);
       constexpr int VE = 16 / sizeof(TC), BOX = 128 / sizeof(TC);  // values of 16 bytes, of a box's row
-      if (p.wide && (ocol + 128 <= p.N || p.N % VE == 0)) {
-        // staged 32 rows x 128 bytes at a time (128-byte swizzle) and stored with TMA, which leaves
-        // out what lies beyond C, but only in steps of 16 bytes along a row
-        const int64_t row0 = orow - lane;
+      // Staged 32 rows x 128 bytes at a time (128-byte swizzle). TMA stores a box where C's rows start on
+      // 16-byte boundaries; it leaves out what lies beyond C, but only in steps of 16 bytes along a
+      // row, so that a ragged end takes the other way: a row at a time, its values by adjacent lanes.
+      const bool tma = p.wide && (ocol + 128 <= p.N || p.N % VE == 0);
+      const int64_t row0 = orow - lane;
+      const int rows = static_cast<int>(max(int64_t(0), min(int64_t(32), p.M - row0)));
 #pragma unroll
-        for (int bx = 0; bx < 128 / BOX; ++bx, ++ocnt) {
-          uint8_t* buf = obuf + (ocnt & 1u) * EPI_BUF_BYTES;
-          if (ocnt >= 2 && lane == 0) bulk_wait_read<1>();
-          __syncwarp();
+      for (int bx = 0; bx < 128 / BOX; ++bx, ++ocnt) {
+        uint8_t* buf = obuf + (ocnt & 1u) * EPI_BUF_BYTES;
+        if (lane == 0) {
+          if (tma)
+            bulk_wait_read<1>();  // the store of the box before last has read this buffer
+          else
+            bulk_wait_read<0>();
+        }
+        __syncwarp();
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            __align__(16) TC y[VE];
+        for (int v = 0; v < 8; ++v) {
+          __align__(16) TC y[VE];
 #pragma unroll
-            for (int e = 0; e < VE; ++e) y[e] = from_f32<TC>(sum[(BOX * bx + VE * v) / 32][(BOX * bx + VE * v) % 32 + e]);
-            *reinterpret_cast<uint4*>(buf + lane * 128 + (v ^ (lane & 7)) * 16) = *reinterpret_cast<const uint4*>(y);
-          }
+          for (int e = 0; e < VE; ++e) y[e] = from_f32<TC>(sum[(BOX * bx + VE * v) / 32][(BOX * bx + VE * v) % 32 + e]);
+          *reinterpret_cast<uint4*>(buf + lane * 128 + (v ^ (lane & 7)) * 16) = *reinterpret_cast<const uint4*>(y);
+        }
+        const int64_t c0 = ocol + BOX * bx;
+        if (tma) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (row0 < p.M && ocol + BOX * bx < p.N)
-              tma_store_2d(&p.tmC, buf, static_cast<int>(ocol) + BOX * bx, static_cast<int>(row0));
+            if (row0 < p.M && c0 < p.N) tma_store_2d(&p.tmC, buf, static_cast<int>(c0), static_cast<int>(row0));
             bulk_commit();
           }
+        } else {
+          __syncwarp();
+          TC* out = static_cast<TC*>(p.c) + row0 * p.ldc + c0;
+#pragma unroll
+          for (int h = 0; h < BOX / 32; ++h) {
+            const int e = 32 * h + lane;
+            if (c0 + e < p.N) {
+#pragma unroll 4
+              for (int r = 0; r < rows; ++r)
+                out[r * p.ldc + e] = *reinterpret_cast<const TC*>(buf + r * 128 + ((e / VE) ^ (r & 7)) * 16 +
+                                                                  (e % VE) * sizeof(TC));
+            }
+          }
+          __syncwarp();  // read before the buffer is staged again
         }
-      } else if (olive) {
-        TC* out = static_cast<TC*>(p.c) + orow * p.ldc + ocol;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (ocol + 32 * c + e < p.N) out[32 * c + e] = from_f32<TC>(sum[c][e]);
       }
     }
     if (lane == 0) bulk_wait<0>();
