@@ -24,6 +24,7 @@
 #include <vector>
 
 #include "../../include/fckl.h"
+#include "score_gemm.cuh"
 #include "simt.cuh"
 #include "tc_gemm.cuh"
 
@@ -62,6 +63,7 @@ enum Kind {
   KIND_BLOCK_MATMUL,
   KIND_HEAD_SKINNY,
   KIND_MATMUL_SKINNY,
+  KIND_DW_REST,
   KIND_COUNT
 };
 const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", "fwd_combine",
@@ -77,7 +79,8 @@ const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", 
                                             "token_order",            "head_logits_stats",
                                             "head_combine",           "head_logit_grad",
                                             "block_quantize",         "block_scaled_matmul",
-                                            "head_skinny",            "block_matmul_skinny"};
+                                            "head_skinny",            "block_matmul_skinny",
+                                            "dw_rest"};
 
 // ------------------------------------------------------------------ process state
 std::mutex g_mu;
@@ -509,6 +512,9 @@ struct Run {
   void* dH = nullptr;
   float* dW = nullptr;
   int splits = 1;  // K-splits of the dH product
+  // scoring: what rounding left of G's entries at a chunk's given tokens, added to dH (may be null)
+  const float* rest = nullptr;
+  const int32_t* rest_tokens = nullptr;
   CUtensorMap tmW_k, tmW_mn, tmDW, tmDWp;
   int w_k_3d = 0, w_mn_3d = 0;  // tmW_k / tmW_mn are 3-D maps
 };
@@ -774,7 +780,20 @@ int chunk_products(Run& r, int set, int64_t r0, int rows, const void* Hc) {
       const int64_t n4 = int64_t(rows) * d / 4;
       const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cdiv(n4, 256), int64_t(r.di->sms) * 8)));
       const int64_t stride = int64_t(pl.rows_alloc) * d;
-      if (r.dtype == FCKL_F32) {
+      if (r.rest) {
+        const __nv_bfloat16* Wb = static_cast<const __nv_bfloat16*>(r.Wb);
+        const int32_t* tok = r.rest_tokens;
+        const int T = pl.K;
+        st = launch(KIND_BWD_DH_REDUCE, s, "dh_rest", [&] {
+          if (r.dtype == FCKL_F32)
+            dh_rest_kernel<float><<<grid, 256, 0, s>>>(dhp, splits, stride, rows, d, tok, r.rest, T, V, Wb,
+                                                       static_cast<float*>(r.dH) + static_cast<size_t>(r0) * d);
+          else
+            dh_rest_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
+                dhp, splits, stride, rows, d, tok, r.rest, T, V, Wb,
+                static_cast<__nv_bfloat16*>(r.dH) + static_cast<size_t>(r0) * d);
+        });
+      } else if (r.dtype == FCKL_F32) {
         float* out = static_cast<float*>(r.dH) + static_cast<size_t>(r0) * d;
         st = launch(KIND_BWD_DH_REDUCE, s, "bwd_dH_reduce",
                     [&] { dh_reduce_kernel<float><<<grid, 256, 0, s>>>(dhp, splits, stride, rows, d, out); });

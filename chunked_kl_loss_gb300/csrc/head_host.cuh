@@ -59,11 +59,13 @@ Plan head_plan(int64_t N, int d, int V, int T, int chunk, int dt, bool backward)
   p.off_sidx = take(R * T * 4);
   p.off_T = take(R * T * 4);
   p.off_sp = take(backward ? R * T * 4 : 0);
+  // rests of the tokens' entries, in pm's place
+  const size_t rests = backward && T <= REST_TOKENS ? R * T : 0;
   p.off_S = take(backward ? R * 4 : 0);
   // statistics: of every HEAD_COLS columns and row of a chunk, or of every block of the skinny kernel
   const size_t skinny = N <= SK_MAX_POS ? size_t(std::min<int64_t>(cdiv(V, SK_ROWS), SK_MAX_BLOCKS)) * N : 0;
   const size_t stat = backward ? 0 : std::max(size_t(cdiv(V, HEAD_COLS)) * R, skinny) * 4;
-  p.off_pm = take(stat);
+  p.off_pm = take(stat + rests * 4);
   p.off_pl = take(stat);
   p.off_pc = take(stat);
   p.off_G = take(backward ? R * p.ldG * 2 : 0);
@@ -135,6 +137,22 @@ int head_prepare(Run& r, int64_t r0, int rows, const float* g, const void** Hl, 
       return FCKL_ERR_CUDA;
     }
     *Hl = pad;
+  }
+  return FCKL_OK;
+}
+
+// Adds the rests of a chunk's tokens to dW.
+int launch_dw_rest(Run& r, const int32_t* tokens, const float* rest, int rows, const __nv_bfloat16* Hc) {
+  const int T = r.pl.K, d = r.pl.d, V = r.pl.V, entries = rows * T;
+  cudaStream_t s = r.s;
+  float* dW = r.dW;
+  for (int first = 0; first < entries; first += REST_WINDOW) {
+    const int end = std::min(entries, first + REST_WINDOW);
+    int st = launch(KIND_DW_REST, s, "dw_rest", [&] {
+      dw_rest_kernel<<<static_cast<unsigned>(end - first), REST_THREADS, 0, s>>>(tokens, rest, first, end, T, V, Hc, d,
+                                                                                  dW);
+    });
+    if (st) return st;
   }
   return FCKL_OK;
 }
@@ -352,10 +370,19 @@ int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, co
       p.lse = lse + r0;
       p.entropy = entropy + r0;
       p.g_entropy = g_entropy ? g_entropy + r0 : nullptr;
+      const bool rest = T > 0 && T <= REST_TOKENS;
+      if (rest) {
+        p.rest = reinterpret_cast<float*>(r.w + pl.off_pm);
+        r.rest = p.rest;
+        r.rest_tokens = p.tokens;
+      }
       st = dtype == FCKL_F32 ? launch_head<HEAD_GRAD, true>(KIND_HEAD_GRAD, r.di, p, r.s, "head_logit_grad")
                              : launch_head<HEAD_GRAD, false>(KIND_HEAD_GRAD, r.di, p, r.s, "head_logit_grad");
       if (st) return st;
       if ((st = chunk_products(r, 0, r0, rows, Hc))) return st;
+      if (rest && dW &&
+          (st = launch_dw_rest(r, p.tokens, p.rest, rows, static_cast<const __nv_bfloat16*>(Hc))))
+        return st;
     }
     return FCKL_OK;
   });

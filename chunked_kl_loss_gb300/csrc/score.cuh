@@ -767,6 +767,7 @@ struct ScoreGradParams {
 };
 constexpr int SCORE_GRAD_VECS = 8;  // vectors per thread of a segment
 constexpr int SCORE_GRAD_STEP = SCORE_THREADS * SCORE_GRAD_VECS;
+constexpr int SCORE_GRAD_RESIDENT = 5;  // blocks of 47 registers a thread on an SM
 
 // A block takes one segment of a row: dense part first, then the (few) tokens of the row that
 // fall into the segment, each written once with all its slots' gradients. Their logits are read
@@ -774,7 +775,7 @@ constexpr int SCORE_GRAD_STEP = SCORE_THREADS * SCORE_GRAD_VECS;
 // gradient is written as zeros without being read (positions that a loss masks out may hold
 // anything).
 template <typename T>
-__global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_grad_kernel(const ScoreGradParams p) {
+__global__ void __launch_bounds__(SCORE_THREADS, SCORE_GRAD_RESIDENT) token_logprobs_grad_kernel(const ScoreGradParams p) {
   constexpr int VE = 16 / sizeof(T);
   constexpr int WARPS = SCORE_THREADS / 32;
   constexpr int PER = TOKENS_MAX / SCORE_THREADS;

@@ -8,7 +8,10 @@
 //                log-partition, rounded to bf16 and stored with TMA into the chunk's gradient
 //                slab, which the dH and dW products read. As in the loss, G is rounded to bf16
 //                because the tensor cores take both operands in one type (half a step, 2^-8 of
-//                each entry, independent over the V or N entries that a product sums).
+//                each entry, independent over the V or N entries that a product sums). A few
+//                entries, those at the given tokens, are most of a gradient, and their rounding
+//                alone would double its error: with up to REST_TOKENS tokens what the rounding
+//                left of them is kept in fp32 and added to dH and dW (dh_rest_kernel, dw_rest_kernel).
 #pragma once
 
 #include "score.cuh"
@@ -22,6 +25,10 @@ enum { HEAD_STATS = 0, HEAD_GRAD = 1 };
 // ordered first (token_order_kernel), and a cursor walks them. Ordering is a launch of 6 us, the
 // comparisons are hidden behind the product.
 constexpr int DIRECT_TOKENS = 2;
+
+constexpr int REST_TOKENS = 8;
+
+__device__ __forceinline__ float rounding_left(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
 
 struct HeadParams {
   CUtensorMap tmA;  // H rows of the chunk
@@ -48,6 +55,7 @@ struct HeadParams {
   const float* lse;
   const float* entropy;
   const float* g_entropy;  // or null
+  float* rest;             // or null; [rows][T] by slot: what the rounding of G left of its entry at a token
 };
 
 // Eight epilogue warps, two per TMEM lane quarter (the loss's product has four): each takes 128 of a
@@ -325,11 +333,21 @@ __global__ void __launch_bounds__(HEAD_THREADS, 1) head_score_kernel(const __gri
 #pragma unroll
               for (int t = 0; t < DIRECT_TOKENS; ++t)
                 if (rel[t] >> 5 == j) sub32(x, rel[t] & 31, -gt[t]);
+#pragma unroll
+              for (int t = 0; t < DIRECT_TOKENS; ++t)
+                if (rel[t] >> 5 == j && p.rest) {
+                  bool first = true;  // a repeated token's entry counts once
+#pragma unroll
+                  for (int o = 0; o < t; ++o) first &= rel[o] != rel[t];
+                  p.rest[tk + t] = first ? rounding_left(pick32(x, rel[t] & 31)) : 0.f;
+                }
             }
             while (nxt < cb + 32) {
-              sub32(x, nxt - cb, -__ldg(p.sgrad + tk + k));
+              const int id = nxt;
+              sub32(x, id - cb, -__ldg(p.sgrad + tk + k));
+              nxt = k + 1 < p.T ? __ldg(ids + k + 1) : INT_MAX;
+              if (p.rest) p.rest[tk + __ldg(p.sslot + tk + k)] = nxt == id ? 0.f : rounding_left(pick32(x, id - cb));
               ++k;
-              nxt = k < p.T ? __ldg(ids + k) : INT_MAX;
             }
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
@@ -408,6 +426,109 @@ __global__ void __launch_bounds__(32 * PRE_WARPS) token_order_kernel(
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     if (lane == 0) gsum[row] = s;
+  }
+}
+
+// dH of a chunk: the K-splits' partials and the tokens' rests, rest_t W[t], summed in fp32 in a fixed
+// order. Four columns per thread.
+template <typename TO>
+__global__ void __launch_bounds__(256) dh_rest_kernel(const float* __restrict__ partial, int splits, int64_t stride,
+                                                      int rows, int d, const int32_t* __restrict__ tokens,
+                                                      const float* __restrict__ rest, int T, int V,
+                                                      const __nv_bfloat16* __restrict__ W, TO* __restrict__ out) {
+  const int64_t n4 = static_cast<int64_t>(rows) * (d / 4);
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += gridDim.x * 256ll) {
+    const int64_t row = i / (d / 4);
+    const int c = static_cast<int>(i - row * (d / 4)) * 4;
+    float4 a = *reinterpret_cast<const float4*>(partial + row * d + c);
+    for (int s = 1; s < splits; ++s) {
+      const float4 b = *reinterpret_cast<const float4*>(partial + s * stride + row * d + c);
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    for (int t = 0; t < T; ++t) {
+      const int id = __ldg(tokens + row * T + t);
+      if (id < 0 || id >= V) continue;
+      const float g = __ldg(rest + row * T + t);
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(W + static_cast<int64_t>(id) * d + c));
+      float w0, w1, w2, w3;
+      unpack2(w.x, w0, w1, __nv_bfloat16{});
+      unpack2(w.y, w2, w3, __nv_bfloat16{});
+      a.x = fmaf(g, w0, a.x), a.y = fmaf(g, w1, a.y), a.z = fmaf(g, w2, a.z), a.w = fmaf(g, w3, a.w);
+    }
+    TO* o = out + row * d + c;
+    if constexpr (sizeof(TO) == 4) {
+      *reinterpret_cast<float4*>(o) = a;
+    } else {
+      uint2 v;
+      v.x = pack_bf16x2(a.x, a.y);
+      v.y = pack_bf16x2(a.z, a.w);
+      *reinterpret_cast<uint2*>(o) = v;
+    }
+  }
+}
+
+// dW[id] += sum of rest h over a window of a chunk's entries (position, slot) with that token, in order.
+// A block per entry looks through the window's tokens: the first entry with an id adds up all of that
+// id's, so that every row of dW has one writer, and the others leave. (Sorting the entries first, in
+// one block, took 25 us for 2048 of them; this takes 12.)
+constexpr int REST_WINDOW = 4096;
+constexpr int REST_THREADS = 256;
+__global__ void __launch_bounds__(REST_THREADS) dw_rest_kernel(const int32_t* __restrict__ tokens,
+                                                               const float* __restrict__ rest, int first, int entries,
+                                                               int T, int V, const __nv_bfloat16* __restrict__ H,
+                                                               int d, float* __restrict__ dW) {
+  constexpr int PER = REST_WINDOW / REST_THREADS;
+  __shared__ int list[REST_WINDOW];
+  __shared__ int wsum[REST_THREADS / 32];
+  const int own = first + blockIdx.x;  // entries of the window: [first, entries)
+  const int id = tokens[own];
+  if (id < 0 || id >= V) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t hit = 0;
+  int earlier = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = first + tid * PER + j;
+    if (e < entries && __ldg(tokens + e) == id) {
+      hit |= 1u << j;
+      earlier |= e < own;
+    }
+  }
+  if (__syncthreads_or(earlier)) return;
+  int at = __popc(hit);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  if (lane == 31) wsum[warp] = at;
+  __syncthreads();
+  int n = 0;
+  at -= __popc(hit);
+#pragma unroll
+  for (int w = 0; w < REST_THREADS / 32; ++w) {
+    if (w < warp) at += wsum[w];
+    n += wsum[w];
+  }
+  while (hit) {
+    list[at++] = first + tid * PER + __ffs(hit) - 1;
+    hit &= hit - 1;
+  }
+  __syncthreads();
+  for (int c = tid * 2; c < d; c += 2 * REST_THREADS) {
+    float* o = dW + static_cast<int64_t>(id) * d + c;
+    float2 a = *reinterpret_cast<const float2*>(o);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int e = list[i];
+      const float g = __ldg(rest + e);
+      float h0, h1;
+      unpack2(__ldg(reinterpret_cast<const uint32_t*>(H + static_cast<int64_t>(e / T) * d + c)), h0, h1,
+              __nv_bfloat16{});
+      a.x = fmaf(g, h0, a.x);
+      a.y = fmaf(g, h1, a.y);
+    }
+    *reinterpret_cast<float2*>(o) = a;
   }
 }
 

@@ -286,7 +286,8 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
                             void* stream);
 
 /* Gradients of sum g_logp logp + sum g_entropy entropy: dH [N, d] of type `dtype` and dW fp32
- * [V, d], both overwritten; one of them may be NULL, and its product is then left out. Each chunk's logits are recomputed; the logit gradient is formed in
+ * [V, d], both overwritten; one of them may be NULL, and its product is then left out.
+ * G's entries at the given tokens, most of a gradient, keep fp32 precision where T <= 8. Each chunk's logits are recomputed; the logit gradient is formed in
  * fp32 and rounded to bf16 for the dH and dW products, as in fckl_backward. The workspace is that
  * of backward = 1 above. */
 int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d,

@@ -215,6 +215,37 @@ def test_projected_autograd(fckl):
 
 
 @gpu
+@pytest.mark.parametrize("N,T,chunk,same", [(1, 1, 1, False), (40, 1, 16, False), (300, 2, 128, True), (64, 3, 64, False),
+                                            (90, 8, 40, True), (700, 1, 512, True)])
+def test_projected_token_entries_keep_precision(fckl, N, T, chunk, same):
+    """Up to 8 tokens: only the dense part of G carries bf16 rounding, not its entries at the tokens
+    (repeated ones, and one token for most positions, among them). dW is compared as fp32; dH's own
+    rounding is bf16's."""
+    d, V = 192, 1500
+    Ht, Wt, tokens = make(N, d, V, T, "bf16", seed=N + T)
+    if same:
+        tokens[::2] = 77
+    _, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, chunk)
+    g = torch.randn(N, T, device="cuda")
+    dH, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=chunk)
+    assert fckl.check() == fckl.OK
+    H, W = exact_inputs(Ht, Wt)
+    tk, gn = tokens.cpu().numpy(), f64(g)
+    gn = np.where(tk < 0, 0, gn)
+    G = orc.logits_gradient(H @ W.T, tk, gn)
+    q = np.exp(orc._log_softmax(H @ W.T)[0])
+    a = np.abs(gn).sum(1, keepdims=True)
+    dz, r = logit_error(H, W)[:, None], (256 + 92) * U + 2.0 ** -21
+    eG = q * a * (2.0 ** -8 * 1.01 + 4 * (dz + r) + 2.0 ** -19) + 8 * U * np.abs(G)
+    sums = 4 * max(N, V // 16) * U
+    close(f64(dW), G.T @ H, eG.T @ np.abs(H) + sums * (np.abs(G).T @ np.abs(H)) + 1e-30)
+    want = G @ W
+    close(f64(dH), want, eG @ np.abs(W) + sums * (np.abs(G) @ np.abs(W)) + 2.0 ** -8 * np.abs(want) + 1e-30)
+    again = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=chunk)
+    assert torch.equal(again[0], dH) and torch.equal(again[1], dW)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_projected_one_gradient(fckl, dtype):
     """A frozen output matrix, or fixed hidden states: the other gradient has the same bits."""
