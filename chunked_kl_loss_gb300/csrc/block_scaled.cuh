@@ -239,14 +239,26 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, 
       : "memory");
 }
 
-// Bounded wait: polls for a while before it reads the clock for its limit (wait_phase reads
-// %globaltimer as soon as its first poll fails).
+// Bounded wait that leaves shared memory alone while it waits: each try may suspend the thread for up
+// to 20 us, where the default polls on (2% of the product at 8192 x 2880 x 201088: its operands
+// keep shared memory's bandwidth busy). After POLLS tries wait_phase applies its time limit.
 constexpr int POLLS = 512;
+__device__ __forceinline__ bool mbar_try_wait_20us(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool poll_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                            unsigned* status) {
 #pragma unroll 1
   for (int i = 0; i < POLLS; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_20us(bar, parity)) return true;
   return wait_phase(bar, parity, abort_flag, status);
 }
 
@@ -324,17 +336,17 @@ struct BlockMatmulParams {
 // MMAs per K-block into one of two 256-column TMEM buffers, and the eight epilogue warps of both
 // CTAs fold each buffer into their registers while the next K-block is multiplied into the other.
 //
-// What bounds it: a K-block is 512 cycles of MMA, and TMEM holds two. A buffer's round (MMA, its
-// commit seen by the epilogue, read into registers, its release seen by the MMA warp) has to fit
-// the MMA of the other one; it takes about 1400 cycles, of which the barriers' hand-offs are more
-// than half, so the MMAs run about 70% of the time. Measured steps at 8192 x 2880 x 201088 (bf16 C):
-// 9.7 ms with cluster-scope release and acquire on that hand-off; 5.8 ms without; 4.25 ms with the
+// What bounds it: a K-block is 512 cycles of MMA at the 8-bit rate, and TMEM holds two. Measured inside
+// the kernel, a K-block's round is 1600 cycles from the issue of its MMAs to their commit (behind the
+// other buffer's), 300 to read the sums and 400 until the buffer is free again at the MMA warp, so a
+// K-block takes 900 to 1100. With one hand-off per tile instead of one per K-block, which cannot apply
+// the scales, the same loop takes 3.2 ms at 8192 x 2880 x 201088. Steps at that size (bf16 C):
+// 9.7 ms with cluster-scope release and acquire on the hand-off; 5.8 ms without; 4.25 ms with the
 // MMA warp converged (its loop was 1000 cycles) and C staged and stored with TMA; 3.7 ms with half
-// the reads, twice as wide; 3.56 ms with the next tile's scales fetched early. With one hand-off per
-// tile instead of one per K-block, which cannot apply the scales, the same loop takes 3.2 ms.
-// Four 128-column buffers (4.5 ms: A is read twice from shared memory, whose bandwidth the MMAs'
-// operands and the copies already fill), sixteen epilogue warps (3.9 ms) and two K-blocks per ring
-// stage were slower.
+// the reads, twice as wide; 3.6 ms with the next tile's scales fetched early and longer suspended
+// waits. Slower: four 128-column buffers (4.5 ms, A is read twice from shared memory), tiles of 128
+// columns with four K-blocks in TMEM (5.6 ms), sixteen epilogue warps (3.9 ms), two K-blocks per
+// ring stage (3.9 ms), one lane waiting for a warp (3.9 ms).
 template <typename TC>
 __global__ void __launch_bounds__(BS_THREADS, 1) block_matmul_kernel(const __grid_constant__ BlockMatmulParams p) {
   extern __shared__ uint8_t smem_raw[];
