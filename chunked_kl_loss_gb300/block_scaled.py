@@ -61,6 +61,18 @@ def _scale_strides(name, s, shape):
     return rs, cs
 
 
+def _out_dtype(out, out_dtype, M, N):
+    import torch
+    if out is not None:
+        if out_dtype not in (None, out.dtype) or tuple(out.shape) != (M, N):
+            raise ValueError(f"out must be [{M}, {N}] of out_dtype")
+        out_dtype = out.dtype
+    out_dtype = out_dtype or torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the product is bfloat16 or float32, not {out_dtype}")
+    return out_dtype
+
+
 def block_quantize(x, rows=1, stream=None):
     """(e4m3 values [R, K], fp32 scales [ceil(R / rows), ceil(K / 128)]) of x [R, K] (bf16, fp16 or
     fp32): each block of ``rows`` (1 or 128) x 128 values is divided by max(amax / 448, 2^-126). The
@@ -102,13 +114,7 @@ def block_scaled_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, ws=Non
     lda, ldb = _pitch("a", a), _pitch("b", b)
     sa = _scale_strides("a_scale", a_scale, (M, kb))
     sb = _scale_strides("b_scale", b_scale, (-(-N // BLOCK), kb))
-    if out is not None:
-        if out_dtype not in (None, out.dtype) or tuple(out.shape) != (M, N):
-            raise ValueError(f"out must be [{M}, {N}] of out_dtype")
-        out_dtype = out.dtype
-    out_dtype = out_dtype or torch.bfloat16
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"the product is bfloat16 or float32, not {out_dtype}")
+    out_dtype = _out_dtype(out, out_dtype, M, N)
     dev = a.device
     _on_device(dev, a=a, a_scale=a_scale, b=b, b_scale=b_scale, out=out)
     with _for_stream(stream, a, a_scale, b, b_scale, out):
@@ -126,6 +132,33 @@ def block_scaled_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, ws=Non
 
 def block_scaled_projection(H, W8, w_scale, out_dtype=None, out=None, ws=None, stream=None):
     """Logits [N, V] of hidden states H [N, K] (bf16, fp16 or fp32) against an output matrix in
-    8 bits: H is quantised by position and block of 128 channels, then multiplied."""
-    H8, h_scale = block_quantize(H, stream=stream)
-    return block_scaled_matmul(H8, h_scale, W8, w_scale, out_dtype=out_dtype, out=out, ws=ws, stream=stream)
+    8 bits: H is quantised by position and block of 128 channels, then multiplied (block_quantize and
+    block_scaled_matmul with one set of checks)."""
+    import torch
+    if H.dim() != 2 or W8.dim() != 2 or H.shape[1] != W8.shape[1]:
+        raise ValueError("expected H [N,K] and W8 [V,K]")
+    code = _value_code(H, "H")
+    N, K = H.shape
+    V = W8.shape[0]
+    kb = -(-K // BLOCK)
+    ldx, ldb = _rows("H", H), _pitch("W8", W8)
+    sb = _scale_strides("w_scale", w_scale, (-(-V // BLOCK), kb))
+    out_dtype = _out_dtype(out, out_dtype, N, V)
+    dev = H.device
+    _on_device(dev, H=H, W8=W8, w_scale=w_scale, out=out)
+    ldq, pitch = -(-K // 16) * 16, -(-kb // 4) * 4
+    with _for_stream(stream, H, W8, w_scale, out):
+        ws = _ws(ws, dev)
+        q = torch.empty(N * ldq, dtype=torch.uint8, device=dev)
+        scale = torch.empty(N * pitch, dtype=torch.float32, device=dev)
+        if out is None:
+            out = torch.empty(N, V, dtype=out_dtype, device=dev)
+    lib, s, p = _pkg.load(), _stream(stream), _address
+    st = lib.fckl_block_quantize(p(H), code, ldx, N, K, 1, p(q), ldq, p(scale), pitch, 1, s)
+    if st != _pkg.OK:
+        raise _pkg.FcklError(st, "fckl_block_quantize")
+    st = lib.fckl_block_scaled_matmul(p(q), ldq, p(scale), pitch, 1, p(W8), ldb, p(w_scale), *sb, N, V, K, p(out),
+                                      _value_code(out, "out"), _rows("out", out), ws.tensor.data_ptr(), ws.nbytes, s)
+    if st != _pkg.OK:
+        raise _pkg.FcklError(st, "fckl_block_scaled_matmul")
+    return out

@@ -452,9 +452,9 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         }
         f.add(a, b);
       }
+      tmax = fmaxf(tmax, m);
       if (p.top) {
         gmax = fmaxf(gmax, m);
-        tmax = fmaxf(tmax, m);
         if (++in_group == p.gsteps || st == steps - 1) {
           gkey[g] = logit_key(gmax);
           g += SCORE_THREADS;
@@ -479,20 +479,34 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   s = sstat[0];
 #pragma unroll
   for (int w = 1; w < WARPS; ++w) s = merge(s, sstat[w]);
-  if (s.m < low_limit<T>()) {  // masked throughout: exact sums, slowly (the same for the whole block)
+  if (s.m < low_limit<T>()) {  // masked throughout (the same for the whole block)
+    const bool nan = s.l != s.l;
     s = RowStat();
-    for (int i = v0 + tid; i < v1; i += SCORE_THREADS) {
-      float x[VE];
-      rv.load(i, x);
-      float m = x[0];
+    if (!__syncthreads_or(tmax > -INFINITY || nan)) {
+      // with -inf alone: nothing is left
+    } else {  // exact sums
+      for (int i0 = v0 + tid; i0 < v1; i0 += STEP) {
+        uint4 w[SCORE_GV];
 #pragma unroll
-      for (int e = 1; e < VE; ++e) m = max_nan(m, x[e]);
-      if (!(m <= s.m)) {
-        RowStat none;
-        none.m = m;
-        s = merge(s, none);
+        for (int j = 0; j < SCORE_GV; ++j) {
+          const int i = i0 + j * SCORE_THREADS;
+          w[j] = rv.words(i < v1 ? i : rv.nvec);
+        }
+#pragma unroll
+        for (int j = 0; j < SCORE_GV; ++j) {
+          float x[VE];
+          unpack16<T>(w[j], x);
+          float m = x[0];
+#pragma unroll
+          for (int e = 1; e < VE; ++e) m = max_nan(m, x[e]);
+          if (!(m <= s.m)) {
+            RowStat none;
+            none.m = m;
+            s = merge(s, none);
+          }
+          if (s.m != -INFINITY || m != m) add_values<VE>(s, x);
+        }
       }
-      if (s.m != -INFINITY || m != m) add_values<VE>(s, x);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {

@@ -279,6 +279,10 @@ def test_argument_errors_launch_nothing(fckl):
     lambda f, x, q, s: f.block_scaled_matmul(q, s[:1], q, s), lambda f, x, q, s: f.block_scaled_matmul(q, s, q, s),
     lambda f, x, q, s: f.block_scaled_matmul(q, s.double(), q, s[:1]),
     lambda f, x, q, s: f.block_scaled_matmul(q, s, q, s[:1], out_dtype=torch.float16),
+    lambda f, x, q, s: f.block_scaled_projection(x, q, s), lambda f, x, q, s: f.block_scaled_projection(x[:, :8], q, s),
+    lambda f, x, q, s: f.block_scaled_projection(x, q, s[:1], out_dtype=torch.float16),
+    lambda f, x, q, s: f.block_scaled_projection(x.double(), q, s[:1]),
+    lambda f, x, q, s: f.block_scaled_projection(x, q, s[:1]),
     lambda f, x, q, s: f.block_scaled_matmul(q[:, :24].contiguous(), s, q[:, :24].contiguous(), s[:1]),
 ])
 def test_binding_refusals(fckl, bad):
