@@ -155,7 +155,8 @@ struct QuantParams {
 constexpr int QUANT_THREADS = 256;
 
 // One scale per row and 128 columns: 16 lanes a row, 8 values each. A thread block takes 16 rows and
-// QUANT_UNROLL adjacent scale blocks of them, whose loads are issued together.
+// QUANT_UNROLL adjacent scale blocks of them, whose loads are issued together (65536 x 2880 bf16:
+// 115 us, 4.9 TB/s; one block at a time 150).
 constexpr int QUANT_UNROLL = 4;
 constexpr int QUANT_ROWS = QUANT_THREADS / 16;
 template <typename T>
@@ -187,7 +188,9 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_rows_kernel(const Quan
 }
 
 // One scale per 128 x 128 block: a thread block each, the values held in registers between the
-// maximum and the conversion.
+// maximum and the conversion. 201088 x 2880 bf16: 320 us (5.4 TB/s, 0.80 of the copy bandwidth) with
+// four blocks per SM (two, at 100 registers: 497; with the division operator and values held as
+// fp32: 980). Loads past L1, 512 threads or five blocks gave nothing.
 template <typename T>
 __global__ void __launch_bounds__(QUANT_THREADS, sizeof(T) == 4 ? 2 : 4) quantize_blocks_kernel(const QuantParams p) {
   constexpr int RSTEP = QUANT_THREADS / 16, STEPS = QB / RSTEP;

@@ -24,7 +24,7 @@ int head_shape(int64_t N, int d, int V, int T, int chunk, int dt) {
 // K-splits (over V) of the dH product: the least estimated time, waves of 256 x 256 tiles over the 76 SM
 // pairs at a K-block's 0.34 us each (1900 TFLOP/s) plus the fp32 partials written and read back
 // (6.8 TB/s). With chunks of 512 rows at d = 1024 the loss's limit of 4 keeps 32 pairs busy (44 us);
-// 9 splits take TIME.
+// 9 splits take 28.
 constexpr int HEAD_MAX_SPLITS = 16;
 int head_splits(int rows, int d, int V) {
   const int64_t kb = cdiv(V, BK), tiles = cdiv(rows, TILE_M) * cdiv(d, 256), pairs = 76;

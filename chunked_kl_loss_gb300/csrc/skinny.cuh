@@ -9,8 +9,10 @@
 // The values go straight from global memory into the operand registers of the warp-level MMAs (m16:
 // rows of W, n8: positions). Such an MMA wants a lane's values from two places of a row; since a sum
 // over k may be taken in any order, a lane's 16 loaded bytes are used for both, and the hidden states
-// are picked from shared memory in the same order. Its rate does not matter: at 8 positions the
-// kernel needs 3% of it. Per block and 16 rows the warps' partial sums meet in shared memory (one
+// are picked from shared memory in the same order. Its rate does not matter: at 8 positions
+// the tensor pipe is 9% busy. 2880 x 201088: 177 us in bf16 (6.5 TB/s, 0.96 of the copy bandwidth) up to 8
+// positions against 210 to 320 with the large product's tiles; in 8 bits 94 us (0.91), and 116 at 16
+// positions, against 150. Per block and 16 rows the warps' partial sums meet in shared memory (one
 // barrier, two buffers), where the epilogue takes over: a thread always serves the same position.
 #pragma once
 
