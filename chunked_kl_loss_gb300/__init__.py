@@ -156,6 +156,15 @@ class Workspace:
         self.tensor = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
     @classmethod
+    def sized(cls, nbytes, device):
+        """A workspace of a size the library gave."""
+        import torch
+        ws = cls.__new__(cls)
+        ws.nbytes = nbytes
+        ws.tensor = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return ws
+
+    @classmethod
     def status(cls, device=None):
         """A workspace that holds only a status word, for the calls over logits."""
         import torch

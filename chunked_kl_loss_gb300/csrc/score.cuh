@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         collect(fits ? tau : tau + 1);
       }
     }
-    int c = n_cand;
+    int c = min(n_cand, p.cand_cap);  // more only if the logits changed while they were read
     if (c < k) {
       // ids in order whose logit is tau, until the set is complete
       for (int base = v0; base < v1 && c < k; base += SCORE_THREADS) {

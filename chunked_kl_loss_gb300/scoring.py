@@ -260,34 +260,66 @@ def _head_args(H, W, tokens):
     return dt, N, d, V, T
 
 
-def _head_ws(ws, N, d, V, T, chunk, dt, device, kind):
+def _head_ws(ws, N, d, V, T, chunk, dt, device, backward):
     import weakref
     if ws is None:
-        ws = _pkg.Workspace(N, d, V, T, chunk, dt, device, kind=kind)
-        _pkg._last_ws = ws
+        n = _pkg.load().fckl_projected_logprobs_workspace_bytes(N, d, V, T, chunk, dt, backward)
+        if n == 0:
+            raise _pkg.FcklError(_pkg.ERR_UNSUPPORTED, "workspace_bytes")
+        ws = _pkg._last_ws = _pkg.Workspace.sized(n, device)
     else:
         _pkg._last_ws = weakref.ref(ws)
     return ws
 
 
-def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
-    """(logp fp32 [N, T], entropy fp32 [N], lse fp32 [N]) of the logits H W^T, ``chunk`` positions
-    at a time. ``ws``: Workspace(N, d, V, T, chunk, kind="projected")."""
+def _projected(dt, N, d, V, T, H, W, tokens, chunk, ws=None, stream=None):
+    """projected_logprobs of checked arguments."""
     import torch
-    dt, N, d, V, T = _head_args(H, W, tokens)
     dev = H.device
-    _on_device(dev, H=H, W=W, tokens=tokens)
-    with _for_stream(stream, H, W, tokens):
-        ws = _head_ws(ws, N, d, V, T, chunk, dt, dev, "projected")
-        logp = torch.empty(N, T, dtype=torch.float32, device=dev)
-        entropy = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, dtype=torch.float32, device=dev)
+    ws = _head_ws(ws, N, d, V, T, chunk, dt, dev, 0)
+    logp = torch.empty(N, T, dtype=torch.float32, device=dev)
+    entropy = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
     p = _address
     st = _pkg.load().fckl_projected_logprobs(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(logp), p(entropy),
                                              p(lse), ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_projected_logprobs")
     return logp, entropy, lse
+
+
+def _projected_backward(dt, N, d, V, T, H, W, tokens, lse, entropy, g_logp, g_entropy, chunk, need, dH=None, dW=None,
+                        ws=None, stream=None):
+    """projected_logprobs_backward of checked arguments."""
+    import torch
+    dev = H.device
+    ws = _head_ws(ws, N, d, V, T, chunk, dt, dev, 1)
+    if not need[0]:
+        dH = None
+    elif dH is None:
+        dH = torch.empty(N, d, dtype=H.dtype, device=dev)
+    if not need[1]:
+        dW = None
+    elif dW is None:
+        dW = torch.empty(V, d, dtype=torch.float32, device=dev)
+    if N == 0 and dW is None:
+        return dH, dW
+    p = _address
+    st = _pkg.load().fckl_projected_logprobs_backward(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(lse), p(entropy),
+                                                      p(g_logp), p(g_entropy), p(dH), p(dW), ws.tensor.data_ptr(),
+                                                      ws.nbytes, _stream(stream))
+    if st != _pkg.OK:
+        raise _pkg.FcklError(st, "fckl_projected_logprobs_backward")
+    return dH, dW
+
+
+def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
+    """(logp fp32 [N, T], entropy fp32 [N], lse fp32 [N]) of the logits H W^T, ``chunk`` positions
+    at a time. ``ws``: Workspace(N, d, V, T, chunk, kind="projected")."""
+    shape = _head_args(H, W, tokens)
+    _on_device(H.device, H=H, W=W, tokens=tokens)
+    with _for_stream(stream, H, W, tokens):
+        return _projected(*shape, H, W, tokens, chunk, ws, stream)
 
 
 def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=None, chunk=2048, ws=None, stream=None,
@@ -312,24 +344,8 @@ def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=No
     if dW is not None:
         _dense("dW", dW, f32, (V, d))
     with _for_stream(stream, H, W, tokens, lse, entropy, g_logp, g_entropy, dH, dW):
-        ws = _head_ws(ws, N, d, V, T, chunk, dt, dev, "projected_backward")
-        if not need[0]:
-            dH = None
-        elif dH is None:
-            dH = torch.empty(N, d, dtype=H.dtype, device=dev)
-        if not need[1]:
-            dW = None
-        elif dW is None:
-            dW = torch.empty(V, d, dtype=f32, device=dev)
-        if N == 0 and dW is None:
-            return dH, dW
-    p = _address
-    st = _pkg.load().fckl_projected_logprobs_backward(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(lse), p(entropy),
-                                                      p(g_logp), p(g_entropy), p(dH), p(dW), ws.tensor.data_ptr(), ws.nbytes,
-                                                      _stream(stream))
-    if st != _pkg.OK:
-        raise _pkg.FcklError(st, "fckl_projected_logprobs_backward")
-    return dH, dW
+        return _projected_backward(dt, N, d, V, T, H, W, tokens, lse, entropy, g_logp, g_entropy, chunk, need, dH, dW,
+                                   ws, stream)
 
 
 def _head_autograd_function():
@@ -338,7 +354,9 @@ def _head_autograd_function():
     class ProjectedLogprobs(torch.autograd.Function):
         @staticmethod
         def forward(ctx, H, W, tokens, chunk):
-            logp, entropy, lse = projected_logprobs(H, W, tokens, chunk)
+            ctx.shape = _head_args(H, W, tokens)
+            _on_device(H.device, H=H, W=W, tokens=tokens)
+            logp, entropy, lse = _projected(*ctx.shape, H, W, tokens, chunk)
             ctx.save_for_backward(H, W, tokens, lse, entropy)
             ctx.chunk = chunk
             ctx.set_materialize_grads(False)
@@ -352,8 +370,8 @@ def _head_autograd_function():
                 return None, None, None, None
             ge = None if g_entropy is None else _upstream(g_entropy, None, H.device)
             gl = _upstream(g_logp, tuple(tokens.shape), H.device)
-            dH, dW = projected_logprobs_backward(H, W, tokens, lse, entropy, gl, ge, chunk=ctx.chunk,
-                                                 need=ctx.needs_input_grad[:2])
+            dH, dW = _projected_backward(*ctx.shape, H, W, tokens, lse, entropy, gl, ge, ctx.chunk,
+                                         ctx.needs_input_grad)
             return dH, None if dW is None else dW.to(W.dtype), None, None
 
     return ProjectedLogprobs
