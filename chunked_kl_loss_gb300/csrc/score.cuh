@@ -555,8 +555,10 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         hi = __reduce_max_sync(0xffffffffu, hi) + 1;  // reached by none (a key is never the largest uint32)
         // a little more, but not so much that nearly every thread counts
         const int bins = min(SCORE_THREADS, v1 - v0);
-        const int enough = k + min(k / 8 + 16, max(0, bins - k) / 4);
-        while (hi - lo > 1) {
+        const int enough = k + min(k / 16 + 4, max(0, bins - k) / 4);
+        // keys of 16-bit logits lie at least KEY_STEP apart: finer differences decide nothing
+        constexpr uint32_t KEY_STEP = sizeof(T) == 4 ? 1u : 1u << 13;
+        while (hi - lo > KEY_STEP) {
           const uint32_t mid = lo + (hi - lo) / 2;
           int n = 0;
 #pragma unroll
