@@ -64,6 +64,7 @@ enum Kind {
   KIND_HEAD_SKINNY,
   KIND_MATMUL_SKINNY,
   KIND_DW_REST,
+  KIND_DW_ROUND,
   KIND_COUNT
 };
 const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", "fwd_combine",
@@ -80,7 +81,7 @@ const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", 
                                             "head_combine",           "head_logit_grad",
                                             "block_quantize",         "block_scaled_matmul",
                                             "head_skinny",            "block_matmul_skinny",
-                                            "dw_rest"};
+                                            "dw_rest",                "dw_round"};
 
 // ------------------------------------------------------------------ process state
 std::mutex g_mu;

@@ -157,6 +157,46 @@ int launch_dw_rest(Run& r, const int32_t* tokens, const float* rest, int rows, c
   return FCKL_OK;
 }
 
+// Rounds dW to bf16 on the caller's stream or, with side, on the side stream after what the caller's
+// holds so far; the caller then joins with `side->join`.
+int launch_dw_round(Run& r, SideStream* side, void* out) {
+  const int64_t n4 = int64_t(r.pl.V) * r.pl.d / 4;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(cdiv(n4, 1024), int64_t(r.di->sms) * (side ? 4 : 8)));
+  const float4* dW = reinterpret_cast<const float4*>(r.dW);
+  uint2* to = static_cast<uint2*>(out);
+  if (!side) {
+    cudaStream_t s = r.s;
+    return launch(KIND_DW_ROUND, s, "dw_round", [&] { dw_round_kernel<<<grid, 256, 0, s>>>(dW, to, n4); });
+  }
+  static bool done[64] = {};
+  {
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    if (!done[r.di->id]) {  // the product's shared-memory split, so that both run on an SM
+      cudaError_t e = cudaFuncSetAttribute(dw_round_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                           cudaSharedmemCarveoutMaxShared);
+      if (e != cudaSuccess) {
+        set_error("cudaFuncSetAttribute(dw_round)", e);
+        return FCKL_ERR_CUDA;
+      }
+      done[r.di->id] = true;
+    }
+  }
+  cudaError_t e = cudaEventRecord(side->fork, r.s);
+  if (e == cudaSuccess) e = cudaStreamWaitEvent(side->s, side->fork, 0);
+  if (e != cudaSuccess) {
+    set_error("fork to the side stream", e);
+    return FCKL_ERR_CUDA;
+  }
+  cudaStream_t s = side->s;
+  const int st = launch(KIND_DW_ROUND, s, "dw_round", [&] { dw_round_kernel<<<grid, 256, 0, s>>>(dW, to, n4); });
+  e = cudaEventRecord(side->join, s);  // whatever failed: nothing of the call stays outside its stream
+  if (e != cudaSuccess && !st) {
+    set_error("join from the side stream", e);
+    return FCKL_ERR_CUDA;
+  }
+  return st;
+}
+
 // Persistent launch of one instance: as many SM pairs as can be resident, capped by the units.
 template <int EPI, bool TF32>
 int launch_head(int kind, DevInfo* di, const HeadParams& p, cudaStream_t s, const char* what) {
@@ -331,13 +371,13 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
 
 int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d,
                                      int V, int T, int chunk, const float* lse, const float* entropy,
-                                     const float* g_logp, const float* g_entropy, void* dH, float* dW, void* ws,
-                                     size_t ws_bytes, void* stream) {
+                                     const float* g_logp, const float* g_entropy, void* dH, float* dW,
+                                     void* dW_bf16, void* ws, size_t ws_bytes, void* stream) {
   return guarded("fckl_projected_logprobs_backward", [&]() -> int {
     Run r;
     int st = head_setup(r, H, W, dtype, tokens, N, d, V, T, chunk, true, ws, ws_bytes, stream);
     if (st) return st;
-    if ((!dH && !dW) || !aligned(dW, 16)) return FCKL_ERR_ARG;
+    if ((!dH && !dW) || !aligned(dW, 16) || (dW_bf16 && (!dW || !aligned(dW_bf16, 16)))) return FCKL_ERR_ARG;
     if (N > 0 && (!lse || !entropy || (T > 0 && !g_logp))) return FCKL_ERR_ARG;
     if (!aligned(lse, 4) || !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4) || !aligned(dH, 16))
       return FCKL_ERR_ARG;
@@ -345,6 +385,7 @@ int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, co
     if (N == 0) {
       cudaError_t e = cudaMemsetAsync(r.status, 0, 4, r.s);
       if (e == cudaSuccess && dW) e = cudaMemsetAsync(dW, 0, size_t(V) * d * 4, r.s);
+      if (e == cudaSuccess && dW_bf16) e = cudaMemsetAsync(dW_bf16, 0, size_t(V) * d * 2, r.s);
       if (e == cudaSuccess) return FCKL_OK;
       set_error("cudaMemsetAsync", e);
       return FCKL_ERR_CUDA;
@@ -379,10 +420,28 @@ int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, co
       st = dtype == FCKL_F32 ? launch_head<HEAD_GRAD, true>(KIND_HEAD_GRAD, r.di, p, r.s, "head_logit_grad")
                              : launch_head<HEAD_GRAD, false>(KIND_HEAD_GRAD, r.di, p, r.s, "head_logit_grad");
       if (st) return st;
-      if ((st = chunk_products(r, 0, r0, rows, Hc))) return st;
+      // dW first, so that its rounding can run beside the last chunk's dH
+      Run part = r;
+      part.dH = nullptr;
+      if (dW && (st = chunk_products(part, 0, r0, rows, Hc))) return st;
       if (rest && dW &&
           (st = launch_dw_rest(r, p.tokens, p.rest, rows, static_cast<const __nv_bfloat16*>(Hc))))
         return st;
+      SideStream* side = nullptr;
+      if (dW_bf16 && r0 + rows >= N) {
+        // beside dH where that is long enough to cover it (as for the loss's side work); at 777 x 1024 x
+        // 32000 the rounding alone takes 25 us, beside a dH of 28 us 70
+        if (dH && overlap_pays(rows, d, V, false) && (st = side_stream(r.di->id, &side))) return st;
+        st = launch_dw_round(r, side, dW_bf16);
+      }
+      part = r;
+      part.dW = nullptr;
+      if (!st && dH) st = chunk_products(part, 0, r0, rows, Hc);
+      if (side) {
+        const int sj = wait_event(r.s, side->join);
+        if (!st) st = sj;
+      }
+      if (st) return st;
     }
     return FCKL_OK;
   });

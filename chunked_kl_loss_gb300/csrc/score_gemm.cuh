@@ -471,6 +471,24 @@ __global__ void __launch_bounds__(256) dh_rest_kernel(const float* __restrict__ 
   }
 }
 
+// dW rounded to bf16, four values per thread and step: runs on a second stream beside the last chunk's
+// dH product, which leaves most of HBM's bandwidth free.
+__global__ void __launch_bounds__(256) dw_round_kernel(const float4* __restrict__ dW, uint2* __restrict__ out,
+                                                       int64_t n4) {
+  constexpr int B = 4;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i0 = blockIdx.x * 256ll + threadIdx.x; i0 < n4; i0 += B * step) {
+    float4 v[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (i0 + b * step < n4) v[b] = __ldcs(dW + i0 + b * step);
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (i0 + b * step < n4)
+        out[i0 + b * step] = make_uint2(pack_bf16x2(v[b].x, v[b].y), pack_bf16x2(v[b].z, v[b].w));
+  }
+}
+
 // dW[id] += sum of rest h over a window of a chunk's entries (position, slot) with that token, in order.
 // A block per entry looks through the window's tokens: the first entry with an id adds up all of that
 // id's, so that every row of dW has one writer, and the others leave. (Sorting the entries first, in

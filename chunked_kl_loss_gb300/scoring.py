@@ -40,7 +40,7 @@ def _set_argtypes(lib):
     lib.fckl_projected_logprobs.argtypes = [vp, vp, i32, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
     lib.fckl_projected_logprobs_backward.restype = i32
     lib.fckl_projected_logprobs_backward.argtypes = [vp, vp, i32, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp,
-                                                     vp, sz, vp]
+                                                     vp, vp, sz, vp]
     lib.fckl_token_logprobs.restype = i32
     lib.fckl_token_logprobs.argtypes = [vp, i32, i64, vp, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fckl_token_logprobs_backward.restype = i32
@@ -289,7 +289,7 @@ def _projected(dt, N, d, V, T, H, W, tokens, chunk, ws=None, stream=None):
 
 
 def _projected_backward(dt, N, d, V, T, H, W, tokens, lse, entropy, g_logp, g_entropy, chunk, need, dH=None, dW=None,
-                        ws=None, stream=None):
+                        ws=None, stream=None, round_dW=False):
     """projected_logprobs_backward of checked arguments."""
     import torch
     dev = H.device
@@ -302,15 +302,16 @@ def _projected_backward(dt, N, d, V, T, H, W, tokens, lse, entropy, g_logp, g_en
         dW = None
     elif dW is None:
         dW = torch.empty(V, d, dtype=torch.float32, device=dev)
+    dW16 = torch.empty(V, d, dtype=W.dtype, device=dev) if round_dW and dW is not None and dt == _pkg.BF16 else None
     if N == 0 and dW is None:
         return dH, dW
     p = _address
     st = _pkg.load().fckl_projected_logprobs_backward(p(H), p(W), dt, p(tokens), N, d, V, T, chunk, p(lse), p(entropy),
-                                                      p(g_logp), p(g_entropy), p(dH), p(dW), ws.tensor.data_ptr(),
-                                                      ws.nbytes, _stream(stream))
+                                                      p(g_logp), p(g_entropy), p(dH), p(dW), p(dW16),
+                                                      ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_projected_logprobs_backward")
-    return dH, dW
+    return dH, dW if dW16 is None else dW16
 
 
 def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
@@ -323,10 +324,11 @@ def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
 
 
 def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=None, chunk=2048, ws=None, stream=None,
-                                dH=None, dW=None, need=(True, True)):
+                                dH=None, dW=None, need=(True, True), round_dW=False):
     """(dH [N, d] in H's dtype, dW fp32 [V, d]) of sum g_logp * logp + sum g_entropy * entropy;
     ``lse`` and ``entropy`` as projected_logprobs returned them. ``need``: which of the two to
-    compute (the other is None and its product is left out).
+    compute (the other is None and its product is left out). ``round_dW``: dW in W's dtype instead,
+    rounded once from the fp32 sums.
     ``ws``: Workspace(N, d, V, T, chunk, kind="projected_backward")."""
     import torch
     dt, N, d, V, T = _head_args(H, W, tokens)
@@ -345,7 +347,7 @@ def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=No
         _dense("dW", dW, f32, (V, d))
     with _for_stream(stream, H, W, tokens, lse, entropy, g_logp, g_entropy, dH, dW):
         return _projected_backward(dt, N, d, V, T, H, W, tokens, lse, entropy, g_logp, g_entropy, chunk, need, dH, dW,
-                                   ws, stream)
+                                   ws, stream, round_dW)
 
 
 def _head_autograd_function():
@@ -371,8 +373,8 @@ def _head_autograd_function():
             ge = None if g_entropy is None else _upstream(g_entropy, None, H.device)
             gl = _upstream(g_logp, tuple(tokens.shape), H.device)
             dH, dW = _projected_backward(*ctx.shape, H, W, tokens, lse, entropy, gl, ge, ctx.chunk,
-                                         ctx.needs_input_grad)
-            return dH, None if dW is None else dW.to(W.dtype), None, None
+                                         ctx.needs_input_grad, round_dW=True)
+            return dH, dW, None, None
 
     return ProjectedLogprobs
 

@@ -287,13 +287,16 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
 
 /* Gradients of sum g_logp logp + sum g_entropy entropy: dH [N, d] of type `dtype` and dW fp32
  * [V, d], both overwritten; one of them may be NULL, and its product is then left out.
+ * dW_bf16: NULL, or bf16 [V, d] that receives dW rounded once (beside the
+ * last dH product, on the library's second stream, where that is long enough; joined back into
+ * `stream` before the call returns). dW is then needed too.
  * G's entries at the given tokens, most of a gradient, keep fp32 precision where T <= 8. Each chunk's logits are recomputed; the logit gradient is formed in
  * fp32 and rounded to bf16 for the dH and dW products, as in fckl_backward. The workspace is that
  * of backward = 1 above. */
 int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d,
                                      int V, int T, int chunk, const float* lse, const float* entropy,
-                                     const float* g_logp, const float* g_entropy, void* dH, float* dW, void* ws,
-                                     size_t ws_bytes, void* stream);
+                                     const float* g_logp, const float* g_entropy, void* dH, float* dW,
+                                     void* dW_bf16, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- Output projection in 8-bit floating point (e4m3) with a scale for each block of 128 along
  * the contraction. Interface additions, no counterpart on the pages: they serve a teacher whose

@@ -260,6 +260,11 @@ def test_projected_one_gradient(fckl, dtype):
     H = Ht.clone().requires_grad_()
     (fckl.fused_token_logprobs(H, Wt, tokens, 32)[0] * g).sum().backward()
     assert torch.equal(H.grad, dH)
+    for need in ((True, True), (False, True)):
+        c, e = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=32, need=need, round_dW=True)
+        assert torch.equal(e, dW.to(Wt.dtype)) and (c is None or torch.equal(c, dH))
+    none, e = fckl.projected_logprobs_backward(Ht[:0], Wt, tokens[:0], lse[:0], ent[:0], g[:0], chunk=32, round_dW=True)
+    assert e.dtype == Wt.dtype and (e == 0).all()
 
 
 @gpu
@@ -282,10 +287,12 @@ def test_projected_deterministic_streams_graph_and_chunks(fckl):
     with torch.cuda.graph(graph):
         e = fckl.projected_logprobs(Ht, Wt, tokens, 100, ws=wf)
         de = fckl.projected_logprobs_backward(Ht, Wt, tokens, e[2], e[1], g, ge, chunk=100, ws=ws)
+        dr = fckl.projected_logprobs_backward(Ht, Wt, tokens, e[2], e[1], g, ge, chunk=100, ws=ws, round_dW=True)
     graph.replay()
     torch.cuda.synchronize()
     assert fckl.check(ws) == fckl.OK and fckl.check(wf) == fckl.OK
     assert all(torch.equal(x, y) for x, y in zip(a + da, e + de))
+    assert torch.equal(dr[0], da[0]) and torch.equal(dr[1], da[1].to(Wt.dtype))
 
 
 @gpu
@@ -322,12 +329,13 @@ def test_argument_errors_launch_nothing(fckl):
         assert fwd(**bad) == fckl.ERR_UNSUPPORTED, bad
     assert fwd(n=256) == fckl.ERR_WORKSPACE
 
-    def bwd(H=p, W=p, dt=0, tok=p, N=64, d=256, V=4096, T=2, chunk=16, lse=p, ent=p, g=p, ge=z, dH=p, dW=p, ws=p,
-            n=big):
-        return lib.fckl_projected_logprobs_backward(H, W, dt, tok, N, d, V, T, chunk, lse, ent, g, ge, dH, dW, ws, n,
-                                                    z)
+    def bwd(H=p, W=p, dt=0, tok=p, N=64, d=256, V=4096, T=2, chunk=16, lse=p, ent=p, g=p, ge=z, dH=p, dW=p, dW16=z,
+            ws=p, n=big):
+        return lib.fckl_projected_logprobs_backward(H, W, dt, tok, N, d, V, T, chunk, lse, ent, g, ge, dH, dW, dW16, ws,
+                                                    n, z)
 
     for bad in (dict(lse=z), dict(ent=z), dict(g=z), dict(dH=z, dW=z), dict(dW=odd), dict(dH=odd),
+                dict(dW=z, dW16=p), dict(dW16=odd),
                 dict(ge=ctypes.c_void_p(257))):
         assert bwd(**bad) == fckl.ERR_ARG, bad
     assert bwd(n=256) == fckl.ERR_WORKSPACE
