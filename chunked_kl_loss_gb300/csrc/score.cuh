@@ -384,7 +384,7 @@ struct ScoreParams {
 // and block 0 sorts the blocks' sets together. Exact for every input, ties included.
 //
 // What bounds it: with many rows HBM. 4096 x 128256 bf16 takes 170 us without alternatives (6.2 TB/s,
-// 0.91 of the copy bandwidth), 193 with one and 232 with 100: the listed groups are read again
+// 0.91 of the copy bandwidth), 193 with one and 228 with 100: the listed groups are read again
 // when part of the 600 rows in flight (155 MB) has left L2, and a block's selection is about 8 us of
 // latency beside the other blocks' streams. A thread's loads run a step ahead of its sums, and two
 // values share an instruction where they can (310 us without either). With few rows it is latency:
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(SCORE_THREADS, SCORE_GRAD_RESIDENT) token_logp
   const float a0 = sg + ge * p.entropy[row];
   // dense part: - q (a0 + ge log q)
   auto dense = [&](float z) {
-    const float lq = max_nan((z - m) - log_s, -1e30f);  // masked: 0 * -1e30 rather than 0 * -inf
+    const float lq = max_nan((z - m) - log_s, Y_FLOOR);  // q is 0 below: 0 * finite, for any ge
     return -ex2_approx(lq * LOG2E) * fmaf(ge, lq, a0);
   };
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(zrow) & 15u) / sizeof(T)) - ov.mis;

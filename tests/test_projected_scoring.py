@@ -151,6 +151,16 @@ def test_projected_sharp(fckl):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("level", [-200.0, 200.0])
+def test_projected_far_from_zero(fckl, dtype, level):
+    """Every logit near -200 or 200: a place past the vocabulary (logit 0 in the last tile) may not
+    count, nor its exponential, inf, reach a product."""
+    Ht, Wt, tokens = make(40, 64, 1001, 2, dtype, 11, sharp=0.01)
+    check(fckl, Ht + level / 64, Wt * 0.125 + 1.0, tokens, 16)
+
+
+@gpu
 def test_projected_large_vocabulary(fckl):
     """The vocabulary of the workloads, a decode-sized batch; forward only."""
     Ht, Wt, tokens = make(3, 256, 201088, 2, "bf16", 4)

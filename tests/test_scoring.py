@@ -235,6 +235,21 @@ def test_gradient(fckl, dtype, N, V, T, mask, pad, offset, with_entropy):
 
 
 @gpu
+@pytest.mark.parametrize("mask", ["inf", "lowest"])
+def test_gradient_of_masked_logits_under_large_upstreams(fckl, mask):
+    """Upstream gradients of 2^60 (a loss scale, say): masked places stay 0, the rest finite."""
+    z, tokens = make(5, 5003, 3, "fp32", seed=4, mask=mask)
+    scale = 2.0 ** 60
+    rng = np.random.default_rng(5)
+    g, ge = (rng.normal(size=s).astype(np.float32) * np.float32(scale) for s in ((5, 3), (5,)))
+    _, ent, norm, _, _ = fckl.token_logprobs(z, tokens)
+    got = f64(fckl.token_logprobs_backward(z, tokens, norm, ent, torch.from_numpy(g).cuda(), torch.from_numpy(ge).cuda()))
+    zz, tk = f64(z), tokens.cpu().numpy()
+    want = orc.logits_gradient(zz, tk, g, ge)
+    close(got / scale, want / scale, grad_tolerance(zz, tk, g / scale, ge / scale, want / scale, "fp32"))
+
+
+@gpu
 def test_gradient_of_rows_without_upstream_is_zero(fckl):
     """Positions that the loss leaves out may hold NaN; nothing of it reaches the gradient."""
     z = torch.randn(4, 1000, device="cuda")
