@@ -26,7 +26,6 @@ namespace fckl {
 constexpr int SCORE_THREADS = 256;
 constexpr int SCORE_GV = 4;            // 16-byte vectors of a group
 constexpr int SCORE_MAX_GROUPS = 8192; // group maxima that one block keeps in shared memory
-constexpr int FEW_TOP = 128;           // alternatives that the threads' maxima bound well
 constexpr int TOKENS_MAX = 1024;       // given tokens, and alternatives, of a row
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -290,6 +289,7 @@ __device__ __forceinline__ unsigned long long pair_key(float z, int id) {
 }
 
 // Sum over the block of one int per thread; every thread gets it. `buf` holds one int per warp.
+template <int NT>
 __device__ __forceinline__ int block_sum(int v, int* buf) {
   v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
@@ -297,16 +297,17 @@ __device__ __forceinline__ int block_sum(int v, int* buf) {
   __syncthreads();
   int s = 0;
 #pragma unroll
-  for (int w = 0; w < SCORE_THREADS / 32; ++w) s += buf[w];
+  for (int w = 0; w < NT / 32; ++w) s += buf[w];
   return s;
 }
 
 // Descending bitonic sort of n (a power of two) 64-bit keys in shared memory.
+template <int NT>
 __device__ __forceinline__ void block_sort(unsigned long long* a, int n) {
   for (int k = 2; k <= n; k <<= 1) {
     for (int j = k >> 1; j > 0; j >>= 1) {
       __syncthreads();
-      for (int i = threadIdx.x; i < n / 2; i += SCORE_THREADS) {
+      for (int i = threadIdx.x; i < n / 2; i += NT) {
         const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
         const unsigned long long x = a[lo], y = a[hi];
         if ((x < y) == ((lo & k) == 0)) {
@@ -321,32 +322,43 @@ __device__ __forceinline__ void block_sort(unsigned long long* a, int n) {
 
 __device__ __forceinline__ int pow2_at_least(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
 
-// Orders n distinct keys in shared memory, largest first. Up to a block's threads each key's place is
-// the number of larger ones (n reads and two barriers instead of a sort's dozens); `a` has room
-// for the next power of two.
+// Orders n distinct keys in shared memory, largest first. Up to ORDER_MAX keys each one's place is the
+// number of larger ones (n reads and two barriers instead of a sort's dozens); `a` has room for the
+// next power of two.
+constexpr int ORDER_MAX = 256;
+template <int NT>
 __device__ __forceinline__ void block_order(unsigned long long* a, int n) {
   const int tid = threadIdx.x;
-  if (n <= SCORE_THREADS) {
+  if (n <= ORDER_MAX) {
+    constexpr int PER = ORDER_MAX / NT;
     __syncthreads();
-    const unsigned long long mine = tid < n ? a[tid] : 0ull;
-    int place = 0;
-    if ((tid & ~31) < n) {  // warps that hold a key
-      const ulonglong2* two = reinterpret_cast<const ulonglong2*>(a);
+    unsigned long long mine[PER];
+    int place[PER];
+#pragma unroll
+    for (int b = 0; b < PER; ++b) {
+      const int i = b * NT + tid;
+      mine[b] = i < n ? a[i] : 0ull;
+      place[b] = 0;
+      if ((i & ~31) < n) {  // warps that hold a key
+        const ulonglong2* two = reinterpret_cast<const ulonglong2*>(a);
 #pragma unroll 4
-      for (int j = 0; j < n / 2; ++j) {
-        const ulonglong2 v = two[j];
-        place += (v.x > mine) + (v.y > mine);
+        for (int j = 0; j < n / 2; ++j) {
+          const ulonglong2 v = two[j];
+          place[b] += (v.x > mine[b]) + (v.y > mine[b]);
+        }
+        if (n & 1) place[b] += a[n - 1] > mine[b];
       }
-      if (n & 1) place += a[n - 1] > mine;
     }
     __syncthreads();
-    if (tid < n) a[place] = mine;
+#pragma unroll
+    for (int b = 0; b < PER; ++b)
+      if (b * NT + tid < n) a[place[b]] = mine[b];
     __syncthreads();
     return;
   }
   const int n2 = pow2_at_least(n);
-  for (int i = n + tid; i < n2; i += SCORE_THREADS) a[i] = 0ull;
-  block_sort(a, n2);
+  for (int i = n + tid; i < n2; i += NT) a[i] = 0ull;
+  block_sort<NT>(a, n2);
 }
 
 struct ScoreParams {
@@ -366,7 +378,7 @@ struct ScoreParams {
   unsigned* status;
 };
 
-// One block per row, or a cluster of `split` blocks that share a row's vectors in order.
+// One block of NT threads per row, or a cluster of `split` blocks that share a row's vectors in order.
 //
 // Statistics: each thread runs over its vectors once and keeps (m, l, t); the block and then the
 // cluster merge them in a fixed order.
@@ -388,12 +400,15 @@ struct ScoreParams {
 // when part of the 600 rows in flight (155 MB) has left L2, and a block's selection is about 8 us of
 // latency beside the other blocks' streams. A thread's loads run a step ahead of its sums, and two
 // values share an instruction where they can (310 us without either). With few rows it is latency:
-// 6.5 us for one row of 201088 over eight blocks, 12 us with 20 alternatives.
-template <typename T>
-__global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const ScoreParams p) {
+// 6.5 us for one row of 201088 over eight blocks, 12 us with 20 alternatives. With many short rows it is
+// the latency of a row's steps too: smaller blocks put more rows on an SM (launch_token_logprobs).
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p) {
   namespace cg = cooperative_groups;
   constexpr int VE = 16 / sizeof(T);
-  constexpr int WARPS = SCORE_THREADS / 32;
+  constexpr int WARPS = NT / 32;
+  constexpr int SETS = NT < SCORE_THREADS ? 2 : 1;  // maxima of a thread that bound the alternatives
+  constexpr int BINS = SETS * NT;
   extern __shared__ __align__(16) unsigned char score_smem[];
   unsigned long long* cand = reinterpret_cast<unsigned long long*>(score_smem);  // [cand_cap]
   uint32_t* gkey = reinterpret_cast<uint32_t*>(cand + (p.top ? p.cand_cap : 0));  // [groups]
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   __shared__ RowStat sstat[WARPS];
   __shared__ RowStat bstat;  // this block's share of the row
   __shared__ int ibuf[WARPS];
-  __shared__ uint32_t tkey[SCORE_THREADS], tau_s;
+  __shared__ uint32_t tkey[BINS], tau_s;
   __shared__ int n_cand, n_live;
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -415,9 +430,11 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   const int c0 = max(0, rv.col(v0)), c1 = min(p.V, rv.col(v1));
 
   // ---- statistics and group maxima
-  constexpr int STEP = SCORE_THREADS * SCORE_GV;
+  constexpr int STEP = NT * SCORE_GV;
   const int steps = (v1 - v0 + STEP - 1) / STEP;
-  float tmax = -INFINITY;  // this thread's largest logit
+  float tmax[SETS];  // this thread's largest logits (two sets: of even and of odd vectors)
+#pragma unroll
+  for (int b = 0; b < SETS; ++b) tmax[b] = -INFINITY;
   RowStat s;
   {
     FastStat f;
@@ -427,7 +444,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
     auto fetch = [&](int st) {
 #pragma unroll
       for (int j = 0; j < SCORE_GV; ++j) {
-        const int i = v0 + st * STEP + j * SCORE_THREADS + tid;
+        const int i = v0 + st * STEP + j * NT + tid;
         next[j] = rv.words(i < v1 ? i : rv.nvec);
       }
     };
@@ -442,10 +459,17 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         w[4 * j + 3] = next[j].w;
       }
       if (st + 1 < steps) fetch(st + 1);  // on its way while this step is summed
-      uint32_t wm = w[0];
+      float m = 0.f;
 #pragma unroll
-      for (int j = 1; j < 4 * SCORE_GV; ++j) wm = max_words(wm, w[j], T{});
-      const float m = max_of_word(wm, T{});
+      for (int b = 0; b < SETS; ++b) {
+        uint32_t wm = w[4 * b];
+#pragma unroll
+        for (int j = 4 * b + 1; j < 4 * SCORE_GV; ++j)
+          if (j / 4 % SETS == b) wm = max_words(wm, w[j], T{});
+        const float mb = max_of_word(wm, T{});
+        tmax[b] = fmaxf(tmax[b], mb);
+        m = b ? max_nan(m, mb) : mb;
+      }
       const float mc = fmaxf(m, low<T>());
       if (mc > f.m) f.raise(mc);
 #pragma unroll
@@ -459,12 +483,11 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         }
         f.add(a, b);
       }
-      tmax = fmaxf(tmax, m);
       if (p.top) {
         gmax = fmaxf(gmax, m);
         if (++in_group == p.gsteps || st == steps - 1) {
           gkey[g] = logit_key(gmax);
-          g += SCORE_THREADS;
+          g += NT;
           gmax = -INFINITY;
           in_group = 0;
         }
@@ -489,14 +512,14 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   if (s.m < low_limit<T>()) {  // masked throughout (the same for the whole block)
     const bool nan = s.l != s.l;
     s = RowStat();
-    if (!__syncthreads_or(tmax > -INFINITY || nan)) {
+    if (!__syncthreads_or(fmaxf(tmax[0], tmax[SETS - 1]) > -INFINITY || nan)) {
       // with -inf alone: nothing is left
     } else {  // exact sums
       for (int i0 = v0 + tid; i0 < v1; i0 += STEP) {
         uint4 w[SCORE_GV];
 #pragma unroll
         for (int j = 0; j < SCORE_GV; ++j) {
-          const int i = i0 + j * SCORE_THREADS;
+          const int i = i0 + j * NT;
           w[j] = rv.words(i < v1 ? i : rv.nvec);
         }
 #pragma unroll
@@ -536,25 +559,26 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
   const int k = min(p.top, c1 - c0);
   if (k > 0 && !(s.l != s.l)) {
     const int per_group = p.gsteps * SCORE_GV;
-    const int ng = ((steps + p.gsteps - 1) / p.gsteps) * SCORE_THREADS;
+    const int ng = ((steps + p.gsteps - 1) / p.gsteps) * NT;
     uint32_t tau = order_key(-INFINITY);
-    if (k <= FEW_TOP) {
-      // the k-th largest of the threads' maxima, or a little less: 256 values, one warp. Each is the
-      // largest of hundreds of logits, so few more than k logits lie above it.
-      tkey[tid] = logit_key(tmax);
+    if (k <= BINS / 2) {
+      // the k-th largest of the threads' maxima, or a little less, by one warp. Each is the largest of
+      // many logits where rows are long, so few more than k logits lie above it.
+#pragma unroll
+      for (int b = 0; b < SETS; ++b) tkey[b * NT + tid] = logit_key(tmax[b]);
       __syncthreads();
       if (warp == 0) {
-        uint32_t key[WARPS], lo = 0xffffffffu, hi = 0;
+        uint32_t key[BINS / 32], lo = 0xffffffffu, hi = 0;
 #pragma unroll
-        for (int j = 0; j < WARPS; ++j) {
+        for (int j = 0; j < BINS / 32; ++j) {
           key[j] = tkey[32 * j + lane];
           lo = min(lo, key[j]);
           hi = max(hi, key[j]);
         }
-        lo = __reduce_min_sync(0xffffffffu, lo);      // reached by all 256
+        lo = __reduce_min_sync(0xffffffffu, lo);      // reached by all
         hi = __reduce_max_sync(0xffffffffu, hi) + 1;  // reached by none (a key is never the largest uint32)
         // a little more, but not so much that nearly every thread counts
-        const int bins = min(SCORE_THREADS, v1 - v0);
+        const int bins = min(BINS, v1 - v0);
         const int enough = k + min(k / 16 + 4, max(0, bins - k) / 4);
         // keys of 16-bit logits lie at least KEY_STEP apart: finer differences decide nothing
         constexpr uint32_t KEY_STEP = sizeof(T) == 4 ? 1u : 1u << 13;
@@ -562,7 +586,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
           const uint32_t mid = lo + (hi - lo) / 2;
           int n = 0;
 #pragma unroll
-          for (int j = 0; j < WARPS; ++j) n += key[j] >= mid;
+          for (int j = 0; j < BINS / 32; ++j) n += key[j] >= mid;
           n = __reduce_add_sync(0xffffffffu, n);
           if (n >= k) {
             lo = mid;
@@ -583,8 +607,8 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
       for (int bit = 31; bit >= 0; --bit) {
         const uint32_t c = prefix | (1u << bit);
         int n = 0;
-        for (int g = tid; g < ng; g += SCORE_THREADS) n += gkey[g] >= c;
-        n = block_sum(n, ibuf);
+        for (int g = tid; g < ng; g += NT) n += gkey[g] >= c;
+        n = block_sum<NT>(n, ibuf);
         if (n >= k) {
           prefix = c;
           if (n <= enough) break;
@@ -596,26 +620,26 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
       __syncthreads();
       if (tid == 0) n_live = n_cand = 0;
       __syncthreads();
-      for (int g = tid; g < ng; g += SCORE_THREADS)
+      for (int g = tid; g < ng; g += NT)
         if (gkey[g] >= cut) live[atomicAdd(&n_live, 1)] = static_cast<uint16_t>(g);
       __syncthreads();
     };
     auto item_vec = [&](int it) {  // vector of item it of the listed groups
       const int g = live[it / per_group], j = it % per_group;
-      const int st = (g / SCORE_THREADS) * p.gsteps + j / SCORE_GV;
-      return v0 + st * STEP + (j % SCORE_GV) * SCORE_THREADS + g % SCORE_THREADS;
+      const int st = (g / NT) * p.gsteps + j / SCORE_GV;
+      return v0 + st * STEP + (j % SCORE_GV) * NT + g % NT;
     };
     // logits at or above cut into cand, as many as fit; n_cand counts them all. Columns outside the
     // row read as -inf, which no cut above it takes.
     auto collect = [&](uint32_t cut) {
       const int items = n_live * per_group;
       constexpr int AT_ONCE = 4;  // vectors of a thread whose loads are issued together
-      for (int it0 = tid; it0 < items; it0 += AT_ONCE * SCORE_THREADS) {
+      for (int it0 = tid; it0 < items; it0 += AT_ONCE * NT) {
         uint4 w[AT_ONCE];
         int vec[AT_ONCE];
 #pragma unroll
         for (int b = 0; b < AT_ONCE; ++b) {
-          const int it = it0 + b * SCORE_THREADS;
+          const int it = it0 + b * NT;
           const int i = it < items ? item_vec(it) : v1;
           vec[b] = i < v1 ? i : rv.nvec;  // no such vector: -inf
           w[b] = rv.words(vec[b]);
@@ -652,7 +676,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
         while (!fits && hi - lo > 1) {
           const uint32_t mid = lo + (hi - lo) / 2;
           int n = 0;
-          for (int it = tid; it < items; it += SCORE_THREADS) {
+          for (int it = tid; it < items; it += NT) {
             const int i = item_vec(it);
             if (i >= v1) continue;
             float x[VE];
@@ -660,7 +684,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
 #pragma unroll
             for (int e = 0; e < VE; ++e) n += logit_key(x[e]) >= mid;
           }
-          n = block_sum(n, ibuf);
+          n = block_sum<NT>(n, ibuf);
           if (n >= k) {
             lo = mid;
             fits = n <= p.cand_cap;
@@ -678,7 +702,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
     int c = min(n_cand, p.cand_cap);  // more only if the logits changed while they were read
     if (c < k) {
       // ids in order whose logit is tau, until the set is complete
-      for (int base = v0; base < v1 && c < k; base += SCORE_THREADS) {
+      for (int base = v0; base < v1 && c < k; base += NT) {
         const int i = base + tid;
         uint32_t hit = 0;
         float x[VE];
@@ -715,7 +739,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
       }
       c = min(c, k);
     }
-    block_order(cand, c);
+    block_order<NT>(cand, c);
   }
 
   // ---- the whole row, in block 0 of the cluster
@@ -732,10 +756,10 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
           const int b = min(p.V, rv.col(min(min(r * per, rv.nvec) + per, rv.nvec)));
           const int kr = min(p.top, max(0, b - a));
           const unsigned long long* theirs = cluster.map_shared_rank(cand, r);
-          for (int i = tid; i < kr; i += SCORE_THREADS) cand[n + i] = theirs[i];
+          for (int i = tid; i < kr; i += NT) cand[n + i] = theirs[i];
           n += kr;
         }
-        block_order(cand, n);
+        block_order<NT>(cand, n);
       }
     }
     cluster.sync();  // the others' shared memory has been read
@@ -750,7 +774,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
     p.norm[2 * row] = s.m;
     p.norm[2 * row + 1] = log_s;
   }
-  for (int t = tid; t < p.T; t += SCORE_THREADS) {
+  for (int t = tid; t < p.T; t += NT) {
     const int id = p.tokens[row * p.T + t];
     float lp = 0.f;
     if (id < -1 || id >= p.V) {
@@ -762,7 +786,7 @@ __global__ void __launch_bounds__(SCORE_THREADS) token_logprobs_kernel(const Sco
     p.logp[row * p.T + t] = lp;
   }
   const bool bad = s.l != s.l;
-  for (int i = tid; i < p.top; i += SCORE_THREADS) {
+  for (int i = tid; i < p.top; i += NT) {
     int id = i;
     float lp = NAN;
     if (!bad) {

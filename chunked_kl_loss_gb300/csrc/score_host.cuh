@@ -41,24 +41,24 @@ int status_ws_checks(const void* ws, size_t ws_bytes) {
   return ws_bytes < STATUS_WS_BYTES ? FCKL_ERR_WORKSPACE : FCKL_OK;
 }
 
-template <typename T>
-int launch_token_logprobs(DevInfo* di, ScoreParams p, int64_t N, cudaStream_t s) {
+template <typename T, int NT>
+int launch_token_logprobs_block(DevInfo* di, ScoreParams p, int64_t N, cudaStream_t s) {
   constexpr int VE = 16 / sizeof(T);
-  constexpr int STEP = SCORE_THREADS * SCORE_GV;
+  constexpr int STEP = NT * SCORE_GV;
   const int64_t nvec = cdiv(p.V, VE) + 1;  // one more where rows start off a 16-byte boundary
   // A row goes to a cluster of blocks where rows alone would leave SMs idle, while each block
   // keeps at least half a step of vectors per thread.
   p.split = 1;
   while (p.split < 8 && N * p.split * 2 <= 2 * int64_t(di->sms) && nvec / (2 * p.split) >= STEP / 2) p.split *= 2;
   const int64_t steps = cdiv(cdiv(nvec, p.split), STEP);
-  p.gsteps = static_cast<int>(cdiv(steps, SCORE_MAX_GROUPS / SCORE_THREADS));
-  p.groups = static_cast<int>(cdiv(steps, p.gsteps)) * SCORE_THREADS;
+  p.gsteps = static_cast<int>(cdiv(steps, SCORE_MAX_GROUPS / NT));
+  p.groups = static_cast<int>(cdiv(steps, p.gsteps)) * NT;
   // twice the alternatives, so that ordinary rows' candidates fit; and the blocks' sets together
   p.cand_cap = 512;
   while (p.cand_cap < 2 * p.top || (p.split > 1 && p.cand_cap < p.split * p.top)) p.cand_cap *= 2;
   const size_t smem = p.top ? size_t(p.cand_cap) * 8 + size_t(p.groups) * 6 : 0;
   constexpr size_t SMEM_MAX = 8 * TOKENS_MAX * 8 + SCORE_MAX_GROUPS * 6;
-  auto k = token_logprobs_kernel<T>;
+  auto k = token_logprobs_kernel<T, NT>;
   {
     static bool done[64] = {};
     std::lock_guard<std::mutex> lk(g_setup_mu);
@@ -88,7 +88,7 @@ int launch_token_logprobs(DevInfo* di, ScoreParams p, int64_t N, cudaStream_t s)
     attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(rows * p.split));
-    cfg.blockDim = dim3(SCORE_THREADS);
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -97,6 +97,24 @@ int launch_token_logprobs(DevInfo* di, ScoreParams p, int64_t N, cudaStream_t s)
     if (st) return st;
   }
   return FCKL_OK;
+}
+
+template <typename T>
+int launch_token_logprobs(DevInfo* di, const ScoreParams& p, int64_t N, cudaStream_t s) {
+  // Blocks of 128 or 64 threads where there are rows for all SMs and a row is short: more rows are then
+  // under way on an SM, and a row's selection keeps fewer warps waiting. 4096 rows, bf16, one alternative,
+  // with 256 / 128 / 64 threads: V = 1000 48 / 25 / 18 us, 8000 45 / 30 / 27, 64000 118 / 103 / 121, 128256
+  // 191 / 201 / 255; with 100 alternatives 2000 75 / 53 / 95, 32000 108 / 107 / 121. 600 rows: 16000
+  // 11.1 / 9.6 / 11.6; 300 rows: 4000 7.3 / 6.6 / 6.8, 16000 8.1 / 8.5 / 10.5.
+  const int64_t nvec = cdiv(p.V, 16 / sizeof(T)) + 1;
+  const bool few = p.top <= 64;
+  int64_t longest = 0;  // row, in vectors, for 128 threads
+  if (N > 4 * int64_t(di->sms)) longest = few ? 8192 : 4096;
+  else if (2 * N > 5 * int64_t(di->sms)) longest = few ? 4096 : 1024;
+  else if (N > di->sms && few) longest = 1024;
+  if (2 * N > 5 * int64_t(di->sms) && few && nvec <= 512) return launch_token_logprobs_block<T, 64>(di, p, N, s);
+  if (p.top <= 128 && nvec <= longest) return launch_token_logprobs_block<T, 128>(di, p, N, s);
+  return launch_token_logprobs_block<T, SCORE_THREADS>(di, p, N, s);
 }
 
 template <typename T>

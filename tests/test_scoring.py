@@ -143,6 +143,36 @@ def test_long_rows(fckl, N):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("N,V,top,mask", [
+    (500, 1, 1, "none"), (460, 9, 3, "inf"), (500, 300, 64, "lowest"), (500, 301, 65, "none"), (470, 2041, 64, "none"),
+    (460, 4100, 64, "inf"), (457, 2001, 100, "inf"), (500, 8190, 128, "none"), (456, 5003, 40, "lowest"),
+    (160, 8200, 64, "none"), (160, 3000, 0, "inf"), (458, 33000, 2, "none"),
+])
+def test_scores_many_rows(fckl, dtype, N, V, top, mask):
+    """More rows than SMs hold: blocks of 64 and 128 threads, on both sides of their limits."""
+    z, tokens = make(N, V, 2, dtype, seed=N + V + top, mask=mask, pad=V % 3, offset=V % 2)
+    check_scores(fckl, z, tokens, top)
+
+
+@gpu
+@pytest.mark.parametrize("V,top", [(1500, 60), (1500, 128), (6000, 64), (6000, 128)])
+def test_alternatives_ties_many_rows(fckl, V, top):
+    rng = np.random.default_rng(V + top)
+    rows = [np.round(rng.normal(size=V) * 2) / 2, np.full(V, -3.25), np.where(rng.random(V) < 0.5, 0.0, -0.0),
+            (rng.random(V) < 0.001) * 4.0, np.sort(rng.normal(size=V)), -np.sort(rng.normal(size=V)),
+            np.minimum(np.arange(V) // 3, 9000) / 64.0, np.where(np.arange(V) < 2 * top, 5.0, rng.normal(size=V)),
+            np.where(np.arange(V) >= V - top - 7, 5.0, -np.inf), np.full(V, -np.inf)]
+    z = np.stack([rows[i % len(rows)] for i in range(500)])
+    z[11, 3], z[24, V - 1] = np.nan, np.inf
+    tokens = torch.zeros(500, 1, dtype=torch.int32, device="cuda")
+    got = fckl.token_logprobs(torch.from_numpy(z).float().cuda(), tokens, top=top)
+    assert torch.isnan(got[0][[11, 24]]).all() and torch.isnan(got[4][[11, 24]]).all()
+    keep = [i for i in range(500) if i not in (11, 24)]
+    check_scores(fckl, torch.from_numpy(z[keep]).float().cuda(), tokens[keep], top, got=tuple(t[keep] for t in got))
+
+
+@gpu
 def test_scores_of_extreme_rows(fckl):
     """NaN and +inf make their own row NaN (alternatives 0..top-1) and no other; large offsets and
     a lone finite value are exact."""
