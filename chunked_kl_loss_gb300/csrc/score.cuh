@@ -813,8 +813,8 @@ struct ScoreGradParams {
   unsigned* status;
 };
 constexpr int SCORE_GRAD_VECS = 8;  // vectors per thread of a segment
-constexpr int SCORE_GRAD_STEP = SCORE_THREADS * SCORE_GRAD_VECS;
-constexpr int SCORE_GRAD_RESIDENT = 5;  // blocks of 47 registers a thread on an SM
+constexpr int SCORE_GRAD_RESIDENT = 5;  // blocks of 256 threads, of 47 registers each, on an SM
+constexpr int SCORE_GRAD_TOKENS = TOKENS_MAX / SCORE_THREADS;  // given tokens per thread
 
 // HBM-bound: 345 us at 4096 x 128256 bf16, read and written once (6.1 TB/s).
 // A block takes one segment of a row: dense part first, then the (few) tokens of the row that
@@ -822,13 +822,13 @@ constexpr int SCORE_GRAD_RESIDENT = 5;  // blocks of 47 registers a thread on an
 // before anything is written, so dlogits may be logits itself. A row without any upstream
 // gradient is written as zeros without being read (positions that a loss masks out may hold
 // anything).
-template <typename T>
-__global__ void __launch_bounds__(SCORE_THREADS, SCORE_GRAD_RESIDENT) token_logprobs_grad_kernel(const ScoreGradParams p) {
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, SCORE_GRAD_RESIDENT * SCORE_THREADS / NT) token_logprobs_grad_kernel(const ScoreGradParams p) {
   constexpr int VE = 16 / sizeof(T);
-  constexpr int WARPS = SCORE_THREADS / 32;
-  constexpr int PER = TOKENS_MAX / SCORE_THREADS;
-  __shared__ int ids[TOKENS_MAX];
-  __shared__ float gs[TOKENS_MAX];
+  constexpr int WARPS = NT / 32;
+  constexpr int PER = SCORE_GRAD_TOKENS;
+  __shared__ int ids[PER * NT];
+  __shared__ float gs[PER * NT];
   __shared__ float wsum[WARPS];
   __shared__ int wany[WARPS];
   const int64_t row = blockIdx.x / p.segs;
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(SCORE_THREADS, SCORE_GRAD_RESIDENT) token_logp
   T* orow = static_cast<T*>(p.dlogits) + row * p.ld_out;
   const RowVecs<T> ov(orow, p.V);  // vectors of the output: every store is wide but the ends
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (ov.nvec + p.segs - 1) / p.segs;  // at most SCORE_GRAD_STEP
+  const int per = (ov.nvec + p.segs - 1) / p.segs;  // at most SCORE_GRAD_VECS NT
   const int v0 = seg * per;
   if (v0 >= ov.nvec) return;
   const int v1 = min(v0 + per, ov.nvec);
@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(SCORE_THREADS, SCORE_GRAD_RESIDENT) token_logp
   float zt[PER];
 #pragma unroll
   for (int a = 0; a < PER; ++a) {
-    const int t = a * SCORE_THREADS + tid;
+    const int t = a * NT + tid;
     zt[a] = 0.f;
     if (t < p.T) {
       const int id = p.tokens[row * p.T + t];
@@ -893,11 +893,11 @@ __global__ void __launch_bounds__(SCORE_THREADS, SCORE_GRAD_RESIDENT) token_logp
   uint4 ahead[GB];
 #pragma unroll
   for (int j = 0; j < SCORE_GRAD_VECS; ++j) {
-    const int i = v0 + j * SCORE_THREADS + tid;
+    const int i = v0 + j * NT + tid;
     if (j % GB == 0) {
 #pragma unroll
       for (int b = 0; b < GB; ++b) {
-        const int ib = i + b * SCORE_THREADS;
+        const int ib = i + b * NT;
         if (same && !zero && ib < v1 && ov.whole(ib)) ahead[b] = *reinterpret_cast<const uint4*>(zrow + ov.col(ib));
       }
     }
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(SCORE_THREADS, SCORE_GRAD_RESIDENT) token_logp
   __syncthreads();  // the dense values are written; the tokens' entries replace theirs
 #pragma unroll
   for (int a = 0; a < PER; ++a) {
-    const int t = a * SCORE_THREADS + tid;
+    const int t = a * NT + tid;
     if (t >= p.T) continue;
     const int id = ids[t];
     if (id < c0 || id >= c1) continue;

@@ -117,14 +117,14 @@ int launch_token_logprobs(DevInfo* di, const ScoreParams& p, int64_t N, cudaStre
   return launch_token_logprobs_block<T, SCORE_THREADS>(di, p, N, s);
 }
 
-template <typename T>
-int launch_token_logprobs_grad(DevInfo* di, ScoreGradParams p, int64_t N, cudaStream_t s) {
-  constexpr int VE = 16 / sizeof(T);
-  // Segments of at most SCORE_GRAD_STEP vectors; up to twice as many where that fills the last wave
+template <typename T, int NT>
+int launch_token_logprobs_grad_block(DevInfo* di, ScoreGradParams p, int64_t N, cudaStream_t s) {
+  constexpr int VE = 16 / sizeof(T), STEP = NT * SCORE_GRAD_VECS;
+  // Segments of at most STEP vectors; up to twice as many where that fills the last wave
   // of blocks better (301 x 50001 fp16: 4 segments a row leave 0.4 of a second wave idle, 17.5 us;
   // 5 segments, 12.5).
-  const int least = static_cast<int>(cdiv(cdiv(p.V, VE) + 1, SCORE_GRAD_STEP));
-  const int64_t slots = int64_t(di->sms) * SCORE_GRAD_RESIDENT;
+  const int least = static_cast<int>(cdiv(cdiv(p.V, VE) + 1, STEP));
+  const int64_t slots = int64_t(di->sms) * (SCORE_GRAD_RESIDENT * SCORE_THREADS / NT);
   double best = 0.0;
   for (int segs = least; segs <= 2 * least; ++segs) {
     const int64_t blocks = N * segs;
@@ -147,10 +147,20 @@ int launch_token_logprobs_grad(DevInfo* di, ScoreGradParams p, int64_t N, cudaSt
     if (p.g_entropy) q.g_entropy = p.g_entropy + r0;
     const unsigned grid = static_cast<unsigned>(rows * p.segs);
     int st = launch(KIND_TOKEN_LOGPROBS_GRAD, s, "token_logprobs_grad",
-                    [&] { token_logprobs_grad_kernel<T><<<grid, SCORE_THREADS, 0, s>>>(q); });
+                    [&] { token_logprobs_grad_kernel<T, NT><<<grid, NT, 0, s>>>(q); });
     if (st) return st;
   }
   return FCKL_OK;
+}
+
+template <typename T>
+int launch_token_logprobs_grad(DevInfo* di, const ScoreGradParams& p, int64_t N, cudaStream_t s) {
+  // Blocks of 128 threads but for long rows: 4096 rows, bf16, with 256 / 128 / 64 threads: V = 1000
+  // 28 / 9.5 / 9.8 us, 8000 46 / 27 / 27, 64000 174 / 173 / 195, 128256 344 / 377 / 382.
+  constexpr int SMALL = 128;
+  if (p.T <= SMALL * SCORE_GRAD_TOKENS && cdiv(p.V, 16 / sizeof(T)) + 1 <= 8192)
+    return launch_token_logprobs_grad_block<T, SMALL>(di, p, N, s);
+  return launch_token_logprobs_grad_block<T, SCORE_THREADS>(di, p, N, s);
 }
 
 }  // namespace

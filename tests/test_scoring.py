@@ -265,6 +265,21 @@ def test_gradient(fckl, dtype, N, V, T, mask, pad, offset, with_entropy):
 
 
 @gpu
+@pytest.mark.parametrize("N,V,T", [(4, 32761, 3), (4, 32765, 2), (3, 65530, 2), (2, 900, 512), (2, 900, 513), (700, 8197, 1)])
+def test_gradient_block_sizes(fckl, N, V, T):
+    """Both sides of the row length and the number of tokens up to which blocks are smaller."""
+    for dtype in ("bf16", "fp32"):
+        z, tokens = make(N, V, T, dtype, seed=V, pad=1, offset=1)
+        rng = np.random.default_rng(V + T)
+        g, ge = rng.normal(size=(N, T)).astype(np.float32), rng.normal(size=N).astype(np.float32)
+        _, ent, norm, _, _ = fckl.token_logprobs(z, tokens)
+        got = fckl.token_logprobs_backward(z, tokens, norm, ent, torch.from_numpy(g).cuda(), torch.from_numpy(ge).cuda())
+        zz, tk = f64(z), tokens.cpu().numpy()
+        want = orc.logits_gradient(zz, tk, g, ge)
+        close(f64(got), want, grad_tolerance(zz, tk, g, ge, want, dtype))
+
+
+@gpu
 @pytest.mark.parametrize("mask", ["inf", "lowest"])
 def test_gradient_of_masked_logits_under_large_upstreams(fckl, mask):
     """Upstream gradients of 2^60 (a loss scale, say): masked places stay 0, the rest finite."""
