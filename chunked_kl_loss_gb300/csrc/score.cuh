@@ -361,6 +361,16 @@ __device__ __forceinline__ void block_order(unsigned long long* a, int n) {
   block_sort<NT>(a, n2);
 }
 
+// 16 bytes from global to shared memory, asynchronously; the groups of copies finish in order.
+__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_async_wait() {  // all but the last PENDING groups are there
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 struct ScoreParams {
   const void* logits;
   int64_t ld;
@@ -399,10 +409,12 @@ struct ScoreParams {
 // 0.91 of the copy bandwidth), 193 with one and 228 with 100: the listed groups are read again
 // when part of the 600 rows in flight (155 MB) has left L2, and a block's selection is about 8 us of
 // latency beside the other blocks' streams. A thread's loads run a step ahead of its sums, and two
-// values share an instruction where they can (310 us without either). With few rows it is latency:
+// values share an instruction where they can (310 us without either). fp32 rows have half the
+// arithmetic per byte and want more bytes on their way than registers hold: with many long rows the
+// loads go through shared memory, two steps ahead (RING; 2048 x 128256, one alternative: 202 to 178 us; bf16 loses 5%). With few rows it is latency:
 // 6.5 us for one row of 201088 over eight blocks, 12 us with 20 alternatives. With many short rows it is
 // the latency of a row's steps too: smaller blocks put more rows on an SM (launch_token_logprobs).
-template <typename T, int NT>
+template <typename T, int NT, int RING>
 __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p) {
   namespace cg = cooperative_groups;
   constexpr int VE = 16 / sizeof(T);
@@ -410,9 +422,11 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
   constexpr int SETS = NT < SCORE_THREADS ? 2 : 1;  // maxima of a thread that bound the alternatives
   constexpr int BINS = SETS * NT;
   extern __shared__ __align__(16) unsigned char score_smem[];
-  unsigned long long* cand = reinterpret_cast<unsigned long long*>(score_smem);  // [cand_cap]
-  uint32_t* gkey = reinterpret_cast<uint32_t*>(cand + (p.top ? p.cand_cap : 0));  // [groups]
-  uint16_t* live = reinterpret_cast<uint16_t*>(gkey + p.groups);                 // [groups]
+  uint32_t* gkey = reinterpret_cast<uint32_t*>(score_smem);  // [groups]
+  // the ring of loads and, once the row has been read, the candidates and the listed groups
+  uint4* ring = reinterpret_cast<uint4*>(gkey + (p.top ? p.groups : 0));    // [RING][SCORE_GV][NT]
+  unsigned long long* cand = reinterpret_cast<unsigned long long*>(ring);   // [cand_cap]
+  uint16_t* live = reinterpret_cast<uint16_t*>(cand + p.cand_cap);          // [groups]
   __shared__ RowStat sstat[WARPS];
   __shared__ RowStat bstat;  // this block's share of the row
   __shared__ int ibuf[WARPS];
@@ -445,20 +459,32 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
 #pragma unroll
       for (int j = 0; j < SCORE_GV; ++j) {
         const int i = v0 + st * STEP + j * NT + tid;
-        next[j] = rv.words(i < v1 ? i : rv.nvec);
+        if constexpr (RING == 0) {
+          next[j] = rv.words(i < v1 ? i : rv.nvec);
+        } else if (i < v1 && rv.whole(i)) {  // a thread reads what it copies: no barrier
+          copy_async16(ring + (st % RING * SCORE_GV + j) * NT + tid, rv.row + static_cast<int64_t>(rv.col(i)));
+        }
       }
+      if constexpr (RING > 0) copy_async_commit();  // steps past the last one are empty
     };
-    fetch(0);
+#pragma unroll
+    for (int st = 0; st < (RING ? RING : 1); ++st) fetch(st);
     for (int st = 0, in_group = 0, g = tid; st < steps; ++st) {
       uint32_t w[4 * SCORE_GV];
+      if constexpr (RING > 0) copy_async_wait<RING - 1>();
 #pragma unroll
       for (int j = 0; j < SCORE_GV; ++j) {
+        if constexpr (RING > 0) {
+          const int i = v0 + st * STEP + j * NT + tid;
+          next[j] = i < v1 && rv.whole(i) ? ring[(st % RING * SCORE_GV + j) * NT + tid]
+                                          : rv.words(i < v1 ? i : rv.nvec);
+        }
         w[4 * j] = next[j].x;
         w[4 * j + 1] = next[j].y;
         w[4 * j + 2] = next[j].z;
         w[4 * j + 3] = next[j].w;
       }
-      if (st + 1 < steps) fetch(st + 1);  // on its way while this step is summed
+      if (RING > 0 || st + 1 < steps) fetch(st + (RING ? RING : 1));  // on its way while this step is summed
       float m = 0.f;
 #pragma unroll
       for (int b = 0; b < SETS; ++b) {

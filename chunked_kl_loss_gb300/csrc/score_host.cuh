@@ -41,7 +41,7 @@ int status_ws_checks(const void* ws, size_t ws_bytes) {
   return ws_bytes < STATUS_WS_BYTES ? FCKL_ERR_WORKSPACE : FCKL_OK;
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int RING = 0>
 int launch_token_logprobs_block(DevInfo* di, ScoreParams p, int64_t N, cudaStream_t s) {
   constexpr int VE = 16 / sizeof(T);
   constexpr int STEP = NT * SCORE_GV;
@@ -56,9 +56,12 @@ int launch_token_logprobs_block(DevInfo* di, ScoreParams p, int64_t N, cudaStrea
   // twice the alternatives, so that ordinary rows' candidates fit; and the blocks' sets together
   p.cand_cap = 512;
   while (p.cand_cap < 2 * p.top || (p.split > 1 && p.cand_cap < p.split * p.top)) p.cand_cap *= 2;
-  const size_t smem = p.top ? size_t(p.cand_cap) * 8 + size_t(p.groups) * 6 : 0;
-  constexpr size_t SMEM_MAX = 8 * TOKENS_MAX * 8 + SCORE_MAX_GROUPS * 6;
-  auto k = token_logprobs_kernel<T, NT>;
+  const size_t ring = size_t(std::min<int64_t>(RING, steps)) * STEP * 16;
+  const size_t smem =
+      p.top ? size_t(p.groups) * 4 + std::max(ring, size_t(p.cand_cap) * 8 + size_t(p.groups) * 2) : ring;
+  constexpr size_t SMEM_MAX =
+      SCORE_MAX_GROUPS * 4 + std::max<size_t>(RING * STEP * 16, 8 * TOKENS_MAX * 8 + SCORE_MAX_GROUPS * 2);
+  auto k = token_logprobs_kernel<T, NT, RING>;
   {
     static bool done[64] = {};
     std::lock_guard<std::mutex> lk(g_setup_mu);
@@ -114,6 +117,14 @@ int launch_token_logprobs(DevInfo* di, const ScoreParams& p, int64_t N, cudaStre
   else if (N > di->sms && few) longest = 1024;
   if (2 * N > 5 * int64_t(di->sms) && few && nvec <= 512) return launch_token_logprobs_block<T, 64>(di, p, N, s);
   if (p.top <= 128 && nvec <= longest) return launch_token_logprobs_block<T, 128>(di, p, N, s);
+  // fp32 rows through the ring in shared memory where an SM has work for several blocks after each other,
+  // or fewer blocks than fit; its three blocks an SM instead of four otherwise cost a wave (one
+  // alternative, without / with: 2048 x 128256 202 / 178 us, 4096 x 50001 155 / 141, 300 x 201088 53 / 45;
+  // 600 x 128256 60 / 75, 1000 x 201088 142 / 149).
+  if constexpr (sizeof(T) == 4) {
+    if ((N >= 8 * int64_t(di->sms) && nvec >= 12000) || (N > di->sms && N <= 3 * int64_t(di->sms) && nvec >= 25000))
+      return launch_token_logprobs_block<T, SCORE_THREADS, 2>(di, p, N, s);
+  }
   return launch_token_logprobs_block<T, SCORE_THREADS>(di, p, N, s);
 }
 

@@ -156,6 +156,23 @@ def test_scores_many_rows(fckl, dtype, N, V, top, mask):
 
 
 @gpu
+@pytest.mark.parametrize("N,V,top,mask", [(1216, 48005, 100, "none"), (1300, 48001, 0, "inf"), (160, 100003, 20, "lowest"),
+                                          (456, 100001, 600, "none"), (1217, 60000, 1024, "inf")])
+def test_scores_many_long_fp32_rows(fckl, N, V, top, mask):
+    """Rows that pass through shared memory; a few of them against the oracle."""
+    rng = torch.Generator("cuda").manual_seed(N)
+    z = torch.randn(N, V + 3, device="cuda", generator=rng)[:, 2:2 + V]
+    if mask != "none":
+        low = -float("inf") if mask == "inf" else torch.finfo(torch.float32).min
+        z.masked_fill_(torch.rand(N, V, device="cuda", generator=rng) > 0.02, low)
+        z[N - 1] = low
+    tokens = torch.randint(0, V, (N, 2), device="cuda", dtype=torch.int32, generator=rng)
+    got = fckl.token_logprobs(z, tokens, top=top)
+    pick = [0, 1, 2, 3, N // 2, N - 2, N - 1]
+    check_scores(fckl, z[pick], tokens[pick], top, got=tuple(t[pick] for t in got))
+
+
+@gpu
 @pytest.mark.parametrize("V,top", [(1500, 60), (1500, 128), (6000, 64), (6000, 128)])
 def test_alternatives_ties_many_rows(fckl, V, top):
     rng = np.random.default_rng(V + top)
