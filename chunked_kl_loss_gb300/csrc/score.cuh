@@ -378,7 +378,7 @@ struct ScoreParams {
   int V, T, top;
   int cand_cap;  // candidates that fit in shared memory (a power of two)
   int groups;    // group maxima kept per block
-  int gsteps;    // steps of SCORE_GV vectors per thread that make up a group
+  int gshift;    // 2^gshift steps of SCORE_GV vectors per thread make up a group
   int split;     // blocks (of a cluster) per row
   float* logp;
   float* entropy;
@@ -406,7 +406,7 @@ struct ScoreParams {
 // and block 0 sorts the blocks' sets together. Exact for every input, ties included.
 //
 // What bounds it: with many rows HBM. 4096 x 128256 bf16 takes 170 us without alternatives (6.2 TB/s,
-// 0.91 of the copy bandwidth), 193 with one and 228 with 100: the listed groups are read again
+// 0.91 of the copy bandwidth), 189 with one and 225 with 100: the listed groups are read again
 // when part of the 600 rows in flight (155 MB) has left L2, and a block's selection is about 8 us of
 // latency beside the other blocks' streams. A thread's loads run a step ahead of its sums, and two
 // values share an instruction where they can (310 us without either). fp32 rows have half the
@@ -422,11 +422,16 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
   constexpr int SETS = NT < SCORE_THREADS ? 2 : 1;  // maxima of a thread that bound the alternatives
   constexpr int BINS = SETS * NT;
   extern __shared__ __align__(16) unsigned char score_smem[];
-  uint32_t* gkey = reinterpret_cast<uint32_t*>(score_smem);  // [groups]
-  // the ring of loads and, once the row has been read, the candidates and the listed groups
-  uint4* ring = reinterpret_cast<uint4*>(gkey + (p.top ? p.groups : 0));    // [RING][SCORE_GV][NT]
-  unsigned long long* cand = reinterpret_cast<unsigned long long*>(ring);   // [cand_cap]
-  uint16_t* live = reinterpret_cast<uint16_t*>(cand + p.cand_cap);          // [groups]
+  unsigned long long* cand = reinterpret_cast<unsigned long long*>(score_smem);  // [cand_cap]
+  uint32_t* gkey = reinterpret_cast<uint32_t*>(cand + (p.top ? p.cand_cap : 0));  // [groups]
+  uint16_t* live = reinterpret_cast<uint16_t*>(gkey + p.groups);                 // [groups]
+  uint4* ring = nullptr;  // [RING][SCORE_GV][NT]
+  if constexpr (RING > 0) {  // the candidates and the listed groups take the ring's place after the row
+    gkey = reinterpret_cast<uint32_t*>(score_smem);
+    ring = reinterpret_cast<uint4*>(gkey + (p.top ? p.groups : 0));
+    cand = reinterpret_cast<unsigned long long*>(ring);
+    live = reinterpret_cast<uint16_t*>(cand + p.cand_cap);
+  }
   __shared__ RowStat sstat[WARPS];
   __shared__ RowStat bstat;  // this block's share of the row
   __shared__ int ibuf[WARPS];
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
       }
       if (p.top) {
         gmax = fmaxf(gmax, m);
-        if (++in_group == p.gsteps || st == steps - 1) {
+        if (++in_group == 1 << p.gshift || st == steps - 1) {
           gkey[g] = logit_key(gmax);
           g += NT;
           gmax = -INFINITY;
@@ -584,8 +589,9 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
   // ---- this block's alternatives: cand[0..k), sorted
   const int k = min(p.top, c1 - c0);
   if (k > 0 && !(s.l != s.l)) {
-    const int per_group = p.gsteps * SCORE_GV;
-    const int ng = ((steps + p.gsteps - 1) / p.gsteps) * NT;
+    static_assert(SCORE_GV == 4 && (NT & (NT - 1)) == 0, "shifts in item_vec");
+    const int item_bits = p.gshift + 2;  // of an item's number: its place in the group
+    const int ng = ((steps - 1 >> p.gshift) + 1) * NT;
     uint32_t tau = order_key(-INFINITY);
     if (k <= BINS / 2) {
       // the k-th largest of the threads' maxima, or a little less, by one warp. Each is the largest of
@@ -651,14 +657,13 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
       __syncthreads();
     };
     auto item_vec = [&](int it) {  // vector of item it of the listed groups
-      const int g = live[it / per_group], j = it % per_group;
-      const int st = (g / NT) * p.gsteps + j / SCORE_GV;
-      return v0 + st * STEP + (j % SCORE_GV) * NT + g % NT;
+      const uint32_t g = live[it >> item_bits], j = it & ((1 << item_bits) - 1);
+      return v0 + static_cast<int>(((g / NT << item_bits) + j) * NT + g % NT);
     };
     // logits at or above cut into cand, as many as fit; n_cand counts them all. Columns outside the
     // row read as -inf, which no cut above it takes.
     auto collect = [&](uint32_t cut) {
-      const int items = n_live * per_group;
+      const int items = n_live << item_bits;
       constexpr int AT_ONCE = 4;  // vectors of a thread whose loads are issued together
       for (int it0 = tid; it0 < items; it0 += AT_ONCE * NT) {
         uint4 w[AT_ONCE];
@@ -696,7 +701,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
       collect(tau + 1);
       if (n_cand > p.cand_cap) {
         // bisect: lo is reached by at least k logits; stop when those at or above it fit
-        const int items = n_live * per_group;
+        const int items = n_live << item_bits;
         uint32_t lo = tau, hi = 0xffffffffu;
         bool fits = false;
         while (!fits && hi - lo > 1) {

@@ -51,8 +51,9 @@ int launch_token_logprobs_block(DevInfo* di, ScoreParams p, int64_t N, cudaStrea
   p.split = 1;
   while (p.split < 8 && N * p.split * 2 <= 2 * int64_t(di->sms) && nvec / (2 * p.split) >= STEP / 2) p.split *= 2;
   const int64_t steps = cdiv(cdiv(nvec, p.split), STEP);
-  p.gsteps = static_cast<int>(cdiv(steps, SCORE_MAX_GROUPS / NT));
-  p.groups = static_cast<int>(cdiv(steps, p.gsteps)) * NT;
+  p.gshift = 0;
+  while (cdiv(steps, int64_t(1) << p.gshift) > SCORE_MAX_GROUPS / NT) ++p.gshift;
+  p.groups = static_cast<int>(cdiv(steps, int64_t(1) << p.gshift)) * NT;
   // twice the alternatives, so that ordinary rows' candidates fit; and the blocks' sets together
   p.cand_cap = 512;
   while (p.cand_cap < 2 * p.top || (p.split > 1 && p.cand_cap < p.split * p.top)) p.cand_cap *= 2;
