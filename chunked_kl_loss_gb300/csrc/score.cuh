@@ -27,7 +27,6 @@ constexpr int SCORE_THREADS = 256;
 constexpr int SCORE_GV = 4;            // 16-byte vectors of a group
 constexpr int SCORE_MAX_GROUPS = 8192; // group maxima that one block keeps in shared memory
 constexpr int TOKENS_MAX = 1024;       // given tokens, and alternatives, of a row
-constexpr float LN2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- values of a row
 // max that keeps a NaN (fmaxf drops it, and a row with one would pass for a good row)
@@ -136,14 +135,15 @@ __device__ __forceinline__ uint4 RowVecs<T>::words(int i) const {
 }
 
 // ---------------------------------------------------------------- running statistics
-// m: maximum so far, l = sum exp(z - m), t = sum y exp(z - m) with y = (z - m) log2(e).
-// y is formed from the difference z - m, which is exact near the maximum and has no overflow at
-// the lowest values of a type; it is held at or above -256, where 2^y is zero, so that masked
-// values add 0 * -256 rather than 0 * -inf.
+// m: maximum so far, l = sum exp(z - m), t = sum (z - m) exp(z - m).
+// Both sums are formed from the difference z - m, which is exact near the maximum; it is held at or
+// above -256, where the exponential is zero, so that values far below the maximum and masked ones
+// add 0 * -256 rather than 0 * -inf.
 struct RowStat {
   float m = -INFINITY, l = 0.f, t = 0.f;
 };
-constexpr float Y_FLOOR = -256.f;
+constexpr float DIFF_FLOOR = -256.f;
+__device__ __forceinline__ float exp_diff(float d) { return ex2_approx(d * LOG2E); }
 
 __device__ __forceinline__ RowStat merge(const RowStat& a, const RowStat& b) {
   RowStat r;
@@ -153,10 +153,10 @@ __device__ __forceinline__ RowStat merge(const RowStat& a, const RowStat& b) {
     r.t = a.t + b.t;
     return r;
   }
-  const float ya = fmaxf((a.m - r.m) * LOG2E, Y_FLOOR), yb = fmaxf((b.m - r.m) * LOG2E, Y_FLOOR);
-  const float fa = ex2_approx(ya), fb = ex2_approx(yb);
+  const float da = fmaxf(a.m - r.m, DIFF_FLOOR), db = fmaxf(b.m - r.m, DIFF_FLOOR);
+  const float fa = exp_diff(da), fb = exp_diff(db);
   r.l = a.l * fa + b.l * fb;
-  r.t = fa * (a.t + ya * a.l) + fb * (b.t + yb * b.l);
+  r.t = fa * (a.t + da * a.l) + fb * (b.t + db * b.l);
   return r;
 }
 
@@ -165,17 +165,19 @@ template <int VE>
 __device__ __forceinline__ void add_values(RowStat& s, const float (&x)[VE]) {
 #pragma unroll
   for (int j = 0; j < VE; ++j) {
-    const float y = max_nan((x[j] - s.m) * LOG2E, Y_FLOOR);
-    const float e = ex2_approx(y);
+    const float d = max_nan(x[j] - s.m, DIFF_FLOOR);
+    const float e = exp_diff(d);
     s.l += e;
-    s.t = fmaf(y, e, s.t);
+    s.t = fmaf(d, e, s.t);
   }
 }
 
 // The fast form of the same sums, for whole groups of 16-byte vectors: two values at a time through
 // the packed fp32 instructions. Values are raised to at least low() first, which stands in for the
-// floor on y (finite times zero is zero): far below any maximum but one that is itself masked. A
-// block whose maximum ends below low_limit() is summed again by add_values.
+// floor on the difference: far below any maximum but one that is itself masked, and near enough to
+// zero that its difference from the largest number of the type is still a finite number of fp32,
+// times an exponential of zero. (The product with log2(e) may overflow; only the exponential takes
+// it.) A block whose maximum ends below low_limit() is summed again by add_values.
 template <typename T>
 __device__ __forceinline__ float low();
 template <>
@@ -257,18 +259,18 @@ struct FastStat {
   unsigned long long l, t;       // the sums, two interleaved parts each
   __device__ __forceinline__ FastStat() : l(pack2(0.f, 0.f)), t(pack2(0.f, 0.f)) {}
   __device__ __forceinline__ void raise(float to) {  // brings the sums to a new maximum
-    const float y = fmaxf((m - to) * LOG2E, Y_FLOOR), f = ex2_approx(y);
-    t = mul2(pack2(f, f), fma2(pack2(y, y), l, t));
+    const float d = fmaxf(m - to, DIFF_FLOOR), f = exp_diff(d);
+    t = mul2(pack2(f, f), fma2(pack2(d, d), l, t));
     l = mul2(pack2(f, f), l);
     m = to;
   }
   __device__ __forceinline__ void add(float a, float b) {
-    const unsigned long long y = mul2(add2(pack2(a, b), pack2(-m, -m)), pack2(LOG2E, LOG2E));
+    const unsigned long long d = add2(pack2(a, b), pack2(-m, -m));
     float ya, yb;
-    unpack2f(y, ya, yb);
+    unpack2f(mul2(d, pack2(LOG2E, LOG2E)), ya, yb);
     const unsigned long long e = pack2(ex2_approx(ya), ex2_approx(yb));
     l = add2(l, e);
-    t = fma2(y, e, t);
+    t = fma2(d, e, t);
   }
   __device__ __forceinline__ RowStat stat() const {
     RowStat s;
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(NT) token_logprobs_kernel(const ScoreParams p)
   const bool nothing = s.m == -INFINITY && s.l == 0.f;
   const float log_s = nothing ? 0.f : logf(s.l);
   if (tid == 0) {
-    const float ent = nothing ? 0.f : log_s - LN2 * (s.t / s.l);
+    const float ent = nothing ? 0.f : log_s - s.t / s.l;
     p.entropy[row] = ent < 0.f ? 0.f : ent;  // rounding may leave a sharp row just below zero
     p.norm[2 * row] = s.m;
     p.norm[2 * row + 1] = log_s;
@@ -915,8 +917,8 @@ __global__ void __launch_bounds__(NT, SCORE_GRAD_RESIDENT * SCORE_THREADS / NT) 
   const float a0 = sg + ge * p.entropy[row];
   // dense part: - q (a0 + ge log q)
   auto dense = [&](float z) {
-    const float lq = max_nan((z - m) - log_s, Y_FLOOR);  // q is 0 below: 0 * finite, for any ge
-    return -ex2_approx(lq * LOG2E) * fmaf(ge, lq, a0);
+    const float lq = max_nan((z - m) - log_s, DIFF_FLOOR);  // q is 0 below: 0 * finite, for any ge
+    return -exp_diff(lq) * fmaf(ge, lq, a0);
   };
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(zrow) & 15u) / sizeof(T)) - ov.mis;
   const bool same = shift == 0;  // logits and output vectors line up

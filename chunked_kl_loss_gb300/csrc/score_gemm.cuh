@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) head_combine_kernel(
     rm[tid] = s.m;
     rs[tid] = log_s;
     if (row < rows) {
-      const float e = log_s - LN2 * (s.t / s.l);
+      const float e = log_s - s.t / s.l;
       entropy[row] = e < 0.f ? 0.f : e;
       lse[row] = s.m + log_s;
     }

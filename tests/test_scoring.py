@@ -442,3 +442,66 @@ def test_binding_refusals(fckl, bad):
     z, t = torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32)
     with pytest.raises((TypeError, ValueError)):
         bad(fckl, z, t)
+
+
+# ------------------------------------------------------------------ the largest numbers of a type
+def far_rows(V, dtype):
+    """Rows with finite logits up to the type's largest: a forced token (set to the largest number, as the
+    mirror image of a mask) beside ordinary, -inf and lowest ones, several, all, and just below."""
+    info = torch.finfo(DT[dtype])
+    rng = np.random.default_rng(V)
+    z = rng.normal(size=(9, V)) * 3
+    z[0, V // 2] = info.max
+    z[1, [0, V // 3, V - 1]] = info.max
+    z[2] = -np.inf
+    z[2, V // 2] = info.max
+    z[3] = info.min
+    z[3, V // 2] = info.max
+    z[4, V // 2] = 0.7 * info.max
+    z[5] = info.max
+    z[6, ::3], z[6, 1::3] = -np.inf, info.min
+    z[6, V // 2] = info.max
+    z[7, V // 2], z[7, 0] = 0.5 * info.max, -0.5 * info.max
+    z[8] *= info.max / 64
+    return z
+
+
+@gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("N,V,top", [(9, 1, 1), (9, 3001, 5), (9, 40003, 300), (504, 1500, 20), (504, 20011, 2),
+                                     (1224, 48005, 3)])
+def test_finite_logits_of_any_size(fckl, dtype, N, V, top):
+    """Finite logits give finite statistics, and gradients, however large they are; with blocks of every
+    size, rows over several blocks, and rows through shared memory. A log-probability past the largest
+    fp32 number is -inf."""
+    nine = torch.from_numpy(far_rows(V, dtype)).to(DT[dtype])
+    zz = nine.double().numpy()
+    z = nine.cuda().repeat(N // 9, 1)
+    rng = np.random.default_rng(1)
+    tk = np.stack([np.full(9, V // 2), rng.integers(0, V, 9)], 1)
+    tokens = torch.from_numpy(tk).int().cuda().repeat(N // 9, 1)
+    got = fckl.token_logprobs(z, tokens, top=top)
+    assert fckl.check() == fckl.OK
+    for t in got:  # whichever rows of the batch: the same bits
+        assert all(torch.equal(t[:9], t[i:i + 9]) for i in range(9, N, 9))
+    logp, ent, norm, ids, lps = (t[:9] for t in got)
+    with np.errstate(over="ignore"):
+        w_logp, w_ent, w_m, w_s = (a.astype(np.float32).astype(np.float64) for a in orc.score(zz, tk))
+        w_ids, w_lps = orc.alternatives(zz, top)
+        w_lps = w_lps.astype(np.float32).astype(np.float64)
+    r = rel_sum(V)
+    close(f64(logp), w_logp, r + 5 * U * np.abs(np.where(np.isfinite(w_logp), w_logp, 0)))
+    close(f64(ent), w_ent, r * (1 + 2 * np.maximum(w_ent, np.log(V))))
+    close(f64(norm)[:, 0], w_m, 0)
+    close(f64(norm)[:, 1], w_s, r + 4 * U * np.abs(w_s))
+    assert np.array_equal(ids.cpu().numpy(), w_ids)
+    close(f64(lps), w_lps, r + 5 * U * np.abs(np.where(np.isfinite(w_lps), w_lps, 0)))
+    g = rng.normal(size=(9, 2)).astype(np.float32)
+    for ge in (rng.normal(size=9).astype(np.float32), np.zeros(9, np.float32), None):
+        gt = torch.from_numpy(g).cuda().repeat(N // 9, 1)
+        get = None if ge is None else torch.from_numpy(ge).cuda().repeat(N // 9)
+        d = fckl.token_logprobs_backward(z, tokens, got[2], got[1], gt, get)
+        assert torch.equal(d[:9], d[-9:])
+        g0 = np.zeros(9) if ge is None else ge
+        want = orc.logits_gradient(zz, tk, g, g0)
+        close(f64(d[:9]), want, grad_tolerance(zz, tk, g, g0, want, dtype))
