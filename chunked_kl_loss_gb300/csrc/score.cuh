@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(NT, SCORE_GRAD_RESIDENT * SCORE_THREADS / NT) 
   const float ge = p.g_entropy ? p.g_entropy[row] : 0.f;
   const float m = p.norm[2 * row], log_s = p.norm[2 * row + 1];
   const bool zero = (!any && ge == 0.f) || m == -INFINITY;
-  const float a0 = sg + ge * p.entropy[row];
+  const float a0 = ge == 0.f ? sg : sg + ge * p.entropy[row];  // not read where it plays no part
   // dense part: - q (a0 + ge log q)
   auto dense = [&](float z) {
     const float lq = max_nan((z - m) - log_s, DIFF_FLOOR);  // q is 0 below: 0 * finite, for any ge

@@ -380,3 +380,18 @@ def test_binding_refusals(fckl, bad):
     H, W = torch.zeros(3, 16, dtype=torch.bfloat16), torch.zeros(50, 16, dtype=torch.bfloat16)
     with pytest.raises((TypeError, ValueError)):
         bad(fckl, H, W, torch.zeros(3, 2, dtype=torch.int32))
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 3])
+def test_projected_gradient_without_entropy_does_not_read_it(fckl, T):
+    """Where no gradient comes in through the entropy, what stands in its place does not matter."""
+    Ht, Wt, tokens = make(70, 128, 900, T, "bf16", 15)
+    _, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, 32)
+    g = torch.randn(70, T, device="cuda")
+    want = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=32)
+    nothing = torch.full_like(ent, float("nan"))
+    assert torch.isfinite(want[1]).all()
+    for ge in (None, torch.zeros(70, device="cuda")):
+        got = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, nothing, g, ge, chunk=32)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

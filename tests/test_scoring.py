@@ -505,3 +505,24 @@ def test_finite_logits_of_any_size(fckl, dtype, N, V, top):
         g0 = np.zeros(9) if ge is None else ge
         want = orc.logits_gradient(zz, tk, g, g0)
         close(f64(d[:9]), want, grad_tolerance(zz, tk, g, g0, want, dtype))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", list(DT))
+def test_gradient_without_entropy_does_not_read_it(fckl, dtype):
+    """Where no gradient comes in through the entropy, what stands in its place does not matter."""
+    z, tokens = make(6, 3001, 2, dtype, seed=2)
+    _, ent, norm, _, _ = fckl.token_logprobs(z, tokens)
+    g = torch.randn(6, 2, device="cuda")
+    want = fckl.token_logprobs_backward(z, tokens, norm, ent, g)
+    nothing = torch.full_like(ent, float("nan"))
+    assert torch.isfinite(want).all()
+    assert torch.equal(fckl.token_logprobs_backward(z, tokens, norm, nothing, g), want)
+    assert torch.equal(fckl.token_logprobs_backward(z, tokens, norm, nothing, g, torch.zeros(6, device="cuda")), want)
+    ge = torch.zeros(6, device="cuda")
+    ge[4] = 0.5
+    mixed = torch.where(ge == 0, nothing, ent)
+    keep = [0, 1, 2, 3, 5]
+    assert torch.equal(fckl.token_logprobs_backward(z, tokens, norm, mixed, g, ge),
+                       fckl.token_logprobs_backward(z, tokens, norm, ent, g, ge))
+    assert torch.equal(fckl.token_logprobs_backward(z, tokens, norm, mixed, g, ge)[keep], want[keep])
