@@ -913,7 +913,8 @@ __global__ void __launch_bounds__(NT, SCORE_GRAD_RESIDENT * SCORE_THREADS / NT) 
   }
   const float ge = p.g_entropy ? p.g_entropy[row] : 0.f;
   const float m = p.norm[2 * row], log_s = p.norm[2 * row + 1];
-  const bool zero = (!any && ge == 0.f) || m == -INFINITY;
+  // nothing upstream, or nothing left by the mask (log s is 0 there, and NaN if a NaN is among the -inf)
+  const bool zero = (!any && ge == 0.f) || (m == -INFINITY && log_s == 0.f);
   const float a0 = ge == 0.f ? sg : sg + ge * p.entropy[row];  // not read where it plays no part
   // dense part: - q (a0 + ge log q)
   auto dense = [&](float z) {

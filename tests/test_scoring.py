@@ -526,3 +526,21 @@ def test_gradient_without_entropy_does_not_read_it(fckl, dtype):
     assert torch.equal(fckl.token_logprobs_backward(z, tokens, norm, mixed, g, ge),
                        fckl.token_logprobs_backward(z, tokens, norm, ent, g, ge))
     assert torch.equal(fckl.token_logprobs_backward(z, tokens, norm, mixed, g, ge)[keep], want[keep])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("N", [4, 400])
+def test_gradient_of_a_nan_row_is_nan(fckl, dtype, N):
+    """A position with an upstream gradient whose logits hold a NaN gets a NaN gradient, whatever else
+    they hold (nothing but NaN, NaN among -inf); only a position that is -inf throughout gets zeros."""
+    z = torch.randn(N, 1200, device="cuda").to(DT[dtype])
+    z[0] = float("nan")
+    z[1] = -float("inf")
+    z[1, 7] = float("nan")
+    z[2] = -float("inf")
+    tokens = torch.full((N, 1), 3, dtype=torch.int32, device="cuda")
+    logp, ent, norm, _, _ = fckl.token_logprobs(z, tokens)
+    d = fckl.token_logprobs_backward(z, tokens, norm, ent, torch.ones(N, 1, device="cuda"))
+    assert torch.isnan(d[0]).all() and torch.isnan(d[1, 7]) and torch.isnan(d[1]).all()
+    assert (d[2] == 0).all() and torch.isfinite(d[3:]).all()
