@@ -174,10 +174,10 @@ __device__ __forceinline__ void add_values(RowStat& s, const float (&x)[VE]) {
 
 // The fast form of the same sums, for whole groups of 16-byte vectors: two values at a time through
 // the packed fp32 instructions. Values are raised to at least low() first, which stands in for the
-// floor on the difference: far below any maximum but one that is itself masked, and near enough to
-// zero that its difference from the largest number of the type is still a finite number of fp32,
-// times an exponential of zero. (The product with log2(e) may overflow; only the exponential takes
-// it.) A block whose maximum ends below low_limit() is summed again by add_values.
+// floor on the difference: far below any maximum but one that is itself masked. A block whose maximum
+// ends below low_limit() is summed again by add_values. Differences are halved, in the same
+// instruction: half the difference of two finite numbers is finite, and finite times an exponential
+// of zero is zero. (Its product with log2(e) may overflow; only the exponential takes that.)
 template <typename T>
 __device__ __forceinline__ float low();
 template <>
@@ -256,21 +256,21 @@ __device__ __forceinline__ uint32_t fill_word(float v) {  // v in every value of
 
 struct FastStat {
   float m = -INFINITY;           // maximum so far, at least low()
-  unsigned long long l, t;       // the sums, two interleaved parts each
+  unsigned long long l, t;       // l and t / 2 of RowStat, two interleaved parts each
   __device__ __forceinline__ FastStat() : l(pack2(0.f, 0.f)), t(pack2(0.f, 0.f)) {}
   __device__ __forceinline__ void raise(float to) {  // brings the sums to a new maximum
     const float d = fmaxf(m - to, DIFF_FLOOR), f = exp_diff(d);
-    t = mul2(pack2(f, f), fma2(pack2(d, d), l, t));
+    t = mul2(pack2(f, f), fma2(pack2(0.5f * d, 0.5f * d), l, t));
     l = mul2(pack2(f, f), l);
     m = to;
   }
   __device__ __forceinline__ void add(float a, float b) {
-    const unsigned long long d = add2(pack2(a, b), pack2(-m, -m));
+    const unsigned long long h = fma2(pack2(a, b), pack2(0.5f, 0.5f), pack2(-0.5f * m, -0.5f * m));
     float ya, yb;
-    unpack2f(mul2(d, pack2(LOG2E, LOG2E)), ya, yb);
+    unpack2f(mul2(h, pack2(2.f * LOG2E, 2.f * LOG2E)), ya, yb);
     const unsigned long long e = pack2(ex2_approx(ya), ex2_approx(yb));
     l = add2(l, e);
-    t = fma2(d, e, t);
+    t = fma2(h, e, t);
   }
   __device__ __forceinline__ RowStat stat() const {
     RowStat s;
@@ -278,7 +278,7 @@ struct FastStat {
     unpack2f(l, a, b);
     s.l = a + b;
     unpack2f(t, a, b);
-    s.t = a + b;
+    s.t = 2.f * (a + b);
     s.m = m;
     return s;
   }

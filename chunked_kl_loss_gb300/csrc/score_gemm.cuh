@@ -18,6 +18,8 @@
 // tensor rate).
 #pragma once
 
+#include <cfloat>
+
 #include "score.cuh"
 #include "tc_gemm.cuh"
 
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(HEAD_THREADS, 1) head_score_kernel(const __gri
           if (cb + 32 > p.V) {
 #pragma unroll
             for (int t = 0; t < 32; ++t)
-              if (cb + t >= p.V) x[t] = low<float>();  // far below any logit, and no 0 * -inf
+              if (cb + t >= p.V) x[t] = -FLT_MAX;  // not above any finite logit, and no 0 * -inf
           }
           const float cm = max32(x);
           if (cm > s[0].m) {
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(HEAD_THREADS, 1) head_score_kernel(const __gri
         const float lse = valid ? __ldg(p.lse + row) : 0.f;
         // the entropy is not read where it plays no part
         const float a0 = !valid ? 0.f : ge == 0.f ? gsum : fmaf(ge, __ldg(p.entropy + row), gsum);
+        const float nge = -2.f * ge, nlse = -0.5f * lse;
         if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -330,9 +333,14 @@ __global__ void __launch_bounds__(HEAD_THREADS, 1) head_score_kernel(const __gri
             if (j == HEAD_COLS / 32 - 1) release_acc(acc);
             const int cb = v0 + 32 * j;
 #pragma unroll
-            for (int t = 0; t < 32; ++t) {
-              const float lq = x[t] - lse;
-              x[t] = -ex2_approx(lq * LOG2E) * fmaf(ge, lq, a0);
+            for (int t = 0; t < 32; t += 2) {
+              // -q (a0 + ge log q) as (-2 ge q) (log q / 2) - a0 q: half the difference of two finite numbers
+              // is finite, and where q is 0 each product is 0
+              const unsigned long long hq = fma2(pack2(x[t], x[t + 1]), pack2(0.5f, 0.5f), pack2(nlse, nlse));
+              float y0, y1;
+              unpack2f(mul2(hq, pack2(2.f * LOG2E, 2.f * LOG2E)), y0, y1);
+              const unsigned long long q = pack2(ex2_approx(y0), ex2_approx(y1));
+              unpack2f(fma2(mul2(q, pack2(nge, nge)), hq, mul2(q, pack2(-a0, -a0))), x[t], x[t + 1]);
             }
             if (direct) {
 #pragma unroll

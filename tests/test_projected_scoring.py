@@ -395,3 +395,60 @@ def test_projected_gradient_without_entropy_does_not_read_it(fckl, T):
     for ge in (None, torch.zeros(70, device="cuda")):
         got = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, nothing, g, ge, chunk=32)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ logits of any finite size
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [5, 40, 600])
+@pytest.mark.parametrize("kind", ["one far up", "up and down"])
+def test_projected_finite_logits_of_any_size(fckl, dtype, N, kind):
+    """One logit of 3e38, and with it one of -3e38, beside ordinary ones: each logit has one product that
+    is not zero, so that it is exact in fp32. q is 1 at that token and 0 elsewhere; the entropy is 0, and
+    the gradient is G = g at the position's token, -g at token 0 (each within bf16's half a step)."""
+    d, V = 64, 1001
+    rng = np.random.default_rng(N)
+    H, W = np.zeros((N, d), np.float32), np.zeros((V, d), np.float32)
+    H[:, 0] = 2.0 ** 64
+    W[2:, 0] = rng.choice([-2.0, -0.5, 0.25, 1.0, 3.0], V - 2) * 2.0 ** -64
+    W[0, 0] = 1.75 * 2.0 ** 63                                       # 2.98e38
+    W[1, 0] = -1.75 * 2.0 ** 63 if kind == "up and down" else 2.0 ** -64
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    Ht, Wt = torch.from_numpy(H).cuda().to(tdt), torch.from_numpy(W).cuda().to(tdt)
+    tk = rng.integers(2, V, size=(N, 1))
+    tk[::2] = 0
+    tokens = torch.from_numpy(tk).int().cuda()
+    logp, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, 512)
+    assert fckl.check() == fckl.OK
+    assert (ent == 0).all() and (lse == 1.75 * 2.0 ** 127).all()
+    want = np.where(tk == 0, 0.0, -1.75 * 2.0 ** 127)
+    close(f64(logp), want, 2 * U * np.abs(want))
+    g = rng.normal(size=(N, 1)).astype(np.float32)
+    gt = torch.from_numpy(g).cuda()
+    for ge in (None, torch.randn(N, device="cuda")):
+        dH, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, gt, ge, chunk=512)
+        assert fckl.check() == fckl.OK
+        G = np.zeros((N, V))
+        np.put_along_axis(G, tk, np.where(tk == 0, 0.0, g.astype(np.float64)), 1)
+        G[:, 0] = np.where(tk[:, 0] == 0, 0.0, -g[:, 0].astype(np.float64))
+        w_dH, w_dW = G @ W.astype(np.float64), G.T @ H.astype(np.float64)
+        close(f64(dH), w_dH, 2.0 ** -7 * (np.abs(G) @ np.abs(W)) * 1.01)
+        close(f64(dW), w_dW, 2.0 ** -8 * (np.abs(G).T @ np.abs(H)) * 1.01 + 4 * N * U * (np.abs(G).T @ np.abs(H)))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [3, 33])
+def test_projected_all_logits_far_down(fckl, dtype, N):
+    """Every logit -2.98e38, equal ones: the places past the vocabulary in the last tile do not count."""
+    d, V = 64, 1001
+    H, W = torch.zeros(N, d), torch.zeros(V, d)
+    H[:, 0], W[:, 0] = -(2.0 ** 64), 1.75 * 2.0 ** 63
+    tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    tokens = torch.arange(N, dtype=torch.int32).view(N, 1).cuda() * 30
+    logp, ent, lse = fckl.projected_logprobs(H.cuda().to(tdt), W.cuda().to(tdt), tokens, 64)
+    assert fckl.check() == fckl.OK
+    r = (256 + 92) * U + 2.0 ** -21
+    assert (lse == -1.75 * 2.0 ** 127).all()
+    close(f64(logp), np.full((N, 1), -np.log(V)), r + 8 * U * np.log(V))
+    close(f64(ent), np.full(N, np.log(V)), r * (1 + 2 * np.log(V)))
