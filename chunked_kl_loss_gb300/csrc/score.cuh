@@ -155,8 +155,9 @@ __device__ __forceinline__ RowStat merge(const RowStat& a, const RowStat& b) {
   }
   const float da = fmaxf(a.m - r.m, DIFF_FLOOR), db = fmaxf(b.m - r.m, DIFF_FLOOR);
   const float fa = exp_diff(da), fb = exp_diff(db);
-  r.l = a.l * fa + b.l * fb;
-  r.t = fa * (a.t + da * a.l) + fb * (b.t + db * b.l);
+  // products and sums that are written out, so that every kernel rounds them alike
+  r.l = fmaf(a.l, fa, __fmul_rn(b.l, fb));
+  r.t = fmaf(fa, fmaf(da, a.l, a.t), __fmul_rn(fb, fmaf(db, b.l, b.t)));
   return r;
 }
 

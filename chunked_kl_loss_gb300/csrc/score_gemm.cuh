@@ -565,27 +565,33 @@ __global__ void __launch_bounds__(REST_THREADS) dw_rest_kernel(const int32_t* __
 
 // Merges the tiles' statistics of R positions per block into the log-partition, the entropy and the
 // tokens' log-probabilities (logp holds the tokens' logits on entry). 1024 / R threads share a
-// position's tiles; the merges have a fixed order. R = 32 reads whole lines; with few positions R = 4
-// keeps more of a position's loads in flight (786 tiles of one position: 16 us with R = 32, 10 with R = 4).
+// position's tiles. R = 32 reads whole lines; with few positions R = 4 keeps more of a position's loads
+// in flight (786 tiles of one position: 16 us with R = 32, 10 with R = 4). The order of the merges is
+// one, so that a position's result does not depend on how many share its chunk: tile t goes to part
+// t mod 256, in ascending order, and the parts are merged in halves. A thread holds 256 R / 1024 parts
+// (2048 positions of 1571 tiles: 20 us, 18 with parts of its own order).
 constexpr int COMBINE_THREADS = 1024;
+constexpr int COMBINE_PARTS = 256;
 template <int R>
 __global__ void __launch_bounds__(COMBINE_THREADS) head_combine_kernel(
     const float* __restrict__ pm, const float* __restrict__ pl, const float* __restrict__ pt, int ld, int tiles,
     int rows, const int32_t* __restrict__ tokens, int T, int V, float* __restrict__ logp,
     float* __restrict__ entropy, float* __restrict__ lse) {
-  constexpr int PARTS = COMBINE_THREADS / R;
+  constexpr int STEP = COMBINE_THREADS / R;      // threads of a position
+  constexpr int OWN = COMBINE_PARTS / STEP;      // parts of a thread: STEP apart
   __shared__ RowStat part[COMBINE_THREADS];
   __shared__ float rm[R], rs[R];
   const int tid = threadIdx.x;
   const int row0 = blockIdx.x * R, row = row0 + tid % R;
-  RowStat s;
+  RowStat own[OWN];
   if (row < rows) {
     constexpr int B = 8;  // the loads of 8 tiles are issued before any of them is merged
-    for (int t0 = tid / R; t0 < tiles; t0 += PARTS * B) {
+    static_assert(B % OWN == 0, "whole rounds of the parts");
+    for (int t0 = tid / R; t0 < tiles; t0 += STEP * B) {
       RowStat x[B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int t = t0 + PARTS * b;
+        const int t = t0 + STEP * b;
         if (t < tiles) {
           const size_t o = static_cast<size_t>(t) * ld + row;
           x[b].m = pm[o];
@@ -594,9 +600,15 @@ __global__ void __launch_bounds__(COMBINE_THREADS) head_combine_kernel(
         }
       }
 #pragma unroll
-      for (int b = 0; b < B; ++b) s = merge(s, x[b]);
+      for (int b = 0; b < B; ++b) own[b % OWN] = merge(own[b % OWN], x[b]);
     }
   }
+#pragma unroll
+  for (int h = OWN / 2; h > 0; h /= 2) {
+#pragma unroll
+    for (int b = 0; b < h; ++b) own[b] = merge(own[b], own[b + h]);
+  }
+  RowStat s = own[0];
   part[tid] = s;
   for (int o = COMBINE_THREADS / 2; o >= R; o >>= 1) {
     __syncthreads();

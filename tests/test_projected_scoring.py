@@ -452,3 +452,16 @@ def test_projected_all_logits_far_down(fckl, dtype, N):
     assert (lse == -1.75 * 2.0 ** 127).all()
     close(f64(logp), np.full((N, 1), -np.log(V)), r + 8 * U * np.log(V))
     close(f64(ent), np.full(N, np.log(V)), r * (1 + 2 * np.log(V)))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_projected_chunk_does_not_change_a_position(fckl, dtype):
+    """Chunks on both sides of the sizes at which the statistics' merge takes another block shape, and a
+    short last chunk: the same bits."""
+    Ht, Wt, tokens = make(1300, 64, 20011, 2, dtype, 12)
+    want = fckl.projected_logprobs(Ht, Wt, tokens, 1300)
+    assert fckl.check() == fckl.OK
+    for chunk in (100, 512, 513, 600, 1299):
+        got = fckl.projected_logprobs(Ht, Wt, tokens, chunk)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), chunk
