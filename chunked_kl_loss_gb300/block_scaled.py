@@ -117,7 +117,7 @@ def block_scaled_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, ws=Non
     out_dtype = _out_dtype(out, out_dtype, M, N)
     dev = a.device
     _on_device(dev, a=a, a_scale=a_scale, b=b, b_scale=b_scale, out=out)
-    with _for_stream(stream, a, a_scale, b, b_scale, out):
+    with _for_stream(stream, a, a_scale, b, b_scale, out, ws):
         ws = _ws(ws, dev)
         if out is None:
             out = torch.empty(M, N, dtype=out_dtype, device=dev)
@@ -147,7 +147,7 @@ def block_scaled_projection(H, W8, w_scale, out_dtype=None, out=None, ws=None, s
     dev = H.device
     _on_device(dev, H=H, W8=W8, w_scale=w_scale, out=out)
     ldq, pitch = -(-K // 16) * 16, -(-kb // 4) * 4
-    with _for_stream(stream, H, W8, w_scale, out):
+    with _for_stream(stream, H, W8, w_scale, out, ws):
         ws = _ws(ws, dev)
         q = torch.empty(N * ldq, dtype=torch.uint8, device=dev)
         scale = torch.empty(N * pitch, dtype=torch.float32, device=dev)

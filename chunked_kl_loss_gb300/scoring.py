@@ -14,9 +14,10 @@ dense); ``tokens [N, T]`` are int32, -1 marks an empty slot. Logits of -inf are 
 ``H [N, d]`` and ``W [V, d]`` are bf16 or fp32 as for the loss; their logits are never stored.
 
 ``stream`` launches on a stream other than the current one: outputs are then allocated for that
-stream and the inputs are marked as used on it; making the inputs' data ready there is the
-caller's part. Under CUDA graph capture call the functions that take gradients directly rather
-than autograd (whose accumulation nodes remember the stream that an eager pass used).
+stream, and the inputs and a workspace passed as ``ws`` are marked as used on it; making the inputs'
+data ready there is the caller's part. Under CUDA graph capture call the functions that take
+gradients directly rather than autograd (whose accumulation nodes remember the stream that an eager
+pass used).
 """
 from __future__ import annotations
 
@@ -123,13 +124,14 @@ _here = contextlib.nullcontext()
 
 
 def _for_stream(stream, *inputs):
-    """Context for allocations that `stream` will use (None: the current stream)."""
+    """Context for allocations that `stream` will use (None: the current stream); `inputs`, a workspace
+    of the caller's among them, are marked as used there."""
     import torch
     if stream is None:
         return _here
     for t in inputs:
         if t is not None:
-            t.record_stream(stream)
+            (t.tensor if isinstance(t, _pkg.Workspace) else t).record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -154,7 +156,7 @@ def token_logprobs(logits, tokens, top=0, ws=None, stream=None):
     dev = logits.device
     _on_device(dev, logits=logits, tokens=tokens)
     f32 = torch.float32
-    with _for_stream(stream, logits, tokens):
+    with _for_stream(stream, logits, tokens, ws):
         ws = _ws(ws, dev)
         logp = torch.empty(N, T, dtype=f32, device=dev)
         entropy = torch.empty(N, dtype=f32, device=dev)
@@ -186,7 +188,7 @@ def token_logprobs_backward(logits, tokens, norm, entropy, g_logp, g_entropy=Non
         _dense("g_entropy", g_entropy, f32, (N,))
     if out is not None and (out.dtype != logits.dtype or out.shape != logits.shape):
         raise ValueError("out must have the logits' type and shape")
-    with _for_stream(stream, logits, tokens, norm, entropy, g_logp, g_entropy, out):
+    with _for_stream(stream, logits, tokens, norm, entropy, g_logp, g_entropy, out, ws):
         ws = _ws(ws, dev)
         if out is None:
             out = torch.empty(N, V, dtype=logits.dtype, device=dev)
@@ -319,7 +321,7 @@ def projected_logprobs(H, W, tokens, chunk, ws=None, stream=None):
     at a time. ``ws``: Workspace(N, d, V, T, chunk, kind="projected")."""
     shape = _head_args(H, W, tokens)
     _on_device(H.device, H=H, W=W, tokens=tokens)
-    with _for_stream(stream, H, W, tokens):
+    with _for_stream(stream, H, W, tokens, ws):
         return _projected(*shape, H, W, tokens, chunk, ws, stream)
 
 
@@ -345,7 +347,7 @@ def projected_logprobs_backward(H, W, tokens, lse, entropy, g_logp, g_entropy=No
         _dense("dH", dH, H.dtype, (N, d))
     if dW is not None:
         _dense("dW", dW, f32, (V, d))
-    with _for_stream(stream, H, W, tokens, lse, entropy, g_logp, g_entropy, dH, dW):
+    with _for_stream(stream, H, W, tokens, lse, entropy, g_logp, g_entropy, dH, dW, ws):
         return _projected_backward(dt, N, d, V, T, H, W, tokens, lse, entropy, g_logp, g_entropy, chunk, need, dH, dW,
                                    ws, stream, round_dW)
 

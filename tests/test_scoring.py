@@ -544,3 +544,63 @@ def test_gradient_of_a_nan_row_is_nan(fckl, dtype, N):
     d = fckl.token_logprobs_backward(z, tokens, norm, ent, torch.ones(N, 1, device="cuda"))
     assert torch.isnan(d[0]).all() and torch.isnan(d[1, 7]) and torch.isnan(d[1]).all()
     assert (d[2] == 0).all() and torch.isfinite(d[3:]).all()
+
+
+def _logits_call(f, ws, s):
+    z = torch.randn(8, 5000, device="cuda")
+    f.token_logprobs(z, torch.zeros(8, 1, dtype=torch.int32, device="cuda"), top=5, ws=ws, stream=s)
+
+
+def _logits_grad_call(f, ws, s):
+    z, t = torch.randn(8, 5000, device="cuda"), torch.zeros(8, 1, dtype=torch.int32, device="cuda")
+    one = torch.ones(8, 2, device="cuda")
+    f.token_logprobs_backward(z, t, one, one[:, 0].contiguous(), one[:, :1].contiguous(), ws=ws, stream=s)
+
+
+def _head_call(f, ws, s):
+    H, W = torch.ones(8, 64, device="cuda").bfloat16(), torch.ones(900, 64, device="cuda").bfloat16()
+    f.projected_logprobs(H, W, torch.zeros(8, 1, dtype=torch.int32, device="cuda"), 8, ws=ws, stream=s)
+
+
+def _head_grad_call(f, ws, s):
+    H, W = torch.ones(8, 64, device="cuda").bfloat16(), torch.ones(900, 64, device="cuda").bfloat16()
+    one = torch.ones(8, 1, device="cuda")
+    f.projected_logprobs_backward(H, W, torch.zeros(8, 1, dtype=torch.int32, device="cuda"), one[:, 0].contiguous(),
+                                  one[:, 0].contiguous(), one, chunk=8, ws=ws, stream=s)
+
+
+def _matmul_call(f, ws, s):
+    a, sa = f.block_quantize(torch.randn(40, 128, device="cuda"))
+    b, sb = f.block_quantize(torch.randn(300, 128, device="cuda"), rows=128)
+    s.wait_stream(torch.cuda.current_stream())
+    f.block_scaled_matmul(a, sa, b, sb, ws=ws, stream=s)
+
+
+def _projection_call(f, ws, s):
+    b, sb = f.block_quantize(torch.randn(300, 128, device="cuda"), rows=128)
+    s.wait_stream(torch.cuda.current_stream())
+    f.block_scaled_projection(torch.randn(40, 128, device="cuda"), b, sb, ws=ws, stream=s)
+
+
+@gpu
+@pytest.mark.parametrize("call", [_logits_call, _logits_grad_call, _head_call, _head_grad_call, _matmul_call,
+                                  _projection_call])
+def test_workspace_given_with_a_stream_outlives_its_last_use(fckl, call):
+    """A workspace that the caller drops right after a call on another stream is not handed out again
+    while that stream still has the call before it."""
+    call(fckl, fckl.Workspace.sized(4 << 20, "cuda"), torch.cuda.Stream())  # set-up out of the way
+    torch.cuda.synchronize()
+    size = 41 << 20
+    ws = fckl.Workspace.sized(size, "cuda")
+    ws.tensor.zero_()
+    torch.cuda.synchronize()
+    at = ws.tensor.data_ptr()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)  # about 0.2 s
+    call(fckl, ws, side)
+    del ws
+    other = torch.empty(size, dtype=torch.uint8, device="cuda")
+    busy = not side.query()
+    torch.cuda.synchronize()
+    assert busy and other.data_ptr() != at
