@@ -465,3 +465,86 @@ def test_projected_chunk_does_not_change_a_position(fckl, dtype):
     for chunk in (100, 512, 513, 600, 1299):
         got = fckl.projected_logprobs(Ht, Wt, tokens, chunk)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), chunk
+
+
+# ------------------------------------------------------------------ dW rounded on the second stream
+def _round_both(fckl, monkeypatch, args, ge, chunk, **kw):
+    """dH, bf16 dW with the rounding beside the last dH product and after it."""
+    out = []
+    for how in ("1", "0"):
+        monkeypatch.setenv("FCKL_OVERLAP", how)
+        out.append(fckl.projected_logprobs_backward(*args, ge, chunk=chunk, round_dW=True, **kw))
+        assert fckl.check() == fckl.OK
+    return out
+
+
+@gpu
+@pytest.mark.parametrize("N,d,V,T,chunk", [
+    (300, 256, 5000, 1, 300), (300, 256, 5000, 3, 100), (301, 128, 3001, 8, 100), (301, 128, 3001, 9, 150),
+    (257, 64, 1000, 2, 256), (40, 8, 300, 0, 7), (1100, 512, 8192, 1, 1024),
+])
+def test_projected_dW_rounded_beside_dH(fckl, monkeypatch, N, d, V, T, chunk):
+    """The fork to the second stream and the join: the bits of the rounding in order, with one and several
+    chunks, a last chunk of few rows, tokens on both sides of the limit of their kept rests, on another
+    stream. dW is overwritten on the caller's stream right behind the call: were it not joined, the
+    rounding could read that."""
+    Ht, Wt, tokens = make(N, d, V, max(T, 1), "bf16", seed=N + V)
+    tokens = tokens[:, :T].contiguous()
+    _, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, chunk)
+    g, ge = torch.randn(N, T, device="cuda"), torch.randn(N, device="cuda")
+    args = (Ht, Wt, tokens, lse, ent, g)
+    dH, dW = fckl.projected_logprobs_backward(*args, ge, chunk=chunk)
+    (a, ra), (b, rb) = _round_both(fckl, monkeypatch, args, ge, chunk)
+    assert torch.equal(a, dH) and torch.equal(b, dH) and torch.equal(ra, rb) and torch.equal(ra, dW.to(Wt.dtype))
+    monkeypatch.setenv("FCKL_OVERLAP", "1")
+    torch.cuda.synchronize()
+    for stream in (None, torch.cuda.Stream()):
+        for _ in range(5):
+            scratch = torch.zeros(V, d, device="cuda")
+            torch.cuda.synchronize()
+            c, rc = fckl.projected_logprobs_backward(*args, ge, chunk=chunk, round_dW=True, dW=scratch, stream=stream)
+            with torch.cuda.stream(stream or torch.cuda.current_stream()):
+                scratch.fill_(float("nan"))
+            torch.cuda.synchronize()
+            assert torch.equal(c, dH) and torch.equal(rc, ra)
+
+
+@gpu
+def test_projected_dW_rounded_beside_dH_in_a_graph(fckl, monkeypatch):
+    """Captured: the second stream joins the capture and leaves it with the call; replays on new inputs
+    give the eager call's bits."""
+    monkeypatch.setenv("FCKL_OVERLAP", "1")
+    N, d, V, T, chunk = 300, 256, 5000, 2, 128
+    Ht, Wt, tokens = make(N, d, V, T, "bf16", 21)
+    g = torch.randn(N, T, device="cuda")
+    _, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, chunk)
+    args = (Ht, Wt, tokens, lse, ent, g)
+    want = fckl.projected_logprobs_backward(*args, chunk=chunk, round_dW=True)
+    ws = fckl.Workspace(N, d, V, T, chunk, kind="projected_backward")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fckl.projected_logprobs_backward(*args, chunk=chunk, round_dW=True, ws=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert fckl.check(ws) == fckl.OK and all(torch.equal(a, b) for a, b in zip(got, want))
+    g.mul_(-0.5)
+    want = fckl.projected_logprobs_backward(*args, chunk=chunk, round_dW=True)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+def test_projected_dW_rounding_rule(fckl, monkeypatch):
+    """A shape at which the library takes the second stream by itself (2 rows d V of 6e11)."""
+    N, d, V = 600, 2048, 250000
+    Ht, Wt, tokens = make(N, d, V, 1, "bf16", 22)
+    _, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, 600)
+    g = torch.randn(N, 1, device="cuda")
+    args = (Ht, Wt, tokens, lse, ent, g)
+    monkeypatch.delenv("FCKL_OVERLAP", raising=False)
+    a = fckl.projected_logprobs_backward(*args, chunk=600, round_dW=True)
+    monkeypatch.setenv("FCKL_OVERLAP", "0")
+    b = fckl.projected_logprobs_backward(*args, chunk=600, round_dW=True)
+    assert fckl.check() == fckl.OK and all(torch.equal(x, y) for x, y in zip(a, b))
