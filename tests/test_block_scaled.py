@@ -289,3 +289,21 @@ def test_binding_refusals(fckl, bad):
     x = torch.zeros(3, 32)
     with pytest.raises((TypeError, ValueError)):
         bad(fckl, x, x.to(torch.float8_e4m3fn), torch.zeros(3, 1))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,decoding", [
+    (15, 333, 200, True), (16, 4097, 384, True), (17, 4097, 384, False),                  # rows
+    (8, 300, 9856, True), (8, 300, 9984, False), (16, 300, 3840, True), (16, 300, 3968, False),  # shared memory
+])
+def test_product_decode_limits(fckl, M, N, K, decoding):
+    """Both sides of each limit of the decoding form, and which form ran."""
+    a, sa = fckl.block_quantize(draw(M, K, "bf16", 1), rows=1)
+    b, sb = fckl.block_quantize(draw(N, K, "bf16", 2), rows=128)
+    fckl.profile_enable(True)
+    fckl.profile_read()
+    check_product(fckl, a, sa, b, sb)
+    torch.cuda.synchronize()
+    ran = {k for k, (_, n) in fckl.profile_read().items() if n}
+    fckl.profile_enable(False)
+    assert ("block_matmul_skinny" in ran) == decoding and ("block_scaled_matmul" in ran) != decoding, ran

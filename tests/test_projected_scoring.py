@@ -548,3 +548,38 @@ def test_projected_dW_rounding_rule(fckl, monkeypatch):
     monkeypatch.setenv("FCKL_OVERLAP", "0")
     b = fckl.projected_logprobs_backward(*args, chunk=600, round_dW=True)
     assert fckl.check() == fckl.OK and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# ------------------------------------------------------------------ limits of the decoding form
+def launches(fckl, call):
+    """Launches of the call by kernel."""
+    fckl.profile_enable(True)
+    fckl.profile_read()
+    out = call()
+    torch.cuda.synchronize()
+    counts = {k: n for k, (_, n) in fckl.profile_read().items() if n}
+    fckl.profile_enable(False)
+    return out, counts
+
+
+@gpu
+@pytest.mark.parametrize("N,d,V,T,decoding", [
+    (15, 64, 333, 1, True), (16, 256, 4097, 1, True), (17, 256, 4097, 1, False),  # positions
+    (16, 64, 33, 32, True), (16, 64, 333, 33, False), (10, 1000, 16, 32, True),   # tokens
+    (16, 1408, 700, 32, True), (16, 1416, 700, 32, False),                        # shared memory
+    (16, 1472, 501, 1, True), (16, 1480, 501, 1, False),
+    (8, 3520, 501, 1, True), (8, 3528, 501, 1, False), (9, 72, 15, 4, True),
+])
+def test_projected_decode_limits(fckl, N, d, V, T, decoding):
+    """Both sides of each limit of the decoding form, and which form ran."""
+    Ht, Wt, tokens = make(N, d, V, T, "bf16", seed=N + V + T)
+    (logp, ent, lse), ran = launches(fckl, lambda: fckl.projected_logprobs(Ht, Wt, tokens, 2048))
+    assert fckl.check() == fckl.OK
+    assert ("head_skinny" in ran) == decoding and ("head_logits_stats" in ran) != decoding, ran
+    H, W = exact_inputs(Ht, Wt)
+    w_logp, w_ent, w_lse = orc.projected(H, W, tokens.cpu().numpy())
+    dz, r = logit_error(H, W), (256 + V // 16 + 80) * U + 2.0 ** -21
+    close(f64(lse), w_lse, dz + r + 8 * U * np.abs(w_lse))
+    close(f64(logp), w_logp, (2 * dz + r)[:, None] + 8 * U * np.abs(w_logp))
+    spread = np.maximum(w_ent, np.log(V)) + 2
+    close(f64(ent), w_ent, (dz * 2 * spread + r * (1 + 2 * spread)))
