@@ -499,9 +499,11 @@ __global__ void __launch_bounds__(256) dw_round_kernel(const float4* __restrict_
 }
 
 // dW[id] += sum of rest h over a window of a chunk's entries (position, slot) with that token, in order.
-// A block per entry looks through the window's tokens: the first entry with an id adds up all of that
-// id's, so that every row of dW has one writer, and the others leave. (Sorting the entries first, in
-// one block, took 25 us for 2048 of them; this takes 12.)
+// A block per entry looks through the window's tokens: the first entries with an id share that row's
+// columns, REST_COLS at a time, and each adds up all of the id's entries in them, so that every element
+// of dW has one writer; the others leave. (Sorting the entries first, in one block, took 25 us for 2048
+// of them; this takes 12.) 2048 x 2880 entries of different tokens take 26 us, of one token 104 us
+// (with one block for all of an id: 24 and 1930).
 constexpr int REST_WINDOW = 4096;
 constexpr int REST_THREADS = 256;
 __global__ void __launch_bounds__(REST_THREADS) dw_rest_kernel(const int32_t* __restrict__ tokens,
@@ -509,23 +511,20 @@ __global__ void __launch_bounds__(REST_THREADS) dw_rest_kernel(const int32_t* __
                                                                int T, int V, const __nv_bfloat16* __restrict__ H,
                                                                int d, float* __restrict__ dW) {
   constexpr int PER = REST_WINDOW / REST_THREADS;
-  __shared__ int list[REST_WINDOW];
+  constexpr int REST_COLS = 2 * REST_THREADS;
+  __shared__ int2 list[REST_WINDOW];  // position and rest of the id's entries
   __shared__ int wsum[REST_THREADS / 32];
+  __shared__ int rank_s;
   const int own = first + blockIdx.x;  // entries of the window: [first, entries)
   const int id = tokens[own];
   if (id < 0 || id >= V) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t hit = 0;
-  int earlier = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = first + tid * PER + j;
-    if (e < entries && __ldg(tokens + e) == id) {
-      hit |= 1u << j;
-      earlier |= e < own;
-    }
+    if (e < entries && __ldg(tokens + e) == id) hit |= 1u << j;
   }
-  if (__syncthreads_or(earlier)) return;
   int at = __popc(hit);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -541,21 +540,25 @@ __global__ void __launch_bounds__(REST_THREADS) dw_rest_kernel(const int32_t* __
     if (w < warp) at += wsum[w];
     n += wsum[w];
   }
+  if (tid == (own - first) / PER) rank_s = at + __popc(hit & ((1u << (own - first) % PER) - 1u));
+  __syncthreads();
+  const int rank = rank_s, share = min(n, (d + REST_COLS - 1) / REST_COLS);
+  if (rank >= share) return;
   while (hit) {
-    list[at++] = first + tid * PER + __ffs(hit) - 1;
+    const int e = first + tid * PER + __ffs(hit) - 1;
+    list[at++] = make_int2(e / T, __float_as_int(__ldg(rest + e)));
     hit &= hit - 1;
   }
   __syncthreads();
-  for (int c = tid * 2; c < d; c += 2 * REST_THREADS) {
+  for (int c = rank * REST_COLS + tid * 2; c < d; c += share * REST_COLS) {
     float* o = dW + static_cast<int64_t>(id) * d + c;
     float2 a = *reinterpret_cast<const float2*>(o);
-#pragma unroll 4
+#pragma unroll 16
     for (int i = 0; i < n; ++i) {
-      const int e = list[i];
-      const float g = __ldg(rest + e);
+      const int2 e = list[i];
+      const float g = __int_as_float(e.y);
       float h0, h1;
-      unpack2(__ldg(reinterpret_cast<const uint32_t*>(H + static_cast<int64_t>(e / T) * d + c)), h0, h1,
-              __nv_bfloat16{});
+      unpack2(__ldg(reinterpret_cast<const uint32_t*>(H + static_cast<int64_t>(e.x) * d + c)), h0, h1, __nv_bfloat16{});
       a.x = fmaf(g, h0, a.x);
       a.y = fmaf(g, h1, a.y);
     }

@@ -583,3 +583,36 @@ def test_projected_decode_limits(fckl, N, d, V, T, decoding):
     close(f64(logp), w_logp, (2 * dz + r)[:, None] + 8 * U * np.abs(w_logp))
     spread = np.maximum(w_ent, np.log(V)) + 2
     close(f64(ent), w_ent, (dz * 2 * spread + r * (1 + 2 * spread)))
+
+
+# ------------------------------------------------------------------ one token for many positions
+@gpu
+@pytest.mark.parametrize("N,d,T,chunk,ids", [
+    (2, 1544, 1, 2, 1), (3, 1544, 2, 2, 1), (40, 1544, 1, 40, 2), (90, 2056, 3, 64, 5), (700, 1032, 1, 512, 1),
+    (600, 520, 8, 600, 3), (5, 512, 1, 5, 1), (5, 520, 1, 5, 1),
+])
+def test_projected_entries_of_one_token(fckl, N, d, T, chunk, ids):
+    """Positions that score the same few tokens (a yes/no judgement, an end of text): the columns of a
+    token's row of dW are shared among blocks, fewer and more of them than the token has entries, and
+    entries of several windows meet in a row. dW as fp32, dH to bf16, both as exact as elsewhere."""
+    V = 600
+    Ht, Wt, tokens = make(N, d, V, T, "bf16", seed=N + d)
+    tokens = torch.where(tokens < 0, tokens, tokens % ids * 7)
+    _, ent, lse = fckl.projected_logprobs(Ht, Wt, tokens, chunk)
+    g = torch.randn(N, T, device="cuda")
+    dH, dW = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=chunk)
+    assert fckl.check() == fckl.OK
+    H, W = exact_inputs(Ht, Wt)
+    tk, gn = tokens.cpu().numpy(), f64(g)
+    gn = np.where(tk < 0, 0, gn)
+    G = orc.logits_gradient(H @ W.T, tk, gn)
+    q = np.exp(orc._log_softmax(H @ W.T)[0])
+    a = np.abs(gn).sum(1, keepdims=True)
+    dz, r = logit_error(H, W)[:, None], (256 + 92) * U + 2.0 ** -21
+    eG = q * a * (2.0 ** -8 * 1.01 + 4 * (dz + r) + 2.0 ** -19) + 8 * U * a * (G != 0)
+    sums = 4 * max(N * T, V // 16) * U
+    close(f64(dW), G.T @ H, eG.T @ np.abs(H) + sums * (np.abs(G).T @ np.abs(H)) + 1e-30)
+    want = G @ W
+    close(f64(dH), want, eG @ np.abs(W) + sums * (np.abs(G) @ np.abs(W)) + 2.0 ** -8 * np.abs(want) + 1e-30)
+    again = fckl.projected_logprobs_backward(Ht, Wt, tokens, lse, ent, g, chunk=chunk)
+    assert torch.equal(again[0], dH) and torch.equal(again[1], dW)
