@@ -75,8 +75,7 @@ def _out_dtype(out, out_dtype, M, N):
 
 def block_quantize(x, rows=1, stream=None):
     """(e4m3 values [R, K], fp32 scales [ceil(R / rows), ceil(K / 128)]) of x [R, K] (bf16, fp16 or
-    fp32): each block of ``rows`` (1 or 128) x 128 values is divided by max(amax / 448, 2^-126). The
-    scales of single rows lie a multiple of 16 bytes apart, as the product reads them four at a time."""
+    fp32): each block of ``rows`` (1 or 128) x 128 values is divided by max(amax / 448, 2^-126)."""
     import torch
     if x.dim() != 2:
         raise ValueError("expected x [R,K]")
@@ -89,13 +88,9 @@ def block_quantize(x, rows=1, stream=None):
     kb = -(-K // BLOCK)
     with _for_stream(stream, x):
         q = torch.empty(R, -(-K // 16) * 16, dtype=torch.float8_e4m3fn, device=x.device)[:, :K]
-        if rows == 1:
-            scale = torch.empty(R, -(-kb // 4) * 4, dtype=torch.float32, device=x.device)[:, :kb]
-        else:
-            scale = torch.empty(-(-R // rows), kb, dtype=torch.float32, device=x.device)
-    rs, cs = (-(-kb // 4) * 4 if rows == 1 else kb), 1
+        scale = torch.empty(-(-R // rows), kb, dtype=torch.float32, device=x.device)
     p = _address
-    st = _pkg.load().fckl_block_quantize(p(x), code, ldx, R, K, rows, p(q), -(-K // 16) * 16, p(scale), rs, cs,
+    st = _pkg.load().fckl_block_quantize(p(x), code, ldx, R, K, rows, p(q), -(-K // 16) * 16, p(scale), kb, 1,
                                          _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_block_quantize")
@@ -146,18 +141,18 @@ def block_scaled_projection(H, W8, w_scale, out_dtype=None, out=None, ws=None, s
     out_dtype = _out_dtype(out, out_dtype, N, V)
     dev = H.device
     _on_device(dev, H=H, W8=W8, w_scale=w_scale, out=out)
-    ldq, pitch = -(-K // 16) * 16, -(-kb // 4) * 4
+    ldq = -(-K // 16) * 16
     with _for_stream(stream, H, W8, w_scale, out, ws):
         ws = _ws(ws, dev)
         q = torch.empty(N * ldq, dtype=torch.uint8, device=dev)
-        scale = torch.empty(N * pitch, dtype=torch.float32, device=dev)
+        scale = torch.empty(N * kb, dtype=torch.float32, device=dev)
         if out is None:
             out = torch.empty(N, V, dtype=out_dtype, device=dev)
     lib, s, p = _pkg.load(), _stream(stream), _address
-    st = lib.fckl_block_quantize(p(H), code, ldx, N, K, 1, p(q), ldq, p(scale), pitch, 1, s)
+    st = lib.fckl_block_quantize(p(H), code, ldx, N, K, 1, p(q), ldq, p(scale), kb, 1, s)
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_block_quantize")
-    st = lib.fckl_block_scaled_matmul(p(q), ldq, p(scale), pitch, 1, p(W8), ldb, p(w_scale), *sb, N, V, K, p(out),
+    st = lib.fckl_block_scaled_matmul(p(q), ldq, p(scale), kb, 1, p(W8), ldb, p(w_scale), *sb, N, V, K, p(out),
                                       _value_code(out, "out"), _rows("out", out), ws.tensor.data_ptr(), ws.nbytes, s)
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_block_scaled_matmul")

@@ -307,3 +307,17 @@ def test_product_decode_limits(fckl, M, N, K, decoding):
     ran = {k for k, (_, n) in fckl.profile_read().items() if n}
     fckl.profile_enable(False)
     assert ("block_matmul_skinny" in ran) == decoding and ("block_scaled_matmul" in ran) != decoding, ran
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 128])
+def test_scales_are_dense(fckl, rows):
+    """Scales come without padding, whatever the number of blocks in a row, and the product takes them."""
+    for K in (1, 128, 129, 600, 2880):
+        x = draw(130, K, "bf16", K)
+        q, scale = fckl.block_quantize(x, rows=rows)
+        assert scale.is_contiguous()
+        same_quantisation(x, rows, q, scale)
+        w, sw = fckl.block_quantize(draw(200, K, "bf16", K + 1), rows=128)
+        if rows == 1:
+            check_product(fckl, q, scale, w, sw)
