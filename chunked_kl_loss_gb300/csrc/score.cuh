@@ -912,11 +912,12 @@ __global__ void __launch_bounds__(NT, SCORE_GRAD_RESIDENT * SCORE_THREADS / NT) 
     sg += wsum[w];
     any |= wany[w];
   }
-  const float ge = p.g_entropy ? p.g_entropy[row] : 0.f;
+  const float ge = p.g_entropy ? p.g_entropy[row] : 0.f, ent = p.entropy[row];
   const float m = p.norm[2 * row], log_s = p.norm[2 * row + 1];
   // nothing upstream, or nothing left by the mask (log s is 0 there, and NaN if a NaN is among the -inf)
   const bool zero = (!any && ge == 0.f) || (m == -INFINITY && log_s == 0.f);
-  const float a0 = ge == 0.f ? sg : sg + ge * p.entropy[row];  // not read where it plays no part
+  // taken from memory beside ge (behind it: 406 us for 346 at 4096 x 128256), left out where it plays no part
+  const float a0 = ge == 0.f ? sg : sg + ge * ent;
   // dense part: - q (a0 + ge log q)
   auto dense = [&](float z) {
     const float lq = max_nan((z - m) - log_s, DIFF_FLOOR);  // q is 0 below: 0 * finite, for any ge

@@ -314,8 +314,8 @@ __global__ void __launch_bounds__(HEAD_THREADS, 1) head_score_kernel(const __gri
       } else {
         const float ge = valid && p.g_entropy ? __ldg(p.g_entropy + row) : 0.f;
         const float lse = valid ? __ldg(p.lse + row) : 0.f;
-        // the entropy is not read where it plays no part
-        const float a0 = !valid ? 0.f : ge == 0.f ? gsum : fmaf(ge, __ldg(p.entropy + row), gsum);
+        const float ent = valid ? __ldg(p.entropy + row) : 0.f;
+        const float a0 = ge == 0.f ? gsum : fmaf(ge, ent, gsum);  // left out where it plays no part
         const float nge = -2.f * ge, nlse = -0.5f * lse;
         if (!warp_wait_phase(&tfull[acc], use & 1u, abort_flag, p.status)) break;
         tc_fence_after();

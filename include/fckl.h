@@ -268,7 +268,7 @@ int fckl_token_logprobs(const void* logits, int dtype, int64_t ld, const int32_t
  *   dlogits : [N, V] of the logits' type, rows ld_out >= V elements apart. It may be `logits`
  *             itself (then ld_out = ld); otherwise the two must not overlap.
  * A position without any upstream gradient gets zeros, whatever its logits hold; where none comes
- * in through the entropy, its entropy is not read (nor by fckl_projected_logprobs_backward). */
+ * in through the entropy, its value does not matter (nor to fckl_projected_logprobs_backward). */
 int fckl_token_logprobs_backward(const void* logits, int dtype, int64_t ld, const int32_t* tokens, int64_t N, int V,
                                  int T, const float* norm, const float* entropy, const float* g_logp,
                                  const float* g_entropy, void* dlogits, int64_t ld_out, void* ws, size_t ws_bytes,
