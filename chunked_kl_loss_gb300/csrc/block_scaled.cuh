@@ -343,7 +343,8 @@ struct BlockMatmulParams {
 // the kernel, a K-block's round is 1600 cycles from the issue of its MMAs to their commit (behind the
 // other buffer's), 300 to read the sums and 400 until the buffer is free again at the MMA warp, so a
 // K-block takes 900 to 1100. With one hand-off per tile instead of one per K-block, which cannot apply
-// the scales, the same loop takes 2.7 ms at 8192 x 2880 x 201088. Steps at that size (bf16 C):
+// the scales, the same loop takes 2.7 ms at 8192 x 2880 x 201088. Steps at that size (bf16 C; single
+// launches, before the power cap sets in: in a sequence of them the last one takes 4.0 ms):
 // 9.7 ms with cluster-scope release and acquire on the hand-off; 5.8 ms without; 4.25 ms with the
 // MMA warp converged (its loop was 1000 cycles) and C staged and stored with TMA; 3.7 ms with half
 // the reads, twice as wide; 3.6 ms with the next tile's scales fetched early and longer suspended

@@ -12,10 +12,10 @@
 //                entries, those at the given tokens, are most of a gradient, and their rounding
 //                alone would double its error: with up to REST_TOKENS tokens what the rounding
 //                left of them is kept in fp32 and added to dH and dW (dh_rest_kernel, dw_rest_kernel).
-// Bound by the tensor cores at large d: 2048 x 2880 x 65536 takes 399 us (1.94 PFLOP/s, tensor pipe 90%
-// busy) with HEAD_STATS and 421 us (85%) with HEAD_GRAD; below d of about 1000 by the epilogue, whose
-// exponentials alone are 2048 cycles per 128 x 256 tile and SM (2048 x 512 x 128256: 196 us, 141 at the
-// tensor rate).
+// Bound by the tensor cores at large d: 2048 x 2880 x 65536 takes 392 us (1.97 PFLOP/s, tensor pipe 90%
+// busy) with HEAD_STATS and 411 us (86%) with HEAD_GRAD; below d of about 1000 by the epilogue, whose
+// exponentials alone are 2048 cycles per 128 x 256 tile and SM (2048 x 512 x 128256: 191 us and 223,
+// 141 at the tensor rate).
 #pragma once
 
 #include <cfloat>

@@ -243,7 +243,8 @@ int fckl_teacher_topk(const void* Ht, const void* Wt, int dtype,
  * (logp 0, no gradient). Any other id outside [0, V) sets FCKL_ERR_INDEX in the status word; its
  * logp is NaN and it takes no part in the gradient. A position with nothing left (every logit
  * -inf) has logp -inf, entropy 0, norm (-inf, 0) and a zero gradient; a NaN or +inf among a
- * position's logits makes its results NaN (its alternatives: ids 0..top-1).
+ * position's logits makes its results and its gradient NaN (its alternatives: ids 0..top-1). Finite
+ * logits may be of any size (a logp below fp32's lowest number is -inf).
  *
  * The workspace of the calls over logits holds only the status word: at least 256 bytes, zeroed
  * once by the caller before its first use. These calls OR into the word and do not clear it
@@ -258,7 +259,10 @@ int fckl_teacher_topk(const void* Ht, const void* Wt, int dtype,
  *   top_idx  : int32 [N, top], the `top` largest logits' ids, largest first, equal logits by
  *              smaller id; 0 <= top <= min(V, 1024). NULL when top = 0, as top_logp.
  *   top_logp : fp32 [N, top], their log-probabilities
- * One launch that reads the logits once. */
+ * One launch that reads the logits once. Up to 128 alternatives it is bound by that reading where there
+ * are many rows; more cost up to four times as much (4096 x 128256 bf16: 258 us with 128, 647 with
+ * 1000; one row 25 us with 100, 201 with 1000). The number of rows sets how a row's sums are split, and
+ * with it their last bits. */
 int fckl_token_logprobs(const void* logits, int dtype, int64_t ld, const int32_t* tokens, int64_t N, int V, int T,
                         int top, float* logp, float* entropy, float* norm, int32_t* top_idx, float* top_logp,
                         void* ws, size_t ws_bytes, void* stream);
@@ -280,7 +284,8 @@ int fckl_token_logprobs_backward(const void* logits, int dtype, int64_t ld, cons
  * alignment are the loss's (T in the place of K, 0 <= T <= 1024; N = 0 is allowed); the workspace's
  * status word is cleared by the call. Hidden states have to be finite, those of positions without
  * an upstream gradient too (dW sums over all positions).
- *   lse : fp32 [N], the log-partition, kept for the backward call */
+ *   lse : fp32 [N], the log-partition, kept for the backward call
+ * A position's results are the same bits in any chunk. */
 size_t fckl_projected_logprobs_workspace_bytes(int64_t N, int d, int V, int T, int chunk, int dtype, int backward);
 int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d, int V,
                             int T, int chunk, float* logp, float* entropy, float* lse, void* ws, size_t ws_bytes,
@@ -291,9 +296,9 @@ int fckl_projected_logprobs(const void* H, const void* W, int dtype, const int32
  * dW_bf16: NULL, or bf16 [V, d] that receives dW rounded once (beside the
  * last dH product, on the library's second stream, where that is long enough; joined back into
  * `stream` before the call returns). dW is then needed too.
- * G's entries at the given tokens, most of a gradient, keep fp32 precision where T <= 8. Each chunk's logits are recomputed; the logit gradient is formed in
- * fp32 and rounded to bf16 for the dH and dW products, as in fckl_backward. The workspace is that
- * of backward = 1 above. */
+ * Each chunk's logits are recomputed; the logit gradient is formed in fp32 and rounded to bf16 for the
+ * dH and dW products, as in fckl_backward. Its entries at the given tokens, most of a gradient, keep
+ * fp32 precision where T <= 8. The workspace is that of backward = 1 above. */
 int fckl_projected_logprobs_backward(const void* H, const void* W, int dtype, const int32_t* tokens, int64_t N, int d,
                                      int V, int T, int chunk, const float* lse, const float* entropy,
                                      const float* g_logp, const float* g_entropy, void* dH, float* dW,
@@ -317,8 +322,8 @@ int fckl_block_quantize(const void* x, int dtype, int64_t ldx, int64_t rows, int
 /* C [M, N] = sum over blocks k of 128 of  sa[m, k] * sb[n / 128, k] * (A_k B_k^T)[m, n]
  * A [M, K] and B [N, K] are e4m3, rows lda and ldb bytes apart (multiples of 16, arrays 16-byte
  * aligned); sa and sb fp32 with the strides of fckl_block_quantize at block_rows 1 and 128. C is
- * FCKL_BF16 or FCKL_F32, rows ldc elements apart. Products and sums are fp32 throughout; a bf16 C is
- * rounded once. ws holds the status word (at least 256 bytes, see fckl_token_logprobs). M = 0 is
+ * FCKL_BF16 or FCKL_F32, rows ldc elements apart. Products and sums are fp32 throughout (sa * sb first:
+ * a normal fp32 number, unless its block's sums are 0 and it is finite); a bf16 C is rounded once. ws holds the status word (at least 256 bytes, see fckl_token_logprobs). M = 0 is
  * allowed. */
 int fckl_block_scaled_matmul(const void* a, int64_t lda, const float* sa, int64_t sa_rs, int64_t sa_cs, const void* b,
                              int64_t ldb, const float* sb, int64_t sb_rs, int64_t sb_cs, int64_t M, int64_t N,
