@@ -79,6 +79,9 @@ def load():
     lib.fckl_teacher_topk.argtypes = [vp, vp, i32, i64, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     scoring._set_argtypes(lib)
     block_scaled._set_argtypes(lib)
+    tied_embedding._set_argtypes(lib)
+    gradient_clip._set_argtypes(lib)
+    logit_rules._set_argtypes(lib)
     lib.fckl_check.restype = i32
     lib.fckl_check.argtypes = [vp, vp]
     lib.fckl_status_string.restype = c.c_char_p
@@ -131,7 +134,8 @@ class Workspace:
     (teacher cache builder keeping each chunk's logits), "topk_overlap" (the same plus a second
     set of one chunk's buffers, with which the builder overlaps consecutive chunks) or
     "topk_min" (the builder's minimum, which projects each chunk twice); "projected" and
-    "projected_backward" (projected_logprobs and its gradient; K is then the tokens per position)."""
+    "projected_backward" (projected_logprobs and its gradient; K is then the tokens per position);
+    "embedding_backward" (embedding_backward; K, chunk and dtype do not matter)."""
 
     def __init__(self, N, d, V, K, chunk, dtype=BF16, device=None, kind="loss"):
         import torch
@@ -148,6 +152,8 @@ class Workspace:
         elif kind in ("projected", "projected_backward"):
             n = int(load().fckl_projected_logprobs_workspace_bytes(N, d, V, K, chunk, dtype,
                                                                    int(kind == "projected_backward")))
+        elif kind == "embedding_backward":
+            n = int(load().fckl_embedding_backward_workspace_bytes(N, d, V))
         else:
             raise ValueError(f"unknown workspace kind {kind!r}")
         if n == 0:
@@ -465,8 +471,11 @@ def profile_read():
     return {n: (ms[i], int(ln[i])) for i, n in enumerate(names)}
 
 
-from . import block_scaled, scoring  # noqa: E402  (they use the names above)
+from . import block_scaled, gradient_clip, logit_rules, scoring, tied_embedding  # noqa: E402  (they use the names above)
 from .block_scaled import *  # noqa: E402,F401,F403
+from .gradient_clip import *  # noqa: E402,F401,F403
+from .logit_rules import *  # noqa: E402,F401,F403
 from .scoring import *  # noqa: E402,F401,F403
+from .tied_embedding import *  # noqa: E402,F401,F403
 
-__all__ += scoring.__all__ + block_scaled.__all__
+__all__ += scoring.__all__ + block_scaled.__all__ + tied_embedding.__all__ + gradient_clip.__all__ + logit_rules.__all__

@@ -65,6 +65,15 @@ enum Kind {
   KIND_MATMUL_SKINNY,
   KIND_DW_REST,
   KIND_DW_ROUND,
+  KIND_EMBEDDING,
+  KIND_SORT_TOKENS,
+  KIND_EMBEDDING_GRAD,
+  KIND_EMBEDDING_JOIN,
+  KIND_SQUARES,
+  KIND_NORM,
+  KIND_CLIP,
+  KIND_ADJUST,
+  KIND_ADJUST_GRAD,
   KIND_COUNT
 };
 const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", "fwd_combine",
@@ -81,7 +90,12 @@ const char* const kKindNames[KIND_COUNT] = {"preprocess",     "fwd_logits_lse", 
                                             "head_combine",           "head_logit_grad",
                                             "block_quantize",         "block_scaled_matmul",
                                             "head_skinny",            "block_matmul_skinny",
-                                            "dw_rest",                "dw_round"};
+                                            "dw_rest",                "dw_round",
+                                            "embedding",              "sort_tokens",
+                                            "embedding_grad",         "embedding_grad_join",
+                                            "gradient_squares",       "gradient_norm",
+                                            "clip_gradients",         "adjust_logits",
+                                            "adjust_logits_grad"};
 
 // ------------------------------------------------------------------ process state
 std::mutex g_mu;
@@ -1445,7 +1459,7 @@ const char* fckl_status_string(int status) {
   switch (status) {
     case FCKL_OK: return "ok";
     case FCKL_ERR_ARG: return "invalid argument (size, null or misaligned pointer)";
-    case FCKL_ERR_INDEX: return "teacher id, or token to score, outside [0, V)";
+    case FCKL_ERR_INDEX: return "teacher id, or token, outside [0, V)";
     case FCKL_ERR_CUDA: return "CUDA error (see fckl_last_error)";
     case FCKL_ERR_TIMEOUT: return "a bounded device wait ran out";
     case FCKL_ERR_WORKSPACE: return "workspace smaller than fckl_workspace_bytes()";
@@ -1645,3 +1659,6 @@ extern "C" int fckl_forward_static(const void* H, const void* W, int dtype, cons
 #include "score_host.cuh"
 #include "head_host.cuh"
 #include "block_scaled_host.cuh"
+#include "embedding_host.cuh"
+#include "clip_host.cuh"
+#include "adjust_host.cuh"

@@ -65,7 +65,7 @@ extern "C" {
 typedef enum {
     FCKL_OK = 0,
     FCKL_ERR_ARG = 1,         /* bad size, null or misaligned pointer */
-    FCKL_ERR_INDEX = 2,       /* a teacher id, or a token to score, outside [0, V) (device-detected) */
+    FCKL_ERR_INDEX = 2,       /* a teacher id, or a token, outside [0, V) (device-detected) */
     FCKL_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed; see fckl_last_error() */
     FCKL_ERR_TIMEOUT = 4,     /* a bounded device wait ran out (device-detected) */
     FCKL_ERR_WORKSPACE = 5,   /* ws_bytes below fckl_workspace_bytes() */
@@ -74,7 +74,7 @@ typedef enum {
                                  holds (device-detected; that position's output is not exact) */
 } fckl_status;
 
-/* FCKL_F16 is taken by the calls over logits and by fckl_block_quantize only. */
+/* FCKL_F16 is taken by the calls over logits, fckl_block_quantize, the embedding and the gradients' norm. */
 typedef enum { FCKL_BF16 = 0, FCKL_F32 = 1, FCKL_F16 = 2 } fckl_dtype;
 
 /* Bytes of device workspace that fckl_forward, fckl_backward and fckl_forward_backward need
@@ -328,6 +328,82 @@ int fckl_block_quantize(const void* x, int dtype, int64_t ldx, int64_t rows, int
 int fckl_block_scaled_matmul(const void* a, int64_t lda, const float* sa, int64_t sa_rs, int64_t sa_cs, const void* b,
                              int64_t ldb, const float* sb, int64_t sb_rs, int64_t sb_cs, int64_t M, int64_t N,
                              int64_t K, void* c, int c_dtype, int64_t ldc, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Around the output matrix. Interface additions, no counterpart on the pages: the other use of W
+ * where embeddings are tied, the gradients' norm, and the rules by which logits are adjusted before they
+ * are scored.
+ *
+ * Tied embedding. tokens is int32 [N] in any order and with repeats; -1 marks an empty slot. Any other
+ * id outside [0, V) sets FCKL_ERR_INDEX in the status word; its row of `out` is NaN and it takes no part
+ * in the gradient. Limits: 0 <= N <= 2^30, V <= 2^30, 1 <= d <= 2^20; rows need only the alignment of
+ * their elements (16 bytes are read fastest).
+ *
+ * fckl_embedding: out[n] = scale * W[tokens[n]] (an empty slot: zeros), of W's type (FCKL_BF16, FCKL_F16
+ * or FCKL_F32): the product is fp32, rounded once. Rows of W lie ldw and rows of out ld_out elements
+ * apart. The two must not overlap. The workspace holds only the status word (see fckl_token_logprobs). */
+int fckl_embedding(const void* W, int dtype, int64_t ldw, const int32_t* tokens, int64_t N, int d, int V, float scale,
+                   void* out, int64_t ld_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradient: dW[v] = (accumulate: dW[v] +) scale * sum of g[n] over the positions n with tokens[n] = v.
+ * g [N, d] of type `dtype`, rows ldg elements apart; dW dense [V, d], FCKL_F32 or of g's type. Without
+ * accumulate all of dW is written, zeros where a token does not occur; with it only the rows of tokens that
+ * occur are read and written, so that the gradient of a tied matrix is added to what fckl_backward left.
+ * Positions are ordered by token first; sums are fp32 in a fixed order and each value is rounded once. dW
+ * must not overlap g. The call clears the workspace's status word. */
+size_t fckl_embedding_backward_workspace_bytes(int64_t N, int d, int V);
+int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t* tokens, int64_t N, int d, int V,
+                            float scale, void* dW, int dW_dtype, int accumulate, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Norm of `count` gradient tensors: norm[0] = sqrt(sum of all elements' squares), fp32. grads, sizes and
+ * dtypes are host arrays (read before the call returns) of device addresses, numbers of elements and types
+ * (FCKL_BF16, FCKL_F16 or FCKL_F32, mixed at will); a tensor's elements are dense, aligned to their own
+ * size; a size of 0 is skipped. Squares are summed in fp32 within 8192 elements and in fp64 beyond, and in
+ * fp64 throughout where fp32 would overflow or lose them; a norm above fp32's largest number is inf, one
+ * over a NaN is NaN. At most 2^20 tensors. */
+size_t fckl_gradient_norm_workspace_bytes(int64_t count);
+int fckl_gradient_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, float* norm,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/* The same norm, and out[i] = c * grads[i] with c = min(1, max_norm / (norm + 1e-6)), the product in fp32,
+ * rounded once to out's type. out[i] may be grads[i] itself (then of its type; nothing is written where
+ * c = 1); otherwise no two tensors may overlap. c is NaN where the norm is, and 0 where it is infinite.
+ * No host synchronisation. The workspace is that of fckl_gradient_norm. */
+int fckl_clip_gradients(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, float max_norm,
+                        void* const* out, const int* out_dtypes, float* norm, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Logits adjusted by each row's rules. history is int32 [N, L], rows ld_h elements apart: a row's tokens so
+ * far are its first lengths[n] entries (NULL: L; held to 0..L), of which the first prompt[n] were given
+ * (NULL: none) and the others generated; -1 is an empty slot. With seen_v: v is among them, c_v: how often
+ * it was generated,
+ *   z1 = z / r  where seen_v and z > 0,  z r  where seen_v and z <= 0,  z  otherwise
+ *   out = z1 - f c_v - p [c_v > 0] + (sum of v's biases);  -inf where v is not allowed, whatever z holds
+ * repetition r > 0, frequency f and presence p are fp32 [N], or NULL and the one value for all rows.
+ * bias_tokens int32 and bias fp32 are [N, B], dense: -1 is an empty slot, a token's several biases are
+ * added in their order. allowed: bits, bit v % 32 of word v / 32, rows ld_allowed words apart (0: one row
+ * for all); NULL: every token. A row may allow none.
+ * logits and out are [N, V] of one type (FCKL_BF16, FCKL_F16 or FCKL_F32), rows ld and ld_out elements
+ * apart. out may be logits (then ld_out = ld): only the places that a rule changes are then read or
+ * written; otherwise the two must not overlap. Arithmetic is fp32, rounded once; a place that no rule
+ * touches keeps its bits. L <= 1048575, B <= 1024, V <= 2^30. An id outside [-1, V) sets FCKL_ERR_INDEX and is
+ * skipped. The workspace holds only the status word. N = 0 is allowed. */
+int fckl_adjust_logits(const void* logits, int dtype, int64_t ld, int64_t N, int V, const int32_t* history, int64_t ld_h,
+                       int L, const int32_t* lengths, const int32_t* prompt, const float* repetition,
+                       float repetition_all, const float* frequency, float frequency_all, const float* presence,
+                       float presence_all, const int32_t* bias_tokens, const float* bias, int B,
+                       const uint32_t* allowed, int64_t ld_allowed, void* out, int64_t ld_out, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* Gradient with respect to the logits: out = g times (seen_v ? (z > 0 ? 1 / r : r) : 1), 0 where v is not
+ * allowed, whatever g holds there. logits are those that went into fckl_adjust_logits (read only at the
+ * history's tokens). g, logits and out are of one type; out may be g, and may be logits. There is no
+ * gradient of the penalties and biases. */
+int fckl_adjust_logits_backward(const void* g, int dtype, int64_t ld_g, const void* logits, int64_t ld, int64_t N, int V,
+                                const int32_t* history, int64_t ld_h, int L, const int32_t* lengths,
+                                const float* repetition, float repetition_all, const uint32_t* allowed,
+                                int64_t ld_allowed, void* out, int64_t ld_out, void* ws, size_t ws_bytes,
+                                void* stream);
 
 /* Interface addition, no counterpart on the pages (they describe no device interface).
  * Synchronises `stream`, returns the status found on the device by the last call that
