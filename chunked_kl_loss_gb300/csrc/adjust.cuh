@@ -9,20 +9,47 @@
 // Arithmetic is fp32, rounded once to the logits' type; a place that no rule touches keeps its bits.
 #pragma once
 
+#include <type_traits>
+
 #include "score.cuh"
+#include "tc_gemm.cuh"
 
 namespace fckl {
 
 constexpr int ADJUST_THREADS = 256;
-constexpr int ADJUST_UNROLL = 4;
+constexpr int ADJUST_UNROLL = 4;      // vectors that a thread has under way
+constexpr int ADJUST_AHEAD = 4;       // history entries that a thread has under way
+constexpr int ADJUST_STAGES = 4;      // of the staged kernel's ring
+constexpr int ADJUST_STAGE_VECS = 1024;  // vectors of a stage (16 KB)
 
-// What a token's word in shared memory holds: how often it was generated, whether it stands in the
-// prompt, and one more than the bias slot that carries the sum of its biases (0: none).
+// What a row's rules have to know of its history.
+enum AdjustKind {
+  ADJUST_COUNTS,  // counts and biases too
+  ADJUST_SEEN,    // which tokens stand in it: the repetition penalty alone
+  ADJUST_GRAD     // the same, and the signs of their logits
+};
+
+// What shared memory holds for a token that a rule touches: how often it was generated, whether it stands
+// in the prompt, and one more than the bias slot that carries the sum of its biases (0: none).
 constexpr uint32_t ADJ_COUNT = 0xfffffu;
 constexpr uint32_t ADJ_GIVEN = 1u << 20;
 constexpr uint32_t ADJ_SEEN = ADJ_COUNT | ADJ_GIVEN;
+constexpr uint32_t ADJ_POSITIVE = 1;  // gradient: the logit is above 0
 constexpr int ADJ_SLOT_SHIFT = 21;
 constexpr int ADJUST_HISTORY_MAX = 0xfffff;
+constexpr uint32_t ADJ_NO_KEY = ~0u;
+
+// Bulk copies between global and shared memory: addresses and sizes are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
 
 struct AdjustParams {
   const void* z;   // logits
@@ -43,143 +70,405 @@ struct AdjustParams {
   int64_t ld_allowed;
   int V;
   int segs, seg_vecs;  // segments of a row, vectors of a segment
+  int stages;          // of the staged kernel
+  int slots_log2;      // of the table of touched tokens; < 0: one word for every token of the segment
   unsigned* status;
 };
 
-template <typename T, int VE>
-struct AdjustVec {
-  T v[VE];
+// Word k of a 16-byte vector with what is not allowed replaced: -inf, or 0 in a gradient.
+template <typename T, bool GRAD>
+__device__ __forceinline__ uint32_t masked_word(uint32_t w, uint32_t m, int k) {
+  const uint32_t none = GRAD ? 0u : fill_word<T>(-INFINITY);
+  if constexpr (sizeof(T) == 4) {
+    return (m >> k) & 1u ? w : none;
+  } else {
+    const uint32_t keep = ((m >> (2 * k)) & 1u ? 0xffffu : 0u) | ((m >> (2 * k + 1)) & 1u ? 0xffff0000u : 0u);
+    return (w & keep) | (none & ~keep);
+  }
+}
+
+// A row's segment and the shared memory of its touched tokens.
+struct AdjustSegment {
+  int mis, v0, v1;     // values from the 16-byte boundary below the row's start; first and last vector
+  int c0, columns;     // its columns
+  int first;           // column of the first vector's first value (below 0 before a row's start)
+  bool table;
+  int words, bits;     // 32-bit words of the table or array, and of one set of bits
+  uint32_t *seen, *positive;  // bits by value from `first` on
+  uint32_t *word, *key;
+  int* btok;
+  float *bsum, *bval;
 };
 
-// One block per (row, segment of seg_vecs vectors). The segment's words are gathered in shared memory
-// from the row's whole history, then the segment is walked once.
-template <typename T, int VE, bool GRAD, bool IN_PLACE>
-__global__ void __launch_bounds__(ADJUST_THREADS) adjust_kernel(const AdjustParams p) {
-  extern __shared__ __align__(16) uint32_t adj_smem[];
-  const int64_t row = blockIdx.x / p.segs;
-  const int seg = blockIdx.x % p.segs;
-  const int tid = threadIdx.x;
-  const T* x = GRAD ? static_cast<const T*>(p.g) + row * p.ld_g : static_cast<const T*>(p.z) + row * p.ld_z;
-  const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
-  T* out = static_cast<T*>(p.out) + row * p.ld_out;
-  const int mis = VE == 1 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T));
-  const int nvec = (p.V + mis + VE - 1) / VE;
-  const int v0 = seg * p.seg_vecs, v1 = min(nvec, v0 + p.seg_vecs);
-  if (v0 >= v1) return;
-  const int base = v0 * VE - mis;  // column of the segment's first word
-  const int words = p.seg_vecs * VE;
-  uint32_t* word = adj_smem;
-  int* btok = reinterpret_cast<int*>(adj_smem + words);
-  float* bsum = reinterpret_cast<float*>(btok + p.B);
-  float* bval = bsum + p.B;
+// Sets of bits, then words and keys, then biases: as much of it as the kind of rules needs.
+template <typename T, int VE, AdjustKind KIND, bool BITS>
+__device__ __forceinline__ AdjustSegment adjust_segment(const AdjustParams& p, const T* out, int seg, uint32_t* smem) {
+  AdjustSegment s;
+  s.mis = VE == 1 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T));
+  const int nvec = (p.V + s.mis + VE - 1) / VE;
+  s.v0 = seg * p.seg_vecs;
+  s.v1 = min(nvec, s.v0 + p.seg_vecs);
+  s.first = s.v0 * VE - s.mis;
+  s.c0 = max(s.first, 0);
+  s.columns = min(s.v1 * VE - s.mis, p.V) - s.c0;
+  s.bits = BITS ? (p.seg_vecs * VE + 127) / 128 * 4 : 0;
+  s.table = p.slots_log2 >= 0;
+  s.words = BITS && KIND != ADJUST_COUNTS ? 0 : s.table ? 1 << p.slots_log2 : p.seg_vecs * VE;
+  s.seen = smem;
+  s.positive = smem + s.bits;
+  s.word = smem + (KIND == ADJUST_GRAD ? 2 : 1) * s.bits;
+  s.key = s.word + s.words;
+  s.btok = reinterpret_cast<int*>(s.word + (s.table ? 2 : 1) * s.words);
+  s.bsum = reinterpret_cast<float*>(s.btok + p.B);
+  s.bval = s.bsum + p.B;
+  return s;
+}
 
-  for (int i = tid; i < words; i += ADJUST_THREADS) word[i] = 0;
+__device__ __forceinline__ uint32_t adjust_hash(int token, int log2) {
+  return (static_cast<uint32_t>(token) * 0x9E3779B1u) >> (32 - log2);
+}
+
+// Gathers the segment's touched tokens from the row's history and biases. Counts and bias slots are kept in
+// a hash table of token ids where those are few, so that its size does not depend on V, else in a word for
+// every token. With BITS a set of bits says which tokens are touched (and in a gradient a second one
+// which logits are above 0). Complete after the caller's next barrier.
+template <typename T, AdjustKind KIND, bool BITS>
+__device__ __forceinline__ void adjust_gather(const AdjustParams& p, const AdjustSegment& s, int64_t row, const T* z) {
+  const int tid = threadIdx.x;
+  const int len = p.lengths ? min(max(p.lengths[row], 0), p.L) : p.L;
+  const int prompt = KIND == ADJUST_COUNTS && p.prompt ? p.prompt[row] : 0;
+  const int32_t* h = p.history + row * p.ld_h;
+  const uint4 zero = make_uint4(0, 0, 0, 0), no_key = make_uint4(ADJ_NO_KEY, ADJ_NO_KEY, ADJ_NO_KEY, ADJ_NO_KEY);
+  const int clear = ((KIND == ADJUST_GRAD ? 2 : 1) * s.bits + s.words) / 4;
+  for (int i = tid; i < clear; i += ADJUST_THREADS) reinterpret_cast<uint4*>(s.seen)[i] = zero;
+  if (s.table)
+    for (int i = tid; i < s.words / 4; i += ADJUST_THREADS) reinterpret_cast<uint4*>(s.key)[i] = no_key;
   for (int b = tid; b < p.B; b += ADJUST_THREADS) {
-    btok[b] = p.bias_tokens[row * p.B + b];
-    bval[b] = p.bias[row * p.B + b];
+    s.btok[b] = p.bias_tokens[row * p.B + b];
+    s.bval[b] = p.bias[row * p.B + b];
   }
   __syncthreads();
-  const int len = p.lengths ? min(max(p.lengths[row], 0), p.L) : p.L;
-  const int prompt = p.prompt ? p.prompt[row] : 0;
-  const int32_t* h = p.history + row * p.ld_h;
-  bool bad = false;
-  for (int i = tid; i < len; i += ADJUST_THREADS) {
-    const int t = h[i];
-    if (t < 0 || t >= p.V) {
-      bad |= t != -1;
-      continue;
+  // The word of a token of the segment. The table has room for every history entry and bias.
+  auto place = [&](int t) -> uint32_t* {
+    if (!s.table) return s.word + (t - s.c0);
+    uint32_t at = adjust_hash(t, p.slots_log2);
+    for (;;) {
+      const uint32_t k = *static_cast<volatile uint32_t*>(s.key + at);
+      if (k == static_cast<uint32_t>(t)) break;
+      if (k == ADJ_NO_KEY) {
+        const uint32_t old = atomicCAS(s.key + at, ADJ_NO_KEY, static_cast<uint32_t>(t));
+        if (old == ADJ_NO_KEY || old == static_cast<uint32_t>(t)) break;
+      }
+      at = (at + 1) & (s.words - 1);
     }
-    const unsigned at = static_cast<unsigned>(t - base);
-    if (at < static_cast<unsigned>(words)) {
-      if (!GRAD && i >= prompt) atomicAdd(&word[at], 1u);
-      else atomicOr(&word[at], ADJ_GIVEN);
+    return s.word + at;
+  };
+  // Sets a token's bit; whether it was not set before.
+  auto mark = [&](uint32_t* bits, int t) {
+    const uint32_t one = 1u << ((t - s.first) & 31);
+    return !(atomicOr(bits + ((t - s.first) >> 5), one) & one);
+  };
+  bool bad = false;
+  constexpr int A = ADJUST_AHEAD;
+  for (int i0 = tid; i0 < len; i0 += A * ADJUST_THREADS) {
+    int t[A];
+    T sign[A];
+#pragma unroll
+    for (int u = 0; u < A; ++u) t[u] = i0 + u * ADJUST_THREADS < len ? h[i0 + u * ADJUST_THREADS] : -1;
+#pragma unroll
+    for (int u = 0; u < A; ++u) {
+      if (static_cast<unsigned>(t[u]) >= static_cast<unsigned>(p.V)) {
+        bad |= t[u] != -1;
+        t[u] = -1;
+      } else if (static_cast<unsigned>(t[u] - s.c0) >= static_cast<unsigned>(s.columns)) {
+        t[u] = -1;
+      } else if (KIND == ADJUST_COUNTS) {
+        if (BITS) mark(s.seen, t[u]);
+        uint32_t* w = place(t[u]);
+        if (i0 + u * ADJUST_THREADS >= prompt) atomicAdd(w, 1u);
+        else atomicOr(w, ADJ_GIVEN);
+      } else {
+        const bool is_new = BITS ? mark(s.seen, t[u]) : atomicOr(place(t[u]), ADJ_GIVEN) == 0;
+        if (KIND == ADJUST_GRAD && is_new) sign[u] = z[t[u]];
+        else t[u] = -1;
+      }
+    }
+    if (KIND == ADJUST_GRAD) {
+#pragma unroll
+      for (int u = 0; u < A; ++u) {
+        if (t[u] < 0 || !(to_f32(sign[u]) > 0.f)) continue;
+        if (BITS) mark(s.positive, t[u]);
+        else atomicOr(place(t[u]), ADJ_POSITIVE);
+      }
     }
   }
   // The first slot of a token takes the sum over its slots, in their order.
   for (int b = tid; b < p.B; b += ADJUST_THREADS) {
-    const int t = btok[b];
-    if (t < 0 || t >= p.V) {
+    const int t = s.btok[b];
+    if (static_cast<unsigned>(t) >= static_cast<unsigned>(p.V)) {
       bad |= t != -1;
       continue;
     }
-    const unsigned at = static_cast<unsigned>(t - base);
-    if (at >= static_cast<unsigned>(words)) continue;
+    if (static_cast<unsigned>(t - s.c0) >= static_cast<unsigned>(s.columns)) continue;
     float sum = 0.f;
     bool first = true;
     for (int j = 0; j < p.B; ++j) {
-      if (btok[j] != t) continue;
+      if (s.btok[j] != t) continue;
       if (j < b) {
         first = false;
         break;
       }
-      sum += bval[j];
+      sum += s.bval[j];
     }
     if (first) {
-      bsum[b] = sum;
-      atomicOr(&word[at], static_cast<uint32_t>(b + 1) << ADJ_SLOT_SHIFT);
+      s.bsum[b] = sum;
+      if (BITS) mark(s.seen, t);
+      atomicOr(place(t), static_cast<uint32_t>(b + 1) << ADJ_SLOT_SHIFT);
     }
   }
   if (bad) atomicOr(p.status, ST_BAD_INDEX);
-  __syncthreads();
+}
 
-  const float r = p.r ? p.r[row] : p.r1;
-  const float f = p.f ? p.f[row] : p.f1;
-  const float pr = p.p ? p.p[row] : p.p1;
-  const uint32_t* allowed = p.allowed ? p.allowed + row * p.ld_allowed : nullptr;
-  const float none = GRAD ? 0.f : -INFINITY;
-  // value at column c with word w
-  auto value = [&](float v, uint32_t w, int c) -> float {
-    if constexpr (GRAD) {
-      if (w) v = to_f32(z[c]) > 0.f ? v / r : v * r;
+// A row's penalties, and a value under what its word says.
+struct AdjustRow {
+  float r, f, p;
+  __device__ __forceinline__ AdjustRow(const AdjustParams& q, int64_t row)
+      : r(q.r ? q.r[row] : q.r1), f(q.f ? q.f[row] : q.f1), p(q.p ? q.p[row] : q.p1) {}
+  __device__ __forceinline__ float repeated(float v, bool positive) const { return positive ? v / r : v * r; }
+  template <AdjustKind KIND>
+  __device__ __forceinline__ float value(float v, uint32_t w, const float* bsum) const {
+    if constexpr (KIND == ADJUST_GRAD) {
+      return repeated(v, w & ADJ_POSITIVE);
     } else {
-      if (w & ADJ_SEEN) v = v > 0.f ? v / r : v * r;
+      if (w & ADJ_SEEN) v = repeated(v, v > 0.f);
       const uint32_t n = w & ADJ_COUNT;
-      if (n) v = v - f * static_cast<float>(n) - pr;
+      if (n) v = v - f * static_cast<float>(n) - p;
       const uint32_t slot = w >> ADJ_SLOT_SHIFT;
       if (slot) v += bsum[slot - 1];
+      return v;
     }
-    return v;
+  }
+};
+
+// Into another tensor whose rows lie alike to the 16-byte boundaries. One block per (row, segment of
+// seg_vecs vectors). The segment streams through a ring of stages in shared memory by bulk copies, which are
+// under way while the threads gather the segment's touched tokens; the threads change the touched and the
+// masked places in the stages, so that what no rule touches passes through no register and a touched
+// place costs no access to memory. Two blocks an SM: one gathers while the other streams.
+template <typename T, AdjustKind KIND>
+__global__ void __launch_bounds__(ADJUST_THREADS) adjust_staged_kernel(const AdjustParams p) {
+  constexpr int VE = 16 / sizeof(T);
+  constexpr int TV = ADJUST_STAGE_VECS, S = ADJUST_STAGES;
+  constexpr int U = TV / ADJUST_THREADS;
+  constexpr uint32_t ALL = (1u << VE) - 1u;
+  constexpr bool GRAD = KIND == ADJUST_GRAD;
+  extern __shared__ __align__(128) uint8_t adj_stage[];
+  __shared__ uint64_t full[S];
+  const int64_t row = blockIdx.x / p.segs;
+  const int tid = threadIdx.x;
+  const T* x = GRAD ? static_cast<const T*>(p.g) + row * p.ld_g : static_cast<const T*>(p.z) + row * p.ld_z;
+  const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
+  T* out = static_cast<T*>(p.out) + row * p.ld_out;
+  const AdjustSegment s = adjust_segment<T, VE, KIND, true>(p, out, blockIdx.x % p.segs,
+                                                            reinterpret_cast<uint32_t*>(adj_stage + p.stages * TV * 16));
+  if (s.v0 >= s.v1) return;
+  // whole vectors [wa, wb), in tiles of a stage; the row's ends, if they are ragged, go value by value
+  const int wa = s.v0 + (s.first < 0), wb = max(wa, s.v1 - (s.v1 * VE - s.mis > p.V));
+  const int tiles = (wb - wa + TV - 1) / TV, stages = p.stages;
+  auto column = [&](int v) { return v * VE - s.mis; };
+  auto load_tile = [&](int k) {
+    const int v = wa + k * TV;
+    const uint32_t bytes = static_cast<uint32_t>(min(TV, wb - v)) * 16;
+    mbar_arrive_expect_tx(&full[k % stages], bytes);
+    bulk_load(adj_stage + (k % stages) * TV * 16, x + column(v), bytes, &full[k % stages]);
   };
+  if (tid == 0) {
+    for (int k = 0; k < S; ++k) mbar_init(&full[k], 1);
+    fence_mbar_init();
+    for (int k = 0; k < min(stages, tiles); ++k) load_tile(k);
+  }
+  adjust_gather<T, KIND, true>(p, s, row, z);
+  const uint32_t* allowed = p.allowed ? p.allowed + row * p.ld_allowed : nullptr;
+  uint32_t lo[U], hi[U];
+  auto fetch_bits = [&](int k) {  // of the thread's vectors of tile k
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = column(min(wa + k * TV + u * ADJUST_THREADS + tid, wb - 1));
+      lo[u] = allowed[c >> 5];
+      hi[u] = allowed[(c + VE - 1) >> 5];
+    }
+  };
+  if (allowed && tiles) fetch_bits(0);
+  const AdjustRow rules(p, row);
+  __syncthreads();
+  auto value = [&](float v, int c) -> float {  // of a touched place
+    if constexpr (KIND == ADJUST_COUNTS) {
+      uint32_t at = c - s.c0;
+      if (s.table) {
+        at = adjust_hash(c, p.slots_log2);
+        while (s.key[at] != static_cast<uint32_t>(c)) at = (at + 1) & (s.words - 1);
+      }
+      return rules.value<KIND>(v, s.word[at], s.bsum);
+    } else if constexpr (GRAD) {
+      return rules.repeated(v, (s.positive[(c - s.first) >> 5] >> ((c - s.first) & 31)) & 1u);
+    } else {
+      return rules.repeated(v, v > 0.f);
+    }
+  };
+  bool ok = true;
+  int k = 0;
+  for (; k < tiles; ++k) {
+    uint4* data = reinterpret_cast<uint4*>(adj_stage + (k % stages) * TV * 16);
+    uint32_t m[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      m[u] = allowed ? __funnelshift_r(lo[u], hi[u], column(wa + k * TV + u * ADJUST_THREADS + tid) & 31) & ALL : ALL;
+    if (allowed && k + 1 < tiles) fetch_bits(k + 1);
+    ok = drain_phase(&full[k % stages], (k / stages) & 1, p.status);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = u * ADJUST_THREADS + tid, v = wa + k * TV + q;
+      if (v >= wb) break;
+      const int b = (v - s.v0) * VE;
+      uint32_t touched = (s.seen[b >> 5] >> (b & 31)) & ALL;
+      while (touched) {
+        const int j = __ffs(touched) - 1;
+        touched &= touched - 1;
+        T* at = reinterpret_cast<T*>(data + q) + j;
+        *at = from_f32<T>(value(to_f32(*at), column(v) + j));
+      }
+      if (m[u] != ALL) {
+        uint4 d = data[q];
+        d.x = masked_word<T, GRAD>(d.x, m[u], 0);
+        d.y = masked_word<T, GRAD>(d.y, m[u], 1);
+        d.z = masked_word<T, GRAD>(d.z, m[u], 2);
+        d.w = masked_word<T, GRAD>(d.w, m[u], 3);
+        data[q] = d;
+      }
+    }
+    fence_proxy_async_smem();
+    if (!__syncthreads_and(ok)) break;
+    if (tid == 0) {
+      const int v = wa + k * TV;
+      bulk_store(out + column(v), data, static_cast<uint32_t>(min(TV, wb - v)) * 16);
+      bulk_commit();
+      if (k >= 1 && k - 1 + stages < tiles) {  // the stage before this one has been read by its store
+        bulk_wait_read<1>();
+        load_tile(k - 1 + stages);
+      }
+    }
+  }
+  if (k < tiles) {  // a copy did not come: leave none under way
+    if (tid == 0)
+      for (int j = k + 1; j < min(tiles, max(k - 1, 0) + stages); ++j) drain_phase(&full[j % stages], (j / stages) & 1, p.status);
+  } else {
+    const int head = min(column(wa), p.V) - s.c0;  // values before the whole vectors, and after them
+    const int tail0 = max(column(wb), s.c0 + head), tail = max(0, s.c0 + s.columns - tail0);
+    if (tid < head + tail) {
+      const int c = tid < head ? s.c0 + tid : tail0 + tid - head, b = c - s.first;
+      T v = x[c];
+      if ((s.seen[b >> 5] >> (b & 31)) & 1u) v = from_f32<T>(value(to_f32(v), c));
+      if (allowed && !((allowed[c >> 5] >> (c & 31)) & 1u)) v = from_f32<T>(GRAD ? 0.f : -INFINITY);
+      out[c] = v;
+    }
+  }
+  if (tid == 0) bulk_wait_read<0>();
+}
+
+// In place, or into rows that lie differently: the segment is copied under the mask (in place: only vectors
+// that hold masked tokens are read or written), then the touched places are written again, each by one
+// thread, from the logits as they came in.
+template <typename T, int VE, AdjustKind KIND, bool IN_PLACE>
+__global__ void __launch_bounds__(ADJUST_THREADS, 5) adjust_kernel(const AdjustParams p) {
+  constexpr bool GRAD = KIND == ADJUST_GRAD;
+  extern __shared__ __align__(16) uint32_t adj_smem[];
+  const int64_t row = blockIdx.x / p.segs;
+  const int tid = threadIdx.x;
+  const T* x = GRAD ? static_cast<const T*>(p.g) + row * p.ld_g : static_cast<const T*>(p.z) + row * p.ld_z;
+  const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
+  T* out = static_cast<T*>(p.out) + row * p.ld_out;
+  const AdjustSegment s = adjust_segment<T, VE, KIND, false>(p, out, blockIdx.x % p.segs, adj_smem);
+  if (s.v0 >= s.v1) return;
+  const int mis = s.mis, v1 = s.v1;
+  adjust_gather<T, KIND, false>(p, s, row, z);
+  if (GRAD) __syncthreads();  // the logits' signs are read: out may be the logits
+
+  const uint32_t* allowed = p.allowed ? p.allowed + row * p.ld_allowed : nullptr;
+  const T none = from_f32<T>(GRAD ? 0.f : -INFINITY);
   auto bit = [&](int c) { return !allowed || ((allowed[c >> 5] >> (c & 31)) & 1u); };
-  for (int i = v0 + tid; i < v1; i += ADJUST_THREADS) {
-    const int c = i * VE - mis;
-    const uint32_t* w = word + (i - v0) * VE;
-    if (c < 0 || c + VE > p.V) {  // an end of the row
-      for (int j = 0; j < VE; ++j) {
-        if (c + j < 0 || c + j >= p.V) continue;
-        if (!bit(c + j)) out[c + j] = from_f32<T>(none);
-        else if (w[j]) out[c + j] = from_f32<T>(value(to_f32(x[c + j]), w[j], c + j));
-        else if (!IN_PLACE) out[c + j] = x[c + j];
+  constexpr uint32_t ALL = (1u << VE) - 1u;
+  constexpr int U = ADJUST_UNROLL;
+  using Raw = std::conditional_t<VE == 1, T, uint4>;
+  if (!IN_PLACE || allowed) {
+    for (int i0 = s.v0 + tid; i0 < v1; i0 += U * ADJUST_THREADS) {
+      // Every load of the step is issued before any of them is used.
+      Raw d[U];
+      uint32_t lo[U], hi[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * ADJUST_THREADS, c = i * VE - mis;
+        const bool whole = i < v1 && c >= 0 && c + VE <= p.V;
+        if (!IN_PLACE && whole) d[u] = *reinterpret_cast<const Raw*>(x + c);
+        lo[u] = hi[u] = ~0u;
+        if (allowed) {
+          const int at = whole ? c : 0;
+          lo[u] = allowed[at >> 5];
+          if (VE > 1) hi[u] = allowed[(at + (whole ? VE - 1 : 0)) >> 5];
+        }
       }
-      continue;
-    }
-    constexpr uint32_t ALL = (1u << VE) - 1u;
-    uint32_t m = ALL;
-    if (allowed) {
-      const int lo = c >> 5, hi = (c + VE - 1) >> 5;
-      m = __funnelshift_r(allowed[lo], hi > lo ? allowed[hi] : 0u, c & 31) & ALL;
-    }
-    uint32_t any = 0;
 #pragma unroll
-    for (int j = 0; j < VE; ++j) any |= w[j];
-    if (IN_PLACE && !any && m == ALL) continue;
-    using Vec = AdjustVec<T, VE>;
-    struct alignas(VE * sizeof(T)) Raw {
-      Vec v;
-    };
-    Raw d;
-    if (m) {
-      d = *reinterpret_cast<const Raw*>(x + c);
-      if (any) {
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * ADJUST_THREADS, c = i * VE - mis;
+        if (i >= v1) break;
+        if (c < 0 || c + VE > p.V) {  // an end of the row
+          for (int j = 0; j < VE; ++j) {
+            if (c + j < 0 || c + j >= p.V) continue;
+            if (!bit(c + j)) out[c + j] = none;
+            else if (!IN_PLACE) out[c + j] = x[c + j];
+          }
+          continue;
+        }
+        const uint32_t m = (VE > 1 ? __funnelshift_r(lo[u], hi[u], c & 31) : lo[u] >> (c & 31)) & ALL;
+        if (IN_PLACE) {
+          if (m == ALL) continue;
+          if (m) d[u] = *reinterpret_cast<const Raw*>(x + c);
+        }
+        if constexpr (VE == 1) {
+          if (!m) d[u] = none;
+        } else {
+          d[u].x = masked_word<T, GRAD>(d[u].x, m, 0);
+          d[u].y = masked_word<T, GRAD>(d[u].y, m, 1);
+          d[u].z = masked_word<T, GRAD>(d[u].z, m, 2);
+          d[u].w = masked_word<T, GRAD>(d[u].w, m, 3);
+        }
+        *reinterpret_cast<Raw*>(out + c) = d[u];
+      }
+    }
+  }
+  __syncthreads();
+
+  const AdjustRow rules(p, row);
+  const int places = s.table ? s.words : s.columns;
+  for (int i0 = tid; i0 < places; i0 += U * ADJUST_THREADS) {
+    uint32_t w[U];
+    int c[U];
+    float v[U];
 #pragma unroll
-        for (int j = 0; j < VE; ++j)
-          if (w[j]) d.v.v[j] = from_f32<T>(value(to_f32(d.v.v[j]), w[j], c + j));
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * ADJUST_THREADS;
+      w[u] = i < places ? s.word[i] : 0;
+      c[u] = !w[u] ? 0 : s.table ? static_cast<int>(s.key[i]) : s.c0 + i;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (w[u]) {
+        v[u] = to_f32(x[c[u]]);
+        if (!bit(c[u])) w[u] = 0;
       }
     }
 #pragma unroll
-    for (int j = 0; j < VE; ++j)
-      if (!((m >> j) & 1u)) d.v.v[j] = from_f32<T>(none);
-    *reinterpret_cast<Raw*>(out + c) = d;
+    for (int u = 0; u < U; ++u)
+      if (w[u]) out[c[u]] = from_f32<T>(rules.value<KIND>(v[u], w[u], s.bsum));
   }
 }
 

@@ -8,7 +8,10 @@
 namespace fckl {
 namespace {
 
-constexpr int ADJUST_SEG_WORDS = 16384;  // words of a segment at most: 64 KB of shared memory
+constexpr int ADJUST_SEG_WORDS = 16384;   // tokens of a segment at most where each has a word (64 KB)
+constexpr int ADJUST_STAGED_WORDS = 8192; // and beside the ring of stages (32 KB)
+constexpr int ADJUST_SEG_BITS = 1 << 18;  // and where each has a bit (32 KB)
+constexpr int ADJUST_TABLE_MAX = 4096;    // slots of the table of touched tokens at most (32 KB)
 
 int adjust_checks(const void* x, int dt, int64_t ld, const AdjustParams& p, int64_t N) {
   if (N < 0 || p.V < 1 || p.L < 0 || p.B < 0 || ld < p.V || p.ld_out < p.V || p.ld_h < p.L || !known_dtype(dt))
@@ -29,16 +32,42 @@ int adjust_checks(const void* x, int dt, int64_t ld, const AdjustParams& p, int6
   return FCKL_OK;
 }
 
-template <typename T, int VE, bool GRAD, bool IN_PLACE>
+// Segments of a row of nvec vectors: at most `most` vectors each, and where rows alone leave SMs idle
+// shorter ones, of at least 2048 tokens.
+int adjust_segments(const DevInfo* di, int64_t N, int64_t nvec, int ve, int64_t most) {
+  int64_t segs = cdiv(nvec, most);
+  while (N * segs < 4 * int64_t(di->sms) && nvec * ve / (2 * segs) >= 2048) segs *= 2;
+  return static_cast<int>(segs);
+}
+
+template <typename T, int VE, AdjustKind KIND, bool IN_PLACE, bool STAGED>
 int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s) {
+  constexpr bool GRAD = KIND == ADJUST_GRAD;
+  constexpr bool WORDS = !STAGED || KIND == ADJUST_COUNTS;
   const int64_t nvec = cdiv(int64_t(p.V) + VE - 1, VE);
-  // Segments small enough for shared memory, and where rows alone leave SMs idle at least 2048 words.
-  p.segs = static_cast<int>(cdiv(nvec * VE, ADJUST_SEG_WORDS));
-  while (N * p.segs < 4 * int64_t(di->sms) && nvec * VE / (2 * p.segs) >= 2048) p.segs *= 2;
+  // The table is at most three quarters full.
+  const int64_t entries = int64_t(p.L) + p.B;
+  p.slots_log2 = 8;
+  while ((int64_t(3) << p.slots_log2) < 4 * entries) ++p.slots_log2;
+  const bool table = (1 << p.slots_log2) <= ADJUST_TABLE_MAX;
+  if (!table) p.slots_log2 = -1;
+  if (STAGED)
+    p.segs = adjust_segments(di, N, nvec, VE, (table || !WORDS ? ADJUST_SEG_BITS : ADJUST_STAGED_WORDS) / VE);
+  else if (IN_PLACE && !p.allowed && table)
+    p.segs = 1;  // places touched here and there: the row stays whole
+  else
+    p.segs = adjust_segments(di, N, nvec, VE, (table ? 2 * ADJUST_SEG_WORDS : ADJUST_SEG_WORDS) / VE);
   p.seg_vecs = static_cast<int>(rup(cdiv(nvec, p.segs), 4));
-  const size_t smem = size_t(p.seg_vecs) * VE * 4 + size_t(p.B) * 12;
-  constexpr size_t SMEM_MAX = size_t(ADJUST_SEG_WORDS + 64) * 4 + size_t(TOKENS_MAX) * 12;
-  auto k = adjust_kernel<T, VE, GRAD, IN_PLACE>;
+  p.stages = static_cast<int>(std::min<int64_t>(ADJUST_STAGES, cdiv(p.seg_vecs, ADJUST_STAGE_VECS)));
+  size_t smem = size_t(p.B) * 12;
+  if (WORDS) smem += (table ? size_t(2) << p.slots_log2 : size_t(p.seg_vecs) * VE) * 4;
+  if (STAGED) smem += size_t(p.stages) * ADJUST_STAGE_VECS * 16 + (GRAD ? 2 : 1) * size_t(rup(int64_t(p.seg_vecs) * VE, 128)) / 8;
+  constexpr size_t SMEM_MAX = size_t(TOKENS_MAX) * 12 + (STAGED ? size_t(ADJUST_STAGES) * ADJUST_STAGE_VECS * 16 +
+                                                                     2 * size_t(ADJUST_SEG_BITS + 256) / 8 + 32768 + 1024
+                                                               : size_t(ADJUST_SEG_WORDS + 64) * 4);
+  void (*k)(AdjustParams);
+  if constexpr (STAGED) k = adjust_staged_kernel<T, KIND>;
+  else k = adjust_kernel<T, VE, KIND, IN_PLACE>;
   {
     static bool done[64] = {};
     std::lock_guard<std::mutex> lk(g_setup_mu);
@@ -75,24 +104,26 @@ int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s)
   return FCKL_OK;
 }
 
-// Whole vectors where every row of the input and of the output lies alike to the 16-byte boundaries.
-template <typename T, bool GRAD>
+// Through shared memory where every row of the input and of the output lies alike to the 16-byte boundaries.
+template <typename T, AdjustKind KIND>
 int launch_adjust(DevInfo* di, const AdjustParams& p, int64_t N, cudaStream_t s) {
+  constexpr bool GRAD = KIND == ADJUST_GRAD;
+  constexpr AdjustKind FULL = GRAD ? ADJUST_GRAD : ADJUST_COUNTS;
   const void* x = GRAD ? p.g : p.z;
   const int64_t ld = GRAD ? p.ld_g : p.ld_z;
   constexpr int VE = 16 / sizeof(T);
-  if (x == p.out) return launch_adjust_kernel<T, VE, GRAD, true>(di, p, N, s);
+  if (x == p.out) return launch_adjust_kernel<T, VE, FULL, true, false>(di, p, N, s);
   const bool alike = (reinterpret_cast<uintptr_t>(x) & 15u) == (reinterpret_cast<uintptr_t>(p.out) & 15u) &&
                      (N == 1 || (ld - p.ld_out) % VE == 0);
-  if (alike) return launch_adjust_kernel<T, VE, GRAD, false>(di, p, N, s);
-  return launch_adjust_kernel<T, 1, GRAD, false>(di, p, N, s);
+  if (alike) return launch_adjust_kernel<T, VE, KIND, false, true>(di, p, N, s);
+  return launch_adjust_kernel<T, 1, FULL, false, false>(di, p, N, s);
 }
 
-template <bool GRAD>
+template <AdjustKind KIND>
 int launch_adjust_type(DevInfo* di, int dt, const AdjustParams& p, int64_t N, cudaStream_t s) {
-  if (dt == FCKL_BF16) return launch_adjust<__nv_bfloat16, GRAD>(di, p, N, s);
-  if (dt == FCKL_F16) return launch_adjust<__half, GRAD>(di, p, N, s);
-  return launch_adjust<float, GRAD>(di, p, N, s);
+  if (dt == FCKL_BF16) return launch_adjust<__nv_bfloat16, KIND>(di, p, N, s);
+  if (dt == FCKL_F16) return launch_adjust<__half, KIND>(di, p, N, s);
+  return launch_adjust<float, KIND>(di, p, N, s);
 }
 
 }  // namespace
@@ -137,7 +168,9 @@ int fckl_adjust_logits(const void* logits, int dtype, int64_t ld, int64_t N, int
     if (N == 0) return FCKL_OK;
     DevInfo* di = nullptr;
     if ((st = device_info(&di))) return st;
-    return launch_adjust_type<false>(di, dtype, p, N, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool counts = frequency || presence || frequency_all != 0.f || presence_all != 0.f || B > 0;
+    return counts ? launch_adjust_type<ADJUST_COUNTS>(di, dtype, p, N, s) : launch_adjust_type<ADJUST_SEEN>(di, dtype, p, N, s);
   });
 }
 
@@ -174,7 +207,7 @@ int fckl_adjust_logits_backward(const void* g, int dtype, int64_t ld_g, const vo
     if (logits == out && ld != ld_out) return FCKL_ERR_ARG;
     DevInfo* di = nullptr;
     if ((st = device_info(&di))) return st;
-    return launch_adjust_type<true>(di, dtype, p, N, static_cast<cudaStream_t>(stream));
+    return launch_adjust_type<ADJUST_GRAD>(di, dtype, p, N, static_cast<cudaStream_t>(stream));
   });
 }
 
