@@ -18,9 +18,11 @@ namespace fckl {
 
 constexpr int ADJUST_THREADS = 256;
 constexpr int ADJUST_UNROLL = 4;      // vectors that a thread has under way
-constexpr int ADJUST_AHEAD = 4;       // history entries that a thread has under way
-constexpr int ADJUST_STAGES = 4;      // of the staged kernel's ring
-constexpr int ADJUST_STAGE_VECS = 1024;  // vectors of a stage (16 KB)
+constexpr int ADJUST_AHEAD = 8;       // history entries that a thread has under way
+constexpr int ADJUST_STAGED_THREADS = 512;
+constexpr int ADJUST_STAGES = 3;       // of each warp's ring in the staged kernel at most
+constexpr int ADJUST_STAGE_VECS = 96;  // vectors of a stage (1.5 KB)
+constexpr int ADJUST_RING_BYTES = ADJUST_STAGED_THREADS / 32 * ADJUST_STAGE_VECS * 16;  // of one stage of all warps
 
 // What a row's rules have to know of its history.
 enum AdjustKind {
@@ -70,7 +72,7 @@ struct AdjustParams {
   int64_t ld_allowed;
   int V;
   int segs, seg_vecs;  // segments of a row, vectors of a segment
-  int stages;          // of the staged kernel
+  int stages;          // of a warp's ring in the staged kernel
   int slots_log2;      // of the table of touched tokens; < 0: one word for every token of the segment
   unsigned* status;
 };
@@ -132,7 +134,7 @@ __device__ __forceinline__ uint32_t adjust_hash(int token, int log2) {
 // a hash table of token ids where those are few, so that its size does not depend on V, else in a word for
 // every token. With BITS a set of bits says which tokens are touched (and in a gradient a second one
 // which logits are above 0). Complete after the caller's next barrier.
-template <typename T, AdjustKind KIND, bool BITS>
+template <typename T, AdjustKind KIND, bool BITS, int NT>
 __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const AdjustSegment& s, int64_t row, const T* z) {
   const int tid = threadIdx.x;
   const int len = p.lengths ? min(max(p.lengths[row], 0), p.L) : p.L;
@@ -140,10 +142,10 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
   const int32_t* h = p.history + row * p.ld_h;
   const uint4 zero = make_uint4(0, 0, 0, 0), no_key = make_uint4(ADJ_NO_KEY, ADJ_NO_KEY, ADJ_NO_KEY, ADJ_NO_KEY);
   const int clear = ((KIND == ADJUST_GRAD ? 2 : 1) * s.bits + s.words) / 4;
-  for (int i = tid; i < clear; i += ADJUST_THREADS) reinterpret_cast<uint4*>(s.seen)[i] = zero;
+  for (int i = tid; i < clear; i += NT) reinterpret_cast<uint4*>(s.seen)[i] = zero;
   if (s.table)
-    for (int i = tid; i < s.words / 4; i += ADJUST_THREADS) reinterpret_cast<uint4*>(s.key)[i] = no_key;
-  for (int b = tid; b < p.B; b += ADJUST_THREADS) {
+    for (int i = tid; i < s.words / 4; i += NT) reinterpret_cast<uint4*>(s.key)[i] = no_key;
+  for (int b = tid; b < p.B; b += NT) {
     s.btok[b] = p.bias_tokens[row * p.B + b];
     s.bval[b] = p.bias[row * p.B + b];
   }
@@ -170,11 +172,11 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
   };
   bool bad = false;
   constexpr int A = ADJUST_AHEAD;
-  for (int i0 = tid; i0 < len; i0 += A * ADJUST_THREADS) {
+  for (int i0 = tid; i0 < len; i0 += A * NT) {
     int t[A];
     T sign[A];
 #pragma unroll
-    for (int u = 0; u < A; ++u) t[u] = i0 + u * ADJUST_THREADS < len ? h[i0 + u * ADJUST_THREADS] : -1;
+    for (int u = 0; u < A; ++u) t[u] = i0 + u * NT < len ? h[i0 + u * NT] : -1;
 #pragma unroll
     for (int u = 0; u < A; ++u) {
       if (static_cast<unsigned>(t[u]) >= static_cast<unsigned>(p.V)) {
@@ -185,7 +187,7 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
       } else if (KIND == ADJUST_COUNTS) {
         if (BITS) mark(s.seen, t[u]);
         uint32_t* w = place(t[u]);
-        if (i0 + u * ADJUST_THREADS >= prompt) atomicAdd(w, 1u);
+        if (i0 + u * NT >= prompt) atomicAdd(w, 1u);
         else atomicOr(w, ADJ_GIVEN);
       } else {
         const bool is_new = BITS ? mark(s.seen, t[u]) : atomicOr(place(t[u]), ADJ_GIVEN) == 0;
@@ -203,7 +205,7 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
     }
   }
   // The first slot of a token takes the sum over its slots, in their order.
-  for (int b = tid; b < p.B; b += ADJUST_THREADS) {
+  for (int b = tid; b < p.B; b += NT) {
     const int t = s.btok[b];
     if (static_cast<unsigned>(t) >= static_cast<unsigned>(p.V)) {
       bad |= t != -1;
@@ -251,51 +253,64 @@ struct AdjustRow {
 };
 
 // Into another tensor whose rows lie alike to the 16-byte boundaries. One block per (row, segment of
-// seg_vecs vectors). The segment streams through a ring of stages in shared memory by bulk copies, which are
-// under way while the threads gather the segment's touched tokens; the threads change the touched and the
-// masked places in the stages, so that what no rule touches passes through no register and a touched
-// place costs no access to memory. Two blocks an SM: one gathers while the other streams.
+// seg_vecs vectors). The segment streams through shared memory by bulk copies, which are under way while
+// the threads gather the segment's touched tokens: every warp has a ring of stages of its own, so that no
+// barrier of the block stands in the stream. The threads change the touched and the masked places in the
+// stages: what no rule touches passes through no register, and a touched place costs no access to
+// memory. Two blocks an SM: one gathers while the other streams.
 template <typename T, AdjustKind KIND>
-__global__ void __launch_bounds__(ADJUST_THREADS) adjust_staged_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(ADJUST_STAGED_THREADS) adjust_staged_kernel(const AdjustParams p) {
   constexpr int VE = 16 / sizeof(T);
-  constexpr int TV = ADJUST_STAGE_VECS, S = ADJUST_STAGES;
-  constexpr int U = TV / ADJUST_THREADS;
+  constexpr int NT = ADJUST_STAGED_THREADS, WARPS = NT / 32, TV = ADJUST_STAGE_VECS;
+  constexpr int U = TV / 32;
   constexpr uint32_t ALL = (1u << VE) - 1u;
   constexpr bool GRAD = KIND == ADJUST_GRAD;
   extern __shared__ __align__(128) uint8_t adj_stage[];
-  __shared__ uint64_t full[S];
+  __shared__ uint64_t bars[WARPS][ADJUST_STAGES];
   const int64_t row = blockIdx.x / p.segs;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const T* x = GRAD ? static_cast<const T*>(p.g) + row * p.ld_g : static_cast<const T*>(p.z) + row * p.ld_z;
   const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
   T* out = static_cast<T*>(p.out) + row * p.ld_out;
   const AdjustSegment s = adjust_segment<T, VE, KIND, true>(p, out, blockIdx.x % p.segs,
-                                                            reinterpret_cast<uint32_t*>(adj_stage + p.stages * TV * 16));
+                                                            reinterpret_cast<uint32_t*>(adj_stage + p.stages * ADJUST_RING_BYTES));
   if (s.v0 >= s.v1) return;
-  // whole vectors [wa, wb), in tiles of a stage; the row's ends, if they are ragged, go value by value
+  // Whole vectors [wa, wb), in tiles of a stage that the warps take in turn; the row's ends, if they are
+  // ragged, go value by value.
   const int wa = s.v0 + (s.first < 0), wb = max(wa, s.v1 - (s.v1 * VE - s.mis > p.V));
-  const int tiles = (wb - wa + TV - 1) / TV, stages = p.stages;
+  const int all_tiles = (wb - wa + TV - 1) / TV;
+  const int tiles = all_tiles > warp ? (all_tiles - warp + WARPS - 1) / WARPS : 0;  // of this warp
+  const int stages = p.stages;
+  uint64_t* full = bars[warp];
+  uint8_t* ring = adj_stage + warp * stages * TV * 16;
   auto column = [&](int v) { return v * VE - s.mis; };
-  auto load_tile = [&](int k) {
-    const int v = wa + k * TV;
-    const uint32_t bytes = static_cast<uint32_t>(min(TV, wb - v)) * 16;
-    mbar_arrive_expect_tx(&full[k % stages], bytes);
-    bulk_load(adj_stage + (k % stages) * TV * 16, x + column(v), bytes, &full[k % stages]);
+  auto tile_at = [&](int k) { return wa + (k * WARPS + warp) * TV; };
+  auto tile_bytes = [&](int k) { return static_cast<uint32_t>(min(TV, wb - tile_at(k))) * 16; };
+  auto load_tile = [&](int k, int stage) {
+    mbar_arrive_expect_tx(&full[stage], tile_bytes(k));
+    bulk_load(ring + stage * TV * 16, x + column(tile_at(k)), tile_bytes(k), &full[stage]);
   };
-  if (tid == 0) {
-    for (int k = 0; k < S; ++k) mbar_init(&full[k], 1);
+  if (lane == 0) {
+    for (int k = 0; k < stages; ++k) mbar_init(&full[k], 1);
     fence_mbar_init();
-    for (int k = 0; k < min(stages, tiles); ++k) load_tile(k);
+    for (int k = 0; k < min(stages, tiles); ++k) load_tile(k, k);
   }
-  adjust_gather<T, KIND, true>(p, s, row, z);
+  adjust_gather<T, KIND, true, NT>(p, s, row, z);
   const uint32_t* allowed = p.allowed ? p.allowed + row * p.ld_allowed : nullptr;
+  // A lane's vectors lie 32 apart, a multiple of 32 values: one shift serves them all, for the mask's bits
+  // and for the touched ones, and their words are at fixed distances.
+  const int own = column(tile_at(0) + lane), mask_shift = own & 31;
+  const uint32_t* mask_lo = allowed + (own >> 5);
+  const uint32_t* mask_hi = allowed + ((own + VE - 1) >> 5);
+  const int seen_at = (tile_at(0) - s.v0 + lane) * VE, seen_shift = seen_at & 31;
+  const uint32_t* seen = s.seen + (seen_at >> 5);
   uint32_t lo[U], hi[U];
-  auto fetch_bits = [&](int k) {  // of the thread's vectors of tile k
+  auto fetch_bits = [&](int k) {  // of the lane's vectors of tile k
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = column(min(wa + k * TV + u * ADJUST_THREADS + tid, wb - 1));
-      lo[u] = allowed[c >> 5];
-      hi[u] = allowed[(c + VE - 1) >> 5];
+      const bool in = tile_at(k) + u * 32 + lane < wb;
+      lo[u] = in ? mask_lo[(k * WARPS * U + u) * VE] : 0;
+      hi[u] = in ? mask_hi[(k * WARPS * U + u) * VE] : 0;
     }
   };
   if (allowed && tiles) fetch_bits(0);
@@ -315,64 +330,73 @@ __global__ void __launch_bounds__(ADJUST_THREADS) adjust_staged_kernel(const Adj
       return rules.repeated(v, v > 0.f);
     }
   };
-  bool ok = true;
-  int k = 0;
+  int k = 0, stage = 0, before = stages - 1;
+  uint32_t phase = 0;
   for (; k < tiles; ++k) {
-    uint4* data = reinterpret_cast<uint4*>(adj_stage + (k % stages) * TV * 16);
-    uint32_t m[U];
+    uint4* data = reinterpret_cast<uint4*>(ring + stage * TV * 16);
+    uint32_t off[U];  // places that are not allowed
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      m[u] = allowed ? __funnelshift_r(lo[u], hi[u], column(wa + k * TV + u * ADJUST_THREADS + tid) & 31) & ALL : ALL;
+    for (int u = 0; u < U; ++u) off[u] = allowed ? ~__funnelshift_r(lo[u], hi[u], mask_shift) & ALL : 0u;
     if (allowed && k + 1 < tiles) fetch_bits(k + 1);
-    ok = drain_phase(&full[k % stages], (k / stages) & 1, p.status);
+    const bool ok = drain_phase(&full[stage], phase, p.status);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int q = u * ADJUST_THREADS + tid, v = wa + k * TV + q;
+      const int q = u * 32 + lane, v = tile_at(k) + q;
       if (v >= wb) break;
-      const int b = (v - s.v0) * VE;
-      uint32_t touched = (s.seen[b >> 5] >> (b & 31)) & ALL;
+      T* at = reinterpret_cast<T*>(data + q);
+      uint32_t touched = (seen[(k * WARPS * U + u) * VE] >> seen_shift) & ALL & ~off[u];
       while (touched) {
         const int j = __ffs(touched) - 1;
         touched &= touched - 1;
-        T* at = reinterpret_cast<T*>(data + q) + j;
-        *at = from_f32<T>(value(to_f32(*at), column(v) + j));
+        at[j] = from_f32<T>(value(to_f32(at[j]), column(v) + j));
       }
-      if (m[u] != ALL) {
+      if (off[u] == ALL) {
+        const uint32_t none = GRAD ? 0u : fill_word<T>(-INFINITY);
+        data[q] = make_uint4(none, none, none, none);
+      } else if (__popc(off[u]) > 2) {
         uint4 d = data[q];
-        d.x = masked_word<T, GRAD>(d.x, m[u], 0);
-        d.y = masked_word<T, GRAD>(d.y, m[u], 1);
-        d.z = masked_word<T, GRAD>(d.z, m[u], 2);
-        d.w = masked_word<T, GRAD>(d.w, m[u], 3);
+        d.x = masked_word<T, GRAD>(d.x, ~off[u], 0);
+        d.y = masked_word<T, GRAD>(d.y, ~off[u], 1);
+        d.z = masked_word<T, GRAD>(d.z, ~off[u], 2);
+        d.w = masked_word<T, GRAD>(d.w, ~off[u], 3);
         data[q] = d;
+      } else {
+        while (off[u]) {
+          at[__ffs(off[u]) - 1] = from_f32<T>(GRAD ? 0.f : -INFINITY);
+          off[u] &= off[u] - 1;
+        }
       }
     }
     fence_proxy_async_smem();
-    if (!__syncthreads_and(ok)) break;
-    if (tid == 0) {
-      const int v = wa + k * TV;
-      bulk_store(out + column(v), data, static_cast<uint32_t>(min(TV, wb - v)) * 16);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    if (lane == 0) {
+      bulk_store(out + column(tile_at(k)), data, tile_bytes(k));
       bulk_commit();
-      if (k >= 1 && k - 1 + stages < tiles) {  // the stage before this one has been read by its store
+      if (k >= 1 && k - 1 + stages < tiles) {  // once the store of the stage before this one has read it
         bulk_wait_read<1>();
-        load_tile(k - 1 + stages);
+        load_tile(k - 1 + stages, before);
       }
     }
-  }
-  if (k < tiles) {  // a copy did not come: leave none under way
-    if (tid == 0)
-      for (int j = k + 1; j < min(tiles, max(k - 1, 0) + stages); ++j) drain_phase(&full[j % stages], (j / stages) & 1, p.status);
-  } else {
-    const int head = min(column(wa), p.V) - s.c0;  // values before the whole vectors, and after them
-    const int tail0 = max(column(wb), s.c0 + head), tail = max(0, s.c0 + s.columns - tail0);
-    if (tid < head + tail) {
-      const int c = tid < head ? s.c0 + tid : tail0 + tid - head, b = c - s.first;
-      T v = x[c];
-      if ((s.seen[b >> 5] >> (b & 31)) & 1u) v = from_f32<T>(value(to_f32(v), c));
-      if (allowed && !((allowed[c >> 5] >> (c & 31)) & 1u)) v = from_f32<T>(GRAD ? 0.f : -INFINITY);
-      out[c] = v;
+    before = stage;
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
     }
   }
-  if (tid == 0) bulk_wait_read<0>();
+  if (k < tiles && lane == 0) {  // a copy did not come: leave none under way
+    for (int j = k + 1; j < min(tiles, max(k - 1, 0) + stages); ++j)
+      drain_phase(&full[j % stages], (j / stages) & 1, p.status);
+  }
+  const int head = min(column(wa), p.V) - s.c0;  // values before the whole vectors, and after them
+  const int tail0 = max(column(wb), s.c0 + head), tail = max(0, s.c0 + s.columns - tail0);
+  if (tid < head + tail) {
+    const int c = tid < head ? s.c0 + tid : tail0 + tid - head, b = c - s.first;
+    T v = x[c];
+    if ((s.seen[b >> 5] >> (b & 31)) & 1u) v = from_f32<T>(value(to_f32(v), c));
+    if (allowed && !((allowed[c >> 5] >> (c & 31)) & 1u)) v = from_f32<T>(GRAD ? 0.f : -INFINITY);
+    out[c] = v;
+  }
+  if (lane == 0) bulk_wait_read<0>();
 }
 
 // In place, or into rows that lie differently: the segment is copied under the mask (in place: only vectors
@@ -390,7 +414,7 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 5) adjust_kernel(const AdjustP
   const AdjustSegment s = adjust_segment<T, VE, KIND, false>(p, out, blockIdx.x % p.segs, adj_smem);
   if (s.v0 >= s.v1) return;
   const int mis = s.mis, v1 = s.v1;
-  adjust_gather<T, KIND, false>(p, s, row, z);
+  adjust_gather<T, KIND, false, ADJUST_THREADS>(p, s, row, z);
   if (GRAD) __syncthreads();  // the logits' signs are read: out may be the logits
 
   const uint32_t* allowed = p.allowed ? p.allowed + row * p.ld_allowed : nullptr;

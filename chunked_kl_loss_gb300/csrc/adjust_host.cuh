@@ -9,7 +9,6 @@ namespace fckl {
 namespace {
 
 constexpr int ADJUST_SEG_WORDS = 16384;   // tokens of a segment at most where each has a word (64 KB)
-constexpr int ADJUST_STAGED_WORDS = 8192; // and beside the ring of stages (32 KB)
 constexpr int ADJUST_SEG_BITS = 1 << 18;  // and where each has a bit (32 KB)
 constexpr int ADJUST_TABLE_MAX = 4096;    // slots of the table of touched tokens at most (32 KB)
 
@@ -40,6 +39,41 @@ int adjust_segments(const DevInfo* di, int64_t N, int64_t nvec, int ve, int64_t 
   return static_cast<int>(segs);
 }
 
+// Stages of a warp's ring: with a word for every token two leave room for a second block on the SM.
+int adjust_stages(int slots_log2, bool words) { return words && slots_log2 < 0 ? 2 : ADJUST_STAGES; }
+
+// Shared memory of a staged block.
+size_t adjust_staged_smem(int64_t seg_vecs, int ve, int slots_log2, bool words, bool grad, int B) {
+  const int64_t tokens = seg_vecs * ve;
+  size_t n = size_t(adjust_stages(slots_log2, words)) * ADJUST_RING_BYTES + (grad ? 2 : 1) * size_t(rup(tokens, 128)) / 8 + size_t(B) * 12;
+  if (words) n += slots_log2 >= 0 ? size_t(8) << slots_log2 : size_t(tokens) * 4;
+  return n;
+}
+
+// Segments of a row in the staged kernel: the number with the least estimated time, in us: waves of blocks
+// that each gather first (2.5 us, and 1 us for every 8 history entries a thread) and then stream at their
+// share of an SM's 44 GB/s.
+int adjust_staged_segments(const DevInfo* di, int64_t N, int64_t nvec, int ve, int slots_log2, bool words, bool grad,
+                           int B, int64_t L) {
+  const int64_t most = words && slots_log2 < 0 ? ADJUST_SEG_WORDS : ADJUST_SEG_BITS;
+  const int64_t least = cdiv(nvec * ve, most);
+  int64_t best = least;
+  double best_us = 1e30;
+  for (int64_t segs = least; segs < least + 64 && (segs == least || nvec * ve / segs >= 2048); ++segs) {
+    const int64_t vecs = rup(cdiv(nvec, segs), 4);
+    const int64_t resident = std::min<int64_t>(3, (227 << 10) / int64_t(adjust_staged_smem(vecs, ve, slots_log2, words, grad, B) + 2048));
+    const int64_t slots = resident * di->sms, blocks = N * segs;
+    const double gather = 2.5 + double(cdiv(L, ADJUST_STAGED_THREADS * 8));
+    const int64_t on_sm = std::min(resident, cdiv(blocks, di->sms));
+    const double us = double(cdiv(blocks, slots)) * (gather + double(vecs) * 32.0 * double(on_sm) / 44e3);
+    if (us < 0.98 * best_us) {
+      best_us = us;
+      best = segs;
+    }
+  }
+  return static_cast<int>(best);
+}
+
 template <typename T, int VE, AdjustKind KIND, bool IN_PLACE, bool STAGED>
 int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s) {
   constexpr bool GRAD = KIND == ADJUST_GRAD;
@@ -52,19 +86,19 @@ int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s)
   const bool table = (1 << p.slots_log2) <= ADJUST_TABLE_MAX;
   if (!table) p.slots_log2 = -1;
   if (STAGED)
-    p.segs = adjust_segments(di, N, nvec, VE, (table || !WORDS ? ADJUST_SEG_BITS : ADJUST_STAGED_WORDS) / VE);
+    p.segs = adjust_staged_segments(di, N, nvec, VE, p.slots_log2, WORDS, GRAD, p.B, p.L);
   else if (IN_PLACE && !p.allowed && table)
     p.segs = 1;  // places touched here and there: the row stays whole
   else
     p.segs = adjust_segments(di, N, nvec, VE, (table ? 2 * ADJUST_SEG_WORDS : ADJUST_SEG_WORDS) / VE);
   p.seg_vecs = static_cast<int>(rup(cdiv(nvec, p.segs), 4));
-  p.stages = static_cast<int>(std::min<int64_t>(ADJUST_STAGES, cdiv(p.seg_vecs, ADJUST_STAGE_VECS)));
-  size_t smem = size_t(p.B) * 12;
-  if (WORDS) smem += (table ? size_t(2) << p.slots_log2 : size_t(p.seg_vecs) * VE) * 4;
-  if (STAGED) smem += size_t(p.stages) * ADJUST_STAGE_VECS * 16 + (GRAD ? 2 : 1) * size_t(rup(int64_t(p.seg_vecs) * VE, 128)) / 8;
-  constexpr size_t SMEM_MAX = size_t(TOKENS_MAX) * 12 + (STAGED ? size_t(ADJUST_STAGES) * ADJUST_STAGE_VECS * 16 +
-                                                                     2 * size_t(ADJUST_SEG_BITS + 256) / 8 + 32768 + 1024
+  p.stages = adjust_stages(p.slots_log2, WORDS);
+  const size_t smem = STAGED ? adjust_staged_smem(p.seg_vecs, VE, p.slots_log2, WORDS, GRAD, p.B)
+                             : (table ? size_t(8) << p.slots_log2 : size_t(p.seg_vecs) * VE * 4) + size_t(p.B) * 12;
+  constexpr size_t SMEM_MAX = size_t(TOKENS_MAX) * 12 + (STAGED ? ADJUST_STAGES * ADJUST_RING_BYTES + 2 * size_t(ADJUST_SEG_BITS + 256) / 8 +
+                                                                     size_t(ADJUST_SEG_WORDS + 64) * 4
                                                                : size_t(ADJUST_SEG_WORDS + 64) * 4);
+  static_assert(SMEM_MAX <= (226 << 10), "");
   void (*k)(AdjustParams);
   if constexpr (STAGED) k = adjust_staged_kernel<T, KIND>;
   else k = adjust_kernel<T, VE, KIND, IN_PLACE>;
@@ -98,7 +132,7 @@ int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s)
     if (p.allowed) q.allowed = p.allowed + r0 * p.ld_allowed;
     const unsigned grid = static_cast<unsigned>(rows * p.segs);
     int st = launch(GRAD ? KIND_ADJUST_GRAD : KIND_ADJUST, s, GRAD ? "adjust_logits_grad" : "adjust_logits",
-                    [&] { k<<<grid, ADJUST_THREADS, smem, s>>>(q); });
+                    [&] { k<<<grid, STAGED ? ADJUST_STAGED_THREADS : ADJUST_THREADS, smem, s>>>(q); });
     if (st) return st;
   }
   return FCKL_OK;
