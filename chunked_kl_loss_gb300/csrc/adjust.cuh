@@ -16,8 +16,8 @@
 
 namespace fckl {
 
-constexpr int ADJUST_THREADS = 256;
-constexpr int ADJUST_UNROLL = 4;      // vectors that a thread has under way
+constexpr int ADJUST_THREADS = 512;
+constexpr int ADJUST_UNROLL = 8;      // vectors that a thread has under way
 constexpr int ADJUST_AHEAD = 8;       // history entries that a thread has under way
 constexpr int ADJUST_STAGED_THREADS = 512;
 constexpr int ADJUST_STAGES = 3;       // of each warp's ring in the staged kernel at most
@@ -399,11 +399,12 @@ __global__ void __launch_bounds__(ADJUST_STAGED_THREADS) adjust_staged_kernel(co
   if (lane == 0) bulk_wait_read<0>();
 }
 
-// In place, or into rows that lie differently: the segment is copied under the mask (in place: only vectors
-// that hold masked tokens are read or written), then the touched places are written again, each by one
-// thread, from the logits as they came in.
+// In place, or into rows that lie differently: the segment is copied under the mask (in place: masked tokens
+// are written and nothing is read), then the touched places are written again, each by one thread, from the
+// logits as they came in.
 template <typename T, int VE, AdjustKind KIND, bool IN_PLACE>
-__global__ void __launch_bounds__(ADJUST_THREADS, 5) adjust_kernel(const AdjustParams p) {
+__global__ void __launch_bounds__(ADJUST_THREADS, 2) adjust_kernel(const AdjustParams p) {
+  static_assert(IN_PLACE || VE == 1, "");
   constexpr bool GRAD = KIND == ADJUST_GRAD;
   extern __shared__ __align__(16) uint32_t adj_smem[];
   const int64_t row = blockIdx.x / p.segs;
@@ -413,7 +414,6 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 5) adjust_kernel(const AdjustP
   T* out = static_cast<T*>(p.out) + row * p.ld_out;
   const AdjustSegment s = adjust_segment<T, VE, KIND, false>(p, out, blockIdx.x % p.segs, adj_smem);
   if (s.v0 >= s.v1) return;
-  const int mis = s.mis, v1 = s.v1;
   adjust_gather<T, KIND, false, ADJUST_THREADS>(p, s, row, z);
   if (GRAD) __syncthreads();  // the logits' signs are read: out may be the logits
 
@@ -422,50 +422,38 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 5) adjust_kernel(const AdjustP
   auto bit = [&](int c) { return !allowed || ((allowed[c >> 5] >> (c & 31)) & 1u); };
   constexpr uint32_t ALL = (1u << VE) - 1u;
   constexpr int U = ADJUST_UNROLL;
-  using Raw = std::conditional_t<VE == 1, T, uint4>;
   if (!IN_PLACE || allowed) {
-    for (int i0 = s.v0 + tid; i0 < v1; i0 += U * ADJUST_THREADS) {
+    for (int i0 = s.v0 + tid; i0 < s.v1; i0 += U * ADJUST_THREADS) {
       // Every load of the step is issued before any of them is used.
-      Raw d[U];
+      T d[U];
       uint32_t lo[U], hi[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * ADJUST_THREADS, c = i * VE - mis;
-        const bool whole = i < v1 && c >= 0 && c + VE <= p.V;
-        if (!IN_PLACE && whole) d[u] = *reinterpret_cast<const Raw*>(x + c);
+        const int i = i0 + u * ADJUST_THREADS, c = i * VE - s.mis;
+        if (!IN_PLACE && i < s.v1) d[u] = x[c];
         lo[u] = hi[u] = ~0u;
-        if (allowed) {
-          const int at = whole ? c : 0;
-          lo[u] = allowed[at >> 5];
-          if (VE > 1) hi[u] = allowed[(at + (whole ? VE - 1 : 0)) >> 5];
+        if (allowed && i < s.v1) {
+          lo[u] = allowed[max(c, 0) >> 5];
+          if (VE > 1) hi[u] = allowed[min(c + VE - 1, p.V - 1) >> 5];
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * ADJUST_THREADS, c = i * VE - mis;
-        if (i >= v1) break;
-        if (c < 0 || c + VE > p.V) {  // an end of the row
-          for (int j = 0; j < VE; ++j) {
-            if (c + j < 0 || c + j >= p.V) continue;
-            if (!bit(c + j)) out[c + j] = none;
-            else if (!IN_PLACE) out[c + j] = x[c + j];
-          }
-          continue;
-        }
-        const uint32_t m = (VE > 1 ? __funnelshift_r(lo[u], hi[u], c & 31) : lo[u] >> (c & 31)) & ALL;
-        if (IN_PLACE) {
-          if (m == ALL) continue;
-          if (m) d[u] = *reinterpret_cast<const Raw*>(x + c);
-        }
-        if constexpr (VE == 1) {
-          if (!m) d[u] = none;
+        const int i = i0 + u * ADJUST_THREADS, c = i * VE - s.mis;
+        if (i >= s.v1) break;
+        if constexpr (!IN_PLACE) {
+          out[c] = (lo[u] >> (c & 31)) & 1u ? d[u] : none;
         } else {
-          d[u].x = masked_word<T, GRAD>(d[u].x, m, 0);
-          d[u].y = masked_word<T, GRAD>(d[u].y, m, 1);
-          d[u].z = masked_word<T, GRAD>(d[u].z, m, 2);
-          d[u].w = masked_word<T, GRAD>(d[u].w, m, 3);
+          // before the row's start (c < 0) and behind its end nothing is masked
+          uint32_t off = c < 0 ? ~lo[u] << -c : ~__funnelshift_r(lo[u], hi[u], c & 31);
+          off &= ALL >> max(0, c + VE - p.V);
+          if (off == ALL) {
+            const uint32_t w = GRAD ? 0u : fill_word<T>(-INFINITY);
+            *reinterpret_cast<uint4*>(out + c) = make_uint4(w, w, w, w);
+          } else {
+            for (; off; off &= off - 1) out[c + __ffs(off) - 1] = none;
+          }
         }
-        *reinterpret_cast<Raw*>(out + c) = d[u];
       }
     }
   }

@@ -10,7 +10,8 @@ namespace {
 
 constexpr int ADJUST_SEG_WORDS = 16384;   // tokens of a segment at most where each has a word (64 KB)
 constexpr int ADJUST_SEG_BITS = 1 << 18;  // and where each has a bit (32 KB)
-constexpr int ADJUST_TABLE_MAX = 4096;    // slots of the table of touched tokens at most (32 KB)
+constexpr int ADJUST_TABLE_LOG2 = 14;     // slots of the table of touched tokens at most (128 KB)
+constexpr size_t ADJUST_SMEM = 226 << 10;
 
 int adjust_checks(const void* x, int dt, int64_t ld, const AdjustParams& p, int64_t N) {
   if (N < 0 || p.V < 1 || p.L < 0 || p.B < 0 || ld < p.V || p.ld_out < p.V || p.ld_h < p.L || !known_dtype(dt))
@@ -31,74 +32,64 @@ int adjust_checks(const void* x, int dt, int64_t ld, const AdjustParams& p, int6
   return FCKL_OK;
 }
 
-// Segments of a row of nvec vectors: at most `most` vectors each, and where rows alone leave SMs idle
-// shorter ones, of at least 2048 tokens.
-int adjust_segments(const DevInfo* di, int64_t N, int64_t nvec, int ve, int64_t most) {
-  int64_t segs = cdiv(nvec, most);
-  while (N * segs < 4 * int64_t(di->sms) && nvec * ve / (2 * segs) >= 2048) segs *= 2;
-  return static_cast<int>(segs);
-}
-
-// Stages of a warp's ring: with a word for every token two leave room for a second block on the SM.
-int adjust_stages(int slots_log2, bool words) { return words && slots_log2 < 0 ? 2 : ADJUST_STAGES; }
-
-// Shared memory of a staged block.
-size_t adjust_staged_smem(int64_t seg_vecs, int ve, int slots_log2, bool words, bool grad, int B) {
-  const int64_t tokens = seg_vecs * ve;
-  size_t n = size_t(adjust_stages(slots_log2, words)) * ADJUST_RING_BYTES + (grad ? 2 : 1) * size_t(rup(tokens, 128)) / 8 + size_t(B) * 12;
+// Shared memory of a block: a ring of stages (staged kernel), sets of bits, the table's or the tokens' words
+// and the biases.
+size_t adjust_smem(int64_t tokens, int stages, int sets, bool words, int slots_log2, int B) {
+  size_t n = size_t(stages) * ADJUST_RING_BYTES + sets * size_t(rup(tokens, 128)) / 8 + size_t(B) * 12;
   if (words) n += slots_log2 >= 0 ? size_t(8) << slots_log2 : size_t(tokens) * 4;
   return n;
 }
 
-// Segments of a row in the staged kernel: the number with the least estimated time, in us: waves of blocks
-// that each gather first (2.5 us, and 1 us for every 8 history entries a thread) and then stream at their
-// share of an SM's 44 GB/s.
-int adjust_staged_segments(const DevInfo* di, int64_t N, int64_t nvec, int ve, int slots_log2, bool words, bool grad,
-                           int B, int64_t L) {
-  const int64_t most = words && slots_log2 < 0 ? ADJUST_SEG_WORDS : ADJUST_SEG_BITS;
-  const int64_t least = cdiv(nvec * ve, most);
-  int64_t best = least;
-  double best_us = 1e30;
-  for (int64_t segs = least; segs < least + 64 && (segs == least || nvec * ve / segs >= 2048); ++segs) {
-    const int64_t vecs = rup(cdiv(nvec, segs), 4);
-    const int64_t resident = std::min<int64_t>(3, (227 << 10) / int64_t(adjust_staged_smem(vecs, ve, slots_log2, words, grad, B) + 2048));
-    const int64_t slots = resident * di->sms, blocks = N * segs;
-    const double gather = 2.5 + double(cdiv(L, ADJUST_STAGED_THREADS * 8));
-    const int64_t on_sm = std::min(resident, cdiv(blocks, di->sms));
-    const double us = double(cdiv(blocks, slots)) * (gather + double(vecs) * 32.0 * double(on_sm) / 44e3);
-    if (us < 0.98 * best_us) {
-      best_us = us;
-      best = segs;
+// How the work is cut: with the table of touched tokens or a word for each, into how many segments a row,
+// and with how many stages. Taken is the least estimated time, in us, of waves of blocks that each gather
+// first (2.5 us, 1 us for every 8 history entries a thread, 1 us for every 64 KB of shared memory cleared)
+// and then stream at their share of an SM's 44 GB/s. The estimates are within a third of what 20 shapes
+// measured; where they are near each other the first, with fewer segments, is taken.
+template <int VE, AdjustKind KIND, bool STAGED>
+size_t adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool streams) {
+  constexpr int NT = STAGED ? ADJUST_STAGED_THREADS : ADJUST_THREADS;
+  constexpr bool WORDS = !STAGED || KIND == ADJUST_COUNTS;
+  constexpr int SETS = STAGED ? (KIND == ADJUST_GRAD ? 2 : 1) : 0;
+  const int64_t nvec = cdiv(int64_t(p.V) + VE - 1, VE);
+  // The table is at most three quarters full.
+  int log2 = 8;
+  while ((int64_t(3) << log2) < 4 * (int64_t(p.L) + p.B)) ++log2;
+  double best = 1e30;
+  size_t best_smem = 0;
+  for (int way = 0; way < 2; ++way) {
+    const bool table = way == 0;
+    if (table ? log2 > ADJUST_TABLE_LOG2 : !WORDS && best_smem) continue;
+    const int64_t most = WORDS && !table ? ADJUST_SEG_WORDS : STAGED ? ADJUST_SEG_BITS : int64_t(1) << 31;
+    const int64_t least = cdiv(nvec * VE, most);
+    for (int64_t segs = least; segs < least + 64 && (segs == least || nvec * VE / segs >= 2048); ++segs) {
+      const int64_t vecs = rup(cdiv(nvec, segs), 4);
+      for (int stages = STAGED ? ADJUST_STAGES : 0; stages >= (STAGED ? 2 : 0); --stages) {
+        const size_t smem = adjust_smem(vecs * VE, stages, SETS, WORDS, table ? log2 : -1, p.B);
+        if (smem > ADJUST_SMEM) continue;
+        const int64_t resident = std::min<int64_t>(STAGED ? 3 : 2, (227 << 10) / int64_t(smem + 1536));
+        const int64_t blocks = N * segs, on_sm = std::min(resident, cdiv(blocks, di->sms));
+        const double gather = 2.5 + double(cdiv(p.L, NT * 8)) + double(smem - size_t(stages) * ADJUST_RING_BYTES) / 65536;
+        const double stream = streams ? double(vecs) * 32.0 * double(on_sm) / 44e3 * (stages == 2 ? 1.1 : 1.0) : 0.0;
+        const double us = double(cdiv(blocks, resident * di->sms)) * (gather + stream);
+        if (us < 0.98 * best) {
+          best = us;
+          best_smem = smem;
+          p.segs = static_cast<int>(segs);
+          p.seg_vecs = static_cast<int>(vecs);
+          p.stages = stages;
+          p.slots_log2 = table ? log2 : -1;
+        }
+        if (!STAGED) break;
+      }
     }
   }
-  return static_cast<int>(best);
+  return best_smem;
 }
 
 template <typename T, int VE, AdjustKind KIND, bool IN_PLACE, bool STAGED>
 int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s) {
   constexpr bool GRAD = KIND == ADJUST_GRAD;
-  constexpr bool WORDS = !STAGED || KIND == ADJUST_COUNTS;
-  const int64_t nvec = cdiv(int64_t(p.V) + VE - 1, VE);
-  // The table is at most three quarters full.
-  const int64_t entries = int64_t(p.L) + p.B;
-  p.slots_log2 = 8;
-  while ((int64_t(3) << p.slots_log2) < 4 * entries) ++p.slots_log2;
-  const bool table = (1 << p.slots_log2) <= ADJUST_TABLE_MAX;
-  if (!table) p.slots_log2 = -1;
-  if (STAGED)
-    p.segs = adjust_staged_segments(di, N, nvec, VE, p.slots_log2, WORDS, GRAD, p.B, p.L);
-  else if (IN_PLACE && !p.allowed && table)
-    p.segs = 1;  // places touched here and there: the row stays whole
-  else
-    p.segs = adjust_segments(di, N, nvec, VE, (table ? 2 * ADJUST_SEG_WORDS : ADJUST_SEG_WORDS) / VE);
-  p.seg_vecs = static_cast<int>(rup(cdiv(nvec, p.segs), 4));
-  p.stages = adjust_stages(p.slots_log2, WORDS);
-  const size_t smem = STAGED ? adjust_staged_smem(p.seg_vecs, VE, p.slots_log2, WORDS, GRAD, p.B)
-                             : (table ? size_t(8) << p.slots_log2 : size_t(p.seg_vecs) * VE * 4) + size_t(p.B) * 12;
-  constexpr size_t SMEM_MAX = size_t(TOKENS_MAX) * 12 + (STAGED ? ADJUST_STAGES * ADJUST_RING_BYTES + 2 * size_t(ADJUST_SEG_BITS + 256) / 8 +
-                                                                     size_t(ADJUST_SEG_WORDS + 64) * 4
-                                                               : size_t(ADJUST_SEG_WORDS + 64) * 4);
-  static_assert(SMEM_MAX <= (226 << 10), "");
+  const size_t smem = adjust_plan<VE, KIND, STAGED>(di, p, N, !IN_PLACE || p.allowed);
   void (*k)(AdjustParams);
   if constexpr (STAGED) k = adjust_staged_kernel<T, KIND>;
   else k = adjust_kernel<T, VE, KIND, IN_PLACE>;
@@ -106,7 +97,7 @@ int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s)
     static bool done[64] = {};
     std::lock_guard<std::mutex> lk(g_setup_mu);
     if (!done[di->id]) {
-      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_MAX));
+      cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ADJUST_SMEM));
       if (e != cudaSuccess) {
         set_error("cudaFuncSetAttribute(adjust)", e);
         return FCKL_ERR_CUDA;
