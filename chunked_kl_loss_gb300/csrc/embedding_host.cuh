@@ -49,6 +49,11 @@ int launch_embedding_pack(int e, const void* W, int64_t ldw, const int32_t* toke
 }
 
 // ------------------------------------------------------------------ gradient
+#ifndef SC_I
+#define SC_I 2048
+#endif
+constexpr int SORT_CTA_ITEMS = SC_I;  // positions of a sorting block, as long as the cluster can grow
+
 struct EmbedGradPlan {
   int passes, bits, cluster, per_cta;
   int tile, tiles;
@@ -63,7 +68,7 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   q.passes = static_cast<int>(cdiv(bits, SORT_BITS));
   q.bits = static_cast<int>(cdiv(bits, q.passes));
   q.cluster = 1;
-  while (q.cluster < 8 && int64_t(q.cluster) * SORT_TILE < N) q.cluster *= 2;
+  while (q.cluster < 8 && int64_t(q.cluster) * SORT_CTA_ITEMS < N) q.cluster *= 2;
   q.per_cta = static_cast<int>(rup(cdiv(N, q.cluster), 32));
   q.tile = static_cast<int>(std::min<int64_t>(GSUM_TILE_MAX, std::max<int64_t>(8, N / 512)));
   q.tiles = static_cast<int>(cdiv(N, q.tile));
@@ -82,13 +87,15 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   return q;
 }
 
-int launch_sort_tokens(const EmbedGradPlan& q, const SortParams& p, cudaStream_t s) {
+int launch_sort_tokens(const DevInfo* di, const EmbedGradPlan& q, const SortParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(q.cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(q.cluster));
+  // two blocks an SM, and no more than have 64 KB to clear
+  const int64_t clear = std::min<int64_t>(cdiv(p.zero_bytes, 65536), 2 * int64_t(di->sms) - q.cluster);
+  cfg.gridDim = dim3(static_cast<unsigned>(q.cluster + rup(clear, q.cluster)));
   cfg.blockDim = dim3(SORT_THREADS);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -99,16 +106,14 @@ int launch_sort_tokens(const EmbedGradPlan& q, const SortParams& p, cudaStream_t
 template <typename T, typename O, int E, bool ADD>
 int launch_embedding_grad(EmbedGradParams p, cudaStream_t s) {
   p.slices = static_cast<int>(cdiv(p.d, GSUM_THREADS * E));
-  p.sum_blocks = int64_t(p.tiles) * p.slices;
-  p.fill_rows = 32;
-  const int64_t grid = p.sum_blocks + (ADD ? 0 : cdiv(p.V, p.fill_rows));
-  if (grid > INT_MAX) return FCKL_ERR_UNSUPPORTED;
-  int st = launch(KIND_EMBEDDING_GRAD, s, "embedding_grad", [&] {
-    embedding_grad_kernel<T, O, E, ADD><<<static_cast<unsigned>(grid), GSUM_THREADS, 0, s>>>(p);
-  });
+  const int64_t blocks = int64_t(p.tiles) * p.slices;
+  if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(blocks);
+  int st = launch(KIND_EMBEDDING_GRAD, s, "embedding_grad",
+                  [&] { embedding_grad_kernel<T, O, E, ADD><<<grid, GSUM_THREADS, 0, s>>>(p); });
   if (st || p.tiles < 2) return st;
   return launch(KIND_EMBEDDING_JOIN, s, "embedding_grad_join", [&] {
-    embedding_grad_join_kernel<O, E, ADD><<<static_cast<unsigned>(p.sum_blocks), GSUM_THREADS, 0, s>>>(p);
+    embedding_grad_join_kernel<O, E, ADD><<<grid, GSUM_THREADS * GJOIN_GROUPS, 0, s>>>(p);
   });
 }
 
@@ -203,7 +208,23 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
     sp.a = reinterpret_cast<uint2*>(w + q.off_a);
     sp.b = reinterpret_cast<uint2*>(w + q.off_b);
     sp.status = status;
-    if ((st = launch_sort_tokens(q, sp, s))) return st;
+    sp.cluster = q.cluster;
+    if (!accumulate) {
+      // whole 16-byte vectors from the first boundary on; what lies before it is short
+      sp.zero = static_cast<uint8_t*>(dW);
+      sp.zero_bytes = int64_t(V) * d * int64_t(bo);
+      const int64_t ahead = std::min<int64_t>(-reinterpret_cast<uintptr_t>(dW) & 15u, sp.zero_bytes);
+      if (ahead) {
+        cudaError_t e = cudaMemsetAsync(dW, 0, size_t(ahead), s);
+        if (e != cudaSuccess) {
+          set_error("cudaMemsetAsync", e);
+          return FCKL_ERR_CUDA;
+        }
+        sp.zero += ahead;
+        sp.zero_bytes -= ahead;
+      }
+    }
+    if ((st = launch_sort_tokens(di, q, sp, s))) return st;
     EmbedGradParams p{};
     p.list = q.passes & 1 ? sp.a : sp.b;
     p.N = static_cast<int>(N);
