@@ -6,8 +6,8 @@
 // The gradient's positions are first put in the order of their tokens, equal tokens in the order of
 // their positions (a radix sort by one cluster). Blocks then walk tiles of the ordered list, each over
 // its own columns: the rows of a token that begins and ends within a tile are summed in registers and
-// written once; a token that crosses a tile's edge leaves one partial sum per tile, and those are added
-// in a fixed order by a second kernel. So every row of dW has one writer, and the sums, all in
+// written once, as are those of a token that runs into the next tile and ends there; a longer run leaves
+// one partial sum per tile, and those are added in a fixed order by a second kernel. So every row of dW has one writer, and the sums, all in
 // fp32, one order: the same call gives the same bits.
 #pragma once
 
@@ -61,19 +61,24 @@ __global__ void __launch_bounds__(EMBED_THREADS)
 }
 
 // ---------------------------------------------------------------- positions in the order of their tokens
-constexpr int SORT_THREADS = 1024;
+#ifndef SO_T
+#define SO_T 512
+#endif
+constexpr int SORT_THREADS = SO_T;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_ITEMS = 8;                        // per thread and tile
+constexpr int SORT_ITEMS = 8192 / SORT_THREADS;                 // per thread and tile
 constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;
 constexpr int SORT_BITS = 9;                         // of a digit at most
 constexpr int SORT_BINS = 1 << SORT_BITS;
+
+static_assert(SORT_THREADS >= SORT_BINS, "a thread for every digit");
 
 struct SortParams {
   const int32_t* tokens;
   int N, V;
   int passes, bits;  // digits and bits of each
   int cluster;       // blocks that sort: the first cluster of the grid; the others write zeros
-  int per_cta;       // positions of one of them
+  int per_log2;      // positions of one of them: a power of two
   uint2* a;          // (token, position), written by the even passes
   uint2* b;          // and by the odd ones
   unsigned* status;
@@ -111,13 +116,15 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
   __shared__ unsigned place[SORT_BINS];                   // where its next item of a digit goes
   __shared__ unsigned sums[SORT_WARPS];
   __shared__ unsigned short wcount[SORT_WARPS][SORT_BINS];  // a tile's numbers per warp, then their ranks
+  extern __shared__ uint2 kept[];  // the items between two passes, if they fit
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int rank = cluster.block_rank(), blocks = p.cluster;
-  const int64_t begin64 = int64_t(rank) * p.per_cta;
+  const int64_t begin64 = int64_t(rank) << p.per_log2;
   const int begin = static_cast<int>(min(begin64, int64_t(p.N)));
-  const int end = static_cast<int>(min(begin64 + p.per_cta, int64_t(p.N)));
-  const bool one_tile = p.per_cta <= SORT_TILE;
-  const int items = one_tile ? (p.per_cta + SORT_THREADS - 1) / SORT_THREADS : SORT_ITEMS;  // rounds of a tile
+  const int end = static_cast<int>(min(begin64 + (int64_t(1) << p.per_log2), int64_t(p.N)));
+  const int per = 1 << p.per_log2;
+  const bool one_tile = per <= SORT_TILE;
+  const int items = one_tile ? (per + SORT_THREADS - 1) / SORT_THREADS : SORT_ITEMS;  // rounds of a tile
   bool bad = false;
   if (rank == 0 && tid == 0) *p.status = 0;
   for (int pass = 0; pass < p.passes; ++pass) {
@@ -125,8 +132,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
     const unsigned dmask = bins - 1;
     const uint2* from = pass & 1 ? p.a : p.b;
     uint2* to = pass & 1 ? p.b : p.a;
+    const bool last = pass + 1 == p.passes;
     auto item = [&](int i) -> uint2 {
-      if (pass) return from[i];
+      if (pass) return one_tile ? kept[i - begin] : from[i];
       const int t = p.tokens[i];
       bad |= t < -1 || t >= p.V;
       return make_uint2(t >= 0 && t < p.V ? t : p.V, i);
@@ -174,7 +182,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
         const int i = t0 + (warp * items + k) * 32 + lane;
         if (k < items && i < end) {
           const unsigned digit = (x[k].x >> shift) & dmask;
-          to[place[digit] + wcount[warp][digit] + order[k]] = x[k];
+          const unsigned at = place[digit] + wcount[warp][digit] + order[k];
+          if (last || !one_tile) to[at] = x[k];
+          else cluster.map_shared_rank(kept, at >> p.per_log2)[at & (per - 1)] = x[k];
         }
       }
     };
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
         if (tid < bins) place[tid] += in_tile;
       }
     }
-    __threadfence();
+    if (!one_tile) __threadfence();
     cluster.sync();  // the pass is written, and every block has read the others' numbers
   }
   if (bad) atomicOr(p.status, ST_BAD_INDEX);
@@ -233,10 +243,10 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
 constexpr int GSUM_THREADS = 128;
 constexpr int GSUM_TILE_MAX = 64;  // entries of a tile at most
 #ifndef GS_A
-#define GS_A 4
+#define GS_A 2
 #endif
 constexpr int GSUM_AHEAD = GS_A;  // rows loaded ahead
-constexpr int GJOIN_GROUPS = 4;    // of threads that share a crossing token's tiles
+constexpr int GJOIN_GROUPS = 4;   // of threads that share a long run's tiles
 
 struct EmbedGradParams {
   const uint2* list;  // (token, position) in order
@@ -266,21 +276,37 @@ struct GradPacks {
   }
 };
 
+// Whether the run of token v that crosses a tile's end, at entry e1 of the list, ends within the next tile.
+// The block where it begins then takes it whole; a longer run leaves a partial sum in every tile.
+__device__ __forceinline__ bool ends_next(const EmbedGradParams& p, int64_t e1, unsigned v) {
+  return e1 + p.tile >= p.N || p.list[e1 + p.tile].x != v;
+}
+
 // One block per (tile of the list, column slice).
 template <typename T, typename O, int E, bool ADD>
 __global__ void __launch_bounds__(GSUM_THREADS) embedding_grad_kernel(const EmbedGradParams p) {
-  __shared__ uint2 entry[GSUM_TILE_MAX + 2];
+  __shared__ uint2 entry[2 * GSUM_TILE_MAX + 2];
   const int tid = threadIdx.x;
   O* dW = static_cast<O*>(p.dW);
   const int tile = static_cast<int>(blockIdx.x / p.slices), slice = static_cast<int>(blockIdx.x % p.slices);
-  const int e0 = tile * p.tile, count = min(p.tile, p.N - e0);
-  // entry[1 + i]: the tile's; entry[0] and entry[count + 1]: its neighbours (no token: V)
+  const int e0 = tile * p.tile, own = min(p.tile, p.N - e0);
+  // entry[1 + i]: the tile's and the next one's; entry[0] and what lies behind the list: no token, V
   const uint2 no_entry = make_uint2(p.V, 0);
-  for (int i = tid; i < count + 2; i += GSUM_THREADS) {
-    const int at = e0 + i - 1;
+  for (int i = tid; i < 2 * p.tile + 2; i += GSUM_THREADS) {
+    const int64_t at = int64_t(e0) + i - 1;
     entry[i] = at >= 0 && at < p.N ? p.list[at] : no_entry;
   }
+  // the entry before the tile before this one: whether a run that comes in began in that tile
+  const unsigned none = p.V, two_before = e0 > p.tile ? p.list[e0 - p.tile - 1].x : none;
   __syncthreads();
+  const unsigned first = entry[1].x, last = entry[own].x;
+  const bool comes_in = first != none && entry[0].x == first, goes_out = last != none && entry[own + 1].x == last;
+  const bool covered = comes_in && goes_out && first == last;
+  // entries at the front that belong to the block before, and behind the tile that belong to this one
+  const int lead = __syncthreads_count(tid < own && entry[1 + tid].x == first);
+  const int more = __syncthreads_count(tid < p.tile && entry[1 + own + tid].x == last);
+  int i0 = comes_in && !covered && two_before != first ? lead : 0;
+  const int count = goes_out && !covered && entry[1 + own + p.tile].x != last ? own + more : own;
   const int c = (slice * GSUM_THREADS + tid) * E;
   if (c >= p.d) return;
   const T* g = static_cast<const T*>(p.g) + c;
@@ -288,9 +314,8 @@ __global__ void __launch_bounds__(GSUM_THREADS) embedding_grad_kernel(const Embe
   float acc[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) acc[j] = 0.f;
-  const unsigned none = p.V;
-  bool begun = entry[1].x != entry[0].x;  // whether the running token begins in this tile
-  for (int i0 = 0; i0 < count; i0 += GSUM_AHEAD) {
+  bool begun = i0 > 0 || !comes_in;  // whether the running token begins in this tile
+  for (; i0 < count; i0 += GSUM_AHEAD) {
     // The rows of the step, and where a token ends in it the row of dW that it is added to, all under way
     // at once.
     P x[GSUM_AHEAD];
@@ -333,70 +358,83 @@ __global__ void __launch_bounds__(GSUM_THREADS) embedding_grad_kernel(const Embe
   }
 }
 
-// Tokens that cross tiles: the block of the tile where such a token begins adds what the tiles left, in
-// four runs of tiles and then those in order.
+// Runs over more than two tiles: the block of the tile where such a run begins adds what the tiles left. Of
+// a few tiles every group of threads takes a column slice; of many the groups share the tiles of each
+// slice, a stretch of them each, and add their sums in order.
 template <typename O, int E, bool ADD>
 __global__ void __launch_bounds__(GSUM_THREADS * GJOIN_GROUPS) embedding_grad_join_kernel(const EmbedGradParams p) {
+  constexpr int NT = GSUM_THREADS * GJOIN_GROUPS;
   __shared__ float part[GJOIN_GROUPS - 1][GSUM_THREADS * E];
-  const int tile = static_cast<int>(blockIdx.x / p.slices), slice = static_cast<int>(blockIdx.x % p.slices);
-  const int e0 = tile * p.tile, e1 = e0 + p.tile;
+  const int tile = static_cast<int>(blockIdx.x), tid = threadIdx.x;
+  const int64_t e0 = int64_t(tile) * p.tile, e1 = e0 + p.tile;
   if (e1 >= p.N) return;
-  const unsigned v = p.list[e1 - 1].x;
-  if (v == static_cast<unsigned>(p.V) || p.list[e1].x != v) return;  // nothing crosses the end
-  if (p.list[e0].x == v && e0 > 0 && p.list[e0 - 1].x == v) return;  // it began before
-  // tiles that begin with the token: they follow each other
-  int more = 0;
-  for (int t0 = tile + 1; t0 < p.tiles; t0 += GSUM_THREADS * GJOIN_GROUPS) {
-    const int t = t0 + threadIdx.x;
+  const unsigned v = p.list[e1 - 1].x, next = p.list[e1].x, first = p.list[e0].x, earlier = p.list[max(e0 - 1, int64_t(0))].x;
+  if (v == static_cast<unsigned>(p.V) || next != v) return;  // nothing crosses the end
+  if (first == v && e0 > 0 && earlier == v) return;          // it began before
+  if (ends_next(p, e1, v)) return;                           // the first tile's block took it whole
+  int more = 0;  // tiles that begin with the token follow each other
+  for (int t0 = tile + 1; t0 < p.tiles; t0 += NT) {
+    const int t = t0 + tid;
     const int n = __syncthreads_count(t < p.tiles && p.list[int64_t(t) * p.tile].x == v);
     more += n;
-    if (n < GSUM_THREADS * GJOIN_GROUPS) break;
+    if (n < NT) break;
   }
-  const int lane = threadIdx.x % GSUM_THREADS, group = threadIdx.x / GSUM_THREADS;
-  const int c = (slice * GSUM_THREADS + lane) * E;
-  float acc[E];
-#pragma unroll
-  for (int j = 0; j < E; ++j) acc[j] = 0.f;
-  if (c < p.d) {
-    auto take = [&](int i) {  // partial sum i of the token: what it began, then the tiles' first ones
-      GradPacks<float, E> x;
-      x.load(p.partial + (int64_t(tile + i) * 2 + (i == 0 ? 1 : 0)) * p.ldp + c);
-      return x;
-    };
-    const int all = more + 1, per = (all + GJOIN_GROUPS - 1) / GJOIN_GROUPS;
-    const int i1 = min(all, (group + 1) * per);
-    for (int i = group * per; i < i1; i += 4) {
+  const int lane = tid % GSUM_THREADS, group = tid / GSUM_THREADS, all = more + 1;
+  // acc += partial sums [k, k1): what the token's first tile began, then the other tiles' first ones
+  auto add = [&](float (&acc)[E], int k, int k1, int c) {
+    for (; k < k1; k += 4) {
       GradPacks<float, E> x[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (i + u < i1) x[u] = take(i + u);
+        if (k + u < k1) x[u].load(p.partial + (int64_t(tile + k + u) * 2 + (k + u == 0 ? 1 : 0)) * p.ldp + c);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (i + u >= i1) break;
+        if (k + u >= k1) break;
 #pragma unroll
         for (int j = 0; j < E; ++j) acc[j] += x[u].v[j / x[u].EP].v[j % x[u].EP];
       }
     }
-  }
-  if (group > 0) {
+  };
+  auto finish = [&](const float (&acc)[E], int c) {
+    O* to = static_cast<O*>(p.dW) + int64_t(v) * p.d + c;
+    GradPacks<O, E> y;
+    if (ADD) y.load(to);
 #pragma unroll
-    for (int j = 0; j < E; ++j) part[group - 1][j * GSUM_THREADS + lane] = acc[j];
+    for (int j = 0; j < E; ++j) {
+      O& o = y.v[j / y.EP].v[j % y.EP];
+      o = from_f32<O>(ADD ? fmaf(p.scale, acc[j], to_f32(o)) : p.scale * acc[j]);
+    }
+    y.store(to);
+  };
+  if (all <= 16) {
+    for (int slice = group; slice < p.slices; slice += GJOIN_GROUPS) {
+      const int c = (slice * GSUM_THREADS + lane) * E;
+      if (c >= p.d) return;
+      float acc[E] = {};
+      add(acc, 0, all, c);
+      finish(acc, c);
+    }
+    return;
   }
-  __syncthreads();
-  if (group > 0 || c >= p.d) return;
-  for (int r = 0; r < GJOIN_GROUPS - 1; ++r) {
+  const int per = (all + GJOIN_GROUPS - 1) / GJOIN_GROUPS;
+  for (int slice = 0; slice < p.slices; ++slice) {
+    const int c = (slice * GSUM_THREADS + lane) * E;
+    float acc[E] = {};
+    if (c < p.d) add(acc, group * per, min(all, (group + 1) * per), c);
+    if (group > 0) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) acc[j] += part[r][j * GSUM_THREADS + lane];
-  }
-  O* at = static_cast<O*>(p.dW) + int64_t(v) * p.d + c;
-  GradPacks<O, E> y;
-  if (ADD) y.load(at);
+      for (int j = 0; j < E; ++j) part[group - 1][j * GSUM_THREADS + lane] = acc[j];
+    }
+    __syncthreads();
+    if (group == 0 && c < p.d) {
+      for (int r = 0; r < GJOIN_GROUPS - 1; ++r) {
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    O& o = y.v[j / y.EP].v[j % y.EP];
-    o = from_f32<O>(ADD ? fmaf(p.scale, acc[j], to_f32(o)) : p.scale * acc[j]);
+        for (int j = 0; j < E; ++j) acc[j] += part[r][j * GSUM_THREADS + lane];
+      }
+      finish(acc, c);
+    }
+    __syncthreads();
   }
-  y.store(at);
 }
 
 }  // namespace fckl

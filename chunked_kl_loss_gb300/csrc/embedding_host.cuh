@@ -49,13 +49,16 @@ int launch_embedding_pack(int e, const void* W, int64_t ldw, const int32_t* toke
 }
 
 // ------------------------------------------------------------------ gradient
+#ifndef GS_T
+#define GS_T 1024
+#endif
 #ifndef SC_I
 #define SC_I 2048
 #endif
 constexpr int SORT_CTA_ITEMS = SC_I;  // positions of a sorting block, as long as the cluster can grow
 
 struct EmbedGradPlan {
-  int passes, bits, cluster, per_cta;
+  int passes, bits, cluster, per_log2;
   int tile, tiles;
   int64_t ldp;
   size_t off_a, off_b, off_partial, total;
@@ -69,8 +72,9 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   q.bits = static_cast<int>(cdiv(bits, q.passes));
   q.cluster = 1;
   while (q.cluster < 8 && int64_t(q.cluster) * SORT_CTA_ITEMS < N) q.cluster *= 2;
-  q.per_cta = static_cast<int>(rup(cdiv(N, q.cluster), 32));
-  q.tile = static_cast<int>(std::min<int64_t>(GSUM_TILE_MAX, std::max<int64_t>(8, N / 512)));
+  q.per_log2 = 5;
+  while ((int64_t(q.cluster) << q.per_log2) < N) ++q.per_log2;
+  q.tile = static_cast<int>(std::min<int64_t>(GSUM_TILE_MAX, std::max<int64_t>(8, N / GS_T)));
   q.tiles = static_cast<int>(cdiv(N, q.tile));
   q.ldp = rup(d, 8);
   size_t o = 0;
@@ -93,10 +97,24 @@ int launch_sort_tokens(const DevInfo* di, const EmbedGradPlan& q, const SortPara
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(q.cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  {
+    static bool done[64] = {};
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    if (!done[di->id]) {
+      cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           SORT_TILE * int(sizeof(uint2)));
+      if (e != cudaSuccess) {
+        set_error("cudaFuncSetAttribute(sort_tokens)", e);
+        return FCKL_ERR_CUDA;
+      }
+      done[di->id] = true;
+    }
+  }
   // two blocks an SM, and no more than have 64 KB to clear
   const int64_t clear = std::min<int64_t>(cdiv(p.zero_bytes, 65536), 2 * int64_t(di->sms) - q.cluster);
   cfg.gridDim = dim3(static_cast<unsigned>(q.cluster + rup(clear, q.cluster)));
   cfg.blockDim = dim3(SORT_THREADS);
+  cfg.dynamicSmemBytes = (1 << p.per_log2) <= SORT_TILE ? sizeof(uint2) << p.per_log2 : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -104,7 +122,7 @@ int launch_sort_tokens(const DevInfo* di, const EmbedGradPlan& q, const SortPara
 }
 
 template <typename T, typename O, int E, bool ADD>
-int launch_embedding_grad(EmbedGradParams p, cudaStream_t s) {
+int launch_embedding_grad(const DevInfo* di, EmbedGradParams p, cudaStream_t s) {
   p.slices = static_cast<int>(cdiv(p.d, GSUM_THREADS * E));
   const int64_t blocks = int64_t(p.tiles) * p.slices;
   if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
@@ -113,26 +131,26 @@ int launch_embedding_grad(EmbedGradParams p, cudaStream_t s) {
                   [&] { embedding_grad_kernel<T, O, E, ADD><<<grid, GSUM_THREADS, 0, s>>>(p); });
   if (st || p.tiles < 2) return st;
   return launch(KIND_EMBEDDING_JOIN, s, "embedding_grad_join", [&] {
-    embedding_grad_join_kernel<O, E, ADD><<<grid, GSUM_THREADS * GJOIN_GROUPS, 0, s>>>(p);
+    embedding_grad_join_kernel<O, E, ADD><<<p.tiles - 1, GSUM_THREADS * GJOIN_GROUPS, 0, s>>>(p);
   });
 }
 
 template <typename T, typename O, bool ADD>
-int launch_embedding_grad_pack(int e, const EmbedGradParams& p, cudaStream_t s) {
+int launch_embedding_grad_pack(const DevInfo* di, int e, const EmbedGradParams& p, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
-    if (e == 8) return launch_embedding_grad<T, O, 8, ADD>(p, s);
-  if (e >= 4) return launch_embedding_grad<T, O, 4, ADD>(p, s);
-  if (e == 2) return launch_embedding_grad<T, O, 2, ADD>(p, s);
-  return launch_embedding_grad<T, O, 1, ADD>(p, s);
+    if (e == 8) return launch_embedding_grad<T, O, 8, ADD>(di, p, s);
+  if (e >= 4) return launch_embedding_grad<T, O, 4, ADD>(di, p, s);
+  if (e == 2) return launch_embedding_grad<T, O, 2, ADD>(di, p, s);
+  return launch_embedding_grad<T, O, 1, ADD>(di, p, s);
 }
 
 template <typename T>
-int launch_embedding_grad_type(int e, int dt, int out_dt, bool add, const EmbedGradParams& p, cudaStream_t s) {
+int launch_embedding_grad_type(const DevInfo* di, int e, int dt, int out_dt, bool add, const EmbedGradParams& p, cudaStream_t s) {
   if (out_dt == FCKL_F32)
-    return add ? launch_embedding_grad_pack<T, float, true>(e, p, s)
-               : launch_embedding_grad_pack<T, float, false>(e, p, s);
+    return add ? launch_embedding_grad_pack<T, float, true>(di, e, p, s)
+               : launch_embedding_grad_pack<T, float, false>(di, e, p, s);
   if constexpr (sizeof(T) == 2)
-    return add ? launch_embedding_grad_pack<T, T, true>(e, p, s) : launch_embedding_grad_pack<T, T, false>(e, p, s);
+    return add ? launch_embedding_grad_pack<T, T, true>(di, e, p, s) : launch_embedding_grad_pack<T, T, false>(di, e, p, s);
   return FCKL_ERR_ARG;
 }
 
@@ -204,7 +222,7 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
     sp.V = V;
     sp.passes = q.passes;
     sp.bits = q.bits;
-    sp.per_cta = q.per_cta;
+    sp.per_log2 = q.per_log2;
     sp.a = reinterpret_cast<uint2*>(w + q.off_a);
     sp.b = reinterpret_cast<uint2*>(w + q.off_b);
     sp.status = status;
@@ -241,9 +259,9 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
     const int e_out = pack_of(dW, d, V, d, bo);
     int e = pack_of(g, ldg, N, d, b);
     if (e_out * bo < 16) e = std::min(e, e_out);  // 16 bytes of dW: several of its packs make one of g's
-    if (dtype == FCKL_BF16) return launch_embedding_grad_type<__nv_bfloat16>(e, dtype, dW_dtype, accumulate != 0, p, s);
-    if (dtype == FCKL_F16) return launch_embedding_grad_type<__half>(e, dtype, dW_dtype, accumulate != 0, p, s);
-    return launch_embedding_grad_type<float>(e, dtype, dW_dtype, accumulate != 0, p, s);
+    if (dtype == FCKL_BF16) return launch_embedding_grad_type<__nv_bfloat16>(di, e, dtype, dW_dtype, accumulate != 0, p, s);
+    if (dtype == FCKL_F16) return launch_embedding_grad_type<__half>(di, e, dtype, dW_dtype, accumulate != 0, p, s);
+    return launch_embedding_grad_type<float>(di, e, dtype, dW_dtype, accumulate != 0, p, s);
   });
 }
 
