@@ -11,8 +11,8 @@
 
 #include <type_traits>
 
+#include "bulk.cuh"
 #include "score.cuh"
-#include "tc_gemm.cuh"
 
 namespace fckl {
 
@@ -40,18 +40,6 @@ constexpr uint32_t ADJ_POSITIVE = 1;  // gradient: the logit is above 0
 constexpr int ADJ_SLOT_SHIFT = 21;
 constexpr int ADJUST_HISTORY_MAX = 0xfffff;
 constexpr uint32_t ADJ_NO_KEY = ~0u;
-
-// Bulk copies between global and shared memory: addresses and sizes are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
 
 struct AdjustParams {
   const void* z;   // logits

@@ -6,13 +6,14 @@
 // The gradient's positions are first put in the order of their tokens, equal tokens in the order of
 // their positions (a radix sort by one cluster). Blocks then walk tiles of the ordered list, each over
 // its own columns: the rows of a token that begins and ends within a tile are summed in registers and
-// written once, as are those of a token that runs into the next tile and ends there; a longer run leaves
-// one partial sum per tile, and those are added in a fixed order by a second kernel. So every row of dW has one writer, and the sums, all in
+// written once; a token that crosses a tile's edge leaves one partial sum per tile, and those are added
+// in a fixed order by a second kernel. So every row of dW has one writer, and the sums, all in
 // fp32, one order: the same call gives the same bits.
 #pragma once
 
 #include <cooperative_groups.h>
 
+#include "bulk.cuh"
 #include "score.cuh"
 
 namespace fckl {
@@ -61,10 +62,7 @@ __global__ void __launch_bounds__(EMBED_THREADS)
 }
 
 // ---------------------------------------------------------------- positions in the order of their tokens
-#ifndef SO_T
-#define SO_T 512
-#endif
-constexpr int SORT_THREADS = SO_T;
+constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_ITEMS = 8192 / SORT_THREADS;                 // per thread and tile
 constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;
@@ -242,10 +240,7 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
 // ---------------------------------------------------------------- sums by token
 constexpr int GSUM_THREADS = 128;
 constexpr int GSUM_TILE_MAX = 64;  // entries of a tile at most
-#ifndef GS_A
-#define GS_A 2
-#endif
-constexpr int GSUM_AHEAD = GS_A;  // rows loaded ahead
+constexpr int GSUM_AHEAD = 2;    // rows loaded ahead
 constexpr int GJOIN_GROUPS = 4;   // of threads that share a long run's tiles
 
 struct EmbedGradParams {
@@ -257,6 +252,8 @@ struct EmbedGradParams {
   float scale;
   int tile, tiles;  // entries of a tile, tiles
   int slices;       // column slices
+  int slice_vecs;   // 16-byte vectors of g in one (ring kernel)
+  unsigned* status;
   float* partial;   // [tiles][2][ldp]: what a tile adds to a token begun before it; what it begins
   int64_t ldp;
 };
@@ -276,37 +273,22 @@ struct GradPacks {
   }
 };
 
-// Whether the run of token v that crosses a tile's end, at entry e1 of the list, ends within the next tile.
-// The block where it begins then takes it whole; a longer run leaves a partial sum in every tile.
-__device__ __forceinline__ bool ends_next(const EmbedGradParams& p, int64_t e1, unsigned v) {
-  return e1 + p.tile >= p.N || p.list[e1 + p.tile].x != v;
-}
-
-// One block per (tile of the list, column slice).
+// One block per (tile of the list, column slice), rows through registers: for rows that do not lie on
+// 16-byte boundaries.
 template <typename T, typename O, int E, bool ADD>
 __global__ void __launch_bounds__(GSUM_THREADS) embedding_grad_kernel(const EmbedGradParams p) {
-  __shared__ uint2 entry[2 * GSUM_TILE_MAX + 2];
+  __shared__ uint2 entry[GSUM_TILE_MAX + 2];
   const int tid = threadIdx.x;
   O* dW = static_cast<O*>(p.dW);
   const int tile = static_cast<int>(blockIdx.x / p.slices), slice = static_cast<int>(blockIdx.x % p.slices);
-  const int e0 = tile * p.tile, own = min(p.tile, p.N - e0);
-  // entry[1 + i]: the tile's and the next one's; entry[0] and what lies behind the list: no token, V
-  const uint2 no_entry = make_uint2(p.V, 0);
-  for (int i = tid; i < 2 * p.tile + 2; i += GSUM_THREADS) {
-    const int64_t at = int64_t(e0) + i - 1;
-    entry[i] = at >= 0 && at < p.N ? p.list[at] : no_entry;
+  const int e0 = tile * p.tile, count = min(p.tile, p.N - e0);
+  // entry[1 + i]: the tile's; entry[0] and entry[count + 1]: its neighbours (no token: V)
+  const unsigned none = p.V;
+  for (int i = tid; i < count + 2; i += GSUM_THREADS) {
+    const int at = e0 + i - 1;
+    entry[i] = at >= 0 && at < p.N ? p.list[at] : make_uint2(none, 0);
   }
-  // the entry before the tile before this one: whether a run that comes in began in that tile
-  const unsigned none = p.V, two_before = e0 > p.tile ? p.list[e0 - p.tile - 1].x : none;
   __syncthreads();
-  const unsigned first = entry[1].x, last = entry[own].x;
-  const bool comes_in = first != none && entry[0].x == first, goes_out = last != none && entry[own + 1].x == last;
-  const bool covered = comes_in && goes_out && first == last;
-  // entries at the front that belong to the block before, and behind the tile that belong to this one
-  const int lead = __syncthreads_count(tid < own && entry[1 + tid].x == first);
-  const int more = __syncthreads_count(tid < p.tile && entry[1 + own + tid].x == last);
-  int i0 = comes_in && !covered && two_before != first ? lead : 0;
-  const int count = goes_out && !covered && entry[1 + own + p.tile].x != last ? own + more : own;
   const int c = (slice * GSUM_THREADS + tid) * E;
   if (c >= p.d) return;
   const T* g = static_cast<const T*>(p.g) + c;
@@ -314,8 +296,8 @@ __global__ void __launch_bounds__(GSUM_THREADS) embedding_grad_kernel(const Embe
   float acc[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) acc[j] = 0.f;
-  bool begun = i0 > 0 || !comes_in;  // whether the running token begins in this tile
-  for (; i0 < count; i0 += GSUM_AHEAD) {
+  bool begun = entry[1].x != entry[0].x;  // whether the running token begins in this tile
+  for (int i0 = 0; i0 < count; i0 += GSUM_AHEAD) {
     // The rows of the step, and where a token ends in it the row of dW that it is added to, all under way
     // at once.
     P x[GSUM_AHEAD];
@@ -358,7 +340,220 @@ __global__ void __launch_bounds__(GSUM_THREADS) embedding_grad_kernel(const Embe
   }
 }
 
-// Runs over more than two tiles: the block of the tile where such a run begins adds what the tiles left. Of
+// The same sums where rows of g and dW lie on 16-byte boundaries. A block takes (a tile of the list, a
+// column chunk of up to 96 vectors), each of its warps a quarter of the tile, one entry to a lane. The
+// entries' rows, and the rows of dW that sums are added to, come by bulk copies into rings of the warp's own
+// in shared memory: what is under way does not depend on registers, and no barrier stands in the stream.
+// Tokens that cross from warp to warp are then joined in shared memory.
+constexpr int GRING_WARPS = 4;
+constexpr int GRING_STAGES = 4;  // rows of g
+constexpr int GRING_OLD = 2;     // rows of dW
+constexpr int GRING_VECS = 96;      // 16-byte vectors of g in a chunk at most
+constexpr int GRING_TILE_MAX = 32 * GRING_WARPS;
+
+// Shared memory of a warp: its rings, which later hold its two partial sums.
+template <typename T, typename O, bool ADD>
+__host__ __device__ constexpr int gring_warp_bytes() {
+  const int rings = GRING_VECS * 16 * (GRING_STAGES + (ADD ? GRING_OLD * int(sizeof(O)) / int(sizeof(T)) : 0));
+  const int sums = 2 * GRING_VECS * 16 / int(sizeof(T)) * 4;
+  return rings > sums ? rings : sums;
+}
+
+template <typename T, typename O, bool ADD>
+__global__ void __launch_bounds__(32 * GRING_WARPS) embedding_grad_ring_kernel(const EmbedGradParams p) {
+  constexpr int VE = 16 / sizeof(T), U = GRING_VECS / 32, S = GRING_STAGES, SO = GRING_OLD;
+  constexpr int STAGE = GRING_VECS * 16, OLD = STAGE * int(sizeof(O)) / int(sizeof(T));
+  constexpr int WARP_BYTES = gring_warp_bytes<T, O, ADD>();
+  constexpr unsigned ALL = 0xffffffffu;
+  extern __shared__ __align__(128) uint8_t gring[];
+  __shared__ uint64_t bars[GRING_WARPS][S + SO];
+  // a warp's first and last token, and whether sums came in (which may end in it) and went out
+  __shared__ unsigned token_in[GRING_WARPS], token_out[GRING_WARPS];
+  __shared__ bool has_in[GRING_WARPS], in_ends[GRING_WARPS], has_out[GRING_WARPS];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int tile = static_cast<int>(blockIdx.x / p.slices), slice = static_cast<int>(blockIdx.x % p.slices);
+  const int own = p.tile / GRING_WARPS;  // entries of a warp
+  const int64_t e0 = int64_t(tile) * p.tile + warp * own;
+  const int count = static_cast<int>(max(int64_t(0), min(int64_t(own), p.N - e0)));
+  const unsigned none = p.V;
+  // an entry to a lane, and its neighbours' tokens
+  const uint2 mine = lane < count ? p.list[e0 + lane] : make_uint2(none, 0);
+  unsigned before = __shfl_up_sync(ALL, mine.x, 1), after = __shfl_down_sync(ALL, mine.x, 1);
+  if (lane == 0) before = e0 > 0 && e0 <= p.N ? p.list[e0 - 1].x : none;
+  if (lane == count - 1) after = e0 + count < p.N ? p.list[e0 + count].x : none;
+  const bool live = lane < count && mine.x != none;
+  const int entries = __popc(__ballot_sync(ALL, live));  // empty slots come last
+  const unsigned ends = __ballot_sync(ALL, live && after != mine.x);
+  const unsigned breaks = entries ? ends | 1u << (entries - 1) : 0u;  // where a sum is written, whole or in part
+  const bool comes_in = __shfl_sync(ALL, live && before == mine.x, 0);
+  unsigned adds = ends;  // sums that belong to dW: they begin and end in this warp
+  if (comes_in && ends) adds &= ends - 1;
+  const int vecs = p.d / VE, v0 = slice * p.slice_vecs, nv = min(p.slice_vecs, vecs - v0);
+  const T* g = static_cast<const T*>(p.g) + int64_t(v0) * VE;
+  O* dW = static_cast<O*>(p.dW) + int64_t(v0) * VE;
+  uint8_t* ring = gring + warp * WARP_BYTES;
+  uint8_t* old_ring = ring + S * STAGE;
+  uint64_t *full = bars[warp], *old_full = bars[warp] + S;
+  const uint32_t bytes = static_cast<uint32_t>(nv) * 16, old_bytes = bytes / sizeof(T) * sizeof(O);
+  auto load_row = [&](int i) {  // all lanes
+    const int pos = __shfl_sync(ALL, static_cast<int>(mine.y), i);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[i % S], bytes);
+      bulk_load(ring + (i % S) * STAGE, g + int64_t(pos) * p.ldg, bytes, &full[i % S]);
+    }
+  };
+  unsigned to_load = ADD ? adds : 0u;  // rows of dW not yet asked for
+  int asked = 0, used = 0;
+  auto load_old = [&]() {
+    if (!to_load) return;
+    const unsigned v = __shfl_sync(ALL, mine.x, __ffs(to_load) - 1);
+    to_load &= to_load - 1;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&old_full[asked % SO], old_bytes);
+      bulk_load(old_ring + (asked % SO) * OLD, dW + int64_t(v) * p.d, old_bytes, &old_full[asked % SO]);
+    }
+    ++asked;
+  };
+  if (lane == 0) {
+    for (int k = 0; k < S + SO; ++k) mbar_init(&full[k], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  for (int i = 0; i < min(S, entries); ++i) load_row(i);
+  for (int k = 0; k < SO; ++k) load_old();
+  float acc[U][VE], in[U][VE];  // the running sum; the one of the token that comes in
+  auto clear = [&](float (&x)[U][VE]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < VE; ++j) x[u][j] = 0.f;
+  };
+  clear(acc);
+  bool ok = true;
+  int i = 0;
+  for (; i < entries; ++i) {
+    ok = drain_phase(&full[i % S], (i / S) & 1, p.status);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = u * 32 + lane;
+      if (q < nv) {
+        float f[VE];
+        unpack16<T>(reinterpret_cast<const uint4*>(ring + (i % S) * STAGE)[q], f);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) acc[u][j] += f[j];
+      }
+    }
+    if (!__all_sync(ALL, ok)) break;  // (and the stage has been read)
+    if (i + S < entries) load_row(i + S);
+    if (!((breaks >> i) & 1u)) continue;
+    if ((adds >> i) & 1u) {
+      const unsigned v = __shfl_sync(ALL, mine.x, i);
+      if (ADD) ok = drain_phase(&old_full[used % SO], (used / SO) & 1, p.status);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = u * 32 + lane;
+        if (q >= nv) continue;
+        GradPacks<O, VE> y;
+        if (ADD) y.load(reinterpret_cast<const O*>(old_ring + (used % SO) * OLD) + q * VE);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          O& o = y.v[j / y.EP].v[j % y.EP];
+          o = from_f32<O>(ADD ? fmaf(p.scale, acc[u][j], to_f32(o)) : p.scale * acc[u][j]);
+        }
+        y.store(dW + int64_t(v) * p.d + q * VE);
+      }
+      if (!__all_sync(ALL, ok)) break;
+      ++used;
+      load_old();
+    } else if (comes_in && !(breaks & ((1u << i) - 1u))) {  // the first sum written: it began before
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < VE; ++j) in[u][j] = acc[u][j];
+    } else {
+      continue;  // the last sum, which goes on: it stays in acc
+    }
+    clear(acc);
+  }
+  if (i < entries && lane == 0) {  // a copy did not come: leave none under way
+    for (int k = i + 1; k < min(i + S, entries); ++k) drain_phase(&full[k % S], (k / S) & 1, p.status);
+    if (ADD)
+      for (int k = used; k < asked; ++k) drain_phase(&old_full[k % SO], (k / SO) & 1, p.status);
+  }
+  // What crosses the warps' edges, through shared memory: a sum that came in, and one that goes on.
+  const bool one_run = comes_in && !ends && entries;          // covers the warp: it counts as coming in
+  const bool goes_on = entries && !((ends >> (entries - 1)) & 1u) && !one_run;
+  float* sums = reinterpret_cast<float*>(ring);
+  __syncwarp();
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int q = u * 32 + lane;
+    if (q >= nv) continue;
+    GradPacks<float, VE> y;
+    if (comes_in) {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) y.v[j / y.EP].v[j % y.EP] = in[u][j];
+      y.store(sums + q * VE);
+    }
+    if (goes_on) {
+#pragma unroll
+      for (int j = 0; j < VE; ++j) y.v[j / y.EP].v[j % y.EP] = acc[u][j];
+      y.store(sums + GRING_VECS * VE + q * VE);
+    }
+  }
+  const unsigned last = __shfl_sync(ALL, mine.x, max(entries - 1, 0));
+  if (lane == 0) {
+    token_in[warp] = mine.x;
+    token_out[warp] = last;
+    has_in[warp] = comes_in;
+    in_ends[warp] = ends != 0;
+    has_out[warp] = goes_on;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x * 4; c < nv * VE; c += 128 * GRING_WARPS) {  // four columns a thread
+    float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool running = false, began = false;
+    auto add = [&](const float* x) {
+      const float4 f = *reinterpret_cast<const float4*>(x + c);
+      run.x += f.x, run.y += f.y, run.z += f.z, run.w += f.w;
+    };
+    auto leave = [&](int which) {  // for the other blocks' part of this token
+      *reinterpret_cast<float4*>(p.partial + (int64_t(tile) * 2 + which) * p.ldp + int64_t(v0) * VE + c) = run;
+    };
+    for (int w = 0; w < GRING_WARPS; ++w) {
+      const float* x = reinterpret_cast<const float*>(gring + w * WARP_BYTES);
+      if (has_in[w]) {
+        add(x);
+        running = true;
+        if (in_ends[w]) {
+          if (began) {
+            O* to = dW + int64_t(token_in[w]) * p.d + c;
+            const float f[4] = {run.x, run.y, run.z, run.w};
+            GradPacks<O, 4> y;
+            if (ADD) y.load(to);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              O& o = y.v[j / y.EP].v[j % y.EP];
+              o = from_f32<O>(ADD ? fmaf(p.scale, f[j], to_f32(o)) : p.scale * f[j]);
+            }
+            y.store(to);
+          } else {
+            leave(0);
+          }
+          running = began = false;
+          run = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      if (has_out[w]) {
+        add(x + GRING_VECS * VE);
+        running = began = true;
+      }
+    }
+    if (running) leave(began ? 1 : 0);
+  }
+}
+
+// Tokens that cross tiles: the block of the tile where such a token begins adds what the tiles left. Of
 // a few tiles every group of threads takes a column slice; of many the groups share the tiles of each
 // slice, a stretch of them each, and add their sums in order.
 template <typename O, int E, bool ADD>
@@ -371,7 +566,6 @@ __global__ void __launch_bounds__(GSUM_THREADS * GJOIN_GROUPS) embedding_grad_jo
   const unsigned v = p.list[e1 - 1].x, next = p.list[e1].x, first = p.list[e0].x, earlier = p.list[max(e0 - 1, int64_t(0))].x;
   if (v == static_cast<unsigned>(p.V) || next != v) return;  // nothing crosses the end
   if (first == v && e0 > 0 && earlier == v) return;          // it began before
-  if (ends_next(p, e1, v)) return;                           // the first tile's block took it whole
   int more = 0;  // tiles that begin with the token follow each other
   for (int t0 = tile + 1; t0 < p.tiles; t0 += NT) {
     const int t = t0 + tid;

@@ -49,17 +49,11 @@ int launch_embedding_pack(int e, const void* W, int64_t ldw, const int32_t* toke
 }
 
 // ------------------------------------------------------------------ gradient
-#ifndef GS_T
-#define GS_T 1024
-#endif
-#ifndef SC_I
-#define SC_I 2048
-#endif
-constexpr int SORT_CTA_ITEMS = SC_I;  // positions of a sorting block, as long as the cluster can grow
+constexpr int GSUM_TILE_MIN = 8;
+constexpr int SORT_CTA_ITEMS = 2048;  // positions of a sorting block, as long as the cluster can grow
 
 struct EmbedGradPlan {
   int passes, bits, cluster, per_log2;
-  int tile, tiles;
   int64_t ldp;
   size_t off_a, off_b, off_partial, total;
 };
@@ -74,8 +68,6 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   while (q.cluster < 8 && int64_t(q.cluster) * SORT_CTA_ITEMS < N) q.cluster *= 2;
   q.per_log2 = 5;
   while ((int64_t(q.cluster) << q.per_log2) < N) ++q.per_log2;
-  q.tile = static_cast<int>(std::min<int64_t>(GSUM_TILE_MAX, std::max<int64_t>(8, N / GS_T)));
-  q.tiles = static_cast<int>(cdiv(N, q.tile));
   q.ldp = rup(d, 8);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -86,7 +78,7 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   take(STATUS_WS_BYTES);
   q.off_a = take(size_t(N) * 8);
   q.off_b = take(size_t(N) * 8);
-  q.off_partial = take(size_t(q.tiles) * 2 * q.ldp * 4);
+  q.off_partial = take(size_t(cdiv(N, GSUM_TILE_MIN)) * 2 * q.ldp * 4);
   q.total = o;
   return q;
 }
@@ -121,15 +113,54 @@ int launch_sort_tokens(const DevInfo* di, const EmbedGradPlan& q, const SortPara
   return launch(KIND_SORT_TOKENS, s, "sort_tokens", [&] { cudaLaunchKernelEx(&cfg, sort_tokens_kernel, p); });
 }
 
+// Entries of a tile: as many as fill the GPU several times over, between GSUM_TILE_MIN and `most`.
+int grad_tile(const DevInfo* di, int64_t N, int64_t slices, int most) {
+  int tile = GSUM_TILE_MIN;
+  while (tile < most && cdiv(N, 2 * tile) * slices >= 4 * int64_t(di->sms)) tile *= 2;
+  return tile;
+}
+
 template <typename T, typename O, int E, bool ADD>
 int launch_embedding_grad(const DevInfo* di, EmbedGradParams p, cudaStream_t s) {
-  p.slices = static_cast<int>(cdiv(p.d, GSUM_THREADS * E));
-  const int64_t blocks = int64_t(p.tiles) * p.slices;
-  if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(blocks);
-  int st = launch(KIND_EMBEDDING_GRAD, s, "embedding_grad",
-                  [&] { embedding_grad_kernel<T, O, E, ADD><<<grid, GSUM_THREADS, 0, s>>>(p); });
+  const int64_t join_slices = cdiv(p.d, GSUM_THREADS * E);
+  int64_t blocks;
+  int st;
+  if constexpr (E * sizeof(T) == 16) {
+    const int64_t vecs = p.d / E;
+    p.slices = static_cast<int>(cdiv(vecs, GRING_VECS));
+    p.slice_vecs = static_cast<int>(cdiv(vecs, p.slices));
+    p.tile = grad_tile(di, p.N, p.slices, GRING_TILE_MAX);
+    p.tiles = static_cast<int>(cdiv(p.N, p.tile));
+    blocks = int64_t(p.tiles) * p.slices;
+    if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
+    constexpr int SMEM = GRING_WARPS * gring_warp_bytes<T, O, ADD>();
+    auto k = embedding_grad_ring_kernel<T, O, ADD>;
+    {
+      static bool done[64] = {};
+      std::lock_guard<std::mutex> lk(g_setup_mu);
+      if (!done[di->id]) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) {
+          set_error("cudaFuncSetAttribute(embedding_grad)", e);
+          return FCKL_ERR_CUDA;
+        }
+        done[di->id] = true;
+      }
+    }
+    st = launch(KIND_EMBEDDING_GRAD, s, "embedding_grad",
+                [&] { k<<<static_cast<unsigned>(blocks), 32 * GRING_WARPS, SMEM, s>>>(p); });
+  } else {
+    p.slices = static_cast<int>(join_slices);
+    p.tile = grad_tile(di, p.N, p.slices, GSUM_TILE_MAX);
+    p.tiles = static_cast<int>(cdiv(p.N, p.tile));
+    blocks = int64_t(p.tiles) * p.slices;
+    if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
+    st = launch(KIND_EMBEDDING_GRAD, s, "embedding_grad", [&] {
+      embedding_grad_kernel<T, O, E, ADD><<<static_cast<unsigned>(blocks), GSUM_THREADS, 0, s>>>(p);
+    });
+  }
   if (st || p.tiles < 2) return st;
+  p.slices = static_cast<int>(join_slices);
   return launch(KIND_EMBEDDING_JOIN, s, "embedding_grad_join", [&] {
     embedding_grad_join_kernel<O, E, ADD><<<p.tiles - 1, GSUM_THREADS * GJOIN_GROUPS, 0, s>>>(p);
   });
@@ -252,8 +283,7 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
     p.ldg = ldg;
     p.dW = dW;
     p.scale = scale;
-    p.tile = q.tile;
-    p.tiles = q.tiles;
+    p.status = status;
     p.partial = reinterpret_cast<float*>(w + q.off_partial);
     p.ldp = q.ldp;
     const int e_out = pack_of(dW, d, V, d, bo);
