@@ -26,10 +26,14 @@ struct alignas(E * sizeof(T)) Pack {
 
 // ---------------------------------------------------------------- lookup
 constexpr int EMBED_THREADS = 256;
+constexpr int EMBED_BLOCKS = 8;  // of an SM: 32 registers a thread
 
-// TPR threads to a row, E values at a time.
-template <typename T, int E, int TPR>
-__global__ void __launch_bounds__(EMBED_THREADS)
+// TPR threads to a row, E values at a time and U of those under way. Bound by memory at random rows of W:
+// many threads with few registers keep more under way than fewer with more (65536 x 2880 bf16 in blocks
+// of 256 threads: 96 us at 4 blocks an SM, 87 at 6, 81 at 8; floor 75), and streaming stores leave L2 to W's
+// frequent rows (103 -> 93 us at 4 blocks). Rows through shared memory by bulk copies took 95.
+template <typename T, int E, int TPR, int U>
+__global__ void __launch_bounds__(EMBED_THREADS, EMBED_BLOCKS)
     embedding_kernel(const T* __restrict__ W, int64_t ldw, const int32_t* __restrict__ tokens, int64_t N, int d, int V,
                      float scale, T* __restrict__ out, int64_t ld_out, unsigned* status) {
   const int lane = threadIdx.x % TPR;
@@ -42,7 +46,6 @@ __global__ void __launch_bounds__(EMBED_THREADS)
   T* dst = out + n * ld_out;
   using P = Pack<T, E>;
   const float fill = t == -1 ? 0.f : NAN;
-  constexpr int U = 4;
   for (int c0 = lane * E; c0 < d; c0 += U * TPR * E) {
     P x[U];
 #pragma unroll
@@ -56,7 +59,10 @@ __global__ void __launch_bounds__(EMBED_THREADS)
       if (c >= d) break;
 #pragma unroll
       for (int j = 0; j < E; ++j) x[u].v[j] = from_f32<T>(in ? to_f32(x[u].v[j]) * scale : fill);
-      *reinterpret_cast<P*>(dst + c) = x[u];
+      if constexpr (sizeof(P) == 16)
+        __stcs(reinterpret_cast<uint4*>(dst + c), *reinterpret_cast<const uint4*>(&x[u]));
+      else
+        *reinterpret_cast<P*>(dst + c) = x[u];
     }
   }
 }
@@ -68,6 +74,7 @@ constexpr int SORT_ITEMS = 8192 / SORT_THREADS;                 // per thread an
 constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;
 constexpr int SORT_BITS = 9;                         // of a digit at most
 constexpr int SORT_BINS = 1 << SORT_BITS;
+constexpr int SORT_CLUSTER_MAX = 16;
 
 static_assert(SORT_THREADS >= SORT_BINS, "a thread for every digit");
 
@@ -154,7 +161,13 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
         if (k >= items) break;
         const int i = t0 + (warp * items + k) * 32 + lane;
         const unsigned digit = i < end ? (x[k].x >> shift) & dmask : ~0u;
-        const unsigned same = __match_any_sync(0xffffffffu, digit);
+        unsigned same = __ballot_sync(0xffffffffu, i < end);  // lanes with the same digit
+#pragma unroll
+        for (int b = 0; b < SORT_BITS; ++b) {
+          const bool set = (digit >> b) & 1u;
+          const unsigned lanes = __ballot_sync(0xffffffffu, set);
+          same &= set ? lanes : ~lanes;
+        }
         unsigned old = 0;
         if (digit != ~0u) old = wcount[warp][digit];
         __syncwarp();

@@ -25,17 +25,29 @@ int pack_of(const void* p, int64_t ld, int64_t rows, int d, size_t bytes) {
 template <typename T, int E>
 int launch_embedding(const void* W, int64_t ldw, const int32_t* tokens, int64_t N, int d, int V, float scale, void* out,
                      int64_t ld_out, unsigned* status, cudaStream_t s) {
-  auto go = [&](auto tpr) {
-    constexpr int TPR = decltype(tpr)::value;
+  auto go = [&](auto tpr, auto u) {
+    constexpr int TPR = decltype(tpr)::value, U = decltype(u)::value;
     const unsigned grid = static_cast<unsigned>(cdiv(N, EMBED_THREADS / TPR));
     return launch(KIND_EMBEDDING, s, "embedding", [&] {
-      embedding_kernel<T, E, TPR><<<grid, EMBED_THREADS, 0, s>>>(static_cast<const T*>(W), ldw, tokens, N, d, V, scale,
-                                                                 static_cast<T*>(out), ld_out, status);
+      embedding_kernel<T, E, TPR, U><<<grid, EMBED_THREADS, 0, s>>>(static_cast<const T*>(W), ldw, tokens, N, d, V, scale,
+                                                                    static_cast<T*>(out), ld_out, status);
     });
   };
+  // As many loads of a thread at once as spread a row evenly over its steps.
+  auto with = [&](auto tpr) {
+    constexpr int TPR = decltype(tpr)::value;
+    const int64_t each = cdiv(cdiv(d, E), TPR), u = cdiv(each, cdiv(each, 4));
+    if constexpr (E * sizeof(T) == 16) {
+      if (u == 1) return go(tpr, std::integral_constant<int, 1>{});
+      if (u == 2) return go(tpr, std::integral_constant<int, 2>{});
+      if (u == 3) return go(tpr, std::integral_constant<int, 3>{});
+    }
+    return go(tpr, std::integral_constant<int, 4>{});
+  };
   const int64_t packs = cdiv(d, E);
-  if (packs <= 128) return go(std::integral_constant<int, 32>{});
-  return go(std::integral_constant<int, 128>{});
+  if (packs <= 32) return with(std::integral_constant<int, 8>{});
+  if (packs <= 128) return with(std::integral_constant<int, 32>{});
+  return with(std::integral_constant<int, 128>{});
 }
 
 template <typename T>
@@ -50,10 +62,10 @@ int launch_embedding_pack(int e, const void* W, int64_t ldw, const int32_t* toke
 
 // ------------------------------------------------------------------ gradient
 constexpr int GSUM_TILE_MIN = 8;
-constexpr int SORT_CTA_ITEMS = 2048;  // positions of a sorting block, as long as the cluster can grow
+constexpr int SORT_CTA_ITEMS = 1024;  // positions of a sorting block, as long as the cluster can grow
 
 struct EmbedGradPlan {
-  int passes, bits, cluster, per_log2;
+  int passes, bits;
   int64_t ldp;
   size_t off_a, off_b, off_partial, total;
 };
@@ -64,10 +76,6 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   while ((int64_t(1) << bits) <= V) ++bits;  // keys 0..V
   q.passes = static_cast<int>(cdiv(bits, SORT_BITS));
   q.bits = static_cast<int>(cdiv(bits, q.passes));
-  q.cluster = 1;
-  while (q.cluster < 8 && int64_t(q.cluster) * SORT_CTA_ITEMS < N) q.cluster *= 2;
-  q.per_log2 = 5;
-  while ((int64_t(q.cluster) << q.per_log2) < N) ++q.per_log2;
   q.ldp = rup(d, 8);
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -83,33 +91,45 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   return q;
 }
 
-int launch_sort_tokens(const DevInfo* di, const EmbedGradPlan& q, const SortParams& p, cudaStream_t s) {
+// Sorts p.tokens with a cluster of up to SORT_CLUSTER_MAX blocks (as many as the device takes).
+int launch_sort_tokens(const DevInfo* di, SortParams p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(q.cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  {
-    static bool done[64] = {};
-    std::lock_guard<std::mutex> lk(g_setup_mu);
-    if (!done[di->id]) {
-      cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           SORT_TILE * int(sizeof(uint2)));
-      if (e != cudaSuccess) {
-        set_error("cudaFuncSetAttribute(sort_tokens)", e);
-        return FCKL_ERR_CUDA;
-      }
-      done[di->id] = true;
-    }
-  }
-  // two blocks an SM, and no more than have 64 KB to clear
-  const int64_t clear = std::min<int64_t>(cdiv(p.zero_bytes, 65536), 2 * int64_t(di->sms) - q.cluster);
-  cfg.gridDim = dim3(static_cast<unsigned>(q.cluster + rup(clear, q.cluster)));
   cfg.blockDim = dim3(SORT_THREADS);
-  cfg.dynamicSmemBytes = (1 << p.per_log2) <= SORT_TILE ? sizeof(uint2) << p.per_log2 : 0;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  static int most[64] = {};
+  {
+    std::lock_guard<std::mutex> lk(g_setup_mu);
+    if (!most[di->id]) {
+      cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           SORT_TILE * int(sizeof(uint2)));
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(sort_tokens_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      int clusters = 0;
+      cfg.gridDim = dim3(SORT_CLUSTER_MAX);
+      cfg.dynamicSmemBytes = SORT_TILE * sizeof(uint2);
+      attr[0].val.clusterDim.x = SORT_CLUSTER_MAX;
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, sort_tokens_kernel, &cfg);
+      if (e != cudaSuccess) {
+        set_error("set-up of sort_tokens", e);
+        return FCKL_ERR_CUDA;
+      }
+      most[di->id] = clusters > 0 ? SORT_CLUSTER_MAX : 8;
+    }
+  }
+  p.cluster = 1;
+  while (p.cluster < most[di->id] && int64_t(p.cluster) * SORT_CTA_ITEMS < p.N) p.cluster *= 2;
+  p.per_log2 = 5;
+  while ((int64_t(p.cluster) << p.per_log2) < p.N) ++p.per_log2;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  cfg.dynamicSmemBytes = (1 << p.per_log2) <= SORT_TILE ? sizeof(uint2) << p.per_log2 : 0;
+  // two blocks an SM, and no more than have 64 KB to clear
+  const int64_t clear = std::min<int64_t>(cdiv(p.zero_bytes, 65536), 2 * int64_t(di->sms) - p.cluster);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.cluster + rup(clear, p.cluster)));
   return launch(KIND_SORT_TOKENS, s, "sort_tokens", [&] { cudaLaunchKernelEx(&cfg, sort_tokens_kernel, p); });
 }
 
@@ -253,11 +273,9 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
     sp.V = V;
     sp.passes = q.passes;
     sp.bits = q.bits;
-    sp.per_log2 = q.per_log2;
     sp.a = reinterpret_cast<uint2*>(w + q.off_a);
     sp.b = reinterpret_cast<uint2*>(w + q.off_b);
     sp.status = status;
-    sp.cluster = q.cluster;
     if (!accumulate) {
       // whole 16-byte vectors from the first boundary on; what lies before it is short
       sp.zero = static_cast<uint8_t*>(dW);
@@ -273,7 +291,7 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
         sp.zero_bytes -= ahead;
       }
     }
-    if ((st = launch_sort_tokens(di, q, sp, s))) return st;
+    if ((st = launch_sort_tokens(di, sp, s))) return st;
     EmbedGradParams p{};
     p.list = q.passes & 1 ? sp.a : sp.b;
     p.N = static_cast<int>(N);

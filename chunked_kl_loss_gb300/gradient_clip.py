@@ -15,7 +15,7 @@ import array
 import ctypes
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _for_stream, _stream, _value_code
+from .scoring import _for_stream, _here, _stream, _value_code
 
 __all__ = ["gradient_norm", "clip_gradients"]
 
@@ -33,8 +33,6 @@ def _set_argtypes(lib):
 
 def _dense(t):
     """Whether a tensor's elements fill one stretch of memory, in whatever order of its dimensions."""
-    if t.is_contiguous():
-        return True
     want = 1
     for stride, size in sorted((st, sz) for st, sz in zip(t.stride(), t.shape) if sz != 1):
         if stride != want:
@@ -45,20 +43,20 @@ def _dense(t):
 
 def _list(name, tensors, device):
     """(addresses, numbers of elements, types) of the tensors, as arrays that the library reads."""
-    codes = {}
-    ptrs, sizes, types = array.array("Q"), array.array("q"), array.array("i")
+    index = -1 if device.type == "cpu" else device.index
     for t in tensors:
-        if t.device != device:
+        if t.get_device() != index:
             raise ValueError(f"{name} must be on one device, got {t.device} beside {device}")
-        code = codes.get(t.dtype)
-        if code is None:
-            code = codes[t.dtype] = _value_code(t, name)
-        if not _dense(t):
+        if not t.is_contiguous() and not _dense(t):
             raise ValueError(f"{name} must be dense in memory, got strides {list(t.stride())}")
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel())
-        types.append(code)
-    return ptrs, sizes, types
+    codes = {}
+    for t in {t.dtype: t for t in tensors}.values():
+        codes[t.dtype] = _value_code(t, name)
+    if len(codes) == 1:
+        types = array.array("i", [*codes.values()]) * len(tensors)
+    else:
+        types = array.array("i", [codes[t.dtype] for t in tensors])
+    return array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]), types
 
 
 def _of(a):
@@ -93,7 +91,7 @@ def gradient_norm(grads, ws=None, stream=None):
     grads = [g for g in grads if g is not None]
     device = _device(grads)
     ptrs, sizes, types = _list("grads", grads, device)
-    with _for_stream(stream, *grads, ws):
+    with _for_stream(stream, ws, *grads) if stream is not None else _here:
         ws, norm = _room(len(grads), ws, device)
     st = _pkg.load().fckl_gradient_norm(_of(ptrs), _of(sizes), _of(types), len(grads), norm.data_ptr(),
                                         ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
@@ -110,7 +108,7 @@ def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
     grads = list(grads)
     if out is not None:
         out = list(out)
-        if len(out) != len(grads) or any((g is None) != (o is None) for g, o in zip(grads, out)):
+        if [g is None for g in grads] != [o is None for o in out]:
             raise ValueError("out must have one tensor for each gradient")
         out = [o for o in out if o is not None]
     grads = [g for g in grads if g is not None]
@@ -121,10 +119,10 @@ def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
     to, to_types = ptrs, types
     if out is not None:
         for g, o in zip(grads, out):
-            if o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous())):
+            if o.shape != g.shape or not (o.is_contiguous() and g.is_contiguous() or o.stride() == g.stride()):
                 raise ValueError("out must have the gradients' shapes and memory orders")
         to, _, to_types = _list("out", out, device)
-    with _for_stream(stream, *grads, *(out or ()), ws):
+    with _for_stream(stream, ws, *grads, *(out or ())) if stream is not None else _here:
         ws, norm = _room(len(grads), ws, device)
     st = _pkg.load().fckl_clip_gradients(_of(ptrs), _of(sizes), _of(types), len(grads), float(max_norm), _of(to),
                                          _of(to_types), norm.data_ptr(), ws.tensor.data_ptr(), ws.nbytes,
