@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import weakref
 
 import chunked_kl_loss_gb300 as _pkg
 from .scoring import _for_stream, _here, _stream, _value_code
@@ -44,14 +45,14 @@ def _dense(t):
 def _list(name, tensors, device):
     """(addresses, numbers of elements, types) of the tensors, as arrays that the library reads."""
     index = -1 if device.type == "cpu" else device.index
-    for t in tensors:
-        if t.get_device() != index:
-            raise ValueError(f"{name} must be on one device, got {t.device} beside {device}")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"{name} must be dense in memory, got strides {list(t.stride())}")
-    codes = {}
-    for t in {t.dtype: t for t in tensors}.values():
-        codes[t.dtype] = _value_code(t, name)
+    if {t.get_device() for t in tensors} - {index}:
+        where = [t.device for t in tensors if t.get_device() != index]
+        raise ValueError(f"{name} must be on one device, got {where[0]} beside {device}")
+    if not all([t.is_contiguous() for t in tensors]):
+        for t in tensors:
+            if not _dense(t):
+                raise ValueError(f"{name} must be dense in memory, got strides {list(t.stride())}")
+    codes = {dtype: _value_code(t, name) for dtype, t in {t.dtype: t for t in tensors}.items()}
     if len(codes) == 1:
         types = array.array("i", [*codes.values()]) * len(tensors)
     else:
@@ -74,7 +75,6 @@ def _device(grads):
 
 def _room(count, ws, device):
     import torch
-    import weakref
     n = _pkg.load().fckl_gradient_norm_workspace_bytes(count)
     if n == 0:
         raise _pkg.FcklError(_pkg.ERR_UNSUPPORTED, "workspace_bytes")
@@ -118,10 +118,10 @@ def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
     ptrs, sizes, types = _list("grads", grads, device)
     to, to_types = ptrs, types
     if out is not None:
-        for g, o in zip(grads, out):
-            if o.shape != g.shape or not (o.is_contiguous() and g.is_contiguous() or o.stride() == g.stride()):
-                raise ValueError("out must have the gradients' shapes and memory orders")
         to, _, to_types = _list("out", out, device)
+        if [g.shape for g in grads] != [o.shape for o in out] or \
+                any([g.stride() != o.stride() for g, o in zip(grads, out) if not (g.is_contiguous() and o.is_contiguous())]):
+            raise ValueError("out must have the gradients' shapes and memory orders")
     with _for_stream(stream, ws, *grads, *(out or ())) if stream is not None else _here:
         ws, norm = _room(len(grads), ws, device)
     st = _pkg.load().fckl_clip_gradients(_of(ptrs), _of(sizes), _of(types), len(grads), float(max_norm), _of(to),

@@ -19,7 +19,7 @@ from __future__ import annotations
 import ctypes
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _address, _dense, _for_stream, _on_device, _rows, _stream, _value_code, _ws
+from .scoring import _address, _dense, _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _ws
 
 __all__ = ["adjust_logits", "adjust_logits_backward", "differentiable_adjusted_logits"]
 
@@ -81,8 +81,10 @@ def _bits(allowed, N, V):
 
 
 def _out(out, like):
-    if out is not None and (out.dtype != like.dtype or out.shape != like.shape):
+    """Row pitch of `out`."""
+    if out.dtype != like.dtype or out.shape != like.shape:
         raise ValueError("out must have the logits' type and shape")
+    return _rows("out", out)
 
 
 def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=1.0, frequency=0.0, presence=0.0,
@@ -114,18 +116,21 @@ def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=1.
         _dense("bias_tokens", bias_tokens, torch.int32, (N, B))
         _dense("bias", bias, torch.float32, (N, B))
     lda = _bits(allowed, N, V)
-    _out(out, logits)
+    ldo = V
+    if out is not None:
+        ldo = _out(out, logits)
     dev = logits.device
-    _on_device(dev, logits=logits, history=history, lengths=lengths, prompt=prompt, repetition=r, frequency=f, presence=p,
-               bias_tokens=bias_tokens, bias=bias, allowed=allowed, out=out)
-    with _for_stream(stream, logits, history, lengths, prompt, r, f, p, bias_tokens, bias, allowed, out, ws):
+    if not _here_all(logits, history, lengths, prompt, r, f, p, bias_tokens, bias, allowed, out):
+        _on_device(dev, logits=logits, history=history, lengths=lengths, prompt=prompt, repetition=r, frequency=f,
+                   presence=p, bias_tokens=bias_tokens, bias=bias, allowed=allowed, out=out)
+    with _here if stream is None else _for_stream(stream, logits, history, lengths, prompt, r, f, p, bias_tokens, bias, allowed, out, ws):
         ws = _ws(ws, dev)
         if out is None:
             out = torch.empty(N, V, dtype=logits.dtype, device=dev)
     a = _address
     st = _pkg.load().fckl_adjust_logits(a(logits), code, ld, N, V, a(history), ldh, L, a(lengths), a(prompt), a(r), r1, a(f),
                                         f1, a(p), p1, a(bias_tokens), a(bias), B, a(allowed), lda, a(out),
-                                        _rows("out", out), ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
+                                        ldo, ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_adjust_logits")
     return out
@@ -149,16 +154,19 @@ def adjust_logits_backward(g, logits, history=None, lengths=None, repetition=1.0
     if r is None and not r1 > 0:
         raise ValueError(f"repetition must be positive, got {r1}")
     lda = _bits(allowed, N, V)
-    _out(out, logits)
+    ldo = V
+    if out is not None:
+        ldo = _out(out, logits)
     dev = logits.device
-    _on_device(dev, logits=logits, g=g, history=history, lengths=lengths, repetition=r, allowed=allowed, out=out)
-    with _for_stream(stream, g, logits, history, lengths, r, allowed, out, ws):
+    if not _here_all(logits, g, history, lengths, r, allowed, out):
+        _on_device(dev, logits=logits, g=g, history=history, lengths=lengths, repetition=r, allowed=allowed, out=out)
+    with _here if stream is None else _for_stream(stream, g, logits, history, lengths, r, allowed, out, ws):
         ws = _ws(ws, dev)
         if out is None:
             out = torch.empty(N, V, dtype=logits.dtype, device=dev)
     a = _address
     st = _pkg.load().fckl_adjust_logits_backward(a(g), code, ldg, a(logits), ld, N, V, a(history), ldh, L, a(lengths), a(r),
-                                                 r1, a(allowed), lda, a(out), _rows("out", out), ws.tensor.data_ptr(),
+                                                 r1, a(allowed), lda, a(out), ldo, ws.tensor.data_ptr(),
                                                  ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_adjust_logits_backward")

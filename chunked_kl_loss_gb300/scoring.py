@@ -80,9 +80,15 @@ def _ws(ws, device):
     return ws
 
 
+_value_codes = {}
+
+
 def _value_code(t, what):
-    import torch
-    code = {torch.bfloat16: _pkg.BF16, torch.float16: _pkg.F16, torch.float32: _pkg.F32}.get(t.dtype)
+    code = _value_codes.get(t.dtype)
+    if code is None:
+        import torch
+        _value_codes.update({torch.bfloat16: _pkg.BF16, torch.float16: _pkg.F16, torch.float32: _pkg.F32})
+        code = _value_codes.get(t.dtype)
     if code is None:
         raise TypeError(f"{what} must be bfloat16, float16 or float32, got {t.dtype}")
     return code
@@ -95,6 +101,18 @@ def _on_device(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _here_all(*tensors):
+    """Whether all tensors (None apart) are on the current CUDA device: what _on_device then need not say."""
+    import torch
+    index = tensors[0].get_device()
+    if index < 0 or index != torch._C._cuda_getDevice():
+        return False
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            return False
+    return True
 
 
 def _dense(name, t, dtype, shape):

@@ -13,9 +13,10 @@ empty slot (a row of zeros, no gradient).
 from __future__ import annotations
 
 import ctypes
+import weakref
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _address, _for_stream, _on_device, _rows, _stream, _value_code, _ws
+from .scoring import _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _ws
 
 __all__ = ["embedding", "embedding_backward", "differentiable_embedding"]
 
@@ -33,7 +34,7 @@ def _set_argtypes(lib):
 
 def _tokens(tokens):
     import torch
-    if tokens.dtype != torch.int32:
+    if tokens.dtype is not torch.int32:
         raise TypeError(f"tokens must be {torch.int32}, got {tokens.dtype}")
     if not tokens.is_contiguous():
         raise ValueError("tokens must be contiguous")
@@ -44,11 +45,11 @@ def _row_matrix(name, t, tokens, d):
     """(row pitch) of a tensor [*tokens.shape, d]: contiguous, or for tokens [N] with rows apart."""
     if tuple(t.shape) != (*tokens.shape, d):
         raise ValueError(f"{name} must be of shape {[*tokens.shape, d]}, got {list(t.shape)}")
-    if t.dim() == 2:
-        return _rows(name, t)
-    if not t.is_contiguous():
+    if t.is_contiguous():
+        return d
+    if t.dim() != 2:
         raise ValueError(f"{name} must be contiguous")
-    return d
+    return _rows(name, t)
 
 
 def embedding(W, tokens, scale=1.0, out=None, ws=None, stream=None):
@@ -61,14 +62,15 @@ def embedding(W, tokens, scale=1.0, out=None, ws=None, stream=None):
     code = _value_code(W, "W")
     V, d = W.shape
     N = _tokens(tokens)
-    ldw = _rows("W", W)
+    ldw = d if W.is_contiguous() else _rows("W", W)
     dev = W.device
     if out is not None:
         if out.dtype != W.dtype:
             raise TypeError(f"out must be {W.dtype}, got {out.dtype}")
         ldo = _row_matrix("out", out, tokens, d)
-    _on_device(dev, W=W, tokens=tokens, out=out)
-    with _for_stream(stream, W, tokens, out, ws):
+    if not _here_all(W, tokens, out):
+        _on_device(dev, W=W, tokens=tokens, out=out)
+    with _here if stream is None else _for_stream(stream, W, tokens, out, ws):
         ws = _ws(ws, dev)
         if out is None:
             out, ldo = torch.empty(*tokens.shape, d, dtype=W.dtype, device=dev), d
@@ -85,7 +87,6 @@ def embedding_backward(g, tokens, V, scale=1.0, dW=None, accumulate=False, dtype
     from the fp32 sums. ``dW``: where it goes; with ``accumulate`` it is added to what is there, and only
     the rows of tokens that occur are touched. ``ws``: Workspace(N, d, V, 0, 0, kind="embedding_backward")."""
     import torch
-    import weakref
     code = _value_code(g, "g")
     N = _tokens(tokens)
     if g.dim() < 1:
@@ -104,9 +105,10 @@ def embedding_backward(g, tokens, V, scale=1.0, dW=None, accumulate=False, dtype
     if dtype not in (torch.float32, g.dtype):
         raise TypeError(f"dW is float32 or of g's type, not {dtype}")
     dev = g.device
-    _on_device(dev, g=g, tokens=tokens, dW=dW)
+    if not _here_all(g, tokens, dW):
+        _on_device(dev, g=g, tokens=tokens, dW=dW)
     lib = _pkg.load()
-    with _for_stream(stream, g, tokens, dW, ws):
+    with _here if stream is None else _for_stream(stream, g, tokens, dW, ws):
         if ws is None:
             n = lib.fckl_embedding_backward_workspace_bytes(N, d, V)
             if n == 0:
