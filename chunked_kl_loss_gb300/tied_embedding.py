@@ -107,23 +107,28 @@ def embedding_backward(g, tokens, V, scale=1.0, dW=None, accumulate=False, dtype
     dev = g.device
     if not _here_all(g, tokens, dW):
         _on_device(dev, g=g, tokens=tokens, dW=dW)
-    lib = _pkg.load()
     with _here if stream is None else _for_stream(stream, g, tokens, dW, ws):
-        if ws is None:
-            n = lib.fckl_embedding_backward_workspace_bytes(N, d, V)
-            if n == 0:
-                raise _pkg.FcklError(_pkg.ERR_UNSUPPORTED, "workspace_bytes")
-            ws = _pkg._last_ws = _pkg.Workspace.sized(n, dev)
-        else:
-            _pkg._last_ws = weakref.ref(ws)
         if dW is None:
             dW = torch.empty(V, d, dtype=dtype, device=dev)
+        _backward(g, code, ldg, tokens, N, d, V, scale, dW, accumulate, ws, stream)
+    return dW
+
+
+def _backward(g, code, ldg, tokens, N, d, V, scale, dW, accumulate=False, ws=None, stream=None):
+    """embedding_backward of checked arguments, into dW."""
+    lib = _pkg.load()
+    if ws is None:
+        n = lib.fckl_embedding_backward_workspace_bytes(N, d, V)
+        if n == 0:
+            raise _pkg.FcklError(_pkg.ERR_UNSUPPORTED, "workspace_bytes")
+        ws = _pkg._last_ws = _pkg.Workspace.sized(n, g.device)
+    else:
+        _pkg._last_ws = weakref.ref(ws)
     st = lib.fckl_embedding_backward(g.data_ptr(), code, ldg, tokens.data_ptr(), N, d, V, float(scale), dW.data_ptr(),
                                      _value_code(dW, "dW"), int(bool(accumulate)), ws.tensor.data_ptr(), ws.nbytes,
                                      _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_embedding_backward")
-    return dW
 
 
 def _autograd_function():
@@ -133,15 +138,17 @@ def _autograd_function():
         @staticmethod
         def forward(ctx, W, tokens, scale):
             ctx.save_for_backward(tokens)
-            ctx.shape = (W.shape[0], W.dtype, scale)
+            ctx.shape = (W.shape, W.dtype, scale)
             return embedding(W, tokens, scale)
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, g):
             tokens, = ctx.saved_tensors
-            V, dtype, scale = ctx.shape
-            return embedding_backward(g.contiguous(), tokens, V, scale, dtype=dtype), None, None
+            (V, d), dtype, scale = ctx.shape
+            dW = torch.empty(V, d, dtype=dtype, device=g.device)
+            _backward(g.contiguous(), _value_code(g, "g"), d, tokens, tokens.numel(), d, V, scale, dW)
+            return dW, None, None
 
     return Embedding
 
