@@ -6,6 +6,7 @@
 // order, so no block waits for another and the same call gives the same bits.
 #pragma once
 
+#include "bulk.cuh"
 #include "score.cuh"
 
 namespace fckl {
@@ -105,6 +106,7 @@ template <int CAP>
 __global__ void __launch_bounds__(CLIP_THREADS)
     squares_kernel(const __grid_constant__ ClipTable<CAP> t, double* partial, unsigned* status) {
   __shared__ double warps[CLIP_THREADS / 32];
+  let_next_begin();
   if (status && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   const int per = (t.units + gridDim.x - 1) / gridDim.x;
   const int u0 = static_cast<int>(min(int64_t(blockIdx.x) * per, int64_t(t.units))), u1 = min(u0 + per, t.units);
@@ -140,6 +142,7 @@ __device__ __forceinline__ double total_of(const double* partial, int partials, 
 
 __global__ void __launch_bounds__(CLIP_THREADS) norm_kernel(const double* partial, int partials, float* norm) {
   __shared__ double warps[CLIP_THREADS / 32];
+  wait_for_previous();
   const double total = total_of(partial, partials, warps);
   if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(total));
 }
@@ -198,6 +201,10 @@ __global__ void __launch_bounds__(CLIP_THREADS)
     clip_kernel(const __grid_constant__ ClipTable<CAP> t, const double* partial, int partials, float max_norm,
                 float* norm) {
   __shared__ double warps[CLIP_THREADS / 32];
+  const int per = (t.units + gridDim.x - 1) / gridDim.x;
+  const int u0 = static_cast<int>(min(int64_t(blockIdx.x) * per, int64_t(t.units))), u1 = min(u0 + per, t.units);
+  int k = u0 < u1 ? tensor_of(t, u1 - 1) : 0;
+  wait_for_previous();
   const double total = sqrt(total_of(partial, partials, warps));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
   const double ratio = static_cast<double>(max_norm) / (total + static_cast<double>(CLIP_EPS));
@@ -206,10 +213,6 @@ __global__ void __launch_bounds__(CLIP_THREADS)
   const double up = ratio < 0x1p-100 ? 0x1p64 : 1.0;
   const float2 c = ratio >= 1.0 ? make_float2(1.f, 1.f)
                                 : make_float2(static_cast<float>(ratio * up), static_cast<float>(1.0 / up));
-  const int per = (t.units + gridDim.x - 1) / gridDim.x;
-  const int u0 = static_cast<int>(min(int64_t(blockIdx.x) * per, int64_t(t.units))), u1 = min(u0 + per, t.units);
-  if (u0 >= u1) return;
-  int k = tensor_of(t, u1 - 1);
   for (int u = u1 - 1; u >= u0; --u) {
     while (u < t.first[k]) --k;
     if (ratio >= 1.0 && t.in[k] == t.out[k]) continue;

@@ -109,16 +109,15 @@ int run_clip(DevInfo* di, const ClipList& l, float max_norm, float* norm, unsign
     partials += grid;
   }
   if (!l.out)
-    return launch(KIND_NORM, s, "gradient_norm",
-                  [&] { norm_kernel<<<1, CLIP_THREADS, 0, s>>>(partial, partials, norm); });
+    return launch_after(KIND_NORM, s, "gradient_norm", 1, CLIP_THREADS, 0, norm_kernel,
+                        static_cast<const double*>(partial), partials, norm);
   for (int i = 0, n = 0; i < l.count || n == 0; ++n) {
     if (launches > 1) i += fill_table(t, l, i);  // of one table: it is still there
     else i = l.count;
     const int grid = clip_grid(di, t.units);
     float* to = n ? nullptr : norm;
-    int st = launch(KIND_CLIP, s, "clip_gradients", [&] {
-      clip_kernel<CAP><<<grid, CLIP_THREADS, 0, s>>>(t, partial, partials, max_norm, to);
-    });
+    int st = launch_after(KIND_CLIP, s, "clip_gradients", static_cast<unsigned>(grid), CLIP_THREADS, 0, clip_kernel<CAP>, t,
+                          static_cast<const double*>(partial), partials, max_norm, to);
     if (st) return st;
   }
   return FCKL_OK;

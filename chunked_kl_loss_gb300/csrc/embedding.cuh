@@ -115,6 +115,7 @@ __device__ __forceinline__ void clear_beside(const SortParams& p) {
 // the rest of the GPU clears it meanwhile.
 __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortParams p) {
   namespace cg = cooperative_groups;
+  let_next_begin();
   if (blockIdx.x >= p.cluster) return clear_beside(p);
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ unsigned hist[SORT_BINS];                    // this block's numbers
@@ -297,6 +298,8 @@ __global__ void __launch_bounds__(GSUM_THREADS) embedding_grad_kernel(const Embe
   const int e0 = tile * p.tile, count = min(p.tile, p.N - e0);
   // entry[1 + i]: the tile's; entry[0] and entry[count + 1]: its neighbours (no token: V)
   const unsigned none = p.V;
+  let_next_begin();
+  wait_for_previous();
   for (int i = tid; i < count + 2; i += GSUM_THREADS) {
     const int at = e0 + i - 1;
     entry[i] = at >= 0 && at < p.N ? p.list[at] : make_uint2(none, 0);
@@ -389,6 +392,13 @@ __global__ void __launch_bounds__(32 * GRING_WARPS) embedding_grad_ring_kernel(c
   const int64_t e0 = int64_t(tile) * p.tile + warp * own;
   const int count = static_cast<int>(max(int64_t(0), min(int64_t(own), p.N - e0)));
   const unsigned none = p.V;
+  uint64_t *full = bars[warp], *old_full = bars[warp] + S;
+  if (lane == 0) {
+    for (int k = 0; k < S + SO; ++k) mbar_init(&full[k], 1);
+    fence_mbar_init();
+  }
+  let_next_begin();
+  wait_for_previous();
   // an entry to a lane, and its neighbours' tokens
   const uint2 mine = lane < count ? p.list[e0 + lane] : make_uint2(none, 0);
   unsigned before = __shfl_up_sync(ALL, mine.x, 1), after = __shfl_down_sync(ALL, mine.x, 1);
@@ -406,7 +416,6 @@ __global__ void __launch_bounds__(32 * GRING_WARPS) embedding_grad_ring_kernel(c
   O* dW = static_cast<O*>(p.dW) + int64_t(v0) * VE;
   uint8_t* ring = gring + warp * WARP_BYTES;
   uint8_t* old_ring = ring + S * STAGE;
-  uint64_t *full = bars[warp], *old_full = bars[warp] + S;
   const uint32_t bytes = static_cast<uint32_t>(nv) * 16, old_bytes = bytes / sizeof(T) * sizeof(O);
   auto load_row = [&](int i) {  // all lanes
     const int pos = __shfl_sync(ALL, static_cast<int>(mine.y), i);
@@ -427,10 +436,6 @@ __global__ void __launch_bounds__(32 * GRING_WARPS) embedding_grad_ring_kernel(c
     }
     ++asked;
   };
-  if (lane == 0) {
-    for (int k = 0; k < S + SO; ++k) mbar_init(&full[k], 1);
-    fence_mbar_init();
-  }
   __syncwarp();
   for (int i = 0; i < min(S, entries); ++i) load_row(i);
   for (int k = 0; k < SO; ++k) load_old();
@@ -576,6 +581,7 @@ __global__ void __launch_bounds__(GSUM_THREADS * GJOIN_GROUPS) embedding_grad_jo
   const int tile = static_cast<int>(blockIdx.x), tid = threadIdx.x;
   const int64_t e0 = int64_t(tile) * p.tile, e1 = e0 + p.tile;
   if (e1 >= p.N) return;
+  wait_for_previous();
   const unsigned v = p.list[e1 - 1].x, next = p.list[e1].x, first = p.list[e0].x, earlier = p.list[max(e0 - 1, int64_t(0))].x;
   if (v == static_cast<unsigned>(p.V) || next != v) return;  // nothing crosses the end
   if (first == v && e0 > 0 && earlier == v) return;          // it began before

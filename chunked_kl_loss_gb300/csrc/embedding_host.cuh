@@ -167,23 +167,20 @@ int launch_embedding_grad(const DevInfo* di, EmbedGradParams p, cudaStream_t s) 
         done[di->id] = true;
       }
     }
-    st = launch(KIND_EMBEDDING_GRAD, s, "embedding_grad",
-                [&] { k<<<static_cast<unsigned>(blocks), 32 * GRING_WARPS, SMEM, s>>>(p); });
+    st = launch_after(KIND_EMBEDDING_GRAD, s, "embedding_grad", static_cast<unsigned>(blocks), 32 * GRING_WARPS, SMEM, k, p);
   } else {
     p.slices = static_cast<int>(join_slices);
     p.tile = grad_tile(di, p.N, p.slices, GSUM_TILE_MAX);
     p.tiles = static_cast<int>(cdiv(p.N, p.tile));
     blocks = int64_t(p.tiles) * p.slices;
     if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
-    st = launch(KIND_EMBEDDING_GRAD, s, "embedding_grad", [&] {
-      embedding_grad_kernel<T, O, E, ADD><<<static_cast<unsigned>(blocks), GSUM_THREADS, 0, s>>>(p);
-    });
+    st = launch_after(KIND_EMBEDDING_GRAD, s, "embedding_grad", static_cast<unsigned>(blocks), GSUM_THREADS, 0,
+                      embedding_grad_kernel<T, O, E, ADD>, p);
   }
   if (st || p.tiles < 2) return st;
   p.slices = static_cast<int>(join_slices);
-  return launch(KIND_EMBEDDING_JOIN, s, "embedding_grad_join", [&] {
-    embedding_grad_join_kernel<O, E, ADD><<<p.tiles - 1, GSUM_THREADS * GJOIN_GROUPS, 0, s>>>(p);
-  });
+  return launch_after(KIND_EMBEDDING_JOIN, s, "embedding_grad_join", static_cast<unsigned>(p.tiles - 1),
+                      GSUM_THREADS * GJOIN_GROUPS, 0, embedding_grad_join_kernel<O, E, ADD>, p);
 }
 
 template <typename T, typename O, bool ADD>

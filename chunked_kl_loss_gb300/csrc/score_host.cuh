@@ -22,6 +22,23 @@ int guarded(const char* where, F&& body) noexcept {
   }
 }
 
+// Launches a kernel that may begin, up to its wait_for_previous(), while the stream's last kernel ends.
+template <class... P, class... A>
+int launch_after(int kind, cudaStream_t s, const char* what, unsigned grid, unsigned block, size_t smem, void (*k)(P...),
+                 const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return launch(kind, s, what, [&] { cudaLaunchKernelEx(&cfg, k, args...); });
+}
+
 size_t value_bytes(int dt) { return dt == FCKL_F32 ? 4 : 2; }
 bool known_dtype(int dt) { return dt == FCKL_BF16 || dt == FCKL_F32 || dt == FCKL_F16; }
 
