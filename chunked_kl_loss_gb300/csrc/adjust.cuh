@@ -19,10 +19,11 @@ namespace fckl {
 constexpr int ADJUST_THREADS = 512;
 constexpr int ADJUST_UNROLL = 8;      // vectors that a thread has under way
 constexpr int ADJUST_AHEAD = 8;       // history entries that a thread has under way
-constexpr int ADJUST_STAGED_THREADS = 512;
+constexpr int ADJUST_STAGED_THREADS = 512;  // of a block, or for short segments
+constexpr int ADJUST_STAGED_FEW = 128;
 constexpr int ADJUST_STAGES = 3;       // of each warp's ring in the staged kernel at most
 constexpr int ADJUST_STAGE_VECS = 96;  // vectors of a stage (1.5 KB)
-constexpr int ADJUST_RING_BYTES = ADJUST_STAGED_THREADS / 32 * ADJUST_STAGE_VECS * 16;  // of one stage of all warps
+constexpr int ADJUST_STAGE_BYTES = ADJUST_STAGE_VECS * 16;
 
 // What a row's rules have to know of its history.
 enum AdjustKind {
@@ -32,12 +33,14 @@ enum AdjustKind {
 };
 
 // What shared memory holds for a token that a rule touches: how often it was generated, whether it stands
-// in the prompt, and one more than the bias slot that carries the sum of its biases (0: none).
+// in the prompt, and TOKENS_MAX less the bias slot that carries the sum of its biases (0: none).
 constexpr uint32_t ADJ_COUNT = 0xfffffu;
 constexpr uint32_t ADJ_GIVEN = 1u << 20;
 constexpr uint32_t ADJ_SEEN = ADJ_COUNT | ADJ_GIVEN;
 constexpr uint32_t ADJ_POSITIVE = 1;  // gradient: the logit is above 0
 constexpr int ADJ_SLOT_SHIFT = 21;
+constexpr int ADJ_SEVERAL = static_cast<int>(0x80000000u);  // of a bias token in shared memory: it has several slots
+constexpr int ADJ_TOKEN = 0x7fffffff;
 constexpr int ADJUST_HISTORY_MAX = 0xfffff;
 constexpr uint32_t ADJ_NO_KEY = ~0u;
 
@@ -133,8 +136,12 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
   for (int i = tid; i < clear; i += NT) reinterpret_cast<uint4*>(s.seen)[i] = zero;
   if (s.table)
     for (int i = tid; i < s.words / 4; i += NT) reinterpret_cast<uint4*>(s.key)[i] = no_key;
+  bool bad = false;
   for (int b = tid; b < p.B; b += NT) {
-    s.btok[b] = p.bias_tokens[row * p.B + b];
+    const int t = p.bias_tokens[row * p.B + b];
+    const bool in = static_cast<unsigned>(t) < static_cast<unsigned>(p.V);
+    bad |= !in && t != -1;
+    s.btok[b] = in ? t : -1;  // what is not a token is an empty slot from here on
     s.bval[b] = p.bias[row * p.B + b];
   }
   __syncthreads();
@@ -158,7 +165,6 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
     const uint32_t one = 1u << ((t - s.first) & 31);
     return !(atomicOr(bits + ((t - s.first) >> 5), one) & one);
   };
-  bool bad = false;
   constexpr int A = ADJUST_AHEAD;
   for (int i0 = tid; i0 < len; i0 += A * NT) {
     int t[A];
@@ -192,28 +198,38 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
       }
     }
   }
-  // The first slot of a token takes the sum over its slots, in their order.
-  for (int b = tid; b < p.B; b += NT) {
-    const int t = s.btok[b];
-    if (static_cast<unsigned>(t) >= static_cast<unsigned>(p.V)) {
-      bad |= t != -1;
-      continue;
-    }
-    if (static_cast<unsigned>(t - s.c0) >= static_cast<unsigned>(s.columns)) continue;
-    float sum = 0.f;
-    bool first = true;
-    for (int j = 0; j < p.B; ++j) {
-      if (s.btok[j] != t) continue;
-      if (j < b) {
-        first = false;
-        break;
-      }
-      sum += s.bval[j];
-    }
-    if (first) {
-      s.bsum[b] = sum;
+  // The first slot of a token takes the sum over its slots, in their order: found by the largest of their
+  // numbers counted down, in the word's upper bits; only a token with several slots looks through all.
+  if (p.B) {
+    __syncthreads();  // the words' lower bits are complete
+    // whether slot b's token lies in the segment; its word then holds a slot's number from the first loop on
+    auto inside = [&](int b) {
+      return s.btok[b] != -1 && static_cast<unsigned>((s.btok[b] & ADJ_TOKEN) - s.c0) < static_cast<unsigned>(s.columns);
+    };
+    for (int b = tid; b < p.B; b += NT) {
+      const int t = s.btok[b];
+      if (!inside(b)) continue;
       if (BITS) mark(s.seen, t);
-      atomicOr(place(t), static_cast<uint32_t>(b + 1) << ADJ_SLOT_SHIFT);
+      uint32_t* w = place(t);
+      atomicMax(w, (*static_cast<volatile uint32_t*>(w) & ((1u << ADJ_SLOT_SHIFT) - 1u)) |
+                       static_cast<uint32_t>(TOKENS_MAX - b) << ADJ_SLOT_SHIFT);
+    }
+    __syncthreads();
+    auto owner = [&](int t) { return TOKENS_MAX - static_cast<int>(*place(t) >> ADJ_SLOT_SHIFT); };
+    for (int b = tid; b < p.B; b += NT) {
+      if (!inside(b)) continue;
+      const int first = owner(s.btok[b] & ADJ_TOKEN);
+      if (first != b) atomicOr(&s.btok[first], ADJ_SEVERAL);
+    }
+    __syncthreads();
+    for (int b = tid; b < p.B; b += NT) {
+      const int t = s.btok[b] & ADJ_TOKEN;
+      if (!inside(b) || owner(t) != b) continue;
+      float sum = s.bval[b];
+      if (s.btok[b] & ADJ_SEVERAL)
+        for (int j = b + 1; j < p.B; ++j)
+          if ((s.btok[j] & ADJ_TOKEN) == t) sum += s.bval[j];
+      s.bsum[b] = sum;
     }
   }
   if (bad) atomicOr(p.status, ST_BAD_INDEX);
@@ -234,7 +250,7 @@ struct AdjustRow {
       const uint32_t n = w & ADJ_COUNT;
       if (n) v = v - f * static_cast<float>(n) - p;
       const uint32_t slot = w >> ADJ_SLOT_SHIFT;
-      if (slot) v += bsum[slot - 1];
+      if (slot) v += bsum[TOKENS_MAX - slot];
       return v;
     }
   }
@@ -246,10 +262,10 @@ struct AdjustRow {
 // barrier of the block stands in the stream. The threads change the touched and the masked places in the
 // stages: what no rule touches passes through no register, and a touched place costs no access to
 // memory. Two blocks an SM: one gathers while the other streams.
-template <typename T, AdjustKind KIND>
-__global__ void __launch_bounds__(ADJUST_STAGED_THREADS) adjust_staged_kernel(const AdjustParams p) {
+template <typename T, AdjustKind KIND, int NT>
+__global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p) {
   constexpr int VE = 16 / sizeof(T);
-  constexpr int NT = ADJUST_STAGED_THREADS, WARPS = NT / 32, TV = ADJUST_STAGE_VECS;
+  constexpr int WARPS = NT / 32, TV = ADJUST_STAGE_VECS;
   constexpr int U = TV / 32;
   constexpr uint32_t ALL = (1u << VE) - 1u;
   constexpr bool GRAD = KIND == ADJUST_GRAD;
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(ADJUST_STAGED_THREADS) adjust_staged_kernel(co
   const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
   T* out = static_cast<T*>(p.out) + row * p.ld_out;
   const AdjustSegment s = adjust_segment<T, VE, KIND, true>(p, out, blockIdx.x % p.segs,
-                                                            reinterpret_cast<uint32_t*>(adj_stage + p.stages * ADJUST_RING_BYTES));
+                                                            reinterpret_cast<uint32_t*>(adj_stage + p.stages * WARPS * ADJUST_STAGE_BYTES));
   if (s.v0 >= s.v1) return;
   // Whole vectors [wa, wb), in tiles of a stage that the warps take in turn; the row's ends, if they are
   // ragged, go value by value.

@@ -12,6 +12,10 @@ constexpr int ADJUST_SEG_WORDS = 16384;   // tokens of a segment at most where e
 constexpr int ADJUST_SEG_BITS = 1 << 18;  // and where each has a bit (32 KB)
 constexpr int ADJUST_TABLE_LOG2 = 14;     // slots of the table of touched tokens at most (128 KB)
 constexpr size_t ADJUST_SMEM = 226 << 10;
+// Segments up to which blocks of 128 threads are considered: more rows are then under way on an SM. 4096
+// rows with 1000 history entries, with 512 / 128 threads: V = 8000 bf16 115 / 70 us, 30000 191 / 160,
+// 128256 376 / 481; 2000 rows of 4000 41 / 18.
+constexpr int ADJUST_FEW_VECS = 4096;
 
 int adjust_checks(const void* x, int dt, int64_t ld, const AdjustParams& p, int64_t N) {
   if (N < 0 || p.V < 1 || p.L < 0 || p.B < 0 || ld < p.V || p.ld_out < p.V || p.ld_h < p.L || !known_dtype(dt))
@@ -32,22 +36,27 @@ int adjust_checks(const void* x, int dt, int64_t ld, const AdjustParams& p, int6
   return FCKL_OK;
 }
 
-// Shared memory of a block: a ring of stages (staged kernel), sets of bits, the table's or the tokens' words
+// Shared memory of a block: its warps' rings (staged kernel), sets of bits, the table's or the tokens' words
 // and the biases.
-size_t adjust_smem(int64_t tokens, int stages, int sets, bool words, int slots_log2, int B) {
-  size_t n = size_t(stages) * ADJUST_RING_BYTES + sets * size_t(rup(tokens, 128)) / 8 + size_t(B) * 12;
+size_t adjust_smem(int64_t tokens, int rings, int sets, bool words, int slots_log2, int B) {
+  size_t n = size_t(rings) * ADJUST_STAGE_BYTES + sets * size_t(rup(tokens, 128)) / 8 + size_t(B) * 12;
   if (words) n += slots_log2 >= 0 ? size_t(8) << slots_log2 : size_t(tokens) * 4;
   return n;
 }
 
-// How the work is cut: with the table of touched tokens or a word for each, into how many segments a row,
-// and with how many stages. Taken is the least estimated time, in us, of waves of blocks that each gather
-// first (2.5 us, 1 us for every 8 history entries a thread, 1 us for every 64 KB of shared memory cleared)
-// and then stream at their share of an SM's 44 GB/s. The estimates are within a third of what 20 shapes
-// measured; where they are near each other the first, with fewer segments, is taken.
+// How the work is cut: into how many segments a row, with the table of touched tokens or a word for each,
+// and in the staged kernel with how many threads and stages. Taken is the least estimated time, in us, of
+// waves of blocks that each gather first (2.5 us, 1 us for every 8 history entries a thread, 1 us for every
+// 64 KB of shared memory cleared) and then stream at their share of an SM's 44 GB/s. From 1 x 201088 to
+// 4096 x 128256 the estimates are 20 to 35% below what is measured, all alike; 64 x 50001 fp32 with 16384
+// history entries: 4 segments and 2 stages 15.8 us, 8 segments 24, 3 stages 23; 16 x 128256 with 4000: 1, 4
+// and 16 segments 29, 12 and 7.6.
+struct AdjustPlan {
+  size_t smem = 0;
+  int threads = 0;
+};
 template <int VE, AdjustKind KIND, bool STAGED>
-size_t adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool streams) {
-  constexpr int NT = STAGED ? ADJUST_STAGED_THREADS : ADJUST_THREADS;
+AdjustPlan adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool streams) {
   constexpr bool WORDS = !STAGED || KIND == ADJUST_COUNTS;
   constexpr int SETS = STAGED ? (KIND == ADJUST_GRAD ? 2 : 1) : 0;
   const int64_t nvec = cdiv(int64_t(p.V) + VE - 1, VE);
@@ -55,54 +64,65 @@ size_t adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool streams) 
   int log2 = 8;
   while ((int64_t(3) << log2) < 4 * (int64_t(p.L) + p.B)) ++log2;
   double best = 1e30;
-  size_t best_smem = 0;
+  AdjustPlan plan;
   for (int way = 0; way < 2; ++way) {
     const bool table = way == 0;
-    if (table ? log2 > ADJUST_TABLE_LOG2 : !WORDS && best_smem) continue;
+    if (table ? log2 > ADJUST_TABLE_LOG2 : !WORDS && plan.smem) continue;
     const int64_t most = WORDS && !table ? ADJUST_SEG_WORDS : STAGED ? ADJUST_SEG_BITS : int64_t(1) << 31;
     const int64_t least = cdiv(nvec * VE, most);
     for (int64_t segs = least; segs < least + 64 && (segs == least || nvec * VE / segs >= 2048); ++segs) {
       const int64_t vecs = rup(cdiv(nvec, segs), 4);
-      for (int stages = STAGED ? ADJUST_STAGES : 0; stages >= (STAGED ? 2 : 0); --stages) {
-        const size_t smem = adjust_smem(vecs * VE, stages, SETS, WORDS, table ? log2 : -1, p.B);
+      for (int choice = 0; choice < (STAGED ? 4 : 1); ++choice) {
+        if ((choice & 2) && vecs > ADJUST_FEW_VECS) continue;
+        const int threads = !STAGED ? ADJUST_THREADS : choice & 2 ? ADJUST_STAGED_FEW : ADJUST_STAGED_THREADS;
+        const int stages = !STAGED ? 0 : choice & 1 ? 2 : ADJUST_STAGES;
+        const int rings = threads / 32 * stages;
+        const size_t smem = adjust_smem(vecs * VE, rings, SETS, WORDS, table ? log2 : -1, p.B);
         if (smem > ADJUST_SMEM) continue;
-        const int64_t resident = std::min<int64_t>(STAGED ? 3 : 2, (227 << 10) / int64_t(smem + 1536));
+        // blocks of an SM: by shared memory, and 64 registers a thread
+        const int64_t resident = std::min<int64_t>(1024 / threads + (STAGED && threads == 512), (227 << 10) / int64_t(smem + 1536));
         const int64_t blocks = N * segs, on_sm = std::min(resident, cdiv(blocks, di->sms));
-        const double gather = 2.5 + double(cdiv(p.L, NT * 8)) + double(smem - size_t(stages) * ADJUST_RING_BYTES) / 65536;
-        const double stream = streams ? double(vecs) * 32.0 * double(on_sm) / 44e3 * (stages == 2 ? 1.1 : 1.0) : 0.0;
+        const double gather = 2.5 + double(cdiv(p.L, threads * 8)) + double(smem - size_t(rings) * ADJUST_STAGE_BYTES) / 65536;
+        // a small block's few copies under way do not draw an SM's whole share
+        const double share = STAGED ? std::min(44e3 / double(on_sm), 44e3 * rings / 32.0) : 44e3 / double(on_sm);
+        const double stream = streams ? double(vecs) * 32.0 / share * (stages == 2 ? 1.1 : 1.0) : 0.0;
         const double us = double(cdiv(blocks, resident * di->sms)) * (gather + stream);
         if (us < 0.98 * best) {
           best = us;
-          best_smem = smem;
+          plan = {smem, threads};
           p.segs = static_cast<int>(segs);
           p.seg_vecs = static_cast<int>(vecs);
           p.stages = stages;
           p.slots_log2 = table ? log2 : -1;
         }
-        if (!STAGED) break;
       }
     }
   }
-  return best_smem;
+  return plan;
 }
 
 template <typename T, int VE, AdjustKind KIND, bool IN_PLACE, bool STAGED>
 int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s) {
   constexpr bool GRAD = KIND == ADJUST_GRAD;
-  const size_t smem = adjust_plan<VE, KIND, STAGED>(di, p, N, !IN_PLACE || p.allowed);
+  const AdjustPlan plan = adjust_plan<VE, KIND, STAGED>(di, p, N, !IN_PLACE || p.allowed);
+  if (!plan.threads) return FCKL_ERR_UNSUPPORTED;
   void (*k)(AdjustParams);
-  if constexpr (STAGED) k = adjust_staged_kernel<T, KIND>;
-  else k = adjust_kernel<T, VE, KIND, IN_PLACE>;
+  if constexpr (STAGED)
+    k = plan.threads == ADJUST_STAGED_FEW ? adjust_staged_kernel<T, KIND, ADJUST_STAGED_FEW>
+                                          : adjust_staged_kernel<T, KIND, ADJUST_STAGED_THREADS>;
+  else
+    k = adjust_kernel<T, VE, KIND, IN_PLACE>;
   {
-    static bool done[64] = {};
+    static bool done[64][2] = {};
+    bool& set = done[di->id][plan.threads == ADJUST_STAGED_FEW];
     std::lock_guard<std::mutex> lk(g_setup_mu);
-    if (!done[di->id]) {
+    if (!set) {
       cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ADJUST_SMEM));
       if (e != cudaSuccess) {
         set_error("cudaFuncSetAttribute(adjust)", e);
         return FCKL_ERR_CUDA;
       }
-      done[di->id] = true;
+      set = true;
     }
   }
   const int64_t rows_max = INT_MAX / p.segs;  // rows of one launch
@@ -123,7 +143,7 @@ int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s)
     if (p.allowed) q.allowed = p.allowed + r0 * p.ld_allowed;
     const unsigned grid = static_cast<unsigned>(rows * p.segs);
     int st = launch(GRAD ? KIND_ADJUST_GRAD : KIND_ADJUST, s, GRAD ? "adjust_logits_grad" : "adjust_logits",
-                    [&] { k<<<grid, STAGED ? ADJUST_STAGED_THREADS : ADJUST_THREADS, smem, s>>>(q); });
+                    [&] { k<<<grid, plan.threads, plan.smem, s>>>(q); });
     if (st) return st;
   }
   return FCKL_OK;
