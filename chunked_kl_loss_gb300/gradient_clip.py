@@ -43,12 +43,13 @@ def _dense(t):
 
 
 def _list(name, tensors, device):
-    """(addresses, numbers of elements, types) of the tensors, as arrays that the library reads."""
+    """(addresses, types, whether all are contiguous) of the tensors, as arrays that the library reads."""
     index = -1 if device.type == "cpu" else device.index
     if {t.get_device() for t in tensors} - {index}:
         where = [t.device for t in tensors if t.get_device() != index]
         raise ValueError(f"{name} must be on one device, got {where[0]} beside {device}")
-    if not all([t.is_contiguous() for t in tensors]):
+    contiguous = all([t.is_contiguous() for t in tensors])
+    if not contiguous:
         for t in tensors:
             if not _dense(t):
                 raise ValueError(f"{name} must be dense in memory, got strides {list(t.stride())}")
@@ -57,7 +58,19 @@ def _list(name, tensors, device):
         types = array.array("i", [*codes.values()]) * len(tensors)
     else:
         types = array.array("i", [codes[t.dtype] for t in tensors])
-    return array.array("Q", [t.data_ptr() for t in tensors]), array.array("q", [t.numel() for t in tensors]), types
+    return array.array("Q", [t.data_ptr() for t in tensors]), types, contiguous
+
+
+def _sizes(tensors):
+    return array.array("q", [t.numel() for t in tensors])
+
+
+def _given(tensors):
+    """The tensors as a list, without None, and where None stood (None: nowhere)."""
+    tensors = list(tensors)
+    if type(None) not in set(map(type, tensors)):
+        return tensors, None
+    return [t for t in tensors if t is not None], [t is None for t in tensors]
 
 
 def _of(a):
@@ -88,9 +101,10 @@ def _room(count, ws, device):
 def gradient_norm(grads, ws=None, stream=None):
     """The 2-norm over all elements of ``grads``, fp32 [1]. Finite gradients of any size are summed without
     overflow. ``ws``: a Workspace of at least fckl_gradient_norm_workspace_bytes(number of tensors)."""
-    grads = [g for g in grads if g is not None]
+    grads, _ = _given(grads)
     device = _device(grads)
-    ptrs, sizes, types = _list("grads", grads, device)
+    ptrs, types, _ = _list("grads", grads, device)
+    sizes = _sizes(grads)
     with _for_stream(stream, ws, *grads) if stream is not None else _here:
         ws, norm = _room(len(grads), ws, device)
     st = _pkg.load().fckl_gradient_norm(_of(ptrs), _of(sizes), _of(types), len(grads), norm.data_ptr(),
@@ -105,22 +119,22 @@ def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
     place, or into ``out``: tensors of the same shapes and memory orders, of any of the three types (the product is
     fp32, rounded once). No two tensors may overlap. A NaN norm makes the gradients NaN, an infinite one
     scales them by 0."""
-    grads = list(grads)
+    grads, gaps = _given(grads)
     if out is not None:
-        out = list(out)
-        if [g is None for g in grads] != [o is None for o in out]:
+        out, out_gaps = _given(out)
+        if len(out) != len(grads) or out_gaps != gaps:
             raise ValueError("out must have one tensor for each gradient")
-        out = [o for o in out if o is not None]
-    grads = [g for g in grads if g is not None]
     if not max_norm >= 0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
     device = _device(grads)
-    ptrs, sizes, types = _list("grads", grads, device)
+    ptrs, types, contiguous = _list("grads", grads, device)
+    sizes = _sizes(grads)
     to, to_types = ptrs, types
     if out is not None:
-        to, _, to_types = _list("out", out, device)
-        if [g.shape for g in grads] != [o.shape for o in out] or \
-                any([g.stride() != o.stride() for g, o in zip(grads, out) if not (g.is_contiguous() and o.is_contiguous())]):
+        to, to_types, as_well = _list("out", out, device)
+        alike = [g.shape for g in grads] == [o.shape for o in out]
+        if not alike or not (contiguous and as_well) and any(
+                [g.stride() != o.stride() for g, o in zip(grads, out) if not (g.is_contiguous() and o.is_contiguous())]):
             raise ValueError("out must have the gradients' shapes and memory orders")
     with _for_stream(stream, ws, *grads, *(out or ())) if stream is not None else _here:
         ws, norm = _room(len(grads), ws, device)

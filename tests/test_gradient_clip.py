@@ -263,7 +263,9 @@ def test_lists_that_the_library_reads(fckl):
     from chunked_kl_loss_gb300 import gradient_clip as m
     cpu = torch.device("cpu")
     a, b = torch.zeros(4, 6), torch.zeros(5, dtype=torch.bfloat16)
-    ptrs, sizes, types = m._list("grads", [a, b, a.t(), a[1:3]], cpu)
+    some = [a, b, a.t(), a[1:3]]
+    (ptrs, types, contiguous), sizes = m._list("grads", some, cpu), m._sizes(some)
+    assert not contiguous and m._list("grads", [a, b], cpu)[2]
     assert list(ptrs) == [a.data_ptr(), b.data_ptr(), a.data_ptr(), a[1:].data_ptr()]
     assert list(sizes) == [24, 5, 24, 12] and list(types) == [fckl.F32, fckl.BF16, fckl.F32, fckl.F32]
     for bad in (a[:, 1:], a[::2], a[:, :1].expand(4, 3), torch.zeros(3).expand(2, 3)):
