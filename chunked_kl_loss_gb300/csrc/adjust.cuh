@@ -93,8 +93,8 @@ struct AdjustSegment {
   float *bsum, *bval;
 };
 
-// Sets of bits, then words and keys, then biases: as much of it as the kind of rules needs.
-template <typename T, int VE, AdjustKind KIND, bool BITS>
+// Sets of bits, then words and keys, then biases: as much of it as the kernel and the kind of rules need.
+template <typename T, int VE, AdjustKind KIND, bool STAGED>
 __device__ __forceinline__ AdjustSegment adjust_segment(const AdjustParams& p, const T* out, int seg, uint32_t* smem) {
   AdjustSegment s;
   s.mis = VE == 1 ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(out) & 15u) / sizeof(T));
@@ -104,12 +104,12 @@ __device__ __forceinline__ AdjustSegment adjust_segment(const AdjustParams& p, c
   s.first = s.v0 * VE - s.mis;
   s.c0 = max(s.first, 0);
   s.columns = min(s.v1 * VE - s.mis, p.V) - s.c0;
-  s.bits = BITS ? (p.seg_vecs * VE + 127) / 128 * 4 : 0;
   s.table = p.slots_log2 >= 0;
-  s.words = BITS && KIND != ADJUST_COUNTS ? 0 : s.table ? 1 << p.slots_log2 : p.seg_vecs * VE;
+  s.bits = STAGED || !s.table ? (p.seg_vecs * VE + 127) / 128 * 4 : 0;
+  s.words = STAGED && KIND != ADJUST_COUNTS ? 0 : s.table ? 1 << p.slots_log2 : p.seg_vecs * VE;
   s.seen = smem;
   s.positive = smem + s.bits;
-  s.word = smem + (KIND == ADJUST_GRAD ? 2 : 1) * s.bits;
+  s.word = smem + (STAGED && KIND == ADJUST_GRAD ? 2 : 1) * s.bits;
   s.key = s.word + s.words;
   s.btok = reinterpret_cast<int*>(s.word + (s.table ? 2 : 1) * s.words);
   s.bsum = reinterpret_cast<float*>(s.btok + p.B);
@@ -123,26 +123,42 @@ __device__ __forceinline__ uint32_t adjust_hash(int token, int log2) {
 
 // Gathers the segment's touched tokens from the row's history and biases. Counts and bias slots are kept in
 // a hash table of token ids where those are few, so that its size does not depend on V, else in a word for
-// every token. With BITS a set of bits says which tokens are touched (and in a gradient a second one
-// which logits are above 0). Complete after the caller's next barrier.
-template <typename T, AdjustKind KIND, bool BITS, int NT>
+// every token. A set of bits says which tokens are touched (not beside the table of the kernel that is not
+// staged), and in a staged gradient a second one which logits are above 0. Complete after the caller's next
+// barrier.
+template <typename T, AdjustKind KIND, bool STAGED, int NT>
 __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const AdjustSegment& s, int64_t row, const T* z) {
   const int tid = threadIdx.x;
+  const int32_t* h = p.history + row * p.ld_h;
+  // The first history entries (whether or not they count: that is known when lengths[row] is here) and
+  // biases are under way while shared memory is cleared, later entries while earlier ones are gathered.
+  constexpr int A = ADJUST_AHEAD;
+  int ahead[A];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < A; ++u) ahead[u] = i0 + u * NT < p.L ? h[i0 + u * NT] : -1;
+  };
+  fetch(tid);
   const int len = p.lengths ? min(max(p.lengths[row], 0), p.L) : p.L;
   const int prompt = KIND == ADJUST_COUNTS && p.prompt ? p.prompt[row] : 0;
-  const int32_t* h = p.history + row * p.ld_h;
   const uint4 zero = make_uint4(0, 0, 0, 0), no_key = make_uint4(ADJ_NO_KEY, ADJ_NO_KEY, ADJ_NO_KEY, ADJ_NO_KEY);
-  const int clear = ((KIND == ADJUST_GRAD ? 2 : 1) * s.bits + s.words) / 4;
+  const int clear = ((STAGED && KIND == ADJUST_GRAD ? 2 : 1) * s.bits + s.words) / 4;
+  int first_token = -1;
+  float first_bias = 0.f;
+  if (tid < p.B) {
+    first_token = p.bias_tokens[row * p.B + tid];
+    first_bias = p.bias[row * p.B + tid];
+  }
   for (int i = tid; i < clear; i += NT) reinterpret_cast<uint4*>(s.seen)[i] = zero;
   if (s.table)
     for (int i = tid; i < s.words / 4; i += NT) reinterpret_cast<uint4*>(s.key)[i] = no_key;
   bool bad = false;
   for (int b = tid; b < p.B; b += NT) {
-    const int t = p.bias_tokens[row * p.B + b];
+    const int t = b == tid ? first_token : p.bias_tokens[row * p.B + b];
     const bool in = static_cast<unsigned>(t) < static_cast<unsigned>(p.V);
     bad |= !in && t != -1;
     s.btok[b] = in ? t : -1;  // what is not a token is an empty slot from here on
-    s.bval[b] = p.bias[row * p.B + b];
+    s.bval[b] = b == tid ? first_bias : p.bias[row * p.B + b];
   }
   __syncthreads();
   // The word of a token of the segment. The table has room for every history entry and bias.
@@ -165,12 +181,12 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
     const uint32_t one = 1u << ((t - s.first) & 31);
     return !(atomicOr(bits + ((t - s.first) >> 5), one) & one);
   };
-  constexpr int A = ADJUST_AHEAD;
   for (int i0 = tid; i0 < len; i0 += A * NT) {
     int t[A];
     T sign[A];
 #pragma unroll
-    for (int u = 0; u < A; ++u) t[u] = i0 + u * NT < len ? h[i0 + u * NT] : -1;
+    for (int u = 0; u < A; ++u) t[u] = i0 + u * NT < len ? ahead[u] : -1;
+    if (i0 + A * NT < len) fetch(i0 + A * NT);
 #pragma unroll
     for (int u = 0; u < A; ++u) {
       if (static_cast<unsigned>(t[u]) >= static_cast<unsigned>(p.V)) {
@@ -179,12 +195,13 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
       } else if (static_cast<unsigned>(t[u] - s.c0) >= static_cast<unsigned>(s.columns)) {
         t[u] = -1;
       } else if (KIND == ADJUST_COUNTS) {
-        if (BITS) mark(s.seen, t[u]);
+        if (STAGED || s.bits) mark(s.seen, t[u]);
         uint32_t* w = place(t[u]);
         if (i0 + u * NT >= prompt) atomicAdd(w, 1u);
         else atomicOr(w, ADJ_GIVEN);
       } else {
-        const bool is_new = BITS ? mark(s.seen, t[u]) : atomicOr(place(t[u]), ADJ_GIVEN) == 0;
+        if (!STAGED && s.bits) mark(s.seen, t[u]);
+        const bool is_new = STAGED ? mark(s.seen, t[u]) : atomicOr(place(t[u]), ADJ_GIVEN) == 0;
         if (KIND == ADJUST_GRAD && is_new) sign[u] = z[t[u]];
         else t[u] = -1;
       }
@@ -193,7 +210,7 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
 #pragma unroll
       for (int u = 0; u < A; ++u) {
         if (t[u] < 0 || !(to_f32(sign[u]) > 0.f)) continue;
-        if (BITS) mark(s.positive, t[u]);
+        if (STAGED) mark(s.positive, t[u]);
         else atomicOr(place(t[u]), ADJ_POSITIVE);
       }
     }
@@ -209,7 +226,7 @@ __device__ __forceinline__ void adjust_gather(const AdjustParams& p, const Adjus
     for (int b = tid; b < p.B; b += NT) {
       const int t = s.btok[b];
       if (!inside(b)) continue;
-      if (BITS) mark(s.seen, t);
+      if (STAGED || s.bits) mark(s.seen, t);
       uint32_t* w = place(t);
       atomicMax(w, (*static_cast<volatile uint32_t*>(w) & ((1u << ADJ_SLOT_SHIFT) - 1u)) |
                        static_cast<uint32_t>(TOKENS_MAX - b) << ADJ_SLOT_SHIFT);
@@ -464,17 +481,11 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) adjust_kernel(const AdjustP
   __syncthreads();
 
   const AdjustRow rules(p, row);
-  const int places = s.table ? s.words : s.columns;
-  for (int i0 = tid; i0 < places; i0 += U * ADJUST_THREADS) {
-    uint32_t w[U];
-    int c[U];
+  // Up to U touched places of the thread at a time (no word: none), from their words to the result.
+  uint32_t w[U];
+  int c[U];
+  auto write = [&]() {
     float v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * ADJUST_THREADS;
-      w[u] = i < places ? s.word[i] : 0;
-      c[u] = !w[u] ? 0 : s.table ? static_cast<int>(s.key[i]) : s.c0 + i;
-    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (w[u]) {
@@ -485,6 +496,29 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) adjust_kernel(const AdjustP
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (w[u]) out[c[u]] = from_f32<T>(rules.value<KIND>(v[u], w[u], s.bsum));
+  };
+  if (s.table) {
+    for (int i0 = tid; i0 < s.words; i0 += U * ADJUST_THREADS) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * ADJUST_THREADS;
+        w[u] = i < s.words ? s.word[i] : 0;
+        c[u] = w[u] ? static_cast<int>(s.key[i]) : 0;
+      }
+      write();
+    }
+  } else {
+    for (int i = tid; i < s.bits; i += ADJUST_THREADS) {
+      for (uint32_t left = s.seen[i]; left;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          c[u] = left ? s.first + i * 32 + __ffs(left) - 1 : s.c0;
+          w[u] = left ? s.word[c[u] - s.c0] : 0;
+          left &= left - 1;
+        }
+        write();
+      }
+    }
   }
 }
 

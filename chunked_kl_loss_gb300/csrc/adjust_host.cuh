@@ -58,7 +58,6 @@ struct AdjustPlan {
 template <int VE, AdjustKind KIND, bool STAGED>
 AdjustPlan adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool streams) {
   constexpr bool WORDS = !STAGED || KIND == ADJUST_COUNTS;
-  constexpr int SETS = STAGED ? (KIND == ADJUST_GRAD ? 2 : 1) : 0;
   const int64_t nvec = cdiv(int64_t(p.V) + VE - 1, VE);
   // The table is at most three quarters full.
   int log2 = 8;
@@ -77,7 +76,8 @@ AdjustPlan adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool strea
         const int threads = !STAGED ? ADJUST_THREADS : choice & 2 ? ADJUST_STAGED_FEW : ADJUST_STAGED_THREADS;
         const int stages = !STAGED ? 0 : choice & 1 ? 2 : ADJUST_STAGES;
         const int rings = threads / 32 * stages;
-        const size_t smem = adjust_smem(vecs * VE, rings, SETS, WORDS, table ? log2 : -1, p.B);
+        const int sets = STAGED && KIND == ADJUST_GRAD ? 2 : STAGED || !table ? 1 : 0;  // of bits
+        const size_t smem = adjust_smem(vecs * VE, rings, sets, WORDS, table ? log2 : -1, p.B);
         if (smem > ADJUST_SMEM) continue;
         // blocks of an SM: by shared memory, and 64 registers a thread
         const int64_t resident = std::min<int64_t>(1024 / threads + (STAGED && threads == 512), (227 << 10) / int64_t(smem + 1536));
