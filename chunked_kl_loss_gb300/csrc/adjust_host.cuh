@@ -46,8 +46,8 @@ size_t adjust_smem(int64_t tokens, int rings, int sets, bool words, int slots_lo
 
 // How the work is cut: into how many segments a row, with the table of touched tokens or a word for each,
 // and in the staged kernel with how many threads and stages. Taken is the least estimated time, in us, of
-// waves of blocks that each gather first (2.5 us, 1 us for every 8 history entries a thread, 1 us for every
-// 64 KB of shared memory cleared) and then stream at their share of an SM's 44 GB/s. From 1 x 201088 to
+// waves of blocks that each gather first (2.5 us, 1 us for every 8 history entries a thread reads, 0.6 us
+// for each that it puts into the table or 0.3 into words, 1 us for every 64 KB of shared memory cleared) and then stream at their share of an SM's 44 GB/s. From 1 x 201088 to
 // 4096 x 128256 the estimates are 20 to 35% below what is measured, all alike; 64 x 50001 fp32 with 16384
 // history entries: 4 segments and 2 stages 15.8 us, 8 segments 24, 3 stages 23; 16 x 128256 with 4000: 1, 4
 // and 16 segments 29, 12 and 7.6.
@@ -69,7 +69,9 @@ AdjustPlan adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool strea
     if (table ? log2 > ADJUST_TABLE_LOG2 : !WORDS && plan.smem) continue;
     const int64_t most = WORDS && !table ? ADJUST_SEG_WORDS : STAGED ? ADJUST_SEG_BITS : int64_t(1) << 31;
     const int64_t least = cdiv(nvec * VE, most);
-    for (int64_t segs = least; segs < least + 64 && (segs == least || nvec * VE / segs >= 2048); ++segs) {
+    // from the fewest segments on, in finer steps first, until they are short or the GPU is full many times
+    for (int64_t segs = least; segs == least || (segs < least + 64 && nvec * VE / segs >= 2048 &&
+                                                 N * segs <= 12 * int64_t(di->sms)); segs += std::max<int64_t>(1, segs / 8)) {
       const int64_t vecs = rup(cdiv(nvec, segs), 4);
       for (int choice = 0; choice < (STAGED ? 4 : 1); ++choice) {
         if ((choice & 2) && vecs > ADJUST_FEW_VECS) continue;
@@ -82,7 +84,9 @@ AdjustPlan adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool strea
         // blocks of an SM: by shared memory, and 64 registers a thread
         const int64_t resident = std::min<int64_t>(1024 / threads + (STAGED && threads == 512), (227 << 10) / int64_t(smem + 1536));
         const int64_t blocks = N * segs, on_sm = std::min(resident, cdiv(blocks, di->sms));
-        const double gather = 2.5 + double(cdiv(p.L, threads * 8)) + double(smem - size_t(rings) * ADJUST_STAGE_BYTES) / 65536;
+        const double gather = 2.5 + double(cdiv(p.L, threads * 8)) +
+                              (WORDS && table ? 0.6 : 0.3) * double(p.L) / double(threads * segs) +
+                              double(smem - size_t(rings) * ADJUST_STAGE_BYTES) / 65536;
         // a small block's few copies under way do not draw an SM's whole share
         const double share = STAGED ? std::min(44e3 / double(on_sm), 44e3 * rings / 32.0) : 44e3 / double(on_sm);
         const double stream = streams ? double(vecs) * 32.0 / share * (stages == 2 ? 1.1 : 1.0) : 0.0;

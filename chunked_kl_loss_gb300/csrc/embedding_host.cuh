@@ -67,8 +67,17 @@ constexpr int SORT_CTA_ITEMS = 1024;  // positions of a sorting block, as long a
 struct EmbedGradPlan {
   int passes, bits;
   int64_t ldp;
+  int tiles;  // that the partial sums have room for
   size_t off_a, off_b, off_partial, total;
 };
+
+// Entries of a tile: as many as leave blocks for the GPU (152 SMs) several times over, between GSUM_TILE_MIN
+// and `most`. More slices never give smaller tiles.
+int grad_tile(int64_t N, int64_t slices, int most) {
+  int tile = GSUM_TILE_MIN;
+  while (tile < most && cdiv(N, 2 * tile) * slices >= 4 * 152) tile *= 2;
+  return tile;
+}
 
 EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   EmbedGradPlan q{};
@@ -86,7 +95,10 @@ EmbedGradPlan embed_grad_plan(int64_t N, int d, int V) {
   take(STATUS_WS_BYTES);
   q.off_a = take(size_t(N) * 8);
   q.off_b = take(size_t(N) * 8);
-  q.off_partial = take(size_t(cdiv(N, GSUM_TILE_MIN)) * 2 * q.ldp * 4);
+  // two partial sums for every tile, at the smallest tiles that any alignment of the rows leads to
+  const int least = grad_tile(N, cdiv(d, 8 * GRING_VECS), GSUM_TILE_MAX);
+  q.tiles = static_cast<int>(cdiv(N, least));
+  q.off_partial = take(size_t(q.tiles) * 2 * q.ldp * 4);
   q.total = o;
   return q;
 }
@@ -133,15 +145,9 @@ int launch_sort_tokens(const DevInfo* di, SortParams p, cudaStream_t s) {
   return launch(KIND_SORT_TOKENS, s, "sort_tokens", [&] { cudaLaunchKernelEx(&cfg, sort_tokens_kernel, p); });
 }
 
-// Entries of a tile: as many as fill the GPU several times over, between GSUM_TILE_MIN and `most`.
-int grad_tile(const DevInfo* di, int64_t N, int64_t slices, int most) {
-  int tile = GSUM_TILE_MIN;
-  while (tile < most && cdiv(N, 2 * tile) * slices >= 4 * int64_t(di->sms)) tile *= 2;
-  return tile;
-}
-
 template <typename T, typename O, int E, bool ADD>
 int launch_embedding_grad(const DevInfo* di, EmbedGradParams p, cudaStream_t s) {
+  const int room = p.tiles;  // of the partial sums
   const int64_t join_slices = cdiv(p.d, GSUM_THREADS * E);
   int64_t blocks;
   int st;
@@ -149,10 +155,10 @@ int launch_embedding_grad(const DevInfo* di, EmbedGradParams p, cudaStream_t s) 
     const int64_t vecs = p.d / E;
     p.slices = static_cast<int>(cdiv(vecs, GRING_VECS));
     p.slice_vecs = static_cast<int>(cdiv(vecs, p.slices));
-    p.tile = grad_tile(di, p.N, p.slices, GRING_TILE_MAX);
+    p.tile = grad_tile(p.N, p.slices, GRING_TILE_MAX);
     p.tiles = static_cast<int>(cdiv(p.N, p.tile));
     blocks = int64_t(p.tiles) * p.slices;
-    if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
+    if (blocks > INT_MAX || p.tiles > room) return FCKL_ERR_UNSUPPORTED;
     constexpr int SMEM = GRING_WARPS * gring_warp_bytes<T, O, ADD>();
     auto k = embedding_grad_ring_kernel<T, O, ADD>;
     {
@@ -170,10 +176,10 @@ int launch_embedding_grad(const DevInfo* di, EmbedGradParams p, cudaStream_t s) 
     st = launch_after(KIND_EMBEDDING_GRAD, s, "embedding_grad", static_cast<unsigned>(blocks), 32 * GRING_WARPS, SMEM, k, p);
   } else {
     p.slices = static_cast<int>(join_slices);
-    p.tile = grad_tile(di, p.N, p.slices, GSUM_TILE_MAX);
+    p.tile = grad_tile(p.N, p.slices, GSUM_TILE_MAX);
     p.tiles = static_cast<int>(cdiv(p.N, p.tile));
     blocks = int64_t(p.tiles) * p.slices;
-    if (blocks > INT_MAX) return FCKL_ERR_UNSUPPORTED;
+    if (blocks > INT_MAX || p.tiles > room) return FCKL_ERR_UNSUPPORTED;
     st = launch_after(KIND_EMBEDDING_GRAD, s, "embedding_grad", static_cast<unsigned>(blocks), GSUM_THREADS, 0,
                       embedding_grad_kernel<T, O, E, ADD>, p);
   }
@@ -299,6 +305,7 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
     p.dW = dW;
     p.scale = scale;
     p.status = status;
+    p.tiles = q.tiles;
     p.partial = reinterpret_cast<float*>(w + q.off_partial);
     p.ldp = q.ldp;
     const int e_out = pack_of(dW, d, V, d, bo);
