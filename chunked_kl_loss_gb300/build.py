@@ -1,6 +1,6 @@
 """Builds the in-tree CUDA library ``_build/libfckl.so`` for sm_103a with nvcc.
 
-One translation unit (kernels + C ABI), one ``-gencode``; takes a few seconds.
+One translation unit (kernels + C ABI), one ``-gencode``; takes about a minute.
 """
 from __future__ import annotations
 

@@ -279,6 +279,13 @@ struct AdjustRow {
 // barrier of the block stands in the stream. The threads change the touched and the masked places in the
 // stages: what no rule touches passes through no register, and a touched place costs no access to
 // memory. Two blocks an SM: one gathers while the other streams.
+// Bound by memory, and by the gather's latency where few blocks share an SM: 4096 x 128256 bf16 without rules
+// 306 us (a plain copy's time), with a mask 319, with 1024 history entries 318, with both 339, with 16 biases
+// too 362 (floor 325; 150 instructions a warp and vector, 2.7 a cycle); the gradient, which reads the logits
+// at the history's tokens, 378. Before: a word in shared
+// memory for every token 1070 us, rows through registers with the touched places written again afterwards
+// 437 to 451, one ring to a block with a barrier for every stage 418. 96 vectors and 3 stages: 2 stages 15%
+// more, 64 vectors 5%, 4 stages of 128 vectors (one block an SM less) 30%.
 template <typename T, AdjustKind KIND, int NT>
 __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p) {
   constexpr int VE = 16 / sizeof(T);
@@ -321,20 +328,20 @@ __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p)
   // A lane's vectors lie 32 apart, a multiple of 32 values: one shift serves them all, for the mask's bits
   // and for the touched ones, and their words are at fixed distances.
   const int own = column(tile_at(0) + lane), mask_shift = own & 31;
-  const uint32_t* mask_lo = allowed + (own >> 5);
-  const uint32_t* mask_hi = allowed + ((own + VE - 1) >> 5);
+  const bool two_words = mask_shift + VE > 32;  // the mask's bits of the lane's vectors
+  const uint32_t* mask = allowed + (own >> 5);
+  constexpr int STEP = WARPS * U * VE;  // words from a tile of the warp to its next
   const int seen_at = (tile_at(0) - s.v0 + lane) * VE, seen_shift = seen_at & 31;
   const uint32_t* seen = s.seen + (seen_at >> 5);
   uint32_t lo[U], hi[U];
-  auto fetch_bits = [&](int k) {  // of the lane's vectors of tile k
+  auto fetch_bits = [&](int left) {  // of the lane's vectors of the tile at `mask`, if they lie before the end
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in = tile_at(k) + u * 32 + lane < wb;
-      lo[u] = in ? mask_lo[(k * WARPS * U + u) * VE] : 0;
-      hi[u] = in ? mask_hi[(k * WARPS * U + u) * VE] : 0;
+      lo[u] = u * 32 < left ? mask[u * VE] : 0;
+      hi[u] = two_words && u * 32 < left ? mask[u * VE + 1] : 0;
     }
   };
-  if (allowed && tiles) fetch_bits(0);
+  if (allowed && tiles) fetch_bits(wb - tile_at(0) - lane);
   const AdjustRow rules(p, row);
   __syncthreads();
   auto value = [&](float v, int c) -> float {  // of a touched place
@@ -358,18 +365,20 @@ __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p)
     uint32_t off[U];  // places that are not allowed
 #pragma unroll
     for (int u = 0; u < U; ++u) off[u] = allowed ? ~__funnelshift_r(lo[u], hi[u], mask_shift) & ALL : 0u;
-    if (allowed && k + 1 < tiles) fetch_bits(k + 1);
+    mask += STEP;
+    if (allowed && k + 1 < tiles) fetch_bits(wb - tile_at(k + 1) - lane);
     const bool ok = drain_phase(&full[stage], phase, p.status);
+    const int left = wb - tile_at(k) - lane;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int q = u * 32 + lane, v = tile_at(k) + q;
-      if (v >= wb) break;
+      if (u * 32 >= left) break;
+      const int q = u * 32 + lane;
       T* at = reinterpret_cast<T*>(data + q);
-      uint32_t touched = (seen[(k * WARPS * U + u) * VE] >> seen_shift) & ALL & ~off[u];
+      uint32_t touched = (seen[u * VE] >> seen_shift) & ALL & ~off[u];
       while (touched) {
         const int j = __ffs(touched) - 1;
         touched &= touched - 1;
-        at[j] = from_f32<T>(value(to_f32(at[j]), column(v) + j));
+        at[j] = from_f32<T>(value(to_f32(at[j]), column(tile_at(k) + q) + j));
       }
       if (off[u] == ALL) {
         const uint32_t none = GRAD ? 0u : fill_word<T>(-INFINITY);
@@ -388,6 +397,7 @@ __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p)
         }
       }
     }
+    seen += STEP;
     fence_proxy_async_smem();
     if (!__all_sync(0xffffffffu, ok)) break;
     if (lane == 0) {
@@ -422,7 +432,9 @@ __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p)
 
 // In place, or into rows that lie differently: the segment is copied under the mask (in place: masked tokens
 // are written and nothing is read), then the touched places are written again, each by one thread, from the
-// logits as they came in.
+// logits as they came in. In place a call is all latency: 1 x 201088 with 1500 history entries 5.5 us in 8
+// segments or so (8.9 in one), 256 x 128256 with 16000 68 us (154 with every token's word looked through
+// instead of a set of bits).
 template <typename T, int VE, AdjustKind KIND, bool IN_PLACE>
 __global__ void __launch_bounds__(ADJUST_THREADS, 2) adjust_kernel(const AdjustParams p) {
   static_assert(IN_PLACE || VE == 1, "");

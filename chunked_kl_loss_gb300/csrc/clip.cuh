@@ -4,6 +4,9 @@
 // graph keeps them). Their elements are cut into units of CLIP_UNIT; every block takes a run of units and
 // leaves one partial sum, and the scaling kernel's blocks each add the same partial sums in the same
 // order, so no block waits for another and the same call gives the same bits.
+// Bound by memory: a model's 983 M gradients, 2.5 GB, are read for the norm, read again and written as 2 GB
+// in 1071 us, 6.5 TB/s (6.7 is a plain copy); the second reading is what the floor of 666 us does not have, and
+// what lies in L2 (129 MB) is all that can be kept. 32 tensors of 8192: 9 us for the two launches.
 #pragma once
 
 #include "bulk.cuh"

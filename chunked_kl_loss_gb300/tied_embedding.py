@@ -8,7 +8,8 @@ Argument marshalling only, as in the package itself: every step runs in the CUDA
     x = fckl.differentiable_embedding(W, tokens)                      # autograd
 
 ``W [V, d]`` is bf16, fp16 or fp32 (rows may lie apart); ``tokens`` are int32 of any shape, -1 marks an
-empty slot (a row of zeros, no gradient).
+empty slot (a row of zeros, no gradient). ``stream`` and CUDA graph capture: as for the scoring calls
+(under capture call embedding_backward rather than autograd).
 """
 from __future__ import annotations
 

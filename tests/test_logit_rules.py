@@ -233,6 +233,50 @@ def test_extreme_logits_under_penalties(fckl, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("N,V,L,B", [(2, 40007, 20000, 30), (3, 300, 16000, 5), (40, 9001, 13000, 2), (2, 5001, 12280, 8),
+                                     (1, 90001, 12300, 1024)])
+def test_long_histories(fckl, dtype, N, V, L, B):
+    """Histories on both sides of what the table of touched tokens takes, into a tensor, in place and off the
+    vectors' boundaries, and the gradient."""
+    z, g = logits(N, V, dtype, N + V), logits(N, V, dtype, N + V + 1)
+    for allowed in (None, 0.9):
+        k = rules(N, V, L, B, V + L, allowed)
+        got = check_adjust(fckl, z, k)
+        own = z.clone()
+        assert torch.equal(fckl.adjust_logits(own, out=own, **k), got)
+        off = place(torch.zeros(N, V, dtype=DT[dtype]), 3, 1, 7.0)
+        assert torch.equal(fckl.adjust_logits(z, out=off, **k), got)
+        d = check_gradient(fckl, g, z, k)
+        kk = {n: k[n] for n in ("history", "lengths", "repetition", "allowed") if n in k}
+        own = g.clone()
+        assert torch.equal(fckl.adjust_logits_backward(own, z, out=own, **kk), d)
+        only = {n: k[n] for n in kk if n != "repetition"}
+        got = check_adjust(fckl, z, dict(only, repetition=1.5))
+        own = z.clone()
+        assert torch.equal(fckl.adjust_logits(own, out=own, repetition=1.5, **only), got)
+
+
+@gpu
+def test_biases_of_one_token(fckl):
+    """A token's several biases are added in their order: all slots one token, and pairs far apart."""
+    z = logits(2, 3000, "fp32", 1)
+    b = torch.randn(2, 1024, device="cuda")
+    t = torch.full((2, 1024), 2999, dtype=torch.int32, device="cuda")
+    t[1] = torch.arange(1024, device="cuda").remainder(512).int()
+    got = fckl.adjust_logits(z, bias_tokens=t, bias=b)
+    want = z.clone()
+    total = np.float32(0)
+    for x in b[0].cpu().numpy():
+        total = np.float32(total + x)
+    want[0, 2999] += float(total)
+    want[1, :512] += b[1, :512] + b[1, 512:]
+    assert torch.equal(got, want)
+    own = z.clone()
+    assert torch.equal(fckl.adjust_logits(own, bias_tokens=t, bias=b, out=own), want)
+
+
+@gpu
 def test_histories_that_meet_the_limits(fckl):
     """Lengths and prompts outside the row are held to it; a token repeated throughout; a long history."""
     N, V, L = 4, 300, 65

@@ -164,6 +164,7 @@ def test_lookup_of_extreme_values(fckl):
     (1, 1, 1, "one"), (1, 2880, 7, "texts"), (7, 8, 3, "texts"), (9, 33, 50, "different"), (64, 40, 64, "one"),
     (65, 40, 3, "empty"), (130, 1030, 513, "texts"), (1000, 24, 2, "texts"), (777, 1022, 100, "texts"),
     (5000, 8, 700, "one"), (9000, 4, 1 << 18, "texts"), (20000, 6, 300, "texts"), (70000, 2, 1000, "texts"),
+    (300, 776, 40, "texts"), (260, 2880, 90, "texts"), (129, 1536, 1, "one"), (2000, 96, 7, "texts"),
 ])
 def test_gradient(fckl, dtype, out, N, d, V, kind):
     """Sizes around a warp, a tile and a sorting block, and more positions than one round of the cluster."""
@@ -190,17 +191,26 @@ def test_gradient_vocabulary_sizes(fckl, V):
 
 
 @gpu
-@pytest.mark.parametrize("N", [8192, 8193, 65536, 65537, 300001])
-def test_gradient_every_position_once(fckl, N):
-    """Around the sizes of the sort's rounds: exact sums of whole numbers, so that a lost or doubled position shows."""
-    V = 1237
-    tokens = draw_tokens(N, V, N)
-    g = torch.arange(N, device="cuda", dtype=torch.float32).remainder(61).view(N, 1) - 30
-    dW = fckl.embedding_backward(g, tokens, V)
-    want = torch.zeros(V, 1, device="cuda", dtype=torch.float64)
-    want.index_add_(0, tokens.clamp(min=0).long(), torch.where(tokens[:, None] < 0, 0.0, g).double())
-    assert torch.equal(dW.double(), want)
-    assert torch.equal(fckl.embedding_backward(g, tokens, V), dW)
+@pytest.mark.parametrize("d", [1, 4])
+@pytest.mark.parametrize("N", [31, 33, 255, 257, 1023, 1025, 8192, 8193, 65536, 65537, 131073, 300001])
+def test_gradient_every_position_once(fckl, N, d):
+    """Around the sizes of a warp's entries, of the tiles, of the clusters and of the sort's rounds: exact sums
+    of whole numbers, so that a lost or doubled position shows. Frequent and rare tokens, one that takes a
+    third of the positions, one alone, and all different; the sums of at most 300001 numbers up to 30 stay
+    below 2^24."""
+    V = 1237 if N < 1e5 else 1 << 19
+    g = torch.arange(N * d, device="cuda", dtype=torch.float32).remainder(61).view(N, d) - 30
+    often = draw_tokens(N, V, N)
+    often[::3] = V // 2
+    for tokens in (draw_tokens(N, V, N), often, draw_tokens(N, V, 1, "one"), draw_tokens(N, V, 1, "different")):
+        dW = fckl.embedding_backward(g, tokens, V)
+        want = torch.zeros(V, d, device="cuda", dtype=torch.float64)
+        want.index_add_(0, tokens.clamp(min=0).long(), torch.where(tokens[:, None] < 0, 0.0, g).double())
+        assert torch.equal(dW.double(), want)
+        assert torch.equal(fckl.embedding_backward(g, tokens, V), dW)
+        old = torch.ones(V, d, device="cuda")
+        assert torch.equal(fckl.embedding_backward(g, tokens, V, dW=old, accumulate=True).double(), want + 1)
+    assert fckl.check() == fckl.OK
 
 
 @gpu
