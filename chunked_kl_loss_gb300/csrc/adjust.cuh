@@ -279,13 +279,13 @@ struct AdjustRow {
 // barrier of the block stands in the stream. The threads change the touched and the masked places in the
 // stages: what no rule touches passes through no register, and a touched place costs no access to
 // memory. Two blocks an SM: one gathers while the other streams.
-// Bound by memory, and by the gather's latency where few blocks share an SM: 4096 x 128256 bf16 without rules
-// 306 us (a plain copy's time), with a mask 319, with 1024 history entries 318, with both 339, with 16 biases
-// too 362 (floor 325; 150 instructions a warp and vector, 2.7 a cycle); the gradient, which reads the logits
-// at the history's tokens, 378. Before: a word in shared
-// memory for every token 1070 us, rows through registers with the touched places written again afterwards
-// 437 to 451, one ring to a block with a barrier for every stage 418. 96 vectors and 3 stages: 2 stages 15%
-// more, 64 vectors 5%, 4 stages of 128 vectors (one block an SM less) 30%.
+// Bound by memory: 4096 x 128256 bf16 without rules 306 us (a plain copy's time), with a mask 317, with 1024
+// history entries, 16 biases and a mask 328 (floor 325); the gradient, which reads the logits at the history's
+// tokens from all over the row before it streams, 372. Before: a word in shared memory for every token 1070
+// us; rows through registers with the touched places written again afterwards 437 to 451; one ring to a
+// block with a barrier for every stage 418; the touched and masked places of each vector for itself instead
+// of the lane's three vectors at once 362 (150 instructions a warp and vector, 2.7 a cycle). Of 96 vectors
+// and 3 stages: 2 stages 15% more, 64 vectors 5%, 4 stages of 128 vectors (one block an SM less) 30%.
 template <typename T, AdjustKind KIND, int NT>
 __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p) {
   constexpr int VE = 16 / sizeof(T);
@@ -362,39 +362,41 @@ __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p)
   uint32_t phase = 0;
   for (; k < tiles; ++k) {
     uint4* data = reinterpret_cast<uint4*>(ring + stage * TV * 16);
-    uint32_t off[U];  // places that are not allowed
-#pragma unroll
-    for (int u = 0; u < U; ++u) off[u] = allowed ? ~__funnelshift_r(lo[u], hi[u], mask_shift) & ALL : 0u;
-    mask += STEP;
-    if (allowed && k + 1 < tiles) fetch_bits(wb - tile_at(k + 1) - lane);
-    const bool ok = drain_phase(&full[stage], phase, p.status);
+    // The lane's places of the tile, a bit each: those that are not allowed, and of the others the touched ones.
+    static_assert(U * VE <= 32, "");
     const int left = wb - tile_at(k) - lane;
+    uint32_t off = 0, touched = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u * 32 >= left) break;
-      const int q = u * 32 + lane;
-      T* at = reinterpret_cast<T*>(data + q);
-      uint32_t touched = (seen[u * VE] >> seen_shift) & ALL & ~off[u];
-      while (touched) {
-        const int j = __ffs(touched) - 1;
-        touched &= touched - 1;
-        at[j] = from_f32<T>(value(to_f32(at[j]), column(tile_at(k) + q) + j));
+      if (allowed) off |= (~__funnelshift_r(lo[u], hi[u], mask_shift) & ALL) << (u * VE);
+      touched |= ((seen[u * VE] >> seen_shift) & ALL) << (u * VE);
+    }
+    touched &= ~off;
+    mask += STEP;
+    if (allowed && k + 1 < tiles) fetch_bits(wb - tile_at(k + 1) - lane);
+    const bool ok = drain_phase(&full[stage], phase, p.status);
+    T* mine = reinterpret_cast<T*>(data + lane);  // place i at value i / VE * 32 VE + i % VE
+    for (; touched; touched &= touched - 1) {
+      const int i = __ffs(touched) - 1, e = i / VE * 32 * VE + i % VE;
+      mine[e] = from_f32<T>(value(to_f32(mine[e]), column(tile_at(k) + lane) + e));
+    }
+    if (__popc(off) <= 4) {
+      for (; off; off &= off - 1) {
+        const int i = __ffs(off) - 1;
+        mine[i / VE * 32 * VE + i % VE] = from_f32<T>(GRAD ? 0.f : -INFINITY);
       }
-      if (off[u] == ALL) {
-        const uint32_t none = GRAD ? 0u : fill_word<T>(-INFINITY);
-        data[q] = make_uint4(none, none, none, none);
-      } else if (__popc(off[u]) > 2) {
-        uint4 d = data[q];
-        d.x = masked_word<T, GRAD>(d.x, ~off[u], 0);
-        d.y = masked_word<T, GRAD>(d.y, ~off[u], 1);
-        d.z = masked_word<T, GRAD>(d.z, ~off[u], 2);
-        d.w = masked_word<T, GRAD>(d.w, ~off[u], 3);
-        data[q] = d;
-      } else {
-        while (off[u]) {
-          at[__ffs(off[u]) - 1] = from_f32<T>(GRAD ? 0.f : -INFINITY);
-          off[u] &= off[u] - 1;
-        }
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t m = (off >> (u * VE)) & ALL;
+        if (!m) continue;
+        uint4 d = m == ALL ? make_uint4(0, 0, 0, 0) : data[u * 32 + lane];
+        d.x = masked_word<T, GRAD>(d.x, ~m, 0);
+        d.y = masked_word<T, GRAD>(d.y, ~m, 1);
+        d.z = masked_word<T, GRAD>(d.z, ~m, 2);
+        d.w = masked_word<T, GRAD>(d.w, ~m, 3);
+        data[u * 32 + lane] = d;
       }
     }
     seen += STEP;

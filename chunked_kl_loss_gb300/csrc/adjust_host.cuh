@@ -82,7 +82,7 @@ AdjustPlan adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool strea
         const size_t smem = adjust_smem(vecs * VE, rings, sets, WORDS, table ? log2 : -1, p.B);
         if (smem > ADJUST_SMEM) continue;
         // blocks of an SM: by shared memory, and 64 registers a thread
-        const int64_t resident = std::min<int64_t>(1024 / threads + (STAGED && threads == 512), (227 << 10) / int64_t(smem + 1536));
+        const int64_t resident = std::min<int64_t>(1024 / threads, (227 << 10) / int64_t(smem + 1536));
         const int64_t blocks = N * segs, on_sm = std::min(resident, cdiv(blocks, di->sms));
         const double gather = 2.5 + double(cdiv(p.L, threads * 8)) +
                               (WORDS && table ? 0.6 : 0.3) * double(p.L) / double(threads * segs) +
