@@ -281,7 +281,7 @@ struct AdjustRow {
 // memory. Two blocks an SM: one gathers while the other streams.
 // Bound by memory: 4096 x 128256 bf16 without rules 306 us (a plain copy's time), with a mask 317, with 1024
 // history entries, 16 biases and a mask 328 (floor 325); the gradient, which reads the logits at the history's
-// tokens from all over the row before it streams, 372. Before: a word in shared memory for every token 1070
+// tokens from all over the row before it streams, 372 (374 with those read ahead of the first barrier). Before: a word in shared memory for every token 1070
 // us; rows through registers with the touched places written again afterwards 437 to 451; one ring to a
 // block with a barrier for every stage 418; the touched and masked places of each vector for itself instead
 // of the lane's three vectors at once 362 (150 instructions a warp and vector, 2.7 a cycle). Of 96 vectors

@@ -358,8 +358,8 @@ int fckl_embedding_backward(const void* g, int dtype, int64_t ldg, const int32_t
 /* Norm of `count` gradient tensors: norm[0] = sqrt(sum of all elements' squares), fp32. grads, sizes and
  * dtypes are host arrays (read before the call returns) of device addresses, numbers of elements and types
  * (FCKL_BF16, FCKL_F16 or FCKL_F32, mixed at will); a tensor's elements are dense, aligned to their own
- * size; a size of 0 is skipped. Squares are summed in fp32 within 8192 elements and in fp64 beyond, and in
- * fp64 throughout where fp32 would overflow or lose them; a norm above fp32's largest number is inf, one
+ * size; a size of 0 is skipped. Squares are summed in fp32 over 32 elements at a time and in fp64 beyond,
+ * and in fp64 throughout where fp32 would overflow or lose them; a norm above fp32's largest number is inf, one
  * over a NaN is NaN. At most 2^20 tensors. */
 size_t fckl_gradient_norm_workspace_bytes(int64_t count);
 int fckl_gradient_norm(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, float* norm,
