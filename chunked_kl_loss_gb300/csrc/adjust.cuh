@@ -281,10 +281,10 @@ struct AdjustRow {
 // memory. Two blocks an SM: one gathers while the other streams.
 // Bound by memory: 4096 x 128256 bf16 without rules 306 us (a plain copy's time), with a mask 317, with 1024
 // history entries, 16 biases and a mask 328 (floor 325); the gradient, which reads the logits at the history's
-// tokens from all over the row before it streams, 372 (374 with those read ahead of the first barrier). Before: a word in shared memory for every token 1070
-// us; rows through registers with the touched places written again afterwards 437 to 451; one ring to a
-// block with a barrier for every stage 418; the touched and masked places of each vector for itself instead
-// of the lane's three vectors at once 362 (150 instructions a warp and vector, 2.7 a cycle). Of 96 vectors
+// tokens from all over the row before it streams, 372 (374 with those read before the first barrier).
+// Before: a word in shared memory for every token 1070 us; rows through registers with the touched places
+// written again afterwards 437 to 451; one ring to a block with a barrier for every stage 418; the touched
+// and masked places of each vector for itself instead of the lane's three vectors at once 362. Of 96 vectors
 // and 3 stages: 2 stages 15% more, 64 vectors 5%, 4 stages of 128 vectors (one block an SM less) 30%.
 template <typename T, AdjustKind KIND, int NT>
 __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p) {
@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p)
   const T* x = GRAD ? static_cast<const T*>(p.g) + row * p.ld_g : static_cast<const T*>(p.z) + row * p.ld_z;
   const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
   T* out = static_cast<T*>(p.out) + row * p.ld_out;
-  const AdjustSegment s = adjust_segment<T, VE, KIND, true>(p, out, blockIdx.x % p.segs,
-                                                            reinterpret_cast<uint32_t*>(adj_stage + p.stages * WARPS * ADJUST_STAGE_BYTES));
+  uint32_t* after_rings = reinterpret_cast<uint32_t*>(adj_stage + p.stages * WARPS * ADJUST_STAGE_BYTES);
+  const AdjustSegment s = adjust_segment<T, VE, KIND, true>(p, out, blockIdx.x % p.segs, after_rings);
   if (s.v0 >= s.v1) return;
   // Whole vectors [wa, wb), in tiles of a stage that the warps take in turn; the row's ends, if they are
   // ragged, go value by value.

@@ -47,10 +47,11 @@ size_t adjust_smem(int64_t tokens, int rings, int sets, bool words, int slots_lo
 // How the work is cut: into how many segments a row, with the table of touched tokens or a word for each,
 // and in the staged kernel with how many threads and stages. Taken is the least estimated time, in us, of
 // waves of blocks that each gather first (2.5 us, 1 us for every 8 history entries a thread reads, 0.6 us
-// for each that it puts into the table or 0.3 into words, 1 us for every 64 KB of shared memory cleared) and then stream at their share of an SM's 44 GB/s. From 1 x 201088 to
-// 4096 x 128256 the estimates are 20 to 35% below what is measured, all alike; 64 x 50001 fp32 with 16384
-// history entries: 4 segments and 2 stages 15.8 us, 8 segments 24, 3 stages 23; 16 x 128256 with 4000: 1, 4
-// and 16 segments 29, 12 and 7.6.
+// for each that it puts into the table or 0.3 into words, 1 us for every 64 KB of shared memory cleared)
+// and then stream at their share of an SM's 44 GB/s. The estimates are mostly 10 to 40% below what is
+// measured, alike for the choices of one shape: 64 x 50001 fp32 with 16384 history entries in 4 segments and
+// 2 stages 14 us, in 8 segments 24, with 3 stages 23; 16 x 128256 with 4000 in 1, 4 and 16 segments 29, 12
+// and 7.6.
 struct AdjustPlan {
   size_t smem = 0;
   int threads = 0;

@@ -70,9 +70,9 @@ __global__ void __launch_bounds__(EMBED_THREADS, EMBED_BLOCKS)
 // ---------------------------------------------------------------- positions in the order of their tokens
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_ITEMS = 8192 / SORT_THREADS;                 // per thread and tile
+constexpr int SORT_ITEMS = 16;  // per thread and tile
 constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;
-constexpr int SORT_BITS = 9;                         // of a digit at most
+constexpr int SORT_BITS = 9;    // of a digit at most
 constexpr int SORT_BINS = 1 << SORT_BITS;
 constexpr int SORT_CLUSTER_MAX = 16;
 
@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortPar
 // ---------------------------------------------------------------- sums by token
 constexpr int GSUM_THREADS = 128;
 constexpr int GSUM_TILE_MAX = 64;  // entries of a tile at most
-constexpr int GSUM_AHEAD = 2;    // rows loaded ahead
-constexpr int GJOIN_GROUPS = 4;   // of threads that share a long run's tiles
+constexpr int GSUM_AHEAD = 2;      // rows loaded ahead
+constexpr int GJOIN_GROUPS = 4;    // of threads that share a long run's tiles
 
 struct EmbedGradParams {
   const uint2* list;  // (token, position) in order
@@ -585,8 +585,8 @@ __global__ void __launch_bounds__(GSUM_THREADS * GJOIN_GROUPS) embedding_grad_jo
   __shared__ float part[GJOIN_GROUPS - 1][GSUM_THREADS * E];
   const int tile = static_cast<int>(blockIdx.x), tid = threadIdx.x;
   const int64_t e0 = int64_t(tile) * p.tile, e1 = e0 + p.tile;
-  if (e1 >= p.N) return;
   wait_for_previous();
+  if (e1 >= p.N) return;
   const unsigned v = p.list[e1 - 1].x, next = p.list[e1].x, first = p.list[e0].x, earlier = p.list[max(e0 - 1, int64_t(0))].x;
   if (v == static_cast<unsigned>(p.V) || next != v) return;  // nothing crosses the end
   if (first == v && e0 > 0 && earlier == v) return;          // it began before

@@ -123,7 +123,8 @@ def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=1.
     if not _here_all(logits, history, lengths, prompt, r, f, p, bias_tokens, bias, allowed, out):
         _on_device(dev, logits=logits, history=history, lengths=lengths, prompt=prompt, repetition=r, frequency=f,
                    presence=p, bias_tokens=bias_tokens, bias=bias, allowed=allowed, out=out)
-    with _here if stream is None else _for_stream(stream, logits, history, lengths, prompt, r, f, p, bias_tokens, bias, allowed, out, ws):
+    used = (logits, history, lengths, prompt, r, f, p, bias_tokens, bias, allowed, out, ws)
+    with _here if stream is None else _for_stream(stream, *used):
         ws = _ws(ws, dev)
         if out is None:
             out = torch.empty(N, V, dtype=logits.dtype, device=dev)
