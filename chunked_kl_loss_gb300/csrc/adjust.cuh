@@ -273,7 +273,7 @@ struct AdjustRow {
   }
 };
 
-// Into another tensor whose rows lie alike to the 16-byte boundaries. One block per (row, segment of
+// Into rows that lie alike to the 16-byte boundaries, or in place under a mask. One block per (row, segment of
 // seg_vecs vectors). The segment streams through shared memory by bulk copies, which are under way while
 // the threads gather the segment's touched tokens: every warp has a ring of stages of its own, so that no
 // barrier of the block stands in the stream. The threads change the touched and the masked places in the
@@ -432,18 +432,18 @@ __global__ void __launch_bounds__(NT) adjust_staged_kernel(const AdjustParams p)
   if (lane == 0) bulk_wait_read<0>();
 }
 
-// In place, or into rows that lie differently: the segment is copied under the mask (in place: masked tokens
-// are written and nothing is read), then the touched places are written again, each by one thread, from the
-// logits as they came in. In place a call is all latency: 1 x 201088 with 1500 history entries 5.5 us in 8
-// segments or so (8.9 in one), 256 x 128256 with 16000 68 us (154 with every token's word looked through
-// instead of a set of bits).
+// In place without a mask, or into rows that lie differently: the segment is copied under the mask (in place
+// there is nothing to copy), then the touched places are written again, each by one thread, from the logits as
+// they came in. In place a call is all latency: 1 x 201088 with 1500 history entries 5.5 us in 8 segments or so
+// (8.9 in one), 256 x 128256 with 16000 62 us (154 with every token's word looked through instead of a set
+// of bits).
 template <typename T, int VE, AdjustKind KIND, bool IN_PLACE>
 __global__ void __launch_bounds__(ADJUST_THREADS, 2) adjust_kernel(const AdjustParams p) {
   static_assert(IN_PLACE || VE == 1, "");
-  constexpr bool GRAD = KIND == ADJUST_GRAD;
   extern __shared__ __align__(16) uint32_t adj_smem[];
   const int64_t row = blockIdx.x / p.segs;
   const int tid = threadIdx.x;
+  constexpr bool GRAD = KIND == ADJUST_GRAD;
   const T* x = GRAD ? static_cast<const T*>(p.g) + row * p.ld_g : static_cast<const T*>(p.z) + row * p.ld_z;
   const T* z = static_cast<const T*>(p.z) + row * p.ld_z;
   T* out = static_cast<T*>(p.out) + row * p.ld_out;
@@ -452,43 +452,28 @@ __global__ void __launch_bounds__(ADJUST_THREADS, 2) adjust_kernel(const AdjustP
   adjust_gather<T, KIND, false, ADJUST_THREADS>(p, s, row, z);
   if (GRAD) __syncthreads();  // the logits' signs are read: out may be the logits
 
-  const uint32_t* allowed = p.allowed ? p.allowed + row * p.ld_allowed : nullptr;
+  const uint32_t* allowed = !IN_PLACE && p.allowed ? p.allowed + row * p.ld_allowed : nullptr;
   const T none = from_f32<T>(GRAD ? 0.f : -INFINITY);
   auto bit = [&](int c) { return !allowed || ((allowed[c >> 5] >> (c & 31)) & 1u); };
-  constexpr uint32_t ALL = (1u << VE) - 1u;
   constexpr int U = ADJUST_UNROLL;
-  if (!IN_PLACE || allowed) {
-    for (int i0 = s.v0 + tid; i0 < s.v1; i0 += U * ADJUST_THREADS) {
+  if constexpr (!IN_PLACE) {
+    for (int c0 = s.v0 + tid; c0 < s.v1; c0 += U * ADJUST_THREADS) {
       // Every load of the step is issued before any of them is used.
       T d[U];
-      uint32_t lo[U], hi[U];
+      uint32_t m[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * ADJUST_THREADS, c = i * VE - s.mis;
-        if (!IN_PLACE && i < s.v1) d[u] = x[c];
-        lo[u] = hi[u] = ~0u;
-        if (allowed && i < s.v1) {
-          lo[u] = allowed[max(c, 0) >> 5];
-          if (VE > 1) hi[u] = allowed[min(c + VE - 1, p.V - 1) >> 5];
+        const int c = c0 + u * ADJUST_THREADS;
+        m[u] = ~0u;
+        if (c < s.v1) {
+          d[u] = x[c];
+          if (allowed) m[u] = allowed[c >> 5];
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * ADJUST_THREADS, c = i * VE - s.mis;
-        if (i >= s.v1) break;
-        if constexpr (!IN_PLACE) {
-          out[c] = (lo[u] >> (c & 31)) & 1u ? d[u] : none;
-        } else {
-          // before the row's start (c < 0) and behind its end nothing is masked
-          uint32_t off = c < 0 ? ~lo[u] << -c : ~__funnelshift_r(lo[u], hi[u], c & 31);
-          off &= ALL >> max(0, c + VE - p.V);
-          if (off == ALL) {
-            const uint32_t w = GRAD ? 0u : fill_word<T>(-INFINITY);
-            *reinterpret_cast<uint4*>(out + c) = make_uint4(w, w, w, w);
-          } else {
-            for (; off; off &= off - 1) out[c + __ffs(off) - 1] = none;
-          }
-        }
+        const int c = c0 + u * ADJUST_THREADS;
+        if (c < s.v1) out[c] = (m[u] >> (c & 31)) & 1u ? d[u] : none;
       }
     }
   }

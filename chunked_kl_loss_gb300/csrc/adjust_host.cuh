@@ -109,7 +109,7 @@ AdjustPlan adjust_plan(const DevInfo* di, AdjustParams& p, int64_t N, bool strea
 template <typename T, int VE, AdjustKind KIND, bool IN_PLACE, bool STAGED>
 int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s) {
   constexpr bool GRAD = KIND == ADJUST_GRAD;
-  const AdjustPlan plan = adjust_plan<VE, KIND, STAGED>(di, p, N, !IN_PLACE || p.allowed);
+  const AdjustPlan plan = adjust_plan<VE, KIND, STAGED>(di, p, N, !IN_PLACE);
   if (!plan.threads) return FCKL_ERR_UNSUPPORTED;
   void (*k)(AdjustParams);
   if constexpr (STAGED)
@@ -154,7 +154,9 @@ int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s)
   return FCKL_OK;
 }
 
-// Through shared memory where every row of the input and of the output lies alike to the 16-byte boundaries.
+// Through shared memory where every row of the input and of the output lies alike to the 16-byte boundaries;
+// in place too if there is a mask (2000 x 50000 bf16 with 2% masked: 97 us; writing the masked places for
+// themselves, without reading the others, took 111, and 72 against 78 at 1024 x 50000 fp32 with 0.4% left).
 template <typename T, AdjustKind KIND>
 int launch_adjust(DevInfo* di, const AdjustParams& p, int64_t N, cudaStream_t s) {
   constexpr bool GRAD = KIND == ADJUST_GRAD;
@@ -162,7 +164,7 @@ int launch_adjust(DevInfo* di, const AdjustParams& p, int64_t N, cudaStream_t s)
   const void* x = GRAD ? p.g : p.z;
   const int64_t ld = GRAD ? p.ld_g : p.ld_z;
   constexpr int VE = 16 / sizeof(T);
-  if (x == p.out) return launch_adjust_kernel<T, VE, FULL, true, false>(di, p, N, s);
+  if (x == p.out && !p.allowed) return launch_adjust_kernel<T, VE, FULL, true, false>(di, p, N, s);
   const bool alike = (reinterpret_cast<uintptr_t>(x) & 15u) == (reinterpret_cast<uintptr_t>(p.out) & 15u) &&
                      (N == 1 || (ld - p.ld_out) % VE == 0);
   if (alike) return launch_adjust_kernel<T, VE, KIND, false, true>(di, p, N, s);

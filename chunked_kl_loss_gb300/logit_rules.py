@@ -92,8 +92,8 @@ def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=1.
     """Logits [N, V] under each row's rules, of the logits' type. A token of the history: z / repetition
     where z > 0, else z * repetition; a generated one: less frequency times its number and less presence;
     then the sum of its biases (``bias_tokens`` int32 [N, B], -1 empty, and ``bias`` fp32 [N, B]); -inf
-    where it is not allowed. ``out`` may be ``logits``: only what a rule changes is then touched. An id
-    outside [-1, V) is skipped and reported by check()."""
+    where it is not allowed. ``out`` may be ``logits``: without a mask only what a rule changes is then
+    touched. An id outside [-1, V) is skipped and reported by check()."""
     import torch
     if logits.dim() != 2:
         raise ValueError("expected logits [N,V]")
@@ -141,7 +141,7 @@ def adjust_logits_backward(g, logits, history=None, lengths=None, repetition=1.0
                            stream=None):
     """Gradient [N, V] with respect to the logits that went into adjust_logits, of the upstream gradient g
     [N, V] (of the logits' type): times the repetition penalty's slope at the history's tokens, 0 where a
-    token is not allowed. ``out`` may be ``g``: only what changes is then touched."""
+    token is not allowed. ``out`` may be ``g``: without a mask only what changes is then touched."""
     import torch
     if logits.dim() != 2 or g.shape != logits.shape:
         raise ValueError("expected logits [N,V] and g [N,V]")

@@ -384,8 +384,8 @@ int fckl_clip_gradients(const void* const* grads, const int64_t* sizes, const in
  * added in their order. allowed: bits, bit v % 32 of word v / 32, rows ld_allowed words apart (0: one row
  * for all); NULL: every token. A row may allow none.
  * logits and out are [N, V] of one type (FCKL_BF16, FCKL_F16 or FCKL_F32), rows ld and ld_out elements
- * apart. out may be logits (then ld_out = ld): only the places that a rule changes are then read or
- * written; otherwise the two must not overlap. Arithmetic is fp32, rounded once; a place that no rule
+ * apart. out may be logits (then ld_out = ld), and without a mask only the places that a rule changes are
+ * then read or written; otherwise the two must not overlap. Arithmetic is fp32, rounded once; a place that no rule
  * touches keeps its bits. L <= 1048575, B <= 1024, V <= 2^30. An id outside [-1, V) sets FCKL_ERR_INDEX and is
  * skipped. The workspace holds only the status word. N = 0 is allowed. */
 int fckl_adjust_logits(const void* logits, int dtype, int64_t ld, int64_t N, int V, const int32_t* history, int64_t ld_h,
