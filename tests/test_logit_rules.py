@@ -154,6 +154,8 @@ def test_gradient(fckl, dtype, N, V, L, B):
         own, zz = g.clone(), z.clone()
         assert fckl.adjust_logits_backward(own, z, out=own, **kk) is own and torch.equal(own, got)
         assert fckl.adjust_logits_backward(g, zz, out=zz, **kk) is zz and torch.equal(zz, got)
+        one = z.clone()  # all three the same tensor
+        assert torch.equal(fckl.adjust_logits_backward(one, one, out=one, **kk), fckl.adjust_logits_backward(z, z, **kk))
 
 
 @gpu
