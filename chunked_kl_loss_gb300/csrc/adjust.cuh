@@ -11,26 +11,14 @@
 
 #include <type_traits>
 
+#include "adjust_plan.h"
 #include "bulk.cuh"
 #include "score.cuh"
 
 namespace fckl {
 
-constexpr int ADJUST_THREADS = 512;
 constexpr int ADJUST_UNROLL = 8;      // vectors that a thread has under way
 constexpr int ADJUST_AHEAD = 8;       // history entries that a thread has under way
-constexpr int ADJUST_STAGED_THREADS = 512;  // of a block, or for short segments
-constexpr int ADJUST_STAGED_FEW = 128;
-constexpr int ADJUST_STAGES = 3;       // of each warp's ring in the staged kernel at most
-constexpr int ADJUST_STAGE_VECS = 96;  // vectors of a stage (1.5 KB)
-constexpr int ADJUST_STAGE_BYTES = ADJUST_STAGE_VECS * 16;
-
-// What a row's rules have to know of its history.
-enum AdjustKind {
-  ADJUST_COUNTS,  // counts and biases too
-  ADJUST_SEEN,    // which tokens stand in it: the repetition penalty alone
-  ADJUST_GRAD     // the same, and the signs of their logits
-};
 
 // What shared memory holds for a token that a rule touches: how often it was generated, whether it stands
 // in the prompt, and TOKENS_MAX less the bias slot that carries the sum of its biases (0: none).

@@ -26,6 +26,7 @@
 #include "../../include/fckl.h"
 #include "score_gemm.cuh"
 #include "simt.cuh"
+#include "sizes.h"
 #include "tc_gemm.cuh"
 
 namespace fckl {
@@ -241,9 +242,6 @@ int make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t 
 
 // ------------------------------------------------------------------ plan / workspace
 constexpr int MAX_SPLITS = 4;    // K-splits of the dH product
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t rup(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
 struct Plan {
   int64_t N;
