@@ -47,6 +47,8 @@ struct AdjustPlan {
   int segs = 0, seg_vecs = 0;  // segments of a row, vectors of a segment
   int stages = 0;              // of a warp's ring in the staged kernel
   int slots_log2 = 0;          // of the table of touched tokens; < 0: one word for every token of the segment
+  int resident = 0;            // blocks that run on an SM at once
+  double us = 0;               // estimated time
 };
 
 // How the work is cut: into how many segments a row, with the table of touched tokens or a word for each,
@@ -83,8 +85,10 @@ AdjustPlan adjust_plan(int sms, int64_t N, int V, int L, int B, bool streams) {
         const int sets = STAGED && KIND == ADJUST_GRAD ? 2 : STAGED || !table ? 1 : 0;  // of bits
         const size_t smem = adjust_smem(vecs * VE, rings, sets, WORDS, table ? log2 : -1, B);
         if (smem > ADJUST_SMEM) continue;
-        // blocks of an SM: by shared memory, and 64 registers a thread
-        const int64_t resident = std::min<int64_t>(1024 / threads, (227 << 10) / int64_t(smem + 1536));
+        // blocks of an SM: by shared memory, and 64 registers a thread. 1.5 KB a block is more than it takes
+        // beside its dynamic part (1 KB and the barriers), so the last blocks that fit would count as none.
+        const int64_t by_smem = std::max<int64_t>(1, (227 << 10) / int64_t(smem + 1536));
+        const int64_t resident = std::min<int64_t>(1024 / threads, by_smem);
         const int64_t blocks = N * segs, on_sm = std::min(resident, cdiv(blocks, sms));
         const double gather = 2.5 + double(cdiv(L, threads * 8)) +
                               (WORDS && table ? 0.6 : 0.3) * double(L) / double(threads * segs) +
@@ -95,7 +99,8 @@ AdjustPlan adjust_plan(int sms, int64_t N, int V, int L, int B, bool streams) {
         const double us = double(cdiv(blocks, resident * sms)) * (gather + stream);
         if (us < 0.98 * best) {
           best = us;
-          plan = {smem, threads, static_cast<int>(segs), static_cast<int>(vecs), stages, table ? log2 : -1};
+          plan = {smem, threads, static_cast<int>(segs), static_cast<int>(vecs), stages, table ? log2 : -1,
+                  static_cast<int>(resident), us};
         }
       }
     }

@@ -260,6 +260,21 @@ def test_long_histories(fckl, dtype, N, V, L, B):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("N,V,L,B", [(1, 201088, 8192, 100), (16, 201088, 8192, 100), (2, 182000, 8000, 300), (2, 210000, 8000, 0),
+                                     (1, 112000, 8000, 1024), (2, 128256, 8000, 860)])
+def test_long_histories_that_fill_shared_memory(fckl, dtype, N, V, L, B):
+    """The largest table of touched tokens, its bits and biases at the size where, with every stage, they just
+    fill a block's shared memory in one segment: into a new tensor, and in place with and without a mask."""
+    z = logits(N, V, dtype, N + V)
+    for allowed in (None, 0.9):
+        k = rules(N, V, L, B, V + L, allowed)
+        got = check_adjust(fckl, z, k)
+        own = z.clone()
+        assert torch.equal(fckl.adjust_logits(own, out=own, **k), got)
+
+
+@gpu
 def test_biases_of_one_token(fckl):
     """A token's several biases are added in their order: all slots one token, and pairs far apart."""
     z = logits(2, 3000, "fp32", 1)
