@@ -16,7 +16,7 @@ import ctypes
 import weakref
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _for_stream, _here, _stream, _value_code
+from .scoring import _for_stream, _here, _stream, _value_code, _written
 
 __all__ = ["gradient_norm", "clip_gradients"]
 
@@ -143,4 +143,5 @@ def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
                                          _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_clip_gradients")
+    _written(*(grads if out is None else out))
     return norm

@@ -19,7 +19,7 @@ from __future__ import annotations
 import ctypes
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _address, _dense, _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _ws
+from .scoring import _address, _dense, _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _written, _ws
 
 __all__ = ["adjust_logits", "adjust_logits_backward", "differentiable_adjusted_logits"]
 
@@ -116,8 +116,8 @@ def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=1.
         _dense("bias_tokens", bias_tokens, torch.int32, (N, B))
         _dense("bias", bias, torch.float32, (N, B))
     lda = _bits(allowed, N, V)
-    ldo = V
-    if out is not None:
+    ldo, given = V, out is not None
+    if given:
         ldo = _out(out, logits)
     dev = logits.device
     if not _here_all(logits, history, lengths, prompt, r, f, p, bias_tokens, bias, allowed, out):
@@ -134,6 +134,8 @@ def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=1.
                                         ldo, ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_adjust_logits")
+    if given:
+        _written(out)
     return out
 
 
@@ -155,8 +157,8 @@ def adjust_logits_backward(g, logits, history=None, lengths=None, repetition=1.0
     if r is None and not r1 > 0:
         raise ValueError(f"repetition must be positive, got {r1}")
     lda = _bits(allowed, N, V)
-    ldo = V
-    if out is not None:
+    ldo, given = V, out is not None
+    if given:
         ldo = _out(out, logits)
     dev = logits.device
     if not _here_all(logits, g, history, lengths, r, allowed, out):
@@ -171,6 +173,8 @@ def adjust_logits_backward(g, logits, history=None, lengths=None, repetition=1.0
                                                  ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_adjust_logits_backward")
+    if given:
+        _written(out)
     return out
 
 

@@ -17,7 +17,7 @@ import ctypes
 import weakref
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _ws
+from .scoring import _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _written, _ws
 
 __all__ = ["embedding", "embedding_backward", "differentiable_embedding"]
 
@@ -65,7 +65,8 @@ def embedding(W, tokens, scale=1.0, out=None, ws=None, stream=None):
     N = _tokens(tokens)
     ldw = d if W.is_contiguous() else _rows("W", W)
     dev = W.device
-    if out is not None:
+    given = out is not None
+    if given:
         if out.dtype != W.dtype:
             raise TypeError(f"out must be {W.dtype}, got {out.dtype}")
         ldo = _row_matrix("out", out, tokens, d)
@@ -79,6 +80,8 @@ def embedding(W, tokens, scale=1.0, out=None, ws=None, stream=None):
                                     ws.tensor.data_ptr(), ws.nbytes, _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_embedding")
+    if given:
+        _written(out)
     return out
 
 
@@ -96,7 +99,8 @@ def embedding_backward(g, tokens, V, scale=1.0, dW=None, accumulate=False, dtype
     ldg = _row_matrix("g", g, tokens, d)
     if accumulate and dW is None:
         raise ValueError("accumulate needs the dW that is added to")
-    if dW is not None:
+    given = dW is not None
+    if given:
         if dtype not in (None, dW.dtype):
             raise TypeError(f"dW must be {dtype}, got {dW.dtype}")
         if tuple(dW.shape) != (V, d) or not dW.is_contiguous():
@@ -112,6 +116,8 @@ def embedding_backward(g, tokens, V, scale=1.0, dW=None, accumulate=False, dtype
         if dW is None:
             dW = torch.empty(V, d, dtype=dtype, device=dev)
         _backward(g, code, ldg, tokens, N, d, V, scale, dW, accumulate, ws, stream)
+    if given:
+        _written(dW)
     return dW
 
 
