@@ -206,8 +206,14 @@ _AdjustedLogits = None
 
 def differentiable_adjusted_logits(logits, history=None, lengths=None, prompt=None, repetition=1.0, frequency=0.0,
                                    presence=0.0, bias_tokens=None, bias=None, allowed=None):
-    """``adjust_logits``, differentiable in the logits (not in the penalties and biases)."""
+    """``adjust_logits``, differentiable in the logits. Penalties and biases have no gradient: one that
+    requires it is refused (detach it)."""
+    import torch
     global _AdjustedLogits
+    if torch.is_grad_enabled():
+        for name, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence), ("bias", bias)):
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} has no gradient: detach it")
     if _AdjustedLogits is None:
         _AdjustedLogits = _autograd_function()
     return _AdjustedLogits.apply(logits, history, lengths, prompt, repetition, frequency, presence, bias_tokens, bias,

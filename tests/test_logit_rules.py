@@ -464,6 +464,41 @@ def test_binding_refusals(fckl, bad):
         bad(fckl, torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("name", ["repetition", "frequency", "presence", "bias"])
+def test_penalties_that_require_a_gradient_are_refused(fckl, name):
+    """The rules have a gradient of the logits alone: none is dropped without notice. Without gradients, and
+    for tensors that ask for none, that check does not apply (and the CPU tensors are refused for where they are)."""
+    z, h = torch.zeros(3, 8, requires_grad=True), torch.zeros(3, 2, dtype=torch.int32)
+    k = dict(history=h, repetition=torch.ones(3), frequency=torch.ones(3), presence=torch.ones(3), bias_tokens=h,
+             bias=torch.ones(3, 2))
+    k[name].requires_grad_()
+    with pytest.raises(ValueError, match=f"{name} has no gradient"):
+        fckl.differentiable_adjusted_logits(z, **k)
+    with pytest.raises(Exception) as e, torch.no_grad():
+        fckl.differentiable_adjusted_logits(z, **k)
+    assert "has no gradient" not in str(e.value)
+    k[name] = k[name].detach()
+    with pytest.raises(Exception) as e:
+        fckl.differentiable_adjusted_logits(z, **k)
+    assert "has no gradient" not in str(e.value)
+
+
+@gpu
+def test_penalties_that_require_no_gradient_here(fckl):
+    """The same tensors detached, or without gradients, give what the direct call gives."""
+    z = logits(3, 40, "fp32", 1).contiguous()
+    k = rules(3, 40, 9, 2, 2)
+    want = fckl.adjust_logits(z, **k)
+    for name in ("repetition", "frequency", "presence", "bias"):
+        own = dict(k, **{name: k[name].clone().requires_grad_()})
+        with pytest.raises(ValueError, match=f"{name} has no gradient"):
+            fckl.differentiable_adjusted_logits(z, **own)
+        with torch.no_grad():
+            assert torch.equal(fckl.differentiable_adjusted_logits(z, **own), want)
+        own[name] = own[name].detach()
+        assert torch.equal(fckl.differentiable_adjusted_logits(z.clone().requires_grad_(), **own), want)
+
+
 # ------------------------------------------------------------------ the oracle (CPU)
 def test_oracle_closed_forms():
     z = np.array([[2.0, -2.0, 1.0, 0.5, 4.0]])
