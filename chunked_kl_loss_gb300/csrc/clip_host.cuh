@@ -24,26 +24,32 @@ size_t clip_workspace(int64_t count) {
   return STATUS_WS_BYTES + size_t(std::max<int64_t>(1, cdiv(count, CLIP_CAP))) * CLIP_BLOCKS * sizeof(double);
 }
 
-// No tensor of a list that is written may overlap another one's input or output, its own input apart.
+// Whether a tensor that is written overlaps another one's input or output (its own input apart). Inputs
+// that are only read may overlap each other.
 bool clip_overlaps(const ClipList& l) {
   struct Span {
     uintptr_t a, b;
+    bool written;
   };
   std::vector<Span> v;
   v.reserve(2 * size_t(l.count));
   bool sorted = true;
-  auto add = [&](const void* p, int64_t bytes) {
+  auto add = [&](const void* p, int64_t bytes, bool written) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     if (!v.empty() && v.back().a > a) sorted = false;
-    v.push_back({a, a + uintptr_t(bytes)});
+    v.push_back({a, a + uintptr_t(bytes), written});
   };
   for (int i = 0; i < l.count; ++i)
-    if (l.n[i]) add(l.out[i], l.n[i] * int64_t(value_bytes(l.out_types[i])));
+    if (l.n[i]) add(l.out[i], l.n[i] * int64_t(value_bytes(l.out_types[i])), true);
   for (int i = 0; i < l.count; ++i)
-    if (l.n[i] && l.in[i] != l.out[i]) add(l.in[i], l.n[i] * int64_t(value_bytes(l.types[i])));
+    if (l.n[i] && l.in[i] != l.out[i]) add(l.in[i], l.n[i] * int64_t(value_bytes(l.types[i])), false);
   if (!sorted) std::sort(v.begin(), v.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
-  for (size_t i = 1; i < v.size(); ++i)
-    if (v[i].a < v[i - 1].b) return true;
+  uintptr_t written_to = 0, any_to = 0;  // where the spans so far end
+  for (const Span& x : v) {
+    if (x.a < (x.written ? any_to : written_to)) return true;
+    if (x.written) written_to = std::max(written_to, x.b);
+    any_to = std::max(any_to, x.b);
+  }
   return false;
 }
 

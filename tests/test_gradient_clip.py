@@ -247,6 +247,44 @@ def test_argument_errors_launch_nothing(fckl):
     assert lib.fckl_launch_count() == before
 
 
+def test_overlaps_that_are_refused(fckl):
+    """Only what is written may overlap nothing: gradients that are read alone may lie in each other, in any
+    order. (The workspace's size is checked after the lists, so that a list that passes gets that far.)"""
+    lib = fckl.load()
+    p, z, before = ctypes.c_void_p(4096), ctypes.c_void_p(0), lib.fckl_launch_count()
+
+    def clip(ptrs, to, sizes):
+        types = [fckl.F32] * len(ptrs)
+        a, b, c, k = _arrays(ptrs, sizes, types)
+        d, _, e, _ = _arrays(to, sizes, types)
+        return lib.fckl_clip_gradients(a, b, c, k, 1.0, d, e, p, p, 0, z)
+
+    A, B, C, D = 1 << 20, 1 << 21, 1 << 22, 1 << 23
+    for ptrs, to, sizes in (((A, A), (C, D), (100, 100)), ((A, A + 40), (C, D), (100, 10)), ((A + 40, A), (D, C), (10, 100)),
+                            ((A, B, A, A + 396), (C, B, D, C + 400), (100, 100, 100, 50)), ((A, A, A), (C, C + 400, D), (100, 100, 1)),
+                            ((A,), (A,), (100,)), ((A, A), (A, C), (0, 100)), ((A, A, A + 20), (D, C, B), (100, 0, 10))):
+        assert clip(ptrs, to, sizes) == fckl.ERR_WORKSPACE, (ptrs, to, sizes)
+    for ptrs, to, sizes in (((A, A), (A, C), (100, 100)), ((A, A), (C, A), (100, 100)), ((A, A), (A, A), (100, 100)),
+                            ((A, B), (C, C), (100, 100)), ((A, B), (C, C + 396), (100, 100)), ((A, B), (C + 396, C), (100, 100)),
+                            ((A, A), (C, A + 396), (100, 100)), ((A, A + 4, B), (C, D, A + 200), (100, 10, 100)),
+                            ((A, A + 40), (C, A + 40), (100, 10)), ((A, B), (C, C + 200), (100, 10)),
+                            ((A, A + 8, A + 200), (C, D, A + 200), (100, 10, 1))):
+        assert clip(ptrs, to, sizes) == fckl.ERR_ARG, (ptrs, to, sizes)
+    assert lib.fckl_launch_count() == before
+
+
+@gpu
+def test_a_gradient_listed_twice(fckl):
+    """Into other tensors: it counts twice, as in gradient_norm. A view of it as well."""
+    a, b = tensor((300, 7), "fp32", 1), tensor((41,), "bf16", 2)
+    grads = [a, b, a, a[10:20]]
+    out = [torch.empty(g.shape, dtype=g.dtype, device="cuda") for g in grads]
+    norm = fckl.clip_gradients(grads, 1.0, out=out)
+    check_norm(norm, grads)
+    check_scaled(out, grads, 1.0)
+    assert torch.equal(norm, fckl.gradient_norm(grads)) and torch.equal(out[0], out[2])
+
+
 @pytest.mark.parametrize("bad", [
     lambda f, g: f.gradient_norm([g]), lambda f, g: f.clip_gradients([g], 1.0), lambda f, g: f.clip_gradients([g], -1.0),
     lambda f, g: f.clip_gradients([g], float("nan")), lambda f, g: f.clip_gradients([g], 1.0, out=[]),
