@@ -16,7 +16,7 @@ import ctypes
 import weakref
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _for_stream, _here, _stream, _value_code, _written
+from .scoring import _for_stream, _here, _stream, _value_code
 
 __all__ = ["gradient_norm", "clip_gradients"]
 
@@ -44,11 +44,12 @@ def _dense(t):
 
 def _list(name, tensors, device):
     """(addresses, types, whether all are contiguous) of the tensors, as arrays that the library reads."""
+    import torch
     index = -1 if device.type == "cpu" else device.index
-    if {t.get_device() for t in tensors} - {index}:
+    if set(map(torch.Tensor.get_device, tensors)) - {index}:
         where = [t.device for t in tensors if t.get_device() != index]
         raise ValueError(f"{name} must be on one device, got {where[0]} beside {device}")
-    contiguous = all([t.is_contiguous() for t in tensors])
+    contiguous = all(map(torch.Tensor.is_contiguous, tensors))
     if not contiguous:
         for t in tensors:
             if not _dense(t):
@@ -58,11 +59,12 @@ def _list(name, tensors, device):
         types = array.array("i", [*codes.values()]) * len(tensors)
     else:
         types = array.array("i", [codes[t.dtype] for t in tensors])
-    return array.array("Q", [t.data_ptr() for t in tensors]), types, contiguous
+    return array.array("Q", list(map(torch.Tensor.data_ptr, tensors))), types, contiguous
 
 
 def _sizes(tensors):
-    return array.array("q", [t.numel() for t in tensors])
+    import torch
+    return array.array("q", list(map(torch.Tensor.numel, tensors)))
 
 
 def _given(tensors):
@@ -119,6 +121,7 @@ def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
     place, or into ``out``: tensors of the same shapes and memory orders, of any of the three types (the product is
     fp32, rounded once). What is written may overlap no other tensor. A NaN norm makes the gradients NaN, an infinite one
     scales them by 0."""
+    import torch
     grads, gaps = _given(grads)
     if out is not None:
         out, out_gaps = _given(out)
@@ -143,5 +146,5 @@ def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
                                          _stream(stream))
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_clip_gradients")
-    _written(*(grads if out is None else out))
+    torch.autograd.graph.increment_version(grads if out is None else out)  # a backward pass that saved them raises
     return norm

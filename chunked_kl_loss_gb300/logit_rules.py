@@ -19,7 +19,7 @@ from __future__ import annotations
 import ctypes
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _address, _dense, _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _written, _ws
+from .scoring import _address, _dense, _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _ws
 
 __all__ = ["adjust_logits", "adjust_logits_backward", "differentiable_adjusted_logits"]
 
@@ -135,7 +135,7 @@ def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=1.
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_adjust_logits")
     if given:
-        _written(out)
+        torch.autograd.graph.increment_version(out)  # a backward pass that saved it raises
     return out
 
 
@@ -174,7 +174,7 @@ def adjust_logits_backward(g, logits, history=None, lengths=None, repetition=1.0
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_adjust_logits_backward")
     if given:
-        _written(out)
+        torch.autograd.graph.increment_version(out)  # a backward pass that saved it raises
     return out
 
 

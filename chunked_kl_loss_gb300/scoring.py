@@ -138,12 +138,6 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _written(*tensors):
-    """Counts the caller's tensors as modified, so that a backward pass that saved them raises."""
-    import torch
-    torch.autograd.graph.increment_version(tensors)
-
-
 _here = contextlib.nullcontext()
 
 

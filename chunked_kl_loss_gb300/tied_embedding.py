@@ -17,7 +17,7 @@ import ctypes
 import weakref
 
 import chunked_kl_loss_gb300 as _pkg
-from .scoring import _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _written, _ws
+from .scoring import _for_stream, _here, _here_all, _on_device, _rows, _stream, _value_code, _ws
 
 __all__ = ["embedding", "embedding_backward", "differentiable_embedding"]
 
@@ -81,7 +81,7 @@ def embedding(W, tokens, scale=1.0, out=None, ws=None, stream=None):
     if st != _pkg.OK:
         raise _pkg.FcklError(st, "fckl_embedding")
     if given:
-        _written(out)
+        torch.autograd.graph.increment_version(out)  # a backward pass that saved it raises
     return out
 
 
@@ -117,7 +117,7 @@ def embedding_backward(g, tokens, V, scale=1.0, dW=None, accumulate=False, dtype
             dW = torch.empty(V, d, dtype=dtype, device=dev)
         _backward(g, code, ldg, tokens, N, d, V, scale, dW, accumulate, ws, stream)
     if given:
-        _written(dW)
+        torch.autograd.graph.increment_version(dW)  # a backward pass that saved it raises
     return dW
 
 
