@@ -80,8 +80,12 @@ int launch_adjust_kernel(DevInfo* di, AdjustParams p, int64_t N, cudaStream_t s)
 }
 
 // Through shared memory where every row of the input and of the output lies alike to the 16-byte boundaries;
-// in place too if there is a mask (2000 x 50000 bf16 with 2% masked: 97 us; writing the masked places for
-// themselves, without reading the others, took 111, and 72 against 78 at 1024 x 50000 fp32 with 0.4% left).
+// in place too if there is a mask (2000 x 50000 bf16 with 2% masked, 1000 history entries and 8 biases: 97 us,
+// 1024 x 50000 fp32 with 0.4% left: 78; writing the masked places for themselves, without reading the others,
+// took 111 and 72). Without a history those 2000 rows take 63 us (floor 62), with 1024 entries anywhere in the
+// row and a frequency penalty 105 (floor 63): the gathering, as into a new tensor (63 and 106). Rows that lie
+// differently go value by value: 4096 rows of 50257 out of 50304 bf16 into a dense tensor, 1024 history entries,
+// 16 biases and a mask, 456 us; into rows that lie alike 260 (floor 129); fp32 476 and 323 (252).
 template <typename T, AdjustKind KIND>
 int launch_adjust(DevInfo* di, const AdjustParams& p, int64_t N, cudaStream_t s) {
   constexpr bool GRAD = KIND == ADJUST_GRAD;

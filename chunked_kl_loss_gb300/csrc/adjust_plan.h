@@ -55,7 +55,8 @@ struct AdjustPlan {
 // and in the staged kernel with how many threads and stages. Taken is the least estimated time, in us, of
 // waves of blocks that each gather first (2.5 us, 1 us for every 8 history entries a thread reads, 0.6 us
 // for each that it puts into the table or 0.3 into words, 1 us for every 64 KB of shared memory cleared)
-// and then stream at their share of an SM's 44 GB/s. The estimates are mostly 10 to 40% below what is
+// and then stream at their share of an SM's 44 GB/s, 10% slower with two stages than with three (4096 x 128256:
+// 15%). The estimates are mostly 10 to 40% below what is
 // measured, alike for the choices of one shape: 64 x 50001 fp32 with 16384 history entries in 4 segments and
 // 2 stages 14 us, in 8 segments 24, with 3 stages 23; 16 x 128256 with 4000 in 1, 4 and 16 segments 29, 12
 // and 7.6.

@@ -8,7 +8,7 @@
 namespace fckl {
 namespace {
 
-constexpr int CLIP_CAP_SMALL = 32, CLIP_CAP = 896;  // tensors of a launch; the larger table fills 29 KB of arguments
+constexpr int CLIP_CAP_SMALL = 32, CLIP_CAP = 896;  // tensors of a launch; the larger table takes 26 KB of arguments
 constexpr int64_t CLIP_COUNT_MAX = 1 << 20;
 
 struct ClipList {

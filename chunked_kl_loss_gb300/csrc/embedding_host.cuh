@@ -63,6 +63,9 @@ int launch_embedding_pack(int e, const void* W, int64_t ldw, const int32_t* toke
 // ------------------------------------------------------------------ gradient
 constexpr int GSUM_TILE_MIN = 8;
 constexpr int SORT_CTA_ITEMS = 1024;  // positions of a sorting block, as long as the cluster can grow
+// SMs that tiles are cut for: a constant, so that the workspace's size and the order of the sums do not depend
+// on the device that is current.
+constexpr int GSUM_SMS = 152;
 
 struct EmbedGradPlan {
   int passes, bits;
@@ -71,11 +74,11 @@ struct EmbedGradPlan {
   size_t off_a, off_b, off_partial, total;
 };
 
-// Entries of a tile: as many as leave blocks for the GPU (152 SMs) several times over, between GSUM_TILE_MIN
-// and `most`. More slices never give smaller tiles.
+// Entries of a tile: as many as leave blocks for the GPU several times over, between GSUM_TILE_MIN and
+// `most`. More slices never give smaller tiles.
 int grad_tile(int64_t N, int64_t slices, int most) {
   int tile = GSUM_TILE_MIN;
-  while (tile < most && cdiv(N, 2 * tile) * slices >= 4 * 152) tile *= 2;
+  while (tile < most && cdiv(N, 2 * tile) * slices >= 4 * GSUM_SMS) tile *= 2;
   return tile;
 }
 
@@ -139,7 +142,8 @@ int launch_sort_tokens(const DevInfo* di, SortParams p, cudaStream_t s) {
   while ((int64_t(p.cluster) << p.per_log2) < p.N) ++p.per_log2;
   attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
   cfg.dynamicSmemBytes = (1 << p.per_log2) <= SORT_TILE ? sizeof(uint2) << p.per_log2 : 0;
-  // two blocks an SM, and no more than have 64 KB to clear
+  // two blocks for every SM (one runs at a time, with the sort's 128 registers a thread), and no more than
+  // have 64 KB to clear
   const int64_t clear = std::min<int64_t>(cdiv(p.zero_bytes, 65536), 2 * int64_t(di->sms) - p.cluster);
   cfg.gridDim = dim3(static_cast<unsigned>(p.cluster + rup(clear, p.cluster)));
   return launch(KIND_SORT_TOKENS, s, "sort_tokens", [&] { cudaLaunchKernelEx(&cfg, sort_tokens_kernel, p); });

@@ -119,8 +119,8 @@ def gradient_norm(grads, ws=None, stream=None):
 def clip_gradients(grads, max_norm, out=None, ws=None, stream=None):
     """Scales ``grads`` by min(1, max_norm / (norm + 1e-6)) and returns the norm before that, fp32 [1]. In
     place, or into ``out``: tensors of the same shapes and memory orders, of any of the three types (the product is
-    fp32, rounded once). What is written may overlap no other tensor. A NaN norm makes the gradients NaN, an infinite one
-    scales them by 0."""
+    fp32, rounded once). What is written may overlap no other tensor. A NaN norm makes the gradients NaN, an
+    infinite gradient scales the others by 0."""
     import torch
     grads, gaps = _given(grads)
     if out is not None:

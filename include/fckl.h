@@ -368,7 +368,9 @@ int fckl_gradient_norm(const void* const* grads, const int64_t* sizes, const int
 /* The same norm, and out[i] = c * grads[i] with c = min(1, max_norm / (norm + 1e-6)), the product in fp32,
  * rounded once to out's type. out[i] may be grads[i] itself (then of its type; nothing is written where
  * c = 1); otherwise nothing that is written may overlap another tensor (FCKL_ERR_ARG), while gradients
- * that are only read may, and count as often as they are listed. c is NaN where the norm is, and 0 where it is infinite.
+ * that are only read may, and count as often as they are listed. c is NaN where the norm is, and 0 where a
+ * gradient is infinite (NaN if max_norm is as well); finite gradients whose norm is above fp32's largest
+ * number are scaled by the true one.
  * No host synchronisation. The workspace is that of fckl_gradient_norm. */
 int fckl_clip_gradients(const void* const* grads, const int64_t* sizes, const int* dtypes, int count, float max_norm,
                         void* const* out, const int* out_dtypes, float* norm, void* ws, size_t ws_bytes,
